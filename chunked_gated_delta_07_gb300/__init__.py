@@ -30,7 +30,9 @@ EXPORTS = ("gdr_chunk_fwd", "gdr_chunk_fwd_ex", "gdr_chunk_fwd_workspace_size",
            "gdr_chunk_fwd_host", "gdr_gate_cumsum", "gdr_wy_repr", "gdr_get_status",
            "gdr_status_string", "gdr_release", "gdr_launch_count", "gdr_profile_enable",
            "gdr_profile_read", "gdr_profile_select", "gdr_chunk_fwd_noalloc", "gdr_recurrent_fwd", "gdr_chunk_bwd", "gdr_chunk_fwd_vec",
-           "gdr_router_topk", "gdr_router_bias_update", "gdr_chunk_bwd_vec")
+           "gdr_router_topk", "gdr_router_bias_update", "gdr_chunk_bwd_vec",
+           "gdr_decay_fwd", "gdr_decay_bwd", "gdr_decay_workspace_size", "gdr_decay_recurrent_fwd",
+           "gdr_layer_norm_fwd", "gdr_layer_norm_bwd")
 
 _lock = threading.Lock()
 _lib = None
@@ -57,6 +59,12 @@ _SIGS = {
     "gdr_router_topk": (_I, [_P] * 5 + [_I64, _I, _I, _I, _P]),
     "gdr_router_bias_update": (_I, [_P] * 3 + [_I, _I, ctypes.c_double, ctypes.c_double, _F, _P]),
     "gdr_chunk_bwd_vec": (_I, [_P] * 15 + [_I, _I64, _I, _I, _I, _I, _F, _I, _P]),
+    "gdr_decay_fwd": (_I, [_P] * 8 + [_I, _I64, _I, _I, _I, _F, _I, _I, _P, _SZ, _P]),
+    "gdr_decay_bwd": (_I, [_P] * 12 + [_I, _I64, _I, _I, _I, _F, _I, _I, _P, _SZ, _P]),
+    "gdr_decay_workspace_size": (_SZ, [_I, _I64, _I, _I, _I, _I, _I, _I, _I]),
+    "gdr_decay_recurrent_fwd": (_I, [_P] * 6 + [_I, _I64, _I, _I, _I, _F, _I, _P]),
+    "gdr_layer_norm_fwd": (_I, [_P] * 6 + [_I64, _I, _I, _F, _I, _P]),
+    "gdr_layer_norm_bwd": (_I, [_P] * 8 + [_I64, _I, _I, _I, _P]),
 }
 
 
@@ -288,6 +296,221 @@ def chunk_bwd(q, k, v, a, beta, dout=None, dhT=None, h0=None, cu_seqlens=None, c
     if rc != GDR_OK:
         raise GdrError(rc, "gdr_chunk_bwd")
     return dq, dkk, dvv, da, dbeta, dh0
+
+
+# ---- linear attention with one constant decay per head -----------------------------------
+def gdr_decay_fwd(q, k, v, log_decay, h0, out, hT, cu_seqlens, B, T, H, dk, dv, scale, dtype, path,
+                  workspace=None, workspace_bytes=0, stream=None) -> int:
+    return lib().gdr_decay_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h0), _ptr(out), _ptr(hT),
+                               _ptr(cu_seqlens), B, T, H, dk, dv, float(scale), dtype, path,
+                               _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def gdr_decay_bwd(q, k, v, log_decay, h0, dout, dhT, dq, dk, dv, dh0, cu_seqlens, B, T, H, dk_dim,
+                  dv_dim, scale, dtype, path, workspace=None, workspace_bytes=0, stream=None) -> int:
+    return lib().gdr_decay_bwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(h0), _ptr(dout), _ptr(dhT),
+                               _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dh0), _ptr(cu_seqlens), B, T, H, dk_dim,
+                               dv_dim, float(scale), dtype, path, _ptr(workspace), workspace_bytes,
+                               _stream(stream))
+
+
+def gdr_decay_workspace_size(B, T, H, dk, dv, packed=False, backward=False, dtype=GDR_BF16,
+                             path=GDR_PATH_AUTO) -> int:
+    return int(lib().gdr_decay_workspace_size(B, T, H, dk, dv, int(packed), int(backward), dtype, path))
+
+
+def gdr_decay_recurrent_fwd(q, k, v, log_decay, state, out, N, T, H, dk, dv, scale, dtype,
+                            stream=None) -> int:
+    return lib().gdr_decay_recurrent_fwd(_ptr(q), _ptr(k), _ptr(v), _ptr(log_decay), _ptr(state), _ptr(out),
+                                         N, T, H, dk, dv, float(scale), dtype, _stream(stream))
+
+
+def check_decay_inputs(q, k, v, log_decay, h0=None, cu_seqlens=None, dout=None, dhT=None, out=None, hT=None):
+    """Check the tensors of a decay call against q [B, T, H, dk], as check_sequence_inputs does;
+    log_decay is fp32 [H].  Returns (B, T, H, dk, dv, N)."""
+    import torch
+    if q is None or q.dim() != 4:
+        raise ValueError("q must be [B, T, H, dk]")
+    dt, dev = q.dtype, q.device
+    if dt not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"q: dtype {dt}, expected bfloat16 or float32")
+    B, T, H, dk = q.shape
+    if v is None or v.dim() != 4:
+        raise ValueError("v must be [B, T, H, dv]")
+    dv = v.shape[3]
+    _expect("q", q, q.shape, dt, dev)
+    _expect("k", k, q.shape, dt, dev)
+    _expect("v", v, (B, T, H, dv), dt, dev)
+    _expect("log_decay", log_decay, (H,), torch.float32, dev)
+    N = B
+    if cu_seqlens is not None:
+        if B != 1:
+            raise ValueError("with cu_seqlens the token tensors are [1, T_total, H, *]")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be [N + 1] with N >= 1")
+        _expect("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, dev)
+        N = cu_seqlens.numel() - 1
+    for name, t in (("h0", h0), ("hT", hT), ("dhT", dhT)):
+        if t is not None:
+            _expect(name, t, (N, H, dk, dv), torch.float32, dev)
+    for name, t in (("out", out), ("dout", dout)):
+        if t is not None:
+            _expect(name, t, (B, T, H, dv), dt, dev)
+    return B, T, H, dk, dv, N
+
+
+def _workspace_bytes(workspace, device):
+    if workspace is None:
+        return 0
+    _require_cuda(workspace, "workspace")
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on q's device")
+    return workspace.numel() * workspace.element_size()
+
+
+def decay_fwd(q, k, v, log_decay, h0=None, cu_seqlens=None, scale=1.0, path="auto", out=None, hT=None,
+              want_state=True, stream=None, workspace=None):
+    """Linear attention with one decay per head: S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,
+    o_t = scale S_t^T q_t.  Returns (out, hT).
+
+    q, k [B,T,H,dk], v [B,T,H,dv] on one CUDA device, of one dtype (bf16 or fp32); log_decay [H]
+    fp32; with cu_seqlens (int32, N+1) B must be 1; h0, hT [N,H,dk,dv] fp32 (hT may be h0)."""
+    import torch
+    B, T, H, dk, dv, N = check_decay_inputs(q, k, v, log_decay, h0, cu_seqlens, out=out, hT=hT)
+    _require_cuda(q)
+    if path not in _PATHS:
+        raise ValueError(f"path must be one of {sorted(_PATHS)}")
+    if out is None:
+        out = torch.empty_like(v)
+    if hT is None and want_state:
+        hT = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device)
+    rc = gdr_decay_fwd(q, k, v, log_decay, h0, out, hT, cu_seqlens, N, T, H, dk, dv, scale, dtype_code(q),
+                       _PATHS[path], workspace, _workspace_bytes(workspace, q.device), stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_decay_fwd")
+    return out, hT
+
+
+def decay_bwd(q, k, v, log_decay, dout, dhT=None, h0=None, cu_seqlens=None, scale=1.0, path="auto",
+              want_dh0=True, stream=None, workspace=None):
+    """Gradients of <dout, out> + <dhT, hT> of decay_fwd: returns (dq, dk, dv, dh0)."""
+    import torch
+    if dout is None:
+        raise ValueError("dout is required")
+    B, T, H, dk, dv, N = check_decay_inputs(q, k, v, log_decay, h0, cu_seqlens, dout=dout, dhT=dhT)
+    _require_cuda(q)
+    if path not in _PATHS:
+        raise ValueError(f"path must be one of {sorted(_PATHS)}")
+    dq, dkk, dvv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    dh0 = torch.empty((N, H, dk, dv), dtype=torch.float32, device=q.device) if want_dh0 else None
+    rc = gdr_decay_bwd(q, k, v, log_decay, h0, dout, dhT, dq, dkk, dvv, dh0, cu_seqlens, N, T, H, dk, dv,
+                       scale, dtype_code(q), _PATHS[path], workspace, _workspace_bytes(workspace, q.device),
+                       stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_decay_bwd")
+    return dq, dkk, dvv, dh0
+
+
+def decay_recurrent_fwd(q, k, v, log_decay, state, scale=1.0, out=None, stream=None):
+    """Decode T tokens of the decay form: q, k [N,T,H,dk], v [N,T,H,dv], log_decay [H] fp32, state
+    [N,H,dk,dv] fp32 updated in place; returns out [N,T,H,dv]."""
+    import torch
+    if state is None:
+        raise ValueError("state is required")
+    N, T, H, dk, dv, _ = check_decay_inputs(q, k, v, log_decay, h0=state, out=out)
+    _require_cuda(q)
+    if out is None:
+        out = torch.empty_like(v)
+    rc = gdr_decay_recurrent_fwd(q, k, v, log_decay, state, out, N, T, H, dk, dv, scale, dtype_code(q), stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_decay_recurrent_fwd")
+    return out
+
+
+# ---- layer norm -----------------------------------------------------------------------------
+def gdr_layer_norm_fwd(x, weight, bias, y, mean, rstd, rows, G, D, eps, dtype, stream=None) -> int:
+    return lib().gdr_layer_norm_fwd(_ptr(x), _ptr(weight), _ptr(bias), _ptr(y), _ptr(mean), _ptr(rstd), rows, G,
+                                    D, float(eps), dtype, _stream(stream))
+
+
+def gdr_layer_norm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, rows, G, D, dtype, stream=None) -> int:
+    return lib().gdr_layer_norm_bwd(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dx),
+                                    _ptr(dweight), _ptr(dbias), rows, G, D, dtype, _stream(stream))
+
+
+def check_norm_inputs(x, weight=None, bias=None, dy=None, mean=None, rstd=None, out=None):
+    """Check the tensors of a layer-norm call against x [.., D]: weight and bias fp32 of shape [D] or
+    of x's last two axes [G, D] (one weight per head), dy and out like x, mean and rstd fp32 [..].
+    Returns (rows, G, D)."""
+    import torch
+    if x is None or x.dim() < 1:
+        raise ValueError("x must be [.., D]")
+    dt, dev = x.dtype, x.device
+    if dt not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"x: dtype {dt}, expected bfloat16 or float32")
+    D = x.shape[-1]
+    if D < 1:
+        raise ValueError("x: the last axis is empty")
+    _expect("x", x, x.shape, dt, dev)
+    G = 1
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            per_head = t.dim() == 2 and x.dim() >= 2
+            if per_head:
+                G = x.shape[-2]
+            _expect(name, t, (x.shape[-2], D) if per_head else (D,), torch.float32, dev)
+    if weight is not None and bias is not None and weight.dim() != bias.dim():
+        raise ValueError("weight and bias must have one shape")
+    for name, t in (("dy", dy), ("out", out)):
+        if t is not None:
+            _expect(name, t, x.shape, dt, dev)
+    for name, t in (("mean", mean), ("rstd", rstd)):
+        if t is not None:
+            _expect(name, t, x.shape[:-1], torch.float32, dev)
+    return x.numel() // D, max(G, 1), D
+
+
+def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, want_stats=True, stream=None):
+    """Layer norm over the last axis: returns (y, mean, rstd); without want_stats the latter two
+    are None.  x [.., D] bf16 or fp32; weight, bias fp32 [D], or [G, D] with x [.., G, D] (one
+    weight per head).  out may be x."""
+    import torch
+    rows, G, D = check_norm_inputs(x, weight, bias, out=out)
+    _require_cuda(x, "x")
+    if out is None:
+        out = torch.empty_like(x)
+    mean = rstd = None
+    if want_stats:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    rc = gdr_layer_norm_fwd(x, weight, bias, out, mean, rstd, rows, G, D, eps, dtype_code(x), stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_layer_norm_fwd")
+    return out, mean, rstd
+
+
+def layer_norm_bwd(dy, x, mean, rstd, weight=None, per_head=False, want_dweight=True, want_dbias=True,
+                   stream=None):
+    """Backward of layer_norm_fwd from its mean and rstd: returns (dx, dweight, dbias), the latter
+    two fp32 with weight's shape (without a weight: [D], or [G, D] if per_head), None where not
+    wanted."""
+    import torch
+    if dy is None or mean is None or rstd is None:
+        raise ValueError("dy, mean and rstd are required")
+    rows, G, D = check_norm_inputs(x, weight, dy=dy, mean=mean, rstd=rstd)
+    _require_cuda(x, "x")
+    if weight is not None:
+        shape = weight.shape
+    else:
+        shape = x.shape[-2:] if per_head else x.shape[-1:]
+        G = max(1, x.shape[-2]) if per_head else 1
+    dx = torch.empty_like(x)
+    dw = torch.empty(shape, dtype=torch.float32, device=x.device) if want_dweight else None
+    db = torch.empty(shape, dtype=torch.float32, device=x.device) if want_dbias else None
+    rc = gdr_layer_norm_bwd(dy, x, mean, rstd, weight, dx, dw, db, rows, G, D, dtype_code(x), stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_layer_norm_bwd")
+    return dx, dw, db
 
 
 def gdr_gate_cumsum(a, G, cu_seqlens, B, T, H, chunk, b, dtype, gate, stream=None) -> int:

@@ -1,15 +1,19 @@
 // gdr_api.cu -- the C ABI: argument checks, per-device state, workspace
 // layout and dispatch to the kernel families.  No arithmetic of the method
 // lives here; every step of the pass runs in the kernels.
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
 #include <deque>
+#include <initializer_list>
 #include <mutex>
 #include <string>
+#include <utility>
 #include <vector>
 
+#include "gdr_decay.cuh"
 #include "gdr_internal.cuh"
 #include "gdr_tc.cuh"
 
@@ -524,6 +528,172 @@ gdr_status_t validate_forward(const void *q, const void *k, const void *v, const
                       path, &s);
 }
 
+// ---------------------------------------------------------------------------
+// linear attention with one constant decay per head
+// ---------------------------------------------------------------------------
+namespace {
+
+// Scratch of one call, every region 256-byte aligned: the plan (packed input), the
+// boundary states of the forward chain and, for the backward pass, of the reversed one.
+struct DecayLayout {
+    size_t plan = 0, slots = 0, slots_rev = 0, copy = 0, total = 0;
+};
+
+struct DecayShape {
+    int N, H, dk, dv;
+    int64_t T_per, T_total;
+    bool varlen;
+};
+
+// Segments of a call.  A pass runs one block (tensor cores) or one column slice (CUDA
+// cores) per (segment, head): `units` per segment and sequence, `slots` at a time.  Equal
+// sequences are cut into the number of segments s that minimises
+//     ceil(units N s / slots) (ceil(tiles / s) + fixed) + (s - 1) / s * local
+// in tiles: whole rounds of the machine, a start-up per segment, and the local pass over
+// the inner segments, which reads half of what the output pass moves.  Packed sequences
+// (lengths unknown on the host) are cut into even shares of all tiles, two per slot, so
+// that one long sequence among short ones is cut too and the rounds even out.
+// GDR_DECAY_SEG_TILES=n cuts into n tiles per segment whatever the sizes (the parity tests
+// run many short segments).
+DecayGeom decay_geom(const DecayShape &s, int64_t units, int64_t slots, int64_t min_tiles, double fixed) {
+    const char *env = std::getenv("GDR_DECAY_SEG_TILES");
+    const int64_t set = env ? std::atoll(env) : 0;
+    DecayGeom g{};
+    g.dense = !s.varlen;
+    g.N = s.N;
+    g.H = s.H;
+    g.T_per = s.T_per;
+    g.T_total = s.T_total;
+    if (g.dense) {
+        const int64_t tiles = std::max<int64_t>(1, (s.T_per + kDecayTile - 1) / kDecayTile);
+        int64_t best = 1;
+        double least = 0;
+        for (int64_t c = 1; c <= 4 * slots && (c == 1 || c * min_tiles <= tiles); ++c) {
+            const int64_t rounds = (units * s.N * c + slots - 1) / slots;
+            const double local = 0.5 * (double)tiles * (double)units * s.N / slots;
+            const double cost = rounds * ((double)((tiles + c - 1) / c) + fixed) + (c - 1.0) / c * local;
+            if (c == 1 || cost < least) {
+                best = c;
+                least = cost;
+            }
+            if (rounds > 8) break;   // enough blocks to even out
+        }
+        const int64_t seg = set > 0 ? set : (tiles + best - 1) / best;
+        g.seg_tokens = seg * kDecayTile;
+        g.segs_per_seq = (tiles + seg - 1) / seg;
+        g.max_segs = g.segs_per_seq * s.N;
+        g.max_slots = g.max_segs - s.N;
+    } else {
+        const int64_t tiles = (s.T_total + kDecayTile - 1) / kDecayTile;
+        const int64_t even = std::max(min_tiles, (tiles * units + 2 * slots - 1) / (2 * slots));
+        const int64_t seg = std::min<int64_t>(set > 0 ? set : even, 1 << 24);
+        g.seg_tokens = seg * kDecayTile;
+        // a sequence of len tokens has ceil(len / seg) segments, at least one
+        g.max_slots = s.T_total / g.seg_tokens;
+        g.max_segs = g.max_slots + s.N;
+    }
+    return g;
+}
+
+gdr_status_t check_decay(const float *log_decay, int B, int64_t T, int H, int dk, int dv, float scale,
+                         gdr_dtype_t dtype, gdr_path_t path, bool varlen, DecayShape *s) {
+    if (dtype != GDR_BF16 && dtype != GDR_F32) return GDR_ERR_INVALID_ARG;
+    if (path != GDR_PATH_AUTO && path != GDR_PATH_SIMT && path != GDR_PATH_TC) return GDR_ERR_INVALID_ARG;
+    if (B < 1 || H < 1 || T < 0 || dk < 1 || dv < 1 || !std::isfinite(scale)) return GDR_ERR_INVALID_ARG;
+    if ((dk != 64 && dk != 128) || (dv != 64 && dv != 128)) return GDR_ERR_UNSUPPORTED;
+    if (T > ((int64_t)1 << 40) || (int64_t)B * T > ((int64_t)1 << 40)) return GDR_ERR_UNSUPPORTED;
+    const int64_t T_total = varlen ? T : (int64_t)B * T;
+    if ((T_total > 0 && (int64_t)H > ((int64_t)1 << 40) / T_total) || (int64_t)H * B > (1 << 26))
+        return GDR_ERR_UNSUPPORTED;
+    if (T_total > 0 && !log_decay) return GDR_ERR_INVALID_ARG;
+    *s = DecayShape{B, H, dk, dv, varlen ? 0 : T, T_total, varlen};
+    return GDR_OK;
+}
+
+// No tensor-core kernel yet: every call runs on the CUDA cores.
+bool decay_tc_ok(gdr_dtype_t, const DecayShape &, std::initializer_list<const void *>) { return false; }
+
+DecayGeom decay_call_geom(const DecayShape &s, bool tc, bool backward, int sms) {
+    const int passes = backward ? 3 : 1;
+    if (tc) return decay_geom(s, (int64_t)s.H * passes, sms, 4, 2.0);
+    // CUDA cores: four resident blocks of 64 columns per SM; passes run one by one
+    return decay_geom(s, (int64_t)s.H * (std::max(s.dk, s.dv) / 64), 4 * (int64_t)sms, 1, 0.1);
+}
+
+DecayLayout decay_layout(const DecayShape &s, const DecayGeom &g, bool backward) {
+    DecayLayout L;
+    const size_t st = sizeof(float) * (size_t)s.H * s.dk * s.dv;
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += align_up(bytes);
+        return at;
+    };
+    L.plan = take(s.varlen ? 3 * sizeof(int64_t) * (size_t)(s.N + 1) : 0);
+    L.slots = take(st * g.max_slots);
+    L.slots_rev = take(backward ? st * g.max_slots : 0);
+    // forward in place (hT = h0) with segments: the entering states' copy
+    L.copy = take(!backward && g.max_slots ? st * s.N : 0);
+    L.total = off;
+    return L;
+}
+
+// The plan of packed input, and the geometry completed with it.
+gdr_status_t decay_plan(DecayGeom *g, const int32_t *cu, const float *log_decay, char *ws, const DecayLayout &L,
+                        int *status, cudaStream_t stream) {
+    g->log_decay = log_decay;
+    if (g->dense) return GDR_OK;
+    int64_t *seq_start = (int64_t *)(ws + L.plan);
+    g->p = Plan{g->N, kDecayTile, (int)(g->seg_tokens / kDecayTile), seq_start, seq_start + (g->N + 1),
+                seq_start + 2 * (g->N + 1)};
+    return launch_plan(cu, g->N, 0, g->T_total, kDecayTile, g->p.seg_chunks, seq_start, seq_start + (g->N + 1),
+                       seq_start + 2 * (g->N + 1), status, stream) == cudaSuccess
+               ? GDR_OK
+               : GDR_ERR_CUDA;
+}
+
+// Runs passes that are independent of each other, after the boundary states of those
+// chains in `chains` (local sums, then their chaining), if there are segments.
+cudaError_t decay_run(const DecayGeom &g, const DecayPass *chains, int nchains, const DecayPass *passes, int n,
+                      gdr_dtype_t dtype, bool tc, DeviceCtx *ctx, cudaStream_t stream) {
+    auto run = [&](const DecayPass *p, int k) {
+        (void)tc, (void)ctx;
+        cudaError_t err = cudaSuccess;
+        for (int i = 0; i < k && err == cudaSuccess; ++i) err = launch_decay_rec(g, p[i], dtype, stream);
+        return err;
+    };
+    if (g.max_slots > 0) {
+        cudaError_t err = run(chains, nchains);
+        for (int i = 0; i < nchains && err == cudaSuccess; ++i) err = launch_decay_combine(g, chains[i], stream);
+        if (err != cudaSuccess) return err;
+    }
+    return run(passes, n);
+}
+
+// Scratch of a call: the caller's workspace, or the internal cache grown to size.
+gdr_status_t take_workspace(DeviceCtx *ctx, void *workspace, size_t workspace_bytes, size_t need, char **ws) {
+    *ws = (char *)workspace;
+    if (*ws) return workspace_bytes < need ? GDR_ERR_NO_WORKSPACE : GDR_OK;
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!grow(&ctx->ws, &ctx->ws_bytes, need)) return GDR_ERR_CUDA;
+    *ws = (char *)ctx->ws;
+    return GDR_OK;
+}
+
+// No output may overlap an input or another output.
+bool outputs_clear(std::initializer_list<std::pair<const void *, size_t>> outs,
+                   std::initializer_list<std::pair<const void *, size_t>> ins) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (const auto &i : ins)
+            if (overlaps(o->first, o->second, i.first, i.second)) return false;
+        for (auto p = o + 1; p != outs.end(); ++p)
+            if (overlaps(o->first, o->second, p->first, p->second)) return false;
+    }
+    return true;
+}
+
+}  // namespace
+
 }  // namespace gdr
 
 using namespace gdr;
@@ -893,6 +1063,196 @@ gdr_status_t gdr_router_bias_update(const int64_t *load, float *bias, double *th
         return GDR_ERR_INVALID_ARG;
     return launch_router_update(load, bias, thresholds, E, (int)mode, q_lo, q_hi, eta,
                                 (cudaStream_t)stream) == cudaSuccess
+               ? GDR_OK
+               : GDR_ERR_CUDA;
+}
+
+size_t gdr_decay_workspace_size(int B, int64_t T, int H, int dk, int dv, int packed, int backward,
+                                gdr_dtype_t dtype, gdr_path_t path) {
+    DecayShape s;
+    const float any = 0.f;   // any address: sizes alone are asked for
+    if (check_decay(&any, B, T, H, dk, dv, 1.f, dtype, path, packed != 0, &s) != GDR_OK) return 0;
+    DeviceCtx *ctx = device_ctx();
+    const int sms = ctx ? ctx->sms : 152;
+    size_t need = 0;   // AUTO: whichever path the pointers' alignment allows
+    for (bool tc : {false, true})
+        if (path == GDR_PATH_AUTO || tc == (path == GDR_PATH_TC))
+            need = std::max(need, decay_layout(s, decay_call_geom(s, tc, backward != 0, sms), backward != 0).total);
+    return need;
+}
+
+gdr_status_t gdr_decay_fwd(const void *q, const void *k, const void *v, const float *log_decay,
+                           const float *h0, void *out, float *hT, const int32_t *cu_seqlens, int B,
+                           int64_t T, int H, int dk, int dv, float scale, gdr_dtype_t dtype,
+                           gdr_path_t path, void *workspace, size_t workspace_bytes,
+                           gdr_stream_t stream_) {
+    DecayShape s;
+    gdr_status_t st = check_decay(log_decay, B, T, H, dk, dv, scale, dtype, path, cu_seqlens != nullptr, &s);
+    if (st != GDR_OK) return st;
+    if (s.T_total > 0 && (!q || !k || !v || !out)) return GDR_ERR_INVALID_ARG;
+    if (!al16(h0) || !al16(hT) || !al16(workspace)) return GDR_ERR_INVALID_ARG;
+    const size_t es = dtype == GDR_BF16 ? 2 : 4, rows = (size_t)s.T_total * H;
+    const size_t kb = rows * dk * es, vb = rows * dv * es, gb = sizeof(float) * (size_t)H;
+    const size_t nst = sizeof(float) * (size_t)B * H * dk * dv, cb = sizeof(int32_t) * (size_t)(B + 1);
+    if (!outputs_clear({{out, vb}, {hT, nst}}, {{q, kb}, {k, kb}, {v, vb}, {log_decay, gb}, {cu_seqlens, cb}}) ||
+        overlaps(out, vb, h0, nst) || (hT != h0 && overlaps(hT, nst, h0, nst)))
+        return GDR_ERR_INVALID_ARG;
+    const bool can_tc = decay_tc_ok(dtype, s, {q, k, v, out});
+    if (path == GDR_PATH_TC && !can_tc) return GDR_ERR_UNSUPPORTED;
+    const bool tc = can_tc && path != GDR_PATH_SIMT;
+    cudaStream_t stream = (cudaStream_t)stream_;
+    if (s.T_total == 0 && !s.varlen) {   // no tokens: hT = h0
+        if (!hT || hT == h0) return GDR_OK;
+        const cudaError_t e = h0 ? cudaMemcpyAsync(hT, h0, nst, cudaMemcpyDeviceToDevice, stream)
+                                 : cudaMemsetAsync(hT, 0, nst, stream);
+        return e == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+    }
+    DeviceCtx *ctx = device_ctx();
+    if (!ctx) return GDR_ERR_CUDA;
+    DecayGeom g = decay_call_geom(s, tc, false, ctx->sms);
+    const DecayLayout L = decay_layout(s, g, false);
+    char *ws;
+    if ((st = take_workspace(ctx, workspace, workspace_bytes, L.total, &ws)) != GDR_OK) return st;
+    if ((st = decay_plan(&g, cu_seqlens, log_decay, ws, L, ctx->d_status, stream)) != GDR_OK) return st;
+    if (hT && hT == h0 && g.max_slots > 0) {
+        // one CTA may read a sequence's entering state after another has written its last
+        if (cudaMemcpyAsync(ws + L.copy, h0, nst, cudaMemcpyDeviceToDevice, stream) != cudaSuccess)
+            return GDR_ERR_CUDA;
+        h0 = (const float *)(ws + L.copy);
+    }
+    float *slots = (float *)(ws + L.slots);
+    const DecayPass chain{nullptr, k, v, nullptr, h0, nullptr, slots, dk, dv, false, false, true, 1.f, 1.f};
+    const DecayPass pass{q, k, v, out, h0, hT, slots, dk, dv, false, false, false, 1.f, scale};
+    return decay_run(g, &chain, 1, &pass, 1, dtype, tc, ctx, stream) == cudaSuccess ? GDR_OK
+                                                                                             : GDR_ERR_CUDA;
+}
+
+gdr_status_t gdr_decay_bwd(const void *q, const void *k, const void *v, const float *log_decay,
+                           const float *h0, const void *dout, const float *dhT, void *dq, void *dk_out,
+                           void *dv_out, float *dh0, const int32_t *cu_seqlens, int B, int64_t T, int H,
+                           int dk, int dv, float scale, gdr_dtype_t dtype, gdr_path_t path,
+                           void *workspace, size_t workspace_bytes, gdr_stream_t stream_) {
+    DecayShape s;
+    gdr_status_t st = check_decay(log_decay, B, T, H, dk, dv, scale, dtype, path, cu_seqlens != nullptr, &s);
+    if (st != GDR_OK) return st;
+    if (s.T_total > 0 && (!q || !k || !v || !dout || !dq || !dk_out || !dv_out)) return GDR_ERR_INVALID_ARG;
+    if (!al16(h0) || !al16(dhT) || !al16(dh0) || !al16(workspace)) return GDR_ERR_INVALID_ARG;
+    const size_t es = dtype == GDR_BF16 ? 2 : 4, rows = (size_t)s.T_total * H;
+    const size_t kb = rows * dk * es, vb = rows * dv * es, gb = sizeof(float) * (size_t)H;
+    const size_t nst = sizeof(float) * (size_t)B * H * dk * dv, cb = sizeof(int32_t) * (size_t)(B + 1);
+    if (!outputs_clear({{dq, kb}, {dk_out, kb}, {dv_out, vb}, {dh0, nst}},
+                       {{q, kb}, {k, kb}, {v, vb}, {dout, vb}, {h0, nst}, {dhT, nst}, {log_decay, gb}, {cu_seqlens, cb}}))
+        return GDR_ERR_INVALID_ARG;
+    const bool can_tc = decay_tc_ok(dtype, s, {q, k, v, dout, dq, dk_out, dv_out});
+    if (path == GDR_PATH_TC && !can_tc) return GDR_ERR_UNSUPPORTED;
+    const bool tc = can_tc && path != GDR_PATH_SIMT;
+    cudaStream_t stream = (cudaStream_t)stream_;
+    if (s.T_total == 0 && !s.varlen) {   // no tokens: dh0 = dhT
+        if (!dh0) return GDR_OK;
+        const cudaError_t e = dhT ? cudaMemcpyAsync(dh0, dhT, nst, cudaMemcpyDeviceToDevice, stream)
+                                  : cudaMemsetAsync(dh0, 0, nst, stream);
+        return e == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+    }
+    DeviceCtx *ctx = device_ctx();
+    if (!ctx) return GDR_ERR_CUDA;
+    DecayGeom g = decay_call_geom(s, tc, true, ctx->sms);
+    const DecayLayout L = decay_layout(s, g, true);
+    char *ws;
+    if ((st = take_workspace(ctx, workspace, workspace_bytes, L.total, &ws)) != GDR_OK) return st;
+    if ((st = decay_plan(&g, cu_seqlens, log_decay, ws, L, ctx->d_status, stream)) != GDR_OK) return st;
+    float *sf = (float *)(ws + L.slots), *sr = (float *)(ws + L.slots_rev);
+    const DecayPass chains[2] = {
+        {nullptr, k, v, nullptr, h0, nullptr, sf, dk, dv, false, false, true, 1.f, 1.f},
+        {nullptr, q, dout, nullptr, dhT, nullptr, sr, dk, dv, false, true, true, scale, 1.f},
+    };
+    const DecayPass passes[3] = {
+        {dout, v, k, dq, h0, nullptr, sf, dv, dk, true, false, false, 1.f, scale},
+        {v, dout, q, dk_out, dhT, nullptr, sr, dv, dk, true, true, false, scale, 1.f},
+        {k, q, dout, dv_out, dhT, dh0, sr, dk, dv, false, true, false, scale, 1.f},
+    };
+    return decay_run(g, chains, 2, passes, 3, dtype, tc, ctx, stream) == cudaSuccess ? GDR_OK
+                                                                                              : GDR_ERR_CUDA;
+}
+
+gdr_status_t gdr_decay_recurrent_fwd(const void *q, const void *k, const void *v, const float *log_decay,
+                                     float *state, void *out, int N, int64_t T, int H, int dk, int dv,
+                                     float scale, gdr_dtype_t dtype, gdr_stream_t stream) {
+    DecayShape s;
+    const gdr_status_t st = check_decay(log_decay, N, T, H, dk, dv, scale, dtype, GDR_PATH_AUTO, false, &s);
+    if (st != GDR_OK) return st;
+    if (T == 0) return GDR_OK;
+    if (!q || !k || !v || !state || !out) return GDR_ERR_INVALID_ARG;
+    if (!al16(state)) return GDR_ERR_INVALID_ARG;
+    const size_t es = dtype == GDR_BF16 ? 2 : 4, rows = (size_t)s.T_total * H;
+    const size_t kb = rows * dk * es, vb = rows * dv * es, gb = sizeof(float) * (size_t)H;
+    const size_t nst = sizeof(float) * (size_t)N * H * dk * dv;
+    if (!outputs_clear({{out, vb}, {state, nst}}, {{q, kb}, {k, kb}, {v, vb}, {log_decay, gb}}))
+        return GDR_ERR_INVALID_ARG;
+    DecayGeom g{};
+    g.dense = true;
+    g.N = N;
+    g.H = H;
+    g.T_per = T;
+    g.T_total = s.T_total;
+    g.seg_tokens = (T + kDecayTile - 1) / kDecayTile * kDecayTile;
+    g.segs_per_seq = 1;
+    g.max_segs = N;
+    g.log_decay = log_decay;
+    const DecayPass pass{q, k, v, out, state, state, nullptr, dk, dv, false, false, false, 1.f, scale};
+    return launch_decay_rec(g, pass, dtype, (cudaStream_t)stream) == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+}
+
+gdr_status_t gdr_layer_norm_fwd(const void *x, const float *weight, const float *bias, void *y, float *mean,
+                                float *rstd, int64_t rows, int G, int D, float eps, gdr_dtype_t dtype,
+                                gdr_stream_t stream) {
+    if (dtype != GDR_BF16 && dtype != GDR_F32) return GDR_ERR_INVALID_ARG;
+    if (rows < 0 || G < 1 || D < 1 || rows % G != 0) return GDR_ERR_INVALID_ARG;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return GDR_ERR_INVALID_ARG;
+    if (D > kNormMaxD || G > (1 << 20) || rows > ((int64_t)1 << 40)) return GDR_ERR_UNSUPPORTED;
+    if (rows == 0) return GDR_OK;
+    if (!x || !y) return GDR_ERR_INVALID_ARG;
+    const size_t xb = (size_t)rows * D * (dtype == GDR_BF16 ? 2 : 4), sb = sizeof(float) * (size_t)rows;
+    const size_t wb = sizeof(float) * (size_t)G * D;
+    // y may be x itself: a row is read whole before it is written
+    if (!outputs_clear({{y, xb}, {mean, sb}, {rstd, sb}}, {{weight, wb}, {bias, wb}}) ||
+        overlaps(mean, sb, x, xb) || overlaps(rstd, sb, x, xb) || (y != x && overlaps(y, xb, x, xb)))
+        return GDR_ERR_INVALID_ARG;
+    DeviceCtx *ctx = device_ctx();
+    if (!ctx) return GDR_ERR_CUDA;
+    return launch_norm_fwd(x, weight, bias, y, mean, rstd, rows, G, D, eps, dtype, ctx->sms,
+                           (cudaStream_t)stream) == cudaSuccess
+               ? GDR_OK
+               : GDR_ERR_CUDA;
+}
+
+gdr_status_t gdr_layer_norm_bwd(const void *dy, const void *x, const float *mean, const float *rstd,
+                                const float *weight, void *dx, float *dweight, float *dbias, int64_t rows,
+                                int G, int D, gdr_dtype_t dtype, gdr_stream_t stream_) {
+    if (dtype != GDR_BF16 && dtype != GDR_F32) return GDR_ERR_INVALID_ARG;
+    if (rows < 0 || G < 1 || D < 1 || rows % G != 0) return GDR_ERR_INVALID_ARG;
+    if (D > kNormMaxD || G > (1 << 20) || rows > ((int64_t)1 << 40)) return GDR_ERR_UNSUPPORTED;
+    const size_t xb = (size_t)rows * D * (dtype == GDR_BF16 ? 2 : 4), sb = sizeof(float) * (size_t)rows;
+    const size_t wb = sizeof(float) * (size_t)G * D;
+    cudaStream_t stream = (cudaStream_t)stream_;
+    if (rows == 0) {   // sums over no rows
+        if (dweight && cudaMemsetAsync(dweight, 0, wb, stream) != cudaSuccess) return GDR_ERR_CUDA;
+        if (dbias && cudaMemsetAsync(dbias, 0, wb, stream) != cudaSuccess) return GDR_ERR_CUDA;
+        return GDR_OK;
+    }
+    if (!dy || !x || !mean || !rstd || !dx) return GDR_ERR_INVALID_ARG;
+    // dx may be dy or x itself: a row of both is read whole before it is written
+    if (!outputs_clear({{dx, xb}, {dweight, wb}, {dbias, wb}}, {{mean, sb}, {rstd, sb}, {weight, wb}}) ||
+        !outputs_clear({{dweight, wb}, {dbias, wb}}, {{dy, xb}, {x, xb}}) ||
+        (dx != dy && overlaps(dx, xb, dy, xb)) || (dx != x && overlaps(dx, xb, x, xb)))
+        return GDR_ERR_INVALID_ARG;
+    DeviceCtx *ctx = device_ctx();
+    if (!ctx) return GDR_ERR_CUDA;
+    char *ws;
+    const size_t need = dweight || dbias ? norm_bwd_scratch_bytes(rows, G, D, dtype, ctx->sms) : 0;
+    const gdr_status_t st = take_workspace(ctx, nullptr, 0, need, &ws);
+    if (st != GDR_OK) return st;
+    return launch_norm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, rows, G, D, dtype, ctx->sms,
+                           (float *)ws, stream) == cudaSuccess
                ? GDR_OK
                : GDR_ERR_CUDA;
 }

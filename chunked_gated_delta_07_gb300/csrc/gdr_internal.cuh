@@ -194,6 +194,16 @@ cudaError_t launch_router_topk(const void *logits, const float *bias, int32_t *i
 cudaError_t launch_router_update(const int64_t *load, float *bias, double *thr, int E, int mode,
                                  double q_lo, double q_hi, float eta, cudaStream_t stream);
 
+// layer norm over the last axis (gdr_norm.cu); `sms` sizes the grids
+constexpr int kNormMaxD = 16384;
+size_t norm_bwd_scratch_bytes(int64_t rows, int G, int D, gdr_dtype_t dtype, int sms);
+cudaError_t launch_norm_fwd(const void *x, const float *w, const float *b, void *y, float *mean, float *rstd,
+                            int64_t rows, int G, int D, float eps, gdr_dtype_t dtype, int sms,
+                            cudaStream_t stream);
+cudaError_t launch_norm_bwd(const void *dy, const void *x, const float *mean, const float *rstd, const float *w,
+                            void *dx, float *dw, float *db, int64_t rows, int G, int D, gdr_dtype_t dtype,
+                            int sms, float *scratch, cudaStream_t stream);
+
 void count_launch(uint64_t n = 1);
 
 // Brackets one kernel launch with CUDA events while profiling is enabled

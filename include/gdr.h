@@ -373,6 +373,107 @@ GDR_API gdr_status_t gdr_chunk_bwd(const void *q, const void *k, const void *v, 
                            int64_t T, int H, int dk, int dv, int chunk, float b,
                            gdr_dtype_t dtype, gdr_gate_t gate, gdr_stream_t stream);
 
+/*
+ * Linear attention with one constant decay per head, for prompts: per (sequence, head)
+ *     S_t = exp(log_decay[h]) S_{t-1} + k_t v_t^T,    o_t = scale * S_t^T q_t
+ * with the dk x dv fp32 state S, from h0 to hT -- the incremental linear-attention layer
+ * ("Evaluating Next-Gen Sparse MoE and Long-Context LLMs", §2.2) without the delta rule's
+ * erase step and with a decay that does not depend on the data.  It is computed in
+ * chunks ("Deep Dive ...", §3.2): inside a tile of 128 tokens the pairwise decays
+ * exp((i - j) log_decay) weigh a dense causal product, and the state passes from tile to
+ * tile.
+ *   q, k       [B, T, H, dk]   v, out [B, T, H, dv]   (dtype; packed input as for
+ *              gdr_chunk_fwd: a leading 1, cu_seqlens with B + 1 offsets, T in all)
+ *   log_decay  [H] fp32 (device), natural logarithms, meant to be <= 0; -inf keeps
+ *              nothing of earlier tokens; above 0 the state grows, which nothing limits
+ *   h0, hT     [N, H, dk, dv] fp32, 16-byte aligned, or NULL (zero / not written); hT
+ *              may be h0 (carried in place)
+ *   scale      finite; multiplies the outputs only, not the state
+ *   path       GDR_PATH_AUTO or GDR_PATH_SIMT: the fp32 CUDA-core kernel
+ *              (GDR_PATH_TC: GDR_ERR_UNSUPPORTED)
+ *   workspace  16-byte aligned device scratch of gdr_decay_workspace_size(...) bytes, or
+ *              NULL: the internal per-device cache (calls that share it must not
+ *              overlap on the GPU)
+ * dk, dv in {64, 128}; B, H >= 1; T >= 0; sequences of no tokens pass h0 on to hT.
+ * States are accumulated in fp32; on the tensor cores the writes enter them with 24
+ * significant bits, while the in-tile weights and the state are rounded to bf16 where
+ * they are multiplied for a (bf16) output.  A NaN or infinity in a token reaches, besides
+ * the outputs after it, those of its own 128-token tile; other sequences never.  Outputs
+ * must not overlap inputs.  Bad offsets: GDR_ERR_BAD_SEQLENS in the status word,
+ * nothing is written.  Asynchronous on `stream`; deterministic.
+ */
+GDR_API gdr_status_t gdr_decay_fwd(const void *q, const void *k, const void *v, const float *log_decay,
+                           const float *h0, void *out, float *hT, const int32_t *cu_seqlens, int B,
+                           int64_t T, int H, int dk, int dv, float scale, gdr_dtype_t dtype,
+                           gdr_path_t path, void *workspace, size_t workspace_bytes,
+                           gdr_stream_t stream);
+
+/*
+ * The gradients of <dout, out> + <dhT, hT> of gdr_decay_fwd with respect to q, k, v and
+ * h0 (log_decay is a constant of the layer and gets none).  With dS_t the gradient of S_t,
+ *     dS_t = exp(log_decay) dS_{t+1} + scale q_t dout_t^T   (dS_T holds dhT too)
+ *     dq_t = scale S_t dout_t,  dk_t = dS_t v_t,  dv_t = dS_t^T k_t,
+ *     dh0 = exp(log_decay) dS_1
+ *   dout [.., H, dv] (dtype);  dhT [N, H, dk, dv] fp32 or NULL (zero)
+ *   dq, dk [.., H, dk], dv [.., H, dv] (dtype);  dh0 [N, H, dk, dv] fp32 or NULL
+ * The states are recomputed, nothing is kept from the forward pass.  dhT and dh0 must be
+ * 16-byte aligned; everything else as for gdr_decay_fwd.
+ */
+GDR_API gdr_status_t gdr_decay_bwd(const void *q, const void *k, const void *v, const float *log_decay,
+                           const float *h0, const void *dout, const float *dhT, void *dq,
+                           void *dk_out, void *dv_out, float *dh0, const int32_t *cu_seqlens, int B,
+                           int64_t T, int H, int dk, int dv, float scale, gdr_dtype_t dtype,
+                           gdr_path_t path, void *workspace, size_t workspace_bytes,
+                           gdr_stream_t stream);
+
+/* Scratch bytes of gdr_decay_fwd (backward = 0) or gdr_decay_bwd (backward = 1) for these
+ * sizes; B is the number of sequences and T the total of tokens where packed = 1.  0 on
+ * invalid sizes, and where no scratch is needed. */
+GDR_API size_t gdr_decay_workspace_size(int B, int64_t T, int H, int dk, int dv, int packed,
+                                int backward, gdr_dtype_t dtype, gdr_path_t path);
+
+/*
+ * The same recurrence token by token, for decoding: advances each sequence's state over T
+ * tokens (T = 1: one step) in place.  q, k [N, T, H, dk], v, out [N, T, H, dv] (dtype),
+ * log_decay [H] fp32, state [N, H, dk, dv] fp32, 16-byte aligned, updated in place.
+ * Nothing is allocated.  T = 0 leaves the state untouched.  Errors as for
+ * gdr_recurrent_fwd; asynchronous on `stream`.
+ */
+GDR_API gdr_status_t gdr_decay_recurrent_fwd(const void *q, const void *k, const void *v,
+                                     const float *log_decay, float *state, void *out, int N,
+                                     int64_t T, int H, int dk, int dv, float scale,
+                                     gdr_dtype_t dtype, gdr_stream_t stream);
+
+/*
+ * Layer norm over the last axis: row r of x (D elements) becomes
+ *     y = (x - mean) * rstd * weight[r % G] + bias[r % G],
+ *     mean = sum(x) / D,   rstd = 1 / sqrt(sum((x - mean)^2) / D + eps)
+ * G = 1 is one weight for all rows; G = H norms every head of a [.., H, D] tensor with its
+ * own weight, as the outputs of an attention without a normaliser need.
+ *   x, y         [rows, D] in dtype (y may be x)
+ *   weight, bias [G, D] fp32, or NULL (1 / 0)
+ *   mean, rstd   [rows] fp32, or NULL: what the backward pass reads
+ * rows >= 0 and a multiple of G; 1 <= D <= 16384 (GDR_ERR_UNSUPPORTED above); eps >= 0 and
+ * finite.  fp32 inside; any alignment of elements.  Asynchronous on `stream`.
+ */
+GDR_API gdr_status_t gdr_layer_norm_fwd(const void *x, const float *weight, const float *bias, void *y,
+                                float *mean, float *rstd, int64_t rows, int G, int D, float eps,
+                                gdr_dtype_t dtype, gdr_stream_t stream);
+
+/*
+ * Its backward pass, from the forward's mean and rstd; xh = (x - mean) rstd:
+ *     dx = rstd (w dy - mean_D(w dy) - xh mean_D(w dy xh))
+ *     dweight[g] = sum over rows r with r % G = g of dy xh,  dbias[g] = sum of dy
+ *   dy, x, dx [rows, D] in dtype (dx may be dy or x); weight [G, D] fp32 or NULL (1)
+ *   dweight, dbias [G, D] fp32, or NULL (not wanted)
+ * The sums over rows are fp32 in a fixed order (no atomics).  Scratch comes from the
+ * internal per-device cache.  Sizes and errors as above; asynchronous on `stream`.
+ */
+GDR_API gdr_status_t gdr_layer_norm_bwd(const void *dy, const void *x, const float *mean,
+                                const float *rstd, const float *weight, void *dx, float *dweight,
+                                float *dbias, int64_t rows, int G, int D, gdr_dtype_t dtype,
+                                gdr_stream_t stream);
+
 /* Synchronise `stream`, then read and clear the current device's status word.
  * Returns GDR_OK, GDR_ERR_BAD_SEQLENS, GDR_ERR_TIMEOUT or GDR_ERR_CUDA. */
 GDR_API gdr_status_t gdr_get_status(gdr_stream_t stream);
