@@ -610,8 +610,14 @@ gdr_status_t check_decay(const float *log_decay, int B, int64_t T, int H, int dk
     return GDR_OK;
 }
 
-// No tensor-core kernel yet: every call runs on the CUDA cores.
-bool decay_tc_ok(gdr_dtype_t, const DecayShape &, std::initializer_list<const void *>) { return false; }
+// True when the tensor-core kernel takes this call: bf16 and every token tensor readable
+// as TMA tiles and writable in 16-byte pieces.
+bool decay_tc_ok(gdr_dtype_t dtype, const DecayShape &s, std::initializer_list<const void *> tensors) {
+    if (dtype != GDR_BF16 || s.T_total == 0 || s.T_total > 0x7fffffff - kDecayTile) return false;
+    for (const void *t : tensors)
+        if (!al16(t)) return false;
+    return true;
+}
 
 DecayGeom decay_call_geom(const DecayShape &s, bool tc, bool backward, int sms) {
     const int passes = backward ? 3 : 1;
@@ -657,7 +663,7 @@ gdr_status_t decay_plan(DecayGeom *g, const int32_t *cu, const float *log_decay,
 cudaError_t decay_run(const DecayGeom &g, const DecayPass *chains, int nchains, const DecayPass *passes, int n,
                       gdr_dtype_t dtype, bool tc, DeviceCtx *ctx, cudaStream_t stream) {
     auto run = [&](const DecayPass *p, int k) {
-        (void)tc, (void)ctx;
+        if (tc) return launch_decay_tc(g, p, k, ctx->sms, ctx->d_status, stream);
         cudaError_t err = cudaSuccess;
         for (int i = 0; i < k && err == cudaSuccess; ++i) err = launch_decay_rec(g, p[i], dtype, stream);
         return err;
