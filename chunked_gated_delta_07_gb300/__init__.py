@@ -77,6 +77,8 @@ class GdrError(RuntimeError):
 def lib():
     """The loaded ``libgdr.so`` (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -103,7 +105,7 @@ def _ptr(x):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -586,6 +588,8 @@ def dtype_code(t) -> int:
 # device.  Nothing here computes any part of the method.
 
 def _expect(name, t, shape, dtype, device):
+    if t is not None and t.shape == shape and t.dtype == dtype and t.device == device and t.is_contiguous():
+        return
     if t is None:
         raise ValueError(f"{name} is required")
     if tuple(t.shape) != tuple(shape):

@@ -545,6 +545,8 @@ struct DecayShape {
     bool varlen;
 };
 
+constexpr int64_t kDecayStepTokens = 8;   // most tokens that decay_step_kernel takes
+
 // Segments of a call.  A pass runs one block (tensor cores) or one column slice (CUDA
 // cores) per (segment, head): `units` per segment and sequence, `slots` at a time.  Equal
 // sequences are cut into the number of segments s that minimises
@@ -1194,6 +1196,12 @@ gdr_status_t gdr_decay_recurrent_fwd(const void *q, const void *k, const void *v
     const size_t nst = sizeof(float) * (size_t)N * H * dk * dv;
     if (!outputs_clear({{out, vb}, {state, nst}}, {{q, kb}, {k, kb}, {v, vb}, {log_decay, gb}}))
         return GDR_ERR_INVALID_ARG;
+    // a few tokens: bound by the state's traffic; more of them: by the arithmetic
+    if (T <= kDecayStepTokens)
+        return launch_decay_step(q, k, v, log_decay, state, out, dtype, N, T, H, dk, dv, scale,
+                                 (cudaStream_t)stream) == cudaSuccess
+                   ? GDR_OK
+                   : GDR_ERR_CUDA;
     DecayGeom g{};
     g.dense = true;
     g.N = N;

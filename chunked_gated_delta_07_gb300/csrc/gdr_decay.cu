@@ -155,6 +155,68 @@ decay_rec_kernel(const DecayGeom g, const DecayPass p) {
     }
 }
 
+// A few tokens of every sequence, the state updated in place.  A block owns 64 columns of
+// one (sequence, head)'s state: 256 threads hold kd / 16 rows x 4 columns each as float4,
+// all loaded before anything else (32 KB a block in flight at kd = 128), so that the
+// pass is bound by the state's traffic, 2 x 4 kd vd bytes.  Sums over kd: a shuffle, then
+// the 8 warps' partial sums through shared memory.
+template <typename T, int KD>
+__global__ void __launch_bounds__(256)
+decay_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__restrict__ v,
+                  const float *__restrict__ log_decay, float *__restrict__ state, T *__restrict__ out, int64_t Tn,
+                  int H, int vd, float scale) {
+    constexpr int kRows = KD / 16;
+    __shared__ float ks[2][KD], qs[2][KD];
+    __shared__ __align__(16) float vs[2][kCols];
+    __shared__ __align__(16) float red[2][8][kCols];
+    const int slices = vd / kCols;
+    const int e0 = (int)(blockIdx.x % slices) * kCols;
+    const int64_t nh = blockIdx.x / slices;
+    const int64_t n = nh / H;
+    const int h = (int)(nh % H);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int c4 = (tid & 15) * 4, r0 = tid >> 4;   // first column; rows r0 + 16 u
+    float4 *S = (float4 *)(state + (nh * KD + r0) * vd + e0 + c4);
+    float4 s[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) s[u] = S[(int64_t)4 * u * vd];
+    const DecayFactor decay(decay_log(log_decay, h));
+    for (int64_t t = 0; t < Tn; ++t) {
+        const int b = t & 1;
+        const int64_t row = (n * Tn + t) * H + h;
+        if (tid < KD) ks[b][tid] = to_f32(k[row * KD + tid]);
+        else if (KD == 64 && tid < 2 * KD) qs[b][tid - KD] = to_f32(q[row * KD + tid - KD]) * scale;
+        if (KD == 128 && tid >= KD) qs[b][tid - KD] = to_f32(q[row * KD + tid - KD]) * scale;
+        if (tid < kCols) vs[b][tid] = to_f32(v[row * vd + e0 + tid]);
+        __syncthreads();
+        const float4 vv = *(const float4 *)&vs[b][c4];
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) {
+            const float kd = ks[b][r0 + 16 * u], qd = qs[b][r0 + 16 * u];
+            s[u] = make_float4(fmaf(kd, vv.x, decay(s[u].x)), fmaf(kd, vv.y, decay(s[u].y)),
+                               fmaf(kd, vv.z, decay(s[u].z)), fmaf(kd, vv.w, decay(s[u].w)));
+            o = make_float4(fmaf(qd, s[u].x, o.x), fmaf(qd, s[u].y, o.y), fmaf(qd, s[u].z, o.z),
+                            fmaf(qd, s[u].w, o.w));
+        }
+        if (t == Tn - 1)
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) S[(int64_t)4 * u * vd] = s[u];
+        o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
+        o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
+        o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
+        o.w += __shfl_xor_sync(0xffffffffu, o.w, 16);
+        if (lane < 16) *(float4 *)&red[b][warp][c4] = o;
+        __syncthreads();
+        if (tid < kCols) {
+            float a = red[b][0][tid];
+#pragma unroll
+            for (int w = 1; w < 8; ++w) a += red[b][w][tid];
+            out[row * vd + e0 + tid] = from_f32<T>(a);
+        }
+    }
+}
+
 // cur = s0; per segment in the order of the pass: cur = lam^len cur + its local sum, the
 // state that enters the next segment, written over the sum.  A block takes 1024 elements
 // of one (sequence, head).
@@ -209,7 +271,27 @@ cudaError_t rec_t(const DecayGeom &g, const DecayPass &p, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
+template <typename T>
+cudaError_t step_t(const void *q, const void *k, const void *v, const float *log_decay, float *state, void *out,
+                   int N, int64_t Tn, int H, int dk, int dv, float scale, cudaStream_t stream) {
+    const int64_t blocks = (int64_t)N * H * (dv / kCols);
+    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+    ProfScope prof(stream, "decay_step_kernel");
+    auto kern = dk == 128 ? decay_step_kernel<T, 128> : decay_step_kernel<T, 64>;
+    kern<<<(unsigned)blocks, 256, 0, stream>>>((const T *)q, (const T *)k, (const T *)v, log_decay, state, (T *)out,
+                                               Tn, H, dv, scale);
+    count_launch();
+    return cudaGetLastError();
+}
+
 }  // namespace
+
+cudaError_t launch_decay_step(const void *q, const void *k, const void *v, const float *log_decay, float *state,
+                              void *out, gdr_dtype_t dtype, int N, int64_t T, int H, int dk, int dv, float scale,
+                              cudaStream_t stream) {
+    return dtype == GDR_BF16 ? step_t<__nv_bfloat16>(q, k, v, log_decay, state, out, N, T, H, dk, dv, scale, stream)
+                             : step_t<float>(q, k, v, log_decay, state, out, N, T, H, dk, dv, scale, stream);
+}
 
 cudaError_t launch_decay_rec(const DecayGeom &g, const DecayPass &p, gdr_dtype_t dtype, cudaStream_t stream) {
     if (dtype == GDR_BF16)

@@ -131,6 +131,10 @@ __device__ __forceinline__ float *decay_state_out(const DecayPass &p, const Deca
 
 // Token by token on the CUDA cores (gdr_decay.cu): any dtype, kd and vd in {64, 128}.
 cudaError_t launch_decay_rec(const DecayGeom &g, const DecayPass &p, gdr_dtype_t dtype, cudaStream_t stream);
+// T tokens of N sequences, the state [N, H, dk, dv] updated in place (gdr_decay.cu).
+cudaError_t launch_decay_step(const void *q, const void *k, const void *v, const float *log_decay, float *state,
+                              void *out, gdr_dtype_t dtype, int N, int64_t T, int H, int dk, int dv, float scale,
+                              cudaStream_t stream);
 // On the tensor cores (gdr_decay_tc.cu): bf16, token tensors 16-byte aligned, fewer than
 // 2^31 - 128 token rows.  Passes of one launch are independent and all local or all not.
 cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, int sms, int *status,

@@ -4,25 +4,28 @@
 // A pass (gdr_decay.cuh) takes tiles of C = 128 tokens of one (segment, head) in order.
 // With rows a_i, b_i, c_i of the tile, S the state that enters it, lam = exp(log_decay) and
 // n tokens in the tile (n = C but at a sequence's end):
-//     P_ij  = s_out s_upd lam^{i-j} (a_i . b_j)  for j <= i, else 0
-//     out_i = s_out lam^{i+1} S^T a_i + sum_j P_ij c_j
+//     f_i   = max(lam^{i+1}, 2^-64)
+//     P_ij  = s_upd lam^{i-j} / f_i (a_i . b_j)  for j <= i, else 0
+//     out_i = s_out f_i (S^T a_i + sum_j P_ij c_j)
 //     S    <- lam^n S + sum_j (s_upd lam^{n-1-j} c_j) b_j^T  (transposed)
 // and for a reversed pass i - j -> j - i, j <= i -> j >= i, lam^{i+1} -> lam^{n-1-i} and
-// lam^{n-1-j} -> lam^{j+1}.  Every power has an exponent >= 0: nothing can overflow, for any
-// decay.  All four products run on the tensor cores with fp32 accumulators in the tensor
+// lam^{n-1-j} -> lam^{j+1}.  Dividing P by the factor of the state's part lets both parts sum in
+// one accumulator; the floor of f keeps P in range for any decay, and what it adds is the
+// state's part taken at 2^-64 where lam^{i+1} is below that.  All four products run on the tensor cores with fp32 accumulators in the tensor
 // memory (TMEM), 128 x 128 each:
 //     Sc = A B^T                     lanes = query tokens i
-//     O  = A S                       lanes = query tokens i; S from shared memory in bf16
 //     S^T <- lam^n S^T + C'^T B      lanes = value index e: the resident state
+//     O  = A S                       lanes = query tokens i; S from shared memory in bf16
 //     O  += P C                      P in TMEM in bf16
-// A tile of one head is 128 KB of HBM traffic (3 loads, 1 store; 2.9 us of an SM's share of
-// the measured bandwidth) and 21 MFLOP (1.6 us of an SM's share of the bf16 rate): the pass
-// is bound by HBM as long as its other work stays out of the way.  So the four stages of a
-// tile run in different warps and overlap those of its neighbours:
-//   warps 0-3   weights: Sc -> P (bf16, over Sc in TMEM); O <- s_out lam^{i+1} O; O -> out
-//   warps 4-7   state:   S^T -> bf16 (shared memory) and lam^n S^T; C' -> TMEM
-//   warp 8      TMA loads of A, B, C, two stages of 96 KB
-//   warp 9      issues every MMA (their order in the tensor pipe is the issue order)
+// in this order.  A tile of one head is 128 KB of HBM traffic (3 loads, 1 store; 2.9 us of an
+// SM's share of the measured bandwidth) and 25 MFLOP (2.0 us of an SM's share of the bf16
+// rate), so the pass can be bound by HBM if its other work stays out of the way.  The stages
+// of a tile run in different warps and overlap those of its neighbours:
+//   warps 0-3    Sc -> P (bf16, over Sc in TMEM); O -> out
+//   warps 4-7    S^T -> bf16 (shared memory) and lam^n S^T (TMEM)
+//   warps 8-11   C' = weighted C -> TMEM, 32 tokens at a time
+//   warp 12      TMA loads of A, B, C, two stages of 96 KB
+//   warp 13      issues every MMA (their order in the tensor pipe is the issue order)
 //
 // Rounding.  The state is fp32 and so are its updates: C' = s_upd lam^{..} C has 24
 // significant bits, so it goes in as the sum of three bf16 numbers that represent it exactly
@@ -58,8 +61,6 @@ constexpr uint32_t kTile = 2 * kBox;       // one tensor's tile: up to two boxes
 constexpr unsigned kFull = 0xffffffffu;
 constexpr uint64_t kWaitNs = 2000000000ull;   // pipeline wait limit: 2 s
 constexpr uint64_t kDrainNs = 2000000000ull;  // drains before exit
-constexpr int kThreads = 32 * 10;
-constexpr int kProducer = 8, kIssuer = 9;     // warps
 
 struct TcMaps {
     CUtensorMap a[kMaxPasses], b[kMaxPasses], c[kMaxPasses];
@@ -120,60 +121,62 @@ __device__ __forceinline__ void zero_rows(uint8_t *tile, int width, int n, int l
             *(uint4 *)(tile + box * kBox + sw128_off(n + i / 8, (i & 7) * 16)) = make_uint4(0, 0, 0, 0);
 }
 
-// 32 tokens (from row r0) of value index e of a C tile, weighted, as the three bf16 terms of
-// the A operand: hi + mid + lo = x w exactly, 16 columns (token pairs) each.  The terms are
-// cut off the top of the fp32 product, 8 significant bits at a time.
-template <typename W>
-__device__ __forceinline__ void weighted_terms(const uint8_t *tile, int e, int r0, W &&weight,
-                                               uint32_t (&hi)[16], uint32_t (&mid)[16], uint32_t (&lo)[16]) {
-    const uint8_t *col = tile + (e >> 6) * kBox + (e & 7) * 2;
-    const uint32_t chunk = (e & 63) >> 3;
+// The weights of a tile's tokens in the update of the state, for one warp: token i has
+// s_upd lam^{len - 1 - i + past} (forward) or s_upd lam^{i + 1 + past}; rows from len on are
+// not the sequence's and have 0.
+__device__ __forceinline__ void tile_weights(float *w, int len, bool rev, float gd, float s_upd, int64_t past,
+                                             int lane) {
+    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float y[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int r = r0 + 2 * i + k;
-            const uint32_t x = *(const uint16_t *)(col + (r >> 3) * 1024 + (r & 7) * 128 + ((chunk ^ (r & 7)) << 4));
-            y[k] = weight(2 * i + k, __uint_as_float(x << 16));
-        }
-        hi[i] = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) y[k] -= __uint_as_float(__float_as_uint(y[k]) & 0xffff0000u);
-        mid[i] = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632);
-#pragma unroll
-        for (int k = 0; k < 2; ++k) y[k] -= __uint_as_float(__float_as_uint(y[k]) & 0xffff0000u);
-        lo[i] = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632);
+    for (int k = 0; k < kC / 32; ++k) {
+        const int i = lane + 32 * k;
+        w[i] = i < len ? s_upd * expf(gd * (float)(past + (rev ? i + 1 : len - 1 - i))) : 0.f;
     }
+    __syncwarp();
 }
 
-// lam^{15-j} (forward) or lam^j: a token's distance within its 16 tokens.
-__device__ __forceinline__ void near_powers(float gd, bool rev, float (&near)[16]) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) near[j] = expf(gd * (float)(rev ? j : 15 - j));
+// Zeroes the rows from n on of the 32 columns from e0 (one warp) of a tile: what a weight
+// of 0 would not silence.
+__device__ __forceinline__ void zero_columns(uint8_t *tile, int e0, int n, int lane) {
+    for (int i = lane; i < (kC - n) * 4; i += 32)
+        *(uint4 *)(tile + (e0 >> 6) * kBox + sw128_off(n + i / 4, (e0 & 63) * 2 + (i & 3) * 16)) =
+            make_uint4(0, 0, 0, 0);
 }
 
-// Quarter q of a tile's C'^T, row e, into three times 16 TMEM columns at `at` (a whole
-// warp).  Token i of the tile has the weight s_upd lam^{len - 1 - i + past} (forward) or
-// s_upd lam^{i + 1 + past}; rows from len on are not the sequence's and count as zero.
-__device__ __forceinline__ void write_terms(uint32_t at, const uint8_t *tile, int e, int vd, int q, int len, bool rev,
-                                            float gd, float s_upd, int64_t past, const float (&near)[16]) {
+// Quarter q (32 tokens) of a tile's C'^T, row e, into three times 16 TMEM columns at `at`
+// (a whole warp): the weighted values x w as the bf16 terms hi + mid + lo = x w exactly, cut
+// off the top of the fp32 product 8 significant bits at a time; a column holds two tokens.
+__device__ __forceinline__ void write_terms(uint32_t at, const uint8_t *tile, int e, bool any, int q,
+                                            const float *w) {
     uint32_t hi[16], mid[16], lo[16];
-    if (e >= vd) {
+    if (any) {
+        const uint8_t *col = tile + (e >> 6) * kBox + (e & 7) * 2 + q * 4096;
+        const uint32_t chunk = (e & 63) >> 3;
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) {
+            const float4 w4 = *(const float4 *)&w[32 * q + 2 * i];
+            const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
+            float y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int r = 2 * i + k;
+                const uint32_t x = *(const uint16_t *)(col + (r >> 3) * 1024 + (r & 7) * 128 + ((chunk ^ (r & 7)) << 4));
+                y[k] = __uint_as_float(x << 16) * wv[k];
+            }
+            hi[i] = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632);
+            hi[i + 1] = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x7632);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] -= __uint_as_float(__float_as_uint(y[k]) & 0xffff0000u);
+            mid[i] = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632);
+            mid[i + 1] = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x7632);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] -= __uint_as_float(__float_as_uint(y[k]) & 0xffff0000u);
+            lo[i] = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632);
+            lo[i + 1] = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x7632);
+        }
+    } else {
 #pragma unroll
         for (int j = 0; j < 16; ++j) hi[j] = mid[j] = lo[j] = 0;
-    } else if (len == kC) {
-        const int64_t n = past + (rev ? 32 * q + 1 : 96 - 32 * q);   // to the further 16 tokens: n + 16
-        const float f0 = s_upd * expf(gd * (float)(rev ? n : n + 16));
-        const float f1 = s_upd * expf(gd * (float)(rev ? n + 16 : n));
-        weighted_terms(tile, e, 32 * q, [&](int j, float x) { return x * ((j < 16 ? f0 : f1) * near[j & 15]); }, hi,
-                       mid, lo);
-    } else {   // a sequence's last tile
-        weighted_terms(tile, e, 32 * q, [&](int j, float x) {
-            const int i = 32 * q + j;
-            const int64_t n = past + (rev ? i + 1 : len - 1 - i);
-            return i < len ? x * (s_upd * expf(gd * (float)n)) : 0.f;
-        }, hi, mid, lo);
     }
     __syncwarp();
     tmem_st16(at, hi);
@@ -181,60 +184,70 @@ __device__ __forceinline__ void write_terms(uint32_t at, const uint8_t *tile, in
     tmem_st16(at + 32, lo);
 }
 
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
     return *(const uint32_t *)&v;
 }
 
-// 32 columns (d0 ..) of row e of a state in memory.
-__device__ __forceinline__ void state_load(const DecayPass &p, const float *in, int d0, int e, uint32_t (&r)[32]) {
+// 16 columns (d0 ..) of row e of a state in memory.
+__device__ __forceinline__ void state_load(const DecayPass &p, const float *in, int d0, int e, uint32_t (&r)[16]) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) r[j] = 0;
+    for (int j = 0; j < 16; ++j) r[j] = 0;
     if (!in || e >= p.vd || d0 >= p.kd) return;
     if (p.transposed) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) *(uint4 *)&r[j] = *(const uint4 *)&in[(int64_t)e * p.kd + d0 + j];
+        for (int j = 0; j < 16; j += 4) *(uint4 *)&r[j] = *(const uint4 *)&in[(int64_t)e * p.kd + d0 + j];
     } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(in[(int64_t)(d0 + j) * p.vd + e]);
+        for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(in[(int64_t)(d0 + j) * p.vd + e]);
     }
 }
-__device__ __forceinline__ void state_store(const DecayPass &p, float *to, int d0, int e, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void state_store(const DecayPass &p, float *to, int d0, int e, const uint32_t (&r)[16]) {
     if (!to || e >= p.vd || d0 >= p.kd) return;
     if (p.transposed) {
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) *(uint4 *)&to[(int64_t)e * p.kd + d0 + j] = *(const uint4 *)&r[j];
+        for (int j = 0; j < 16; j += 4) *(uint4 *)&to[(int64_t)e * p.kd + d0 + j] = *(const uint4 *)&r[j];
     } else {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) to[(int64_t)(d0 + j) * p.vd + e] = __uint_as_float(r[j]);
+        for (int j = 0; j < 16; ++j) to[(int64_t)(d0 + j) * p.vd + e] = __uint_as_float(r[j]);
     }
 }
 
-// 32 TMEM columns of the warp's lanes, complete (the wait names the registers, so that no
-// use of them moves above it).
-__device__ __forceinline__ void tmem_get32(uint32_t at, uint32_t (&r)[32]) {
-    tmem_ld32(at, r);
+// Waits for the warp's TMEM loads; names the registers of one of them, so that no use of
+// those moves above the wait.
+__device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                   "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :
                  : "memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t (&r)[32]) {
-    uint32_t h[16];
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) h[j] = r[16 * k + j];
-        tmem_st16(at + 16 * k, h);
+// f(m, r) for 16 columns at a time from `at`, the next ones on their way meanwhile (an even
+// number of pieces).  Rolled up: the warps of a block run five different programs, and
+// their loops have to stay in the instruction caches together.
+template <typename F> __device__ __forceinline__ void tmem_columns(uint32_t at, int pieces, F &&f) {
+    uint32_t r0[16], r1[16];
+    tmem_ld16(at, r0);
+#pragma unroll 1
+    for (int m = 0; m < pieces; m += 2) {
+        tmem_arrived(r0);
+        tmem_ld16(at + 16 * (m + 1), r1);
+        f(m, r0);
+        tmem_arrived(r1);
+        if (m + 2 < pieces) tmem_ld16(at + 16 * (m + 2), r0);
+        f(m + 1, r1);
     }
 }
 
 // ---------------------------------------------------------------------------
 // the output pass
 // ---------------------------------------------------------------------------
+constexpr int kOutThreads = 32 * 14, kOutProducer = 12, kOutIssuer = 13;   // warps
 // TMEM columns
 constexpr uint32_t kColS = 0;      // Sc, then P in its first 64 columns
 constexpr uint32_t kColO = 128;
@@ -246,7 +259,8 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kStage = 3 * kTile;               // A, B, C
 constexpr uint32_t kOffH = 2 * kStage;               // the state in bf16, [e][d], K-major
 constexpr uint32_t kOffBar = kOffH + kTile;
-constexpr uint32_t kSmemOut = kOffBar + 256 + 1024;  // + alignment slack
+constexpr uint32_t kOffW = kOffBar + 256;            // weights of a tile's tokens, a copy per warp
+constexpr uint32_t kSmemOut = kOffW + 4 * kC * 4;
 static_assert(kSmemOut <= 232448, "shared memory");
 
 struct OutBars {
@@ -268,14 +282,14 @@ struct OutBars {
 };
 static_assert(sizeof(OutBars) <= 256, "barriers");
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kOutThreads, 1)
 decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs A) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t smem[];
     OutBars &bar = *(OutBars *)(smem + kOffBar);
     volatile int *stop = &bar.stop;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int H = A.g.H;
+    if (!GDR_INBOUNDS((smem_u32(smem) & 1023u) == 0)) return;   // swizzled tiles start on 1 KB
 
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
@@ -317,7 +331,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
     uint32_t it = 0;   // tiles so far: the use number of every once-a-tile barrier
     Unit u;
 
-    if (warp == kProducer) {
+    if (warp == kOutProducer) {
         bool ok = true;
         for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
             if (!unit_of(A, n, false, u)) continue;
@@ -342,7 +356,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
         // never leave with a copy in flight
         for (uint32_t k = it >= 2 ? it - 2 : 0; k < it; ++k)
             __all_sync(kFull, mbar_wait(&bar.full[k & 1], (k >> 1) & 1u, kDrainNs));
-    } else if (warp == kIssuer) {
+    } else if (warp == kOutIssuer) {
         const uint32_t s0 = smem_u32(smem);
         bool ok = true;
         for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
@@ -361,8 +375,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 const uint32_t sa = s0 + st * kStage, sb = sa + kTile, sc = sb + kTile;
                 if (!(ok = wait(&bar.full[st], it >> 1))) break;
                 if (len < kC) {
-                    zero_rows(sp + kTile, p.kd, len, lane);
-                    zero_rows(sp + 2 * kTile, p.vd, len, lane);
+                    zero_rows(sp + kTile, p.kd, len, lane);   // of C: by the warps that weigh it
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
@@ -379,17 +392,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                     mma_commit(&bar.s_full);
                 }
                 __syncwarp();
-                if (!(ok = wait(&bar.h_ready, it)) || (it && !(ok = wait(&bar.o_free, it - 1)))) break;
-                tc_fence_after();
-                if (elect_one()) {
-                    for (int k = 0; k < p.kd / 16; ++k) {
-                        const uint64_t o = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
-                        mma_f16_ss(tm + kColO, dA + o, dH + o, id_o1, k > 0);
-                    }
-                    mma_commit(&bar.o1_full);
-                    mma_commit(&bar.free_a[st]);
-                }
-                __syncwarp();
+                if (!(ok = wait(&bar.h_ready, it))) break;
                 for (int q = 0; q < 4 && ok; ++q) {
                     const uint32_t slot = q & 1;
                     if (!(ok = wait(&bar.v_ready[slot], 2 * it + (q >> 1)))) break;
@@ -406,7 +409,18 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                     }
                     __syncwarp();
                 }
-                if (!ok || !(ok = wait(&bar.p_ready, it))) break;
+                if (!ok || (it && !(ok = wait(&bar.o_free, it - 1)))) break;
+                tc_fence_after();
+                if (elect_one()) {
+                    for (int k = 0; k < p.kd / 16; ++k) {
+                        const uint64_t o = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
+                        mma_f16_ss(tm + kColO, dA + o, dH + o, id_o1, k > 0);
+                    }
+                    mma_commit(&bar.o1_full);
+                    mma_commit(&bar.free_a[st]);
+                }
+                __syncwarp();
+                if (!(ok = wait(&bar.p_ready, it))) break;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -431,95 +445,67 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             if (!unit_of(A, n, false, u)) continue;
             const DecayPass &p = A.pass[u.pass];
             const bool rev = p.rev;
-            const float gd = decay_log(A.g.log_decay, u.h);
-            const float g2 = gd * 1.4426950408889634f;
-            const float sw = p.s_out * p.s_upd;
-            // lam^{|i-j|} over a block of 16 columns = (the row's distance to the block's near
-            // end) x (the column's distance to it); the latter here
-            float near[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) near[j] = exp2f(g2 * (float)(rev ? j : 15 - j));
+            // log2 lam; below -200 (lam / f < 2^-136) a weight is 0 whatever lam is, and the
+            // differences of its multiples below stay exact enough
+            const float g2 = fmaxf(decay_log(A.g.log_decay, u.h) * 1.4426950408889634f, -200.f);
+            const float l_upd = p.s_upd;
             for (int i = 0; i < u.tiles; ++i, ++it) {
                 int64_t t;
                 int len;
                 tile_of(u, rev, i, t, len);
+                // log2 of the row's f
+                const float lf = fmaxf(g2 * (float)(rev ? max(len - 1 - row, 0) : row + 1), -64.f);
                 if (!(ok = wait(&bar.s_full, it))) break;
                 tc_fence_after();
-                {
-#pragma unroll 1
-                    for (int m = 0; m < 4; ++m) {
-                        uint32_t x[32], o[16];
-                        tmem_get32(lanes + kColS + 32 * m, x);
+                tmem_columns(lanes + kColS, 8, [&](int m, const uint32_t (&x)[16]) {
+                    uint32_t o[8];
+                    if (rev ? 16 * m + 15 < 32 * warp : 16 * m > 32 * warp + 31) {   // no pair of the warp's rows
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) {
-                            const int c0 = 32 * m + 16 * b;
-                            float y[16];
-                            const bool none = rev ? c0 + 15 < 32 * warp : c0 > 32 * warp + 31;
-                            const bool all = rev ? c0 >= 32 * warp + 31 : c0 + 15 <= 32 * warp;
-                            if (none) {
+                        for (int j = 0; j < 8; ++j) o[j] = 0;
+                    } else {
+                        // distance of column 16 m + j: d + j step
+                        const int d = rev ? 16 * m - row : row - 16 * m, step = rev ? 1 : -1;
+                        const float l0 = fmaf(g2, (float)d, -lf), l1 = rev ? g2 : -g2;
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) y[j] = 0.f;
-                            } else if (all) {
-                                const float far = sw * exp2f(g2 * (float)(rev ? c0 - row : row - c0 - 15));
+                        for (int j = 0; j < 8; ++j) {
+                            float y[2];
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) y[j] = __uint_as_float(x[16 * b + j]) * (far * near[j]);
-                            } else {
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) {
-                                    const int d = rev ? c0 + j - row : row - c0 - j;
-                                    y[j] = d >= 0 ? __uint_as_float(x[16 * b + j]) * (sw * exp2f(g2 * (float)d)) : 0.f;
-                                }
-                            }
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) o[8 * b + j] = pack2(y[2 * j], y[2 * j + 1]);
+                            for (int k = 0; k < 2; ++k)
+                                y[k] = d + (2 * j + k) * step >= 0
+                                           ? l_upd * __uint_as_float(x[2 * j + k]) * exp2_approx(fmaf((float)(2 * j + k), l1, l0))
+                                           : 0.f;
+                            o[j] = pack2(y[0], y[1]);
                         }
-                        tmem_st16(lanes + kColS + 16 * m, o);
                     }
-                }
-                if (!(ok = wait(&bar.o1_full, it))) break;
-                tc_fence_after();
-                {
-                    const float f = p.s_out * exp2f(g2 * (float)(rev ? max(len - 1 - row, 0) : row + 1));
-#pragma unroll 1
-                    for (int m = 0; m < p.vd / 32; ++m) {
-                        uint32_t x[32];
-                        tmem_get32(lanes + kColO + 32 * m, x);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
-                        tmem_st32(lanes + kColO + 32 * m, x);
-                    }
-                }
+                    tmem_st8(lanes + kColS + 8 * m, o);
+                });
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_ready);
                 if (!(ok = wait(&bar.o_full, it))) break;
                 tc_fence_after();
-                {
-                    __nv_bfloat16 *dst = (__nv_bfloat16 *)p.out + ((t + row) * H + u.h) * (int64_t)p.vd;
-#pragma unroll 1
-                    for (int m = 0; m < p.vd / 32; ++m) {
-                        uint32_t x[32];
-                        tmem_get32(lanes + kColO + 32 * m, x);
-                        if (row < len) {
+                const float f = p.s_out * exp2f(lf);
+                __nv_bfloat16 *dst = (__nv_bfloat16 *)p.out + ((t + row) * H + u.h) * (int64_t)p.vd;
+                tmem_columns(lanes + kColO, p.vd / 16, [&](int m, const uint32_t (&x)[16]) {
+                    if (row < len) {
 #pragma unroll
-                            for (int j = 0; j < 32; j += 8) {
-                                uint32_t o[4];
+                        for (int j = 0; j < 16; j += 8) {
+                            uint32_t o[4];
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    o[k] = pack2(__uint_as_float(x[j + 2 * k]), __uint_as_float(x[j + 2 * k + 1]));
-                                *(uint4 *)(dst + 32 * m + j) = make_uint4(o[0], o[1], o[2], o[3]);
-                            }
+                            for (int k = 0; k < 4; ++k)
+                                o[k] = pack2(f * __uint_as_float(x[j + 2 * k]), f * __uint_as_float(x[j + 2 * k + 1]));
+                            *(uint4 *)(dst + 16 * m + j) = make_uint4(o[0], o[1], o[2], o[3]);
                         }
-                        __syncwarp();
                     }
-                }
+                    __syncwarp();
+                });
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.o_free);
             }
         }
-    } else {
+    } else if (warp < 8) {
         // ---- state: thread = value index (TMEM lane)
         const int e = tid - 128;
         const uint32_t lanes = tm + ((uint32_t)((warp - 4) * 32) << 16);
@@ -527,84 +513,103 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
         for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
             if (!unit_of(A, n, false, u)) continue;
             const DecayPass &p = A.pass[u.pass];
-            const bool rev = p.rev;
             const float gd = decay_log(A.g.log_decay, u.h);
             const float *in = decay_state_in(p, u.seg, H, u.h);
             float *to = decay_state_out(p, u.seg, H, u.h);
             if (u.tiles == 0) {   // an empty sequence: the state goes through
-                for (int d0 = 0; d0 < p.kd; d0 += 32) {
-                    uint32_t r[32];
+                for (int d0 = 0; d0 < p.kd; d0 += 16) {
+                    uint32_t r[16];
                     state_load(p, in, d0, e, r);
                     state_store(p, to, d0, e, r);
                 }
                 continue;
             }
-            float near[16];
-            near_powers(gd, rev, near);
             for (int i = 0; i < u.tiles; ++i, ++it) {
-                const uint32_t st = it & 1;
                 int64_t t;
                 int len;
-                tile_of(u, rev, i, t, len);
+                tile_of(u, p.rev, i, t, len);
+                const DecayFactor decay(gd * (float)len);
+                // 16 columns of the entering state: to shared memory in bf16, and decayed
+                auto take = [&](int m, uint32_t (&r)[16]) {
+#pragma unroll
+                    for (int j = 0; j < 16; j += 8) {
+                        uint32_t o[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            o[k] = pack2(__uint_as_float(r[j + 2 * k]), __uint_as_float(r[j + 2 * k + 1]));
+                        *(uint4 *)(smem + kOffH + (m >> 2) * kBox + sw128_off(e, (16 * (m & 3) + j) * 2)) =
+                            make_uint4(o[0], o[1], o[2], o[3]);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(decay(__uint_as_float(r[j])));
+                    tmem_st16(lanes + kColH + 16 * m, r);
+                };
                 // the update of S^T is complete, and the bf16 state read
                 if (it && !((ok = wait(&bar.kv_full, it - 1)) && (ok = wait(&bar.o1_full, it - 1)))) break;
                 tc_fence_after();
-                {
-                    const DecayFactor decay(gd * (float)len);
-                    const int nm = p.kd / 32;
-                    uint32_t r[32];
+                if (i == 0) {
 #pragma unroll 1
-                    for (int m = 0; m < nm; ++m) {
-                        if (i == 0) {
-                            state_load(p, in, 32 * m, e, r);
-                            __syncwarp();
-                        } else {
-                            tmem_get32(lanes + kColH + 32 * m, r);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 32; j += 8) {
-                            uint32_t o[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                o[k] = pack2(__uint_as_float(r[j + 2 * k]), __uint_as_float(r[j + 2 * k + 1]));
-                            *(uint4 *)(smem + kOffH + (m >> 1) * kBox + sw128_off(e, (32 * (m & 1) + j) * 2)) =
-                                make_uint4(o[0], o[1], o[2], o[3]);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            r[j] = __float_as_uint(decay(__uint_as_float(r[j])));
-                        tmem_st32(lanes + kColH + 32 * m, r);
+                    for (int m = 0; m < p.kd / 16; ++m) {
+                        uint32_t r[16];
+                        state_load(p, in, 16 * m, e, r);
+                        __syncwarp();
+                        take(m, r);
                     }
+                } else {
+                    tmem_columns(lanes + kColH, p.kd / 16, take);
                 }
                 fence_proxy_async_smem();
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.h_ready);
+            }
+            if (ok && to) {
+                if (!(ok = wait(&bar.kv_full, it - 1))) break;
+                tc_fence_after();
+                tmem_columns(lanes + kColH, p.kd / 16, [&](int m, const uint32_t (&r)[16]) {
+                    state_store(p, to, 16 * m, e, r);
+                    __syncwarp();
+                });
+            }
+        }
+    } else {
+        // ---- weighted values: thread = value index (TMEM lane)
+        const int e = tid - 256;
+        const uint32_t lanes = tm + ((uint32_t)((warp - 8) * 32) << 16);
+        float *w = (float *)(smem + kOffW) + (warp - 8) * kC;
+        bool ok = true;
+        for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
+            if (!unit_of(A, n, false, u)) continue;
+            const DecayPass &p = A.pass[u.pass];
+            const float gd = decay_log(A.g.log_decay, u.h);
+            int wlen = -1;   // tokens of the tile that w is for
+            for (int i = 0; i < u.tiles; ++i, ++it) {
+                const uint32_t st = it & 1;
+                int64_t t;
+                int len;
+                tile_of(u, p.rev, i, t, len);
+                if (len != wlen) tile_weights(w, len, p.rev, gd, p.s_upd, 0, lane);
+                wlen = len;
                 if (!(ok = wait(&bar.full[st], it >> 1))) break;
-                const uint8_t *ct = smem + st * kStage + 2 * kTile;
+                uint8_t *ct = smem + st * kStage + 2 * kTile;
+                if (len < kC && e < p.vd) {
+                    zero_columns(ct, e & ~31, len, lane);
+                    fence_proxy_async_smem();   // the product with P reads them too
+                    __syncwarp();
+                }
+#pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     const uint32_t slot = q & 1, use = 2 * it + (q >> 1);
                     if (use && !(ok = wait(&bar.v_free[slot], use - 1))) break;
                     tc_fence_after();
-                    write_terms(lanes + kColV + slot * kSlotCols, ct, e, p.vd, q, len, rev, gd, p.s_upd, 0, near);
+                    write_terms(lanes + kColV + slot * kSlotCols, ct, e, e < p.vd, q, w);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.v_ready[slot]);
                 }
                 if (!ok) break;
-            }
-            if (ok && to) {
-                if (!(ok = wait(&bar.kv_full, it - 1))) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int m = 0; m < p.kd / 32; ++m) {
-                    uint32_t r[32];
-                    tmem_get32(lanes + kColH + 32 * m, r);
-                    state_store(p, to, 32 * m, e, r);
-                    __syncwarp();
-                }
             }
         }
     }
@@ -622,10 +627,12 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
 // Every write's weight is its distance to the segment's end, so the accumulator needs no
 // decay on the way: the tensor cores sum C'^T B over all tiles.  The two groups of four
 // warps take the tiles in turn, each with its own buffer of C' in TMEM.
+constexpr int kLocThreads = 32 * 10, kLocProducer = 8, kLocIssuer = 9;     // warps
 constexpr int kLocStages = 3;
 constexpr uint32_t kLocStage = 2 * kTile;                    // B, C
 constexpr uint32_t kLocOffBar = kLocStages * kLocStage;
-constexpr uint32_t kSmemLocal = kLocOffBar + 256 + 1024;
+constexpr uint32_t kLocOffW = kLocOffBar + 256;              // weights, a copy per warp
+constexpr uint32_t kSmemLocal = kLocOffW + 8 * kC * 4;
 constexpr uint32_t kLocColV = 128;                           // two buffers of 4 x 48 columns
 static_assert(kLocColV + 2 * 4 * kSlotCols <= kTmemCols, "TMEM");
 
@@ -639,14 +646,14 @@ struct LocalBars {
 };
 static_assert(sizeof(LocalBars) <= 256, "barriers");
 
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kLocThreads, 1)
 decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs A) {
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = (uint8_t *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    extern __shared__ __align__(1024) uint8_t smem[];
     LocalBars &bar = *(LocalBars *)(smem + kLocOffBar);
     volatile int *stop = &bar.stop;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int H = A.g.H;
+    if (!GDR_INBOUNDS((smem_u32(smem) & 1023u) == 0)) return;   // swizzled tiles start on 1 KB
     if (tid == 0) {
         for (int i = 0; i < kLocStages; ++i) {
             mbar_init(&bar.full[i], 1);
@@ -680,7 +687,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
     uint32_t it = 0, nu = 0;   // tiles and units so far
     Unit u;
 
-    if (warp == kProducer) {
+    if (warp == kLocProducer) {
         bool ok = true;
         for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
             if (!unit_of(A, n, true, u) || u.tiles == 0) continue;
@@ -702,7 +709,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
         }
         for (uint32_t k = it >= kLocStages ? it - kLocStages : 0; k < it; ++k)
             __all_sync(kFull, mbar_wait(&bar.full[k % kLocStages], (k / kLocStages) & 1u, kDrainNs));
-    } else if (warp == kIssuer) {
+    } else if (warp == kLocIssuer) {
         const uint32_t s0 = smem_u32(smem);
         bool ok = true;
         for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
@@ -746,6 +753,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
     } else {
         const int grp = warp >> 2, e = tid & 127;
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
+        float *w = (float *)(smem + kLocOffW) + warp * kC;
         bool ok = true;
         for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
             if (!unit_of(A, n, true, u)) continue;
@@ -755,15 +763,13 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
             float *to = decay_state_out(p, u.seg, H, u.h);
             if (u.tiles == 0) {
                 if (grp == 0)
-                    for (int d0 = 0; d0 < p.kd; d0 += 32) {
-                        uint32_t r[32];
+                    for (int d0 = 0; d0 < p.kd; d0 += 16) {
+                        uint32_t r[16];
                         state_load(p, nullptr, d0, e, r);
                         state_store(p, to, d0, e, r);
                     }
                 continue;
             }
-            float near[16];
-            near_powers(gd, rev, near);
             for (int i = 0; i < u.tiles; ++i, ++it) {
                 const uint32_t st = it % kLocStages, buf = it & 1;
                 if (buf != (uint32_t)grp) continue;
@@ -771,15 +777,19 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                 int len;
                 tile_of(u, rev, i, t, len);
                 const uint32_t use = it >> 1;
+                // past the tile: its distance to the segment's end (its start, reversed)
+                tile_weights(w, len, rev, gd, p.s_upd, rev ? t - u.t0 : u.t1 - t - len, lane);
                 if (!(ok = wait(&bar.full[st], it / kLocStages))) break;
                 if (use && !(ok = wait(&bar.v_free[buf], use - 1))) break;
                 tc_fence_after();
-                const uint8_t *ct = smem + st * kLocStage + kTile;
-                for (int q = 0; q < 4; ++q) {
-                    // past the tile: its distance to the segment's end (its start, reversed)
-                    write_terms(lanes + kLocColV + (buf * 4 + q) * kSlotCols, ct, e, p.vd, q, len, rev, gd, p.s_upd,
-                                rev ? t - u.t0 : u.t1 - t - len, near);
+                uint8_t *ct = smem + st * kLocStage + kTile;
+                if (len < kC && e < p.vd) {
+                    zero_columns(ct, e & ~31, len, lane);
+                    __syncwarp();
                 }
+#pragma unroll 1
+                for (int q = 0; q < 4; ++q)
+                    write_terms(lanes + kLocColV + (buf * 4 + q) * kSlotCols, ct, e, e < p.vd, q, w);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -788,13 +798,10 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
             if (ok && grp == 0) {
                 if (!(ok = wait(&bar.h_full, nu))) break;
                 tc_fence_after();
-#pragma unroll 1
-                for (int m = 0; m < p.kd / 32; ++m) {
-                    uint32_t r[32];
-                    tmem_get32(lanes + 32 * m, r);
-                    state_store(p, to, 32 * m, e, r);
+                tmem_columns(lanes, p.kd / 16, [&](int m, const uint32_t (&r)[16]) {
+                    state_store(p, to, 16 * m, e, r);
                     __syncwarp();
-                }
+                });
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.h_free);
@@ -845,7 +852,7 @@ cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, 
     const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (err != cudaSuccess) return err;
     ProfScope prof(stream, local ? "decay_local_kernel" : "decay_out_kernel");
-    kern<<<(unsigned)std::min<int64_t>(args.units, sms), kThreads, bytes, stream>>>(maps, args);
+    kern<<<(unsigned)std::min<int64_t>(args.units, sms), local ? kLocThreads : kOutThreads, bytes, stream>>>(maps, args);
     count_launch();
     return cudaGetLastError();
 }
