@@ -11,27 +11,34 @@
 // and for a reversed pass i - j -> j - i, j <= i -> j >= i, lam^{i+1} -> lam^{n-1-i} and
 // lam^{n-1-j} -> lam^{j+1}.  Dividing P by the factor of the state's part lets both parts sum in
 // one accumulator; the floor of f keeps P in range for any decay, and what it adds is the
-// state's part taken at 2^-64 where lam^{i+1} is below that.  All four products run on the tensor cores with fp32 accumulators in the tensor
-// memory (TMEM), 128 x 128 each:
+// state's part taken at 2^-64 where lam^{i+1} is below that.
+//
+// The state is kept as S = 2^-y S^ with y in [0, 1).  A tile's decay lam^n = 2^-x moves
+// y + x: its whole part scales S^ by a power of two, which the tensor cores do as they read
+// the accumulator, and the rest becomes the next y, which goes into the weights.  So no warp
+// ever rewrites the state.  (A whole part of 64 or more: the old state is left out of the sum.)
+//
+// All four products run on the tensor cores with fp32 accumulators in the tensor memory
+// (TMEM), 128 x 128 each:
 //     Sc = A B^T                     lanes = query tokens i
-//     S^T <- lam^n S^T + C'^T B      lanes = value index e: the resident state
-//     O  = A S                       lanes = query tokens i; S from shared memory in bf16
+//     S^^T <- 2^-k S^^T + C'^T B     lanes = value index e: the resident state
+//     O  = A S^                      lanes = query tokens i; S^ from shared memory in bf16
 //     O  += P C                      P in TMEM in bf16
 // in this order.  A tile of one head is 128 KB of HBM traffic (3 loads, 1 store; 2.9 us of an
 // SM's share of the measured bandwidth) and 25 MFLOP (2.0 us of an SM's share of the bf16
 // rate), so the pass can be bound by HBM if its other work stays out of the way.  The stages
 // of a tile run in different warps and overlap those of its neighbours:
 //   warps 0-3    Sc -> P (bf16, over Sc in TMEM); O -> out
-//   warps 4-7    S^T -> bf16 (shared memory) and lam^n S^T (TMEM)
-//   warps 8-11   C' = weighted C -> TMEM, 32 tokens at a time
-//   warp 12      TMA loads of A, B, C, two stages of 96 KB
-//   warp 13      issues every MMA (their order in the tensor pipe is the issue order)
+//   warps 4-7    S^^T -> bf16 (shared memory)
+//   warps 8-15   C' = weighted C -> TMEM, 16 tokens at a time, two groups in turn
+//   warp 16      TMA loads of A, B, C, two stages of 96 KB
+//   warp 17      issues every MMA (their order in the tensor pipe is the issue order)
 //
-// Rounding.  The state is fp32 and so are its updates: C' = s_upd lam^{..} C has 24
-// significant bits, so it goes in as the sum of three bf16 numbers that represent it exactly
-// (three products instead of one; two would leave 2^-17 in hT and dh0).  P and the state
-// as a factor of O are rounded to bf16: each adds an error of at most 2^-9 of its part of
-// an output that is itself rounded to bf16.
+// Rounding.  The state is fp32 and so are its updates: C' has 24 significant bits, so it goes
+// in as the sum of three bf16 numbers that represent it exactly (three products instead of
+// one; two would leave 2^-17 in hT and dh0).  P and the state as a factor of O are rounded to
+// bf16: each adds an error of at most 2^-8 of its part of an output that is itself rounded
+// to bf16 (2.3e-3 in the mean square over the outputs against 1.7e-3 for their rounding alone).
 //
 // A block is persistent: it walks the units (segment, head, pass) with a stride of the grid
 // and its pipeline runs on across them.  The three passes of a backward call are
@@ -74,6 +81,23 @@ struct TcArgs {
     uint64_t wait_ns;
 };
 
+// Waits (a whole warp) until `b` has completed its use number `use` (from 0).  False if that
+// takes longer than the limit (0: look once), or once another wait of the block has run
+// out, which sets the status word.
+__device__ __forceinline__ bool wait_use(uint64_t *b, uint32_t use, uint64_t limit_ns, volatile int *stop,
+                                         int *status) {
+    if (__all_sync(kFull, limit_ns ? mbar_try_wait(b, use & 1u) : mbar_test_wait(b, use & 1u))) return true;
+    if (limit_ns) {
+        const uint64_t t0 = globaltimer_ns();
+        do {
+            if (__all_sync(kFull, mbar_try_wait(b, use & 1u))) return true;
+        } while (__all_sync(kFull, !*stop && globaltimer_ns() - t0 <= limit_ns));
+    }
+    if (!*stop) set_status(status, GDR_ERR_TIMEOUT);
+    *stop = 1;
+    return false;
+}
+
 // One unit of a block's walk.
 struct Unit {
     int pass, h;
@@ -107,6 +131,9 @@ __device__ __forceinline__ void tile_of(const Unit &u, bool rev, int i, int64_t 
     n = (int)min((int64_t)kC, u.t1 - t);
 }
 
+// Descriptor offset of K-step k (16 of up to 128 elements) of a K-major tile.
+__device__ constexpr uint64_t k_major(uint32_t k) { return ((k >> 2) * kBox + (k & 3) * 32) >> 4; }
+
 __device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *map, int width, int h, int64_t t,
                                           uint64_t *bar) {
     tma_load_3d(dst, map, 0, h, (int)t, bar);
@@ -121,18 +148,23 @@ __device__ __forceinline__ void zero_rows(uint8_t *tile, int width, int n, int l
             *(uint4 *)(tile + box * kBox + sw128_off(n + i / 8, (i & 7) * 16)) = make_uint4(0, 0, 0, 0);
 }
 
-// The weights of a tile's tokens in the update of the state, for one warp: token i has
-// s_upd lam^{len - 1 - i + past} (forward) or s_upd lam^{i + 1 + past}; rows from len on are
-// not the sequence's and have 0.
-__device__ __forceinline__ void tile_weights(float *w, int len, bool rev, float gd, float s_upd, int64_t past,
-                                             int lane) {
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < kC / 32; ++k) {
-        const int i = lane + 32 * k;
-        w[i] = i < len ? s_upd * expf(gd * (float)(past + (rev ? i + 1 : len - 1 - i))) : 0.f;
-    }
-    __syncwarp();
+// log2 lam; below -200 every power but the zeroth is out of the range of fp32 and its
+// reciprocals, whatever lam is, and differences of multiples stay exact enough.
+__device__ __forceinline__ float decay_log2(float gd) { return fmaxf(gd * 1.4426950408889634f, -200.f); }
+
+// The exponent y of the state S = 2^-y S^ after a tile of len tokens; returns the whole part,
+// the power of two that S^ is scaled down by (0 for a growing state).
+__device__ __forceinline__ int advance_exponent(float &y, float g2, int len) {
+    y = fmaf(-g2, (float)len, y);
+    const float whole = fmaxf(floorf(y), 0.f);
+    y -= whole;
+    return (int)whole;
+}
+
+// A token's weight in the update of the state: s_upd lam^{len - 1 - i + past} (forward) or
+// s_upd lam^{i + 1 + past}; rows from len on are not the sequence's and have 0.
+__device__ __forceinline__ float token_weight(int i, int len, bool rev, float gd, float s_upd, int64_t past) {
+    return i < len ? s_upd * expf(gd * (float)(past + (rev ? i + 1 : len - 1 - i))) : 0.f;
 }
 
 // Zeroes the rows from n on of the 32 columns from e0 (one warp) of a tile: what a weight
@@ -143,45 +175,58 @@ __device__ __forceinline__ void zero_columns(uint8_t *tile, int e0, int n, int l
             make_uint4(0, 0, 0, 0);
 }
 
-// Quarter q (32 tokens) of a tile's C'^T, row e, into three times 16 TMEM columns at `at`
-// (a whole warp): the weighted values x w as the bf16 terms hi + mid + lo = x w exactly, cut
+// 16 tokens (from 16 k) of a tile's C'^T, row e, into three times 8 TMEM columns at `at` (a
+// whole warp): the weighted values x w as the bf16 terms hi + mid + lo = x w exactly, cut
 // off the top of the fp32 product 8 significant bits at a time; a column holds two tokens.
-__device__ __forceinline__ void write_terms(uint32_t at, const uint8_t *tile, int e, bool any, int q,
+// w: the 16 weights.
+__device__ __forceinline__ void write_terms(uint32_t at, const uint8_t *tile, int e, bool any, int k,
                                             const float *w) {
-    uint32_t hi[16], mid[16], lo[16];
+    uint32_t hi[8], mid[8], lo[8];
     if (any) {
-        const uint8_t *col = tile + (e >> 6) * kBox + (e & 7) * 2 + q * 4096;
+        const uint8_t *col = tile + (e >> 6) * kBox + (e & 7) * 2 + k * 2048;
         const uint32_t chunk = (e & 63) >> 3;
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-            const float4 w4 = *(const float4 *)&w[32 * q + 2 * i];
+        for (int i = 0; i < 8; i += 2) {
+            const float4 w4 = *(const float4 *)&w[2 * i];
             const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
             float y[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int r = 2 * i + k;
+            for (int j = 0; j < 4; ++j) {
+                const int r = 2 * i + j;
                 const uint32_t x = *(const uint16_t *)(col + (r >> 3) * 1024 + (r & 7) * 128 + ((chunk ^ (r & 7)) << 4));
-                y[k] = __uint_as_float(x << 16) * wv[k];
+                y[j] = __uint_as_float(x << 16) * wv[j];
             }
             hi[i] = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632);
             hi[i + 1] = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x7632);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] -= __uint_as_float(__float_as_uint(y[k]) & 0xffff0000u);
+            for (int j = 0; j < 4; ++j) y[j] -= __uint_as_float(__float_as_uint(y[j]) & 0xffff0000u);
             mid[i] = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632);
             mid[i + 1] = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x7632);
 #pragma unroll
-            for (int k = 0; k < 4; ++k) y[k] -= __uint_as_float(__float_as_uint(y[k]) & 0xffff0000u);
+            for (int j = 0; j < 4; ++j) y[j] -= __uint_as_float(__float_as_uint(y[j]) & 0xffff0000u);
             lo[i] = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632);
             lo[i + 1] = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x7632);
         }
     } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) hi[j] = mid[j] = lo[j] = 0;
+        for (int j = 0; j < 8; ++j) hi[j] = mid[j] = lo[j] = 0;
     }
     __syncwarp();
-    tmem_st16(at, hi);
-    tmem_st16(at + 16, mid);
-    tmem_st16(at + 32, lo);
+    tmem_st8(at, hi);
+    tmem_st8(at + 8, mid);
+    tmem_st8(at + 16, lo);
+}
+
+// 32 bytes of a row, in one piece where `wide` (the address is a multiple of 32).
+__device__ __forceinline__ void store32(void *dst, const uint32_t (&o)[8], bool wide) {
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(o[0]), "r"(o[1]),
+                     "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                     : "memory");
+    } else {
+        ((uint4 *)dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        ((uint4 *)dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -247,20 +292,22 @@ template <typename F> __device__ __forceinline__ void tmem_columns(uint32_t at, 
 // ---------------------------------------------------------------------------
 // the output pass
 // ---------------------------------------------------------------------------
-constexpr int kOutThreads = 32 * 14, kOutProducer = 12, kOutIssuer = 13;   // warps
+constexpr int kOutThreads = 32 * 18, kOutProducer = 16, kOutIssuer = 17;   // warps
 // TMEM columns
 constexpr uint32_t kColS = 0;      // Sc, then P in its first 64 columns
 constexpr uint32_t kColO = 128;
 constexpr uint32_t kColH = 256;    // S^T
-constexpr uint32_t kColV = 384;    // C'^T: two slots of 32 tokens x 3 terms
-constexpr uint32_t kSlotCols = 48;
+constexpr uint32_t kColV = 384;    // C'^T: slots of 16 tokens x 3 terms
+constexpr uint32_t kSlotCols = 24, kSlots = 5, kParts = kC / 16;   // kParts uses of slots per tile
+constexpr uint32_t kColZero = kColV + kSlots * kSlotCols;          // 8 columns of zeros
 constexpr uint32_t kTmemCols = 512;
+static_assert(kColZero + 8 <= kTmemCols, "TMEM");
 // shared memory
 constexpr uint32_t kStage = 3 * kTile;               // A, B, C
 constexpr uint32_t kOffH = 2 * kStage;               // the state in bf16, [e][d], K-major
 constexpr uint32_t kOffBar = kOffH + kTile;
-constexpr uint32_t kOffW = kOffBar + 256;            // weights of a tile's tokens, a copy per warp
-constexpr uint32_t kSmemOut = kOffW + 4 * kC * 4;
+constexpr uint32_t kOffW = kOffBar + 256;            // weights of a group's 64 tokens, a copy per warp
+constexpr uint32_t kSmemOut = kOffW + 8 * (kC / 2) * 4;
 static_assert(kSmemOut <= 232448, "shared memory");
 
 struct OutBars {
@@ -268,14 +315,14 @@ struct OutBars {
     uint64_t free_a[2];    // the stage's A is read
     uint64_t free_bc[2];   // ... its B and C
     uint64_t s_full;       // Sc complete
-    uint64_t p_ready;      // P written, O scaled (4 warps)
-    uint64_t o1_full;      // O = A S complete (the bf16 state is read)
+    uint64_t p_ready;      // P written (4 warps)
+    uint64_t o1_full;      // O = A S^ complete (the bf16 state is read)
     uint64_t o_full;       // O complete
     uint64_t o_free;       // O read (4 warps)
-    uint64_t h_ready;      // the bf16 state written, S^T scaled (4 warps)
-    uint64_t v_ready[2];   // a slot of C' written (4 warps)
-    uint64_t v_free[2];    // ... read
-    uint64_t kv_full;      // the tile's update of S^T complete
+    uint64_t h_ready;      // the bf16 state written (4 warps)
+    uint64_t v_ready[kSlots];   // a slot of C' written (4 warps)
+    uint64_t v_free[kSlots];    // ... read
+    uint64_t kv_full;      // the tile's update of S^ complete
     uint64_t fin;          // every MMA of the block complete
     uint32_t tmem;
     int stop;
@@ -296,6 +343,8 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             mbar_init(&bar.full[i], 1);
             mbar_init(&bar.free_a[i], 1);
             mbar_init(&bar.free_bc[i], 1);
+        }
+        for (uint32_t i = 0; i < kSlots; ++i) {
             mbar_init(&bar.v_ready[i], 4);
             mbar_init(&bar.v_free[i], 1);
         }
@@ -320,14 +369,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
     tc_fence_after();
     const uint32_t tm = bar.tmem;
 
-    // Waits (whole warp) until `b` has completed its use number `use` (from 0); false once
-    // any wait of the block has run out.
-    auto wait = [&](uint64_t *b, uint32_t use) {
-        if (__all_sync(kFull, mbar_wait(b, use & 1u, A.wait_ns)) && !*stop) return true;
-        if (lane == 0 && !*stop) set_status(A.status, GDR_ERR_TIMEOUT);
-        *stop = 1;
-        return false;
-    };
+    auto wait = [&](uint64_t *b, uint32_t use) { return wait_use(b, use, A.wait_ns, stop, A.status); };
     uint32_t it = 0;   // tiles so far: the use number of every once-a-tile barrier
     Unit u;
 
@@ -358,14 +400,18 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             __all_sync(kFull, mbar_wait(&bar.full[k & 1], (k >> 1) & 1u, kDrainNs));
     } else if (warp == kOutIssuer) {
         const uint32_t s0 = smem_u32(smem);
+        const bool lead = elect_one();
         bool ok = true;
         for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
             if (!unit_of(A, n, false, u)) continue;
             const DecayPass &p = A.pass[u.pass];
+            const uint32_t kd16 = (uint32_t)p.kd / 16;
             const uint32_t id_s = instr_desc(kC, kC, 1, false, false);
             const uint32_t id_o1 = instr_desc(kC, p.vd, 1, false, false);
             const uint32_t id_o2 = instr_desc(kC, p.vd, 1, false, true);
             const uint32_t id_h = instr_desc(kC, p.kd, 1, false, true);
+            const float g2 = decay_log2(decay_log(A.g.log_decay, u.h));
+            float y = 0.f;
             for (int i = 0; i < u.tiles; ++i, ++it) {
                 const uint32_t st = it & 1;
                 int64_t t;
@@ -384,57 +430,49 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 const uint64_t dBt = smem_desc(sb, kBox, 1024, kSw128), dCt = smem_desc(sc, kBox, 1024, kSw128);
                 const uint64_t dH = smem_desc(s0 + kOffH, 16, 1024, kSw128);
                 // the previous tile's P is read: its product precedes this one in the pipe
-                if (elect_one()) {
-                    for (int k = 0; k < p.kd / 16; ++k) {
-                        const uint64_t o = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
-                        mma_f16_ss(tm + kColS, dA + o, dB + o, id_s, k > 0);
-                    }
-                    mma_commit(&bar.s_full);
-                }
-                __syncwarp();
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k)
+                    if (k < kd16) mma_f16_ss_if(lead, tm + kColS, dA + k_major(k), dB + k_major(k), id_s, k > 0);
+                mma_commit_if(lead, &bar.s_full);
                 if (!(ok = wait(&bar.h_ready, it))) break;
-                for (int q = 0; q < 4 && ok; ++q) {
-                    const uint32_t slot = q & 1;
-                    if (!(ok = wait(&bar.v_ready[slot], 2 * it + (q >> 1)))) break;
+                // the state's power of two: 15 at a time on products with zeros, the rest with
+                // the first one that adds something
+                int down = advance_exponent(y, g2, len);
+                const bool keep = down < 64;
+                for (; keep && down > 15; down -= 15)
+                    mma_f16_ts_scaled_if(lead, tm + kColH, tm + kColZero, dBt, id_h, 15);
+#pragma unroll 1
+                for (uint32_t k = 0; k < kParts; ++k) {
+                    const uint32_t part = it * kParts + k, slot = part % kSlots;
+                    if (!(ok = wait(&bar.v_ready[slot], part / kSlots))) break;
                     tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int term = 0; term < 3; ++term)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                mma_f16_ts(tm + kColH, tm + kColV + slot * kSlotCols + term * 16 + k * 8,
-                                           dBt + (((q * 2 + k) * 2048) >> 4), id_h, 1);
-                        mma_commit(&bar.v_free[slot]);
-                        if (q == 3) mma_commit(&bar.kv_full);
-                    }
-                    __syncwarp();
+                    const uint32_t av = tm + kColV + slot * kSlotCols;
+                    const uint64_t db = dBt + ((k * 2048) >> 4);
+                    if (k == 0 && keep) mma_f16_ts_scaled_if(lead, tm + kColH, av, db, id_h, down);
+                    else mma_f16_ts_if(lead, tm + kColH, av, db, id_h, k > 0);
+                    mma_f16_ts_if(lead, tm + kColH, av + 8, db, id_h, 1);
+                    mma_f16_ts_if(lead, tm + kColH, av + 16, db, id_h, 1);
+                    mma_commit_if(lead, &bar.v_free[slot]);
                 }
+                mma_commit_if(lead, &bar.kv_full);
                 if (!ok || (it && !(ok = wait(&bar.o_free, it - 1)))) break;
                 tc_fence_after();
-                if (elect_one()) {
-                    for (int k = 0; k < p.kd / 16; ++k) {
-                        const uint64_t o = ((k >> 2) * kBox + (k & 3) * 32) >> 4;
-                        mma_f16_ss(tm + kColO, dA + o, dH + o, id_o1, k > 0);
-                    }
-                    mma_commit(&bar.o1_full);
-                    mma_commit(&bar.free_a[st]);
-                }
-                __syncwarp();
+#pragma unroll
+                for (uint32_t k = 0; k < 8; ++k)
+                    if (k < kd16) mma_f16_ss_if(lead, tm + kColO, dA + k_major(k), dH + k_major(k), id_o1, k > 0);
+                mma_commit_if(lead, &bar.o1_full);
+                mma_commit_if(lead, &bar.free_a[st]);
                 if (!(ok = wait(&bar.p_ready, it))) break;
                 tc_fence_after();
-                if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kC / 16; ++k)
-                        mma_f16_ts(tm + kColO, tm + kColS + k * 8, dCt + ((k * 2048) >> 4), id_o2, 1);
-                    mma_commit(&bar.o_full);
-                    mma_commit(&bar.free_bc[st]);
-                }
-                __syncwarp();
+                for (uint32_t k = 0; k < kC / 16; ++k)
+                    mma_f16_ts_if(lead, tm + kColO, tm + kColS + k * 8, dCt + ((k * 2048) >> 4), id_o2, 1);
+                mma_commit_if(lead, &bar.o_full);
+                mma_commit_if(lead, &bar.free_bc[st]);
             }
         }
         // no tensor-core operation may still run when the TMEM is released
-        if (elect_one()) mma_commit(&bar.fin);
-        __syncwarp();
+        mma_commit_if(lead, &bar.fin);
         __all_sync(kFull, mbar_wait(&bar.fin, 0, kDrainNs));
     } else if (warp < 4) {
         // ---- weights and outputs: thread = token row of the tile
@@ -445,16 +483,16 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             if (!unit_of(A, n, false, u)) continue;
             const DecayPass &p = A.pass[u.pass];
             const bool rev = p.rev;
-            // log2 lam; below -200 (lam / f < 2^-136) a weight is 0 whatever lam is, and the
-            // differences of its multiples below stay exact enough
-            const float g2 = fmaxf(decay_log(A.g.log_decay, u.h) * 1.4426950408889634f, -200.f);
+            const float g2 = decay_log2(decay_log(A.g.log_decay, u.h));
+            float y = 0.f;
             const float l_upd = p.s_upd;
             for (int i = 0; i < u.tiles; ++i, ++it) {
                 int64_t t;
                 int len;
                 tile_of(u, rev, i, t, len);
-                // log2 of the row's f
-                const float lf = fmaxf(g2 * (float)(rev ? max(len - 1 - row, 0) : row + 1), -64.f);
+                // log2 of the row's f, and of the state's factor
+                const float lf = fmaxf(g2 * (float)(rev ? max(len - 1 - row, 0) : row + 1), -64.f) - y;
+                advance_exponent(y, g2, len);
                 if (!(ok = wait(&bar.s_full, it))) break;
                 tc_fence_after();
                 tmem_columns(lanes + kColS, 8, [&](int m, const uint32_t (&x)[16]) {
@@ -468,13 +506,13 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                         const float l0 = fmaf(g2, (float)d, -lf), l1 = rev ? g2 : -g2;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            float y[2];
+                            float v[2];
 #pragma unroll
                             for (int k = 0; k < 2; ++k)
-                                y[k] = d + (2 * j + k) * step >= 0
+                                v[k] = d + (2 * j + k) * step >= 0
                                            ? l_upd * __uint_as_float(x[2 * j + k]) * exp2_approx(fmaf((float)(2 * j + k), l1, l0))
                                            : 0.f;
-                            o[j] = pack2(y[0], y[1]);
+                            o[j] = pack2(v[0], v[1]);
                         }
                     }
                     tmem_st8(lanes + kColS + 8 * m, o);
@@ -486,17 +524,15 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 if (!(ok = wait(&bar.o_full, it))) break;
                 tc_fence_after();
                 const float f = p.s_out * exp2f(lf);
+                const bool wide = (uintptr_t)p.out % 32 == 0;
                 __nv_bfloat16 *dst = (__nv_bfloat16 *)p.out + ((t + row) * H + u.h) * (int64_t)p.vd;
                 tmem_columns(lanes + kColO, p.vd / 16, [&](int m, const uint32_t (&x)[16]) {
                     if (row < len) {
+                        uint32_t o[8];
 #pragma unroll
-                        for (int j = 0; j < 16; j += 8) {
-                            uint32_t o[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                o[k] = pack2(f * __uint_as_float(x[j + 2 * k]), f * __uint_as_float(x[j + 2 * k + 1]));
-                            *(uint4 *)(dst + 16 * m + j) = make_uint4(o[0], o[1], o[2], o[3]);
-                        }
+                        for (int j = 0; j < 8; ++j)
+                            o[j] = pack2(f * __uint_as_float(x[2 * j]), f * __uint_as_float(x[2 * j + 1]));
+                        store32(dst + 16 * m, o, wide);
                     }
                     __syncwarp();
                 });
@@ -509,11 +545,17 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
         // ---- state: thread = value index (TMEM lane)
         const int e = tid - 128;
         const uint32_t lanes = tm + ((uint32_t)((warp - 4) * 32) << 16);
+        {
+            const uint32_t zero[8] = {};
+            tmem_st8(lanes + kColZero, zero);
+            tmem_st_wait();   // the first h_ready publishes it
+        }
         bool ok = true;
         for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
             if (!unit_of(A, n, false, u)) continue;
             const DecayPass &p = A.pass[u.pass];
-            const float gd = decay_log(A.g.log_decay, u.h);
+            const float g2 = decay_log2(decay_log(A.g.log_decay, u.h));
+            float y = 0.f;
             const float *in = decay_state_in(p, u.seg, H, u.h);
             float *to = decay_state_out(p, u.seg, H, u.h);
             if (u.tiles == 0) {   // an empty sequence: the state goes through
@@ -528,9 +570,9 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 int64_t t;
                 int len;
                 tile_of(u, p.rev, i, t, len);
-                const DecayFactor decay(gd * (float)len);
-                // 16 columns of the entering state: to shared memory in bf16, and decayed
-                auto take = [&](int m, uint32_t (&r)[16]) {
+                advance_exponent(y, g2, len);
+                // 16 columns of the entering state, to shared memory in bf16
+                auto take = [&](int m, const uint32_t (&r)[16]) {
 #pragma unroll
                     for (int j = 0; j < 16; j += 8) {
                         uint32_t o[4];
@@ -540,11 +582,8 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                         *(uint4 *)(smem + kOffH + (m >> 2) * kBox + sw128_off(e, (16 * (m & 3) + j) * 2)) =
                             make_uint4(o[0], o[1], o[2], o[3]);
                     }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(decay(__uint_as_float(r[j])));
-                    tmem_st16(lanes + kColH + 16 * m, r);
                 };
-                // the update of S^T is complete, and the bf16 state read
+                // the update of S^ is complete, and the bf16 state read
                 if (it && !((ok = wait(&bar.kv_full, it - 1)) && (ok = wait(&bar.o1_full, it - 1)))) break;
                 tc_fence_after();
                 if (i == 0) {
@@ -554,12 +593,13 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                         state_load(p, in, 16 * m, e, r);
                         __syncwarp();
                         take(m, r);
+                        tmem_st16(lanes + kColH + 16 * m, r);
                     }
+                    tmem_st_wait();
                 } else {
                     tmem_columns(lanes + kColH, p.kd / 16, take);
                 }
                 fence_proxy_async_smem();
-                tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.h_ready);
@@ -567,43 +607,59 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             if (ok && to) {
                 if (!(ok = wait(&bar.kv_full, it - 1))) break;
                 tc_fence_after();
-                tmem_columns(lanes + kColH, p.kd / 16, [&](int m, const uint32_t (&r)[16]) {
+                const float f = exp2f(-y);
+                tmem_columns(lanes + kColH, p.kd / 16, [&](int m, uint32_t (&r)[16]) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(f * __uint_as_float(r[j]));
                     state_store(p, to, 16 * m, e, r);
                     __syncwarp();
                 });
             }
         }
     } else {
-        // ---- weighted values: thread = value index (TMEM lane)
-        const int e = tid - 256;
-        const uint32_t lanes = tm + ((uint32_t)((warp - 8) * 32) << 16);
-        float *w = (float *)(smem + kOffW) + (warp - 8) * kC;
+        // ---- weighted values: thread = value index (TMEM lane); group grp takes every other
+        // 16 tokens, its token l = 16 a + j being the tile's 16 (2 a + grp) + j
+        const int grp = (warp - 8) >> 2, e = tid & 127;
+        const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
+        float *w = (float *)(smem + kOffW) + (warp - 8) * (kC / 2);
         bool ok = true;
         for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
             if (!unit_of(A, n, false, u)) continue;
             const DecayPass &p = A.pass[u.pass];
-            const float gd = decay_log(A.g.log_decay, u.h);
-            int wlen = -1;   // tokens of the tile that w is for
+            const float gd = decay_log(A.g.log_decay, u.h), g2 = decay_log2(gd);
+            float y = 0.f, w0 = 0.f, w1 = 0.f;
+            int wlen = -1;   // tokens of the tile that w0, w1 are for
             for (int i = 0; i < u.tiles; ++i, ++it) {
                 const uint32_t st = it & 1;
                 int64_t t;
                 int len;
                 tile_of(u, p.rev, i, t, len);
-                if (len != wlen) tile_weights(w, len, p.rev, gd, p.s_upd, 0, lane);
-                wlen = len;
+                if (len != wlen) {
+                    const int tok = 16 * (2 * (lane >> 4) + grp) + (lane & 15);
+                    w0 = token_weight(tok, len, p.rev, gd, p.s_upd, 0);
+                    w1 = token_weight(tok + 64, len, p.rev, gd, p.s_upd, 0);
+                    wlen = len;
+                }
+                advance_exponent(y, g2, len);
+                const float up = exp2f(y);   // into S^ after the tile
+                __syncwarp();                // the last tile's weights are read
+                w[lane] = w0 * up;
+                w[lane + 32] = w1 * up;
+                __syncwarp();
                 if (!(ok = wait(&bar.full[st], it >> 1))) break;
                 uint8_t *ct = smem + st * kStage + 2 * kTile;
                 if (len < kC && e < p.vd) {
+                    // both groups write the same zeros; the product with P reads them too
                     zero_columns(ct, e & ~31, len, lane);
-                    fence_proxy_async_smem();   // the product with P reads them too
+                    fence_proxy_async_smem();
                     __syncwarp();
                 }
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q) {
-                    const uint32_t slot = q & 1, use = 2 * it + (q >> 1);
+                for (int a = 0; a < 4; ++a) {
+                    const uint32_t part = it * kParts + 2 * a + grp, slot = part % kSlots, use = part / kSlots;
                     if (use && !(ok = wait(&bar.v_free[slot], use - 1))) break;
                     tc_fence_after();
-                    write_terms(lanes + kColV + slot * kSlotCols, ct, e, e < p.vd, q, w);
+                    write_terms(lanes + kColV + slot * kSlotCols, ct, e, e < p.vd, 2 * a + grp, w + 16 * a);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -633,8 +689,8 @@ constexpr uint32_t kLocStage = 2 * kTile;                    // B, C
 constexpr uint32_t kLocOffBar = kLocStages * kLocStage;
 constexpr uint32_t kLocOffW = kLocOffBar + 256;              // weights, a copy per warp
 constexpr uint32_t kSmemLocal = kLocOffW + 8 * kC * 4;
-constexpr uint32_t kLocColV = 128;                           // two buffers of 4 x 48 columns
-static_assert(kLocColV + 2 * 4 * kSlotCols <= kTmemCols, "TMEM");
+constexpr uint32_t kLocColV = 128;                           // two buffers of a tile each
+static_assert(kLocColV + 2 * kParts * kSlotCols <= kTmemCols, "TMEM");
 
 struct LocalBars {
     uint64_t full[kLocStages], free[kLocStages];
@@ -678,12 +734,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
     __syncthreads();
     tc_fence_after();
     const uint32_t tm = bar.tmem;
-    auto wait = [&](uint64_t *b, uint32_t use) {
-        if (__all_sync(kFull, mbar_wait(b, use & 1u, A.wait_ns)) && !*stop) return true;
-        if (lane == 0 && !*stop) set_status(A.status, GDR_ERR_TIMEOUT);
-        *stop = 1;
-        return false;
-    };
+    auto wait = [&](uint64_t *b, uint32_t use) { return wait_use(b, use, A.wait_ns, stop, A.status); };
     uint32_t it = 0, nu = 0;   // tiles and units so far
     Unit u;
 
@@ -711,6 +762,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
             __all_sync(kFull, mbar_wait(&bar.full[k % kLocStages], (k / kLocStages) & 1u, kDrainNs));
     } else if (warp == kLocIssuer) {
         const uint32_t s0 = smem_u32(smem);
+        const bool lead = elect_one();
         bool ok = true;
         for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
             if (!unit_of(A, n, true, u) || u.tiles == 0) continue;
@@ -731,24 +783,21 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                 if (!(ok = wait(&bar.v_ready[buf], it >> 1))) break;
                 tc_fence_after();
                 const uint64_t dBt = smem_desc(s0 + st * kLocStage, kBox, 1024, kSw128);
-                if (elect_one()) {
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int term = 0; term < 3; ++term)
-#pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                mma_f16_ts(tm, tm + kLocColV + (buf * 4 + q) * kSlotCols + term * 16 + k * 8,
-                                           dBt + (((q * 2 + k) * 2048) >> 4), id_h, i + q + term + k > 0);
-                    mma_commit(&bar.v_free[buf]);
-                    mma_commit(&bar.free[st]);
-                    if (i == u.tiles - 1) mma_commit(&bar.h_full);
+#pragma unroll 1
+                for (uint32_t k = 0; k < kParts; ++k) {
+                    const uint32_t av = tm + kLocColV + (buf * kParts + k) * kSlotCols;
+                    const uint64_t db = dBt + ((k * 2048) >> 4);
+                    mma_f16_ts_if(lead, tm, av, db, id_h, i + k > 0);
+                    mma_f16_ts_if(lead, tm, av + 8, db, id_h, 1);
+                    mma_f16_ts_if(lead, tm, av + 16, db, id_h, 1);
                 }
-                __syncwarp();
+                mma_commit_if(lead, &bar.v_free[buf]);
+                mma_commit_if(lead, &bar.free[st]);
+                if (i == u.tiles - 1) mma_commit_if(lead, &bar.h_full);
             }
             ++nu;
         }
-        if (elect_one()) mma_commit(&bar.fin);
-        __syncwarp();
+        mma_commit_if(lead, &bar.fin);
         __all_sync(kFull, mbar_wait(&bar.fin, 0, kDrainNs));
     } else {
         const int grp = warp >> 2, e = tid & 127;
@@ -778,7 +827,12 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                 tile_of(u, rev, i, t, len);
                 const uint32_t use = it >> 1;
                 // past the tile: its distance to the segment's end (its start, reversed)
-                tile_weights(w, len, rev, gd, p.s_upd, rev ? t - u.t0 : u.t1 - t - len, lane);
+                const int64_t past = rev ? t - u.t0 : u.t1 - t - len;
+                __syncwarp();   // the last tile's weights are read
+#pragma unroll
+                for (int k = 0; k < kC / 32; ++k)
+                    w[lane + 32 * k] = token_weight(lane + 32 * k, len, rev, gd, p.s_upd, past);
+                __syncwarp();
                 if (!(ok = wait(&bar.full[st], it / kLocStages))) break;
                 if (use && !(ok = wait(&bar.v_free[buf], use - 1))) break;
                 tc_fence_after();
@@ -788,8 +842,8 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                     __syncwarp();
                 }
 #pragma unroll 1
-                for (int q = 0; q < 4; ++q)
-                    write_terms(lanes + kLocColV + (buf * 4 + q) * kSlotCols, ct, e, e < p.vd, q, w);
+                for (uint32_t k = 0; k < kParts; ++k)
+                    write_terms(lanes + kLocColV + (buf * kParts + k) * kSlotCols, ct, e, e < p.vd, k, w + 16 * k);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
