@@ -533,10 +533,10 @@ gdr_status_t validate_forward(const void *q, const void *k, const void *v, const
 // ---------------------------------------------------------------------------
 namespace {
 
-// Scratch of one call, every region 256-byte aligned: the plan (packed input), the
-// boundary states of the forward chain and, for the backward pass, of the reversed one.
+// Scratch of one call, every region 256-byte aligned: the plan and two unit counters (packed
+// input), the boundary states of the forward chain and, for the backward pass, of the reversed one.
 struct DecayLayout {
-    size_t plan = 0, slots = 0, slots_rev = 0, copy = 0, total = 0;
+    size_t plan = 0, next = 0, slots = 0, slots_rev = 0, copy = 0, total = 0;
 };
 
 struct DecayShape {
@@ -553,8 +553,8 @@ constexpr int64_t kDecayStepTokens = 8;   // most tokens that decay_step_kernel 
 //     ceil(units N s / slots) (ceil(tiles / s) + fixed) + (s - 1) / s * local
 // in tiles: whole rounds of the machine, a start-up per segment, and the local pass over
 // the inner segments, which reads half of what the output pass moves.  Packed sequences
-// (lengths unknown on the host) are cut into even shares of all tiles, two per slot, so
-// that one long sequence among short ones is cut too and the rounds even out.
+// (lengths unknown on the host) are cut into even shares of all tiles, six per slot, so
+// that one long sequence among short ones is cut too and the slots end together.
 // GDR_DECAY_SEG_TILES=n cuts into n tiles per segment whatever the sizes (the parity tests
 // run many short segments).
 DecayGeom decay_geom(const DecayShape &s, int64_t units, int64_t slots, int64_t min_tiles, double fixed) {
@@ -587,7 +587,7 @@ DecayGeom decay_geom(const DecayShape &s, int64_t units, int64_t slots, int64_t 
         g.max_slots = g.max_segs - s.N;
     } else {
         const int64_t tiles = (s.T_total + kDecayTile - 1) / kDecayTile;
-        const int64_t even = std::max(min_tiles, (tiles * units + 2 * slots - 1) / (2 * slots));
+        const int64_t even = std::max(min_tiles, (tiles * units + 6 * slots - 1) / (6 * slots));
         const int64_t seg = std::min<int64_t>(set > 0 ? set : even, 1 << 24);
         g.seg_tokens = seg * kDecayTile;
         // a sequence of len tokens has ceil(len / seg) segments, at least one
@@ -638,6 +638,7 @@ DecayLayout decay_layout(const DecayShape &s, const DecayGeom &g, bool backward)
         return at;
     };
     L.plan = take(s.varlen ? 3 * sizeof(int64_t) * (size_t)(s.N + 1) : 0);
+    L.next = take(s.varlen ? 2 * sizeof(unsigned long long) : 0);
     L.slots = take(st * g.max_slots);
     L.slots_rev = take(backward ? st * g.max_slots : 0);
     // forward in place (hT = h0) with segments: the entering states' copy
@@ -663,9 +664,17 @@ gdr_status_t decay_plan(DecayGeom *g, const int32_t *cu, const float *log_decay,
 // Runs passes that are independent of each other, after the boundary states of those
 // chains in `chains` (local sums, then their chaining), if there are segments.
 cudaError_t decay_run(const DecayGeom &g, const DecayPass *chains, int nchains, const DecayPass *passes, int n,
-                      gdr_dtype_t dtype, bool tc, DeviceCtx *ctx, cudaStream_t stream) {
+                      gdr_dtype_t dtype, bool tc, DeviceCtx *ctx, char *ws, const DecayLayout &L,
+                      cudaStream_t stream) {
+    unsigned long long *next = g.dense ? nullptr : (unsigned long long *)(ws + L.next);
+    if (tc && next) {
+        const cudaError_t err = cudaMemsetAsync(next, 0, 2 * sizeof(*next), stream);
+        if (err != cudaSuccess) return err;
+    }
     auto run = [&](const DecayPass *p, int k) {
-        if (tc) return launch_decay_tc(g, p, k, ctx->sms, ctx->d_status, stream);
+        if (tc)
+            return launch_decay_tc(g, p, k, ctx->sms, next ? next + (p->local ? 1 : 0) : nullptr, ctx->d_status,
+                                   stream);
         cudaError_t err = cudaSuccess;
         for (int i = 0; i < k && err == cudaSuccess; ++i) err = launch_decay_rec(g, p[i], dtype, stream);
         return err;
@@ -1131,7 +1140,7 @@ gdr_status_t gdr_decay_fwd(const void *q, const void *k, const void *v, const fl
     float *slots = (float *)(ws + L.slots);
     const DecayPass chain{nullptr, k, v, nullptr, h0, nullptr, slots, dk, dv, false, false, true, 1.f, 1.f};
     const DecayPass pass{q, k, v, out, h0, hT, slots, dk, dv, false, false, false, 1.f, scale};
-    return decay_run(g, &chain, 1, &pass, 1, dtype, tc, ctx, stream) == cudaSuccess ? GDR_OK
+    return decay_run(g, &chain, 1, &pass, 1, dtype, tc, ctx, ws, L, stream) == cudaSuccess ? GDR_OK
                                                                                              : GDR_ERR_CUDA;
 }
 
@@ -1178,7 +1187,7 @@ gdr_status_t gdr_decay_bwd(const void *q, const void *k, const void *v, const fl
         {v, dout, q, dk_out, dhT, nullptr, sr, dv, dk, true, true, false, scale, 1.f},
         {k, q, dout, dv_out, dhT, dh0, sr, dk, dv, false, true, false, scale, 1.f},
     };
-    return decay_run(g, chains, 2, passes, 3, dtype, tc, ctx, stream) == cudaSuccess ? GDR_OK
+    return decay_run(g, chains, 2, passes, 3, dtype, tc, ctx, ws, L, stream) == cudaSuccess ? GDR_OK
                                                                                               : GDR_ERR_CUDA;
 }
 

@@ -137,8 +137,9 @@ cudaError_t launch_decay_step(const void *q, const void *k, const void *v, const
                               cudaStream_t stream);
 // On the tensor cores (gdr_decay_tc.cu): bf16, token tensors 16-byte aligned, fewer than
 // 2^31 - 128 token rows.  Passes of one launch are independent and all local or all not.
-cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, int sms, int *status,
-                            cudaStream_t stream);
+// `next`: a zeroed counter that hands out the units, or null (units of equal length).
+cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, int sms, unsigned long long *next,
+                            int *status, cudaStream_t stream);
 // Chains the local sums in `slots` into boundary states, from s0 (null: zero).
 cudaError_t launch_decay_combine(const DecayGeom &g, const DecayPass &p, cudaStream_t stream);
 

@@ -28,11 +28,11 @@
 // SM's share of the measured bandwidth) and 25 MFLOP (2.0 us of an SM's share of the bf16
 // rate), so the pass can be bound by HBM if its other work stays out of the way.  The stages
 // of a tile run in different warps and overlap those of its neighbours:
-//   warps 0-3    Sc -> P (bf16, over Sc in TMEM); O -> out
-//   warps 4-7    S^^T -> bf16 (shared memory)
-//   warps 8-15   C' = weighted C -> TMEM, 16 tokens at a time, two groups in turn
-//   warp 16      TMA loads of A, B, C, two stages of 96 KB
-//   warp 17      issues every MMA (their order in the tensor pipe is the issue order)
+//   warps 0-7    Sc -> P (bf16, over Sc in TMEM); O -> out; half of the columns each group
+//   warps 8-11   S^^T -> bf16 (shared memory)
+//   warps 12-19  C' = weighted C -> TMEM, 16 tokens at a time, two groups in turn
+//   warp 20      TMA loads of A, B, C, two stages of 96 KB
+//   warp 21      issues every MMA (their order in the tensor pipe is the issue order)
 //
 // Rounding.  The state is fp32 and so are its updates: C' has 24 significant bits, so it goes
 // in as the sum of three bf16 numbers that represent it exactly (three products instead of
@@ -41,7 +41,8 @@
 // to bf16 (2.3e-3 in the mean square over the outputs against 1.7e-3 for their rounding alone).
 //
 // A block is persistent: it walks the units (segment, head, pass) with a stride of the grid
-// and its pipeline runs on across them.  The three passes of a backward call are
+// (equal sequences) or takes the next one from a counter (packed ones), and its pipeline
+// runs on across them.  The three passes of a backward call are
 // neighbouring units, so that what they share is read from the L2 by all but the first.
 // Every wait is bounded; one that runs out sets the status word and the block unwinds.
 #include <cudaTypedefs.h>
@@ -70,66 +71,98 @@ constexpr uint64_t kWaitNs = 2000000000ull;   // pipeline wait limit: 2 s
 constexpr uint64_t kDrainNs = 2000000000ull;  // drains before exit
 
 struct TcMaps {
-    CUtensorMap a[kMaxPasses], b[kMaxPasses], c[kMaxPasses];
+    CUtensorMap a[kMaxPasses], b[kMaxPasses], c[kMaxPasses], o[kMaxPasses];
 };
 struct TcArgs {
     DecayGeom g;
     DecayPass pass[kMaxPasses];
     int npass;
     int64_t units;      // max_segs * H * npass
+    unsigned long long *next;   // the next unit to take, or null: units by stride
     int *status;
     uint64_t wait_ns;
 };
 
+// The rest of a wait that its first look did not end.  The warp sleeps meanwhile, in pieces
+// of up to 0.1 ms.
+__device__ __noinline__ bool wait_long(uint64_t *b, uint32_t parity, uint64_t limit_ns, volatile int *stop,
+                                       int *status) {
+    const uint64_t t0 = globaltimer_ns();
+    while (__all_sync(kFull, !*stop && globaltimer_ns() - t0 < limit_ns))
+        if (__all_sync(kFull, mbar_try_wait_for(b, parity, 100000))) return true;
+    if (!*stop) set_status(status, GDR_ERR_TIMEOUT);
+    *stop = 1;
+    return false;
+}
 // Waits (a whole warp) until `b` has completed its use number `use` (from 0).  False if that
 // takes longer than the limit (0: look once), or once another wait of the block has run
 // out, which sets the status word.
 __device__ __forceinline__ bool wait_use(uint64_t *b, uint32_t use, uint64_t limit_ns, volatile int *stop,
                                          int *status) {
     if (__all_sync(kFull, limit_ns ? mbar_try_wait(b, use & 1u) : mbar_test_wait(b, use & 1u))) return true;
-    if (limit_ns) {
-        const uint64_t t0 = globaltimer_ns();
-        do {
-            if (__all_sync(kFull, mbar_try_wait(b, use & 1u))) return true;
-        } while (__all_sync(kFull, !*stop && globaltimer_ns() - t0 <= limit_ns));
-    }
-    if (!*stop) set_status(status, GDR_ERR_TIMEOUT);
-    *stop = 1;
-    return false;
+    return wait_long(b, use & 1u, limit_ns, stop, status);
 }
 
-// One unit of a block's walk.
+// One unit of a block's walk, put into shared memory by the producer for all warps.
 struct Unit {
-    int pass, h;
-    DecaySeg seg;
-    int64_t t0, t1;   // tokens it runs (a local pass: those that reach the segment's end)
-    int tiles;
+    int64_t t0, t1;    // tokens it runs (a local pass: those that reach the segment's end)
+    const float *in;   // entering state (null: zero) and where to leave the last one (or null)
+    float *to;
+    float gd;          // the head's log-decay
+    int pass, h, tiles;   // tiles < 0: no more units
 };
+constexpr uint32_t kRing = 4;   // units announced ahead
 
 // False where unit u has nothing to do.
 __device__ __forceinline__ bool unit_of(const TcArgs &A, int64_t u, bool local, Unit &o) {
     o.pass = (int)(u % A.npass);
     const int64_t sh = u / A.npass;
     o.h = (int)(sh % A.g.H);
-    if (!decay_segment(A.g, sh / A.g.H, o.seg)) return false;
-    const bool rev = A.pass[o.pass].rev;
-    o.t0 = o.seg.t0;
-    o.t1 = o.seg.t1;
+    DecaySeg seg;
+    if (!decay_segment(A.g, sh / A.g.H, seg)) return false;
+    const DecayPass &p = A.pass[o.pass];
+    o.gd = decay_log(A.g.log_decay, o.h);
+    o.t0 = seg.t0;
+    o.t1 = seg.t1;
     if (local) {
-        if (rev ? o.seg.first : o.seg.last) return false;   // no boundary behind it
+        if (p.rev ? seg.first : seg.last) return false;   // no boundary behind it
         // whole tiles: the segment is one (reversed: but for its sequence's last tile)
-        const int64_t reach = (decay_reach(decay_log(A.g.log_decay, o.h), o.t1 - o.t0) + kC - 1) / kC * kC;
-        if (rev) o.t1 = min(o.t1, o.t0 + reach); else o.t0 = max(o.t0, o.t1 - reach);
+        const int64_t reach = (decay_reach(o.gd, o.t1 - o.t0) + kC - 1) / kC * kC;
+        if (p.rev) o.t1 = min(o.t1, o.t0 + reach); else o.t0 = max(o.t0, o.t1 - reach);
     }
     o.tiles = (int)((o.t1 - o.t0 + kC - 1) / kC);
-    return GDR_INBOUNDS(o.seg.t0 >= 0 && o.seg.t1 <= A.g.T_total && o.seg.slot <= A.g.max_slots);
+    o.in = decay_state_in(p, seg, A.g.H, o.h);
+    o.to = decay_state_out(p, seg, A.g.H, o.h);
+    return GDR_INBOUNDS(seg.t0 >= 0 && seg.t1 <= A.g.T_total && seg.slot <= A.g.max_slots);
 }
-// Tile i of a unit in the order of its pass: first token and number of tokens.
-__device__ __forceinline__ void tile_of(const Unit &u, bool rev, int i, int64_t &t, int &n) {
-    const int64_t at = rev ? u.tiles - 1 - i : i;
-    t = u.t0 + at * kC;
-    n = (int)min((int64_t)kC, u.t1 - t);
+// The block's next unit (one warp): those of its stride, or whatever comes next; false at
+// the end.  `n`: the last one (blockIdx.x - gridDim.x at the start).
+__device__ __forceinline__ bool take_unit(const TcArgs &A, bool local, int64_t &n, Unit &u) {
+    do {
+        if (A.next) {
+            unsigned long long x = 0;
+            if ((threadIdx.x & 31) == 0) x = atomicAdd(A.next, 1ull);
+            n = (int64_t)__shfl_sync(kFull, x, 0);
+        } else {
+            n += gridDim.x;
+        }
+        if (n >= A.units) return false;
+    } while (!unit_of(A, n, local, u));
+    return true;
 }
+// The tiles of a unit in the order of its pass, in registers: a role's loop reads neither
+// shared memory nor parameters for its bookkeeping.
+struct Walk {
+    int tiles, short_at, short_len;   // one tile (the last of the tokens) may be short
+    bool rev;
+    __device__ __forceinline__ Walk(const Unit &u, bool rev)
+        : tiles(u.tiles), short_at(rev ? 0 : u.tiles - 1),
+          short_len((int)(u.t1 - u.t0 - (int64_t)(u.tiles - 1) * kC)), rev(rev) {}
+    __device__ __forceinline__ int len(int i) const { return i == short_at ? short_len : kC; }
+    __device__ __forceinline__ int64_t first(const Unit &u, int i) const {   // token
+        return u.t0 + (int64_t)(rev ? tiles - 1 - i : i) * kC;
+    }
+};
 
 // Descriptor offset of K-step k (16 of up to 128 elements) of a K-major tile.
 __device__ constexpr uint64_t k_major(uint32_t k) { return ((k >> 2) * kBox + (k & 3) * 32) >> 4; }
@@ -175,6 +208,36 @@ __device__ __forceinline__ void zero_columns(uint8_t *tile, int e0, int n, int l
             make_uint4(0, 0, 0, 0);
 }
 
+// Two fp32 numbers in a 64-bit register (the first in the low half) and their products and
+// sums, one instruction for both.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+    return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo);
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t tops(uint64_t y) {   // the upper 16 bits of both
+    return __byte_perm((uint32_t)y, (uint32_t)(y >> 32), 0x7632);
+}
+// What is left of both after their upper 16 bits (exact).
+__device__ __forceinline__ uint64_t rest(uint64_t y) {
+    return add2(y, (y & 0xffff0000ffff0000ull) ^ 0x8000000080000000ull);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *(const uint32_t *)&v;
+}
+__device__ __forceinline__ uint32_t pack2(uint64_t y) {
+    return pack2(__uint_as_float((uint32_t)y), __uint_as_float((uint32_t)(y >> 32)));
+}
+
 // 16 tokens (from 16 k) of a tile's C'^T, row e, into three times 8 TMEM columns at `at` (a
 // whole warp): the weighted values x w as the bf16 terms hi + mid + lo = x w exactly, cut
 // off the top of the fp32 product 8 significant bits at a time; a column holds two tokens.
@@ -187,25 +250,22 @@ __device__ __forceinline__ void write_terms(uint32_t at, const uint8_t *tile, in
         const uint32_t chunk = (e & 63) >> 3;
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
-            const float4 w4 = *(const float4 *)&w[2 * i];
-            const float wv[4] = {w4.x, w4.y, w4.z, w4.w};
-            float y[4];
+            const ulonglong2 w4 = *(const ulonglong2 *)&w[2 * i];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int r = 2 * i + j;
-                const uint32_t x = *(const uint16_t *)(col + (r >> 3) * 1024 + (r & 7) * 128 + ((chunk ^ (r & 7)) << 4));
-                y[j] = __uint_as_float(x << 16) * wv[j];
+            for (int j = 0; j < 2; ++j) {
+                uint32_t x[2];
+#pragma unroll
+                for (int l = 0; l < 2; ++l) {
+                    const int r = 2 * (i + j) + l;
+                    const uint32_t at16 = (r >> 3) * 1024 + (r & 7) * 128 + ((chunk ^ (r & 7)) << 4);
+                    x[l] = (uint32_t)*(const uint16_t *)(col + at16) << 16;
+                }
+                uint64_t y = mul2((uint64_t)x[1] << 32 | x[0], j ? w4.y : w4.x);
+                hi[i + j] = tops(y);
+                y = rest(y);
+                mid[i + j] = tops(y);
+                lo[i + j] = tops(rest(y));
             }
-            hi[i] = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632);
-            hi[i + 1] = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x7632);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] -= __uint_as_float(__float_as_uint(y[j]) & 0xffff0000u);
-            mid[i] = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632);
-            mid[i + 1] = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x7632);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) y[j] -= __uint_as_float(__float_as_uint(y[j]) & 0xffff0000u);
-            lo[i] = __byte_perm(__float_as_uint(y[0]), __float_as_uint(y[1]), 0x7632);
-            lo[i + 1] = __byte_perm(__float_as_uint(y[2]), __float_as_uint(y[3]), 0x7632);
         }
     } else {
 #pragma unroll
@@ -217,28 +277,11 @@ __device__ __forceinline__ void write_terms(uint32_t at, const uint8_t *tile, in
     tmem_st8(at + 16, lo);
 }
 
-// 32 bytes of a row, in one piece where `wide` (the address is a multiple of 32).
-__device__ __forceinline__ void store32(void *dst, const uint32_t (&o)[8], bool wide) {
-    if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(o[0]), "r"(o[1]),
-                     "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
-                     : "memory");
-    } else {
-        ((uint4 *)dst)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-        ((uint4 *)dst)[1] = make_uint4(o[4], o[5], o[6], o[7]);
-    }
-}
-
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *(const uint32_t *)&v;
-}
-
 // 16 columns (d0 ..) of row e of a state in memory.
 __device__ __forceinline__ void state_load(const DecayPass &p, const float *in, int d0, int e, uint32_t (&r)[16]) {
 #pragma unroll
@@ -272,29 +315,28 @@ __device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16]) {
                  :
                  : "memory");
 }
-// f(m, r) for 16 columns at a time from `at`, the next ones on their way meanwhile (an even
-// number of pieces).  Rolled up: the warps of a block run five different programs, and
-// their loops have to stay in the instruction caches together.
+// f(m, r) for 16 columns at a time from `at`, the next ones on their way meanwhile.  One
+// copy of f: the warps of a block run six different programs, which have to stay in the
+// instruction caches together.
 template <typename F> __device__ __forceinline__ void tmem_columns(uint32_t at, int pieces, F &&f) {
-    uint32_t r0[16], r1[16];
-    tmem_ld16(at, r0);
+    uint32_t next[16], r[16];
+    tmem_ld16(at, next);
 #pragma unroll 1
-    for (int m = 0; m < pieces; m += 2) {
-        tmem_arrived(r0);
-        tmem_ld16(at + 16 * (m + 1), r1);
-        f(m, r0);
-        tmem_arrived(r1);
-        if (m + 2 < pieces) tmem_ld16(at + 16 * (m + 2), r0);
-        f(m + 1, r1);
+    for (int m = 0; m < pieces; ++m) {
+        tmem_arrived(next);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) r[j] = next[j];
+        if (m + 1 < pieces) tmem_ld16(at + 16 * (m + 1), next);
+        f(m, r);
     }
 }
 
 // ---------------------------------------------------------------------------
 // the output pass
 // ---------------------------------------------------------------------------
-constexpr int kOutThreads = 32 * 18, kOutProducer = 16, kOutIssuer = 17;   // warps
+constexpr int kOutThreads = 32 * 22, kOutProducer = 20, kOutIssuer = 21;   // warps
 // TMEM columns
-constexpr uint32_t kColS = 0;      // Sc, then P in its first 64 columns
+constexpr uint32_t kColS = 0;      // Sc; P in the first 32 columns of each of its halves
 constexpr uint32_t kColO = 128;
 constexpr uint32_t kColH = 256;    // S^T
 constexpr uint32_t kColV = 384;    // C'^T: slots of 16 tokens x 3 terms
@@ -306,19 +348,21 @@ static_assert(kColZero + 8 <= kTmemCols, "TMEM");
 constexpr uint32_t kStage = 3 * kTile;               // A, B, C
 constexpr uint32_t kOffH = 2 * kStage;               // the state in bf16, [e][d], K-major
 constexpr uint32_t kOffBar = kOffH + kTile;
-constexpr uint32_t kOffW = kOffBar + 256;            // weights of a group's 64 tokens, a copy per warp
-constexpr uint32_t kSmemOut = kOffW + 8 * (kC / 2) * 4;
+constexpr uint32_t kOffW = kOffBar + 320;            // weights of a group's 64 tokens, a copy per warp
+constexpr uint32_t kOffRing = kOffW + 8 * (kC / 2) * 4;
+constexpr uint32_t kSmemOut = kOffRing + kRing * sizeof(Unit);
 static_assert(kSmemOut <= 232448, "shared memory");
 
 struct OutBars {
+    uint64_t u_full[kRing], u_free[kRing];   // a unit announced / done with (21 warps)
     uint64_t full[2];      // a stage's tiles have arrived
-    uint64_t free_a[2];    // the stage's A is read
+    uint64_t free_a[2];    // the stage's A is read, and the outputs that went through it (8 warps)
     uint64_t free_bc[2];   // ... its B and C
     uint64_t s_full;       // Sc complete
-    uint64_t p_ready;      // P written (4 warps)
+    uint64_t p_ready;      // P written (8 warps)
     uint64_t o1_full;      // O = A S^ complete (the bf16 state is read)
     uint64_t o_full;       // O complete
-    uint64_t o_free;       // O read (4 warps)
+    uint64_t o_free;       // O read (8 warps)
     uint64_t h_ready;      // the bf16 state written (4 warps)
     uint64_t v_ready[kSlots];   // a slot of C' written (4 warps)
     uint64_t v_free[kSlots];    // ... read
@@ -327,21 +371,26 @@ struct OutBars {
     uint32_t tmem;
     int stop;
 };
-static_assert(sizeof(OutBars) <= 256, "barriers");
+static_assert(sizeof(OutBars) <= 320, "barriers");
 
 __global__ void __launch_bounds__(kOutThreads, 1)
 decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs A) {
     extern __shared__ __align__(1024) uint8_t smem[];
     OutBars &bar = *(OutBars *)(smem + kOffBar);
+    Unit *ring = (Unit *)(smem + kOffRing);
     volatile int *stop = &bar.stop;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int H = A.g.H;
     if (!GDR_INBOUNDS((smem_u32(smem) & 1023u) == 0)) return;   // swizzled tiles start on 1 KB
 
     if (tid == 0) {
+        for (uint32_t i = 0; i < kRing; ++i) {
+            mbar_init(&bar.u_full[i], 1);
+            mbar_init(&bar.u_free[i], 21);
+        }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.full[i], 1);
-            mbar_init(&bar.free_a[i], 1);
+            mbar_init(&bar.free_a[i], 8);
             mbar_init(&bar.free_bc[i], 1);
         }
         for (uint32_t i = 0; i < kSlots; ++i) {
@@ -349,10 +398,10 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             mbar_init(&bar.v_free[i], 1);
         }
         mbar_init(&bar.s_full, 1);
-        mbar_init(&bar.p_ready, 4);
+        mbar_init(&bar.p_ready, 8);
         mbar_init(&bar.o1_full, 1);
         mbar_init(&bar.o_full, 1);
-        mbar_init(&bar.o_free, 4);
+        mbar_init(&bar.o_free, 8);
         mbar_init(&bar.h_ready, 4);
         mbar_init(&bar.kv_full, 1);
         mbar_init(&bar.fin, 1);
@@ -371,26 +420,45 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
 
     auto wait = [&](uint64_t *b, uint32_t use) { return wait_use(b, use, A.wait_ns, stop, A.status); };
     uint32_t it = 0;   // tiles so far: the use number of every once-a-tile barrier
-    Unit u;
+    // Walks the announced units (every warp but the producer): f(unit) until the end or until
+    // it returns false.
+    auto each_unit = [&](auto &&f) {
+        for (uint32_t k = 0;; ++k) {
+            if (!wait(&bar.u_full[k % kRing], k / kRing)) return;
+            const Unit &u = ring[k % kRing];
+            if (u.tiles < 0 || !f(u)) return;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.u_free[k % kRing]);
+        }
+    };
 
     if (warp == kOutProducer) {
         bool ok = true;
-        for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
-            if (!unit_of(A, n, false, u)) continue;
+        int64_t n = (int64_t)blockIdx.x - gridDim.x;
+        for (uint32_t k = 0; ok; ++k) {
+            Unit u;
+            if (!take_unit(A, false, n, u)) u.tiles = -1;
+            if (k >= kRing && !(ok = wait(&bar.u_free[k % kRing], k / kRing - 1))) break;
+            if (lane == 0) {
+                ring[k % kRing] = u;
+                mbar_arrive(&bar.u_full[k % kRing]);
+            }
+            __syncwarp();
+            if (u.tiles < 0) break;
             const DecayPass &p = A.pass[u.pass];
-            for (int i = 0; i < u.tiles; ++i, ++it) {
+            const Walk walk(u, p.rev);
+            const int kd = p.kd, vd = p.vd;
+            for (int i = 0; i < walk.tiles; ++i, ++it) {
                 const uint32_t st = it & 1;
                 if (it >= 2 && !((ok = wait(&bar.free_a[st], (it >> 1) - 1)) && (ok = wait(&bar.free_bc[st], (it >> 1) - 1))))
                     break;
                 if (lane == 0) {
-                    int64_t t;
-                    int len;
-                    tile_of(u, p.rev, i, t, len);
+                    const int64_t t = walk.first(u, i);
                     uint8_t *s = smem + st * kStage;
-                    mbar_arrive_expect_tx(&bar.full[st], (2 * p.kd + p.vd) / 64 * kBox);
-                    load_tile(s, &maps.a[u.pass], p.kd, u.h, t, &bar.full[st]);
-                    load_tile(s + kTile, &maps.b[u.pass], p.kd, u.h, t, &bar.full[st]);
-                    load_tile(s + 2 * kTile, &maps.c[u.pass], p.vd, u.h, t, &bar.full[st]);
+                    mbar_arrive_expect_tx(&bar.full[st], (2 * kd + vd) / 64 * kBox);
+                    load_tile(s, &maps.a[u.pass], kd, u.h, t, &bar.full[st]);
+                    load_tile(s + kTile, &maps.b[u.pass], kd, u.h, t, &bar.full[st]);
+                    load_tile(s + 2 * kTile, &maps.c[u.pass], vd, u.h, t, &bar.full[st]);
                 }
                 __syncwarp();
             }
@@ -401,27 +469,26 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
     } else if (warp == kOutIssuer) {
         const uint32_t s0 = smem_u32(smem);
         const bool lead = elect_one();
-        bool ok = true;
-        for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
-            if (!unit_of(A, n, false, u)) continue;
+        each_unit([&](const Unit &u) {
+            bool ok = true;
             const DecayPass &p = A.pass[u.pass];
-            const uint32_t kd16 = (uint32_t)p.kd / 16;
+            const Walk walk(u, p.rev);
+            const int kd = p.kd;
+            const uint32_t kd16 = (uint32_t)kd / 16;
             const uint32_t id_s = instr_desc(kC, kC, 1, false, false);
             const uint32_t id_o1 = instr_desc(kC, p.vd, 1, false, false);
             const uint32_t id_o2 = instr_desc(kC, p.vd, 1, false, true);
-            const uint32_t id_h = instr_desc(kC, p.kd, 1, false, true);
-            const float g2 = decay_log2(decay_log(A.g.log_decay, u.h));
+            const uint32_t id_h = instr_desc(kC, kd, 1, false, true);
+            const float g2 = decay_log2(u.gd);
             float y = 0.f;
-            for (int i = 0; i < u.tiles; ++i, ++it) {
+            for (int i = 0; i < walk.tiles; ++i, ++it) {
                 const uint32_t st = it & 1;
-                int64_t t;
-                int len;
-                tile_of(u, p.rev, i, t, len);
+                const int len = walk.len(i);
                 uint8_t *sp = smem + st * kStage;
                 const uint32_t sa = s0 + st * kStage, sb = sa + kTile, sc = sb + kTile;
                 if (!(ok = wait(&bar.full[st], it >> 1))) break;
                 if (len < kC) {
-                    zero_rows(sp + kTile, p.kd, len, lane);   // of C: by the warps that weigh it
+                    zero_rows(sp + kTile, kd, len, lane);   // of C: by the warps that weigh it
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
@@ -435,12 +502,11 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                     if (k < kd16) mma_f16_ss_if(lead, tm + kColS, dA + k_major(k), dB + k_major(k), id_s, k > 0);
                 mma_commit_if(lead, &bar.s_full);
                 if (!(ok = wait(&bar.h_ready, it))) break;
-                // the state's power of two: 15 at a time on products with zeros, the rest with
-                // the first one that adds something
+                // the state's power of two, on products with zeros
                 int down = advance_exponent(y, g2, len);
                 const bool keep = down < 64;
-                for (; keep && down > 15; down -= 15)
-                    mma_f16_ts_scaled_if(lead, tm + kColH, tm + kColZero, dBt, id_h, 15);
+                for (; keep && down > 0; down -= 15)
+                    mma_f16_ts_scaled_if(lead, tm + kColH, tm + kColZero, dBt, id_h, min(down, 15));
 #pragma unroll 1
                 for (uint32_t k = 0; k < kParts; ++k) {
                     const uint32_t part = it * kParts + k, slot = part % kSlots;
@@ -448,8 +514,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                     tc_fence_after();
                     const uint32_t av = tm + kColV + slot * kSlotCols;
                     const uint64_t db = dBt + ((k * 2048) >> 4);
-                    if (k == 0 && keep) mma_f16_ts_scaled_if(lead, tm + kColH, av, db, id_h, down);
-                    else mma_f16_ts_if(lead, tm + kColH, av, db, id_h, k > 0);
+                    mma_f16_ts_if(lead, tm + kColH, av, db, id_h, keep || k > 0);
                     mma_f16_ts_if(lead, tm + kColH, av + 8, db, id_h, 1);
                     mma_f16_ts_if(lead, tm + kColH, av + 16, db, id_h, 1);
                     mma_commit_if(lead, &bar.v_free[slot]);
@@ -461,61 +526,74 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 for (uint32_t k = 0; k < 8; ++k)
                     if (k < kd16) mma_f16_ss_if(lead, tm + kColO, dA + k_major(k), dH + k_major(k), id_o1, k > 0);
                 mma_commit_if(lead, &bar.o1_full);
-                mma_commit_if(lead, &bar.free_a[st]);
                 if (!(ok = wait(&bar.p_ready, it))) break;
                 tc_fence_after();
 #pragma unroll
                 for (uint32_t k = 0; k < kC / 16; ++k)
-                    mma_f16_ts_if(lead, tm + kColO, tm + kColS + k * 8, dCt + ((k * 2048) >> 4), id_o2, 1);
+                    mma_f16_ts_if(lead, tm + kColO, tm + kColS + (k >> 2) * 64 + (k & 3) * 8, dCt + ((k * 2048) >> 4), id_o2, 1);
                 mma_commit_if(lead, &bar.o_full);
                 mma_commit_if(lead, &bar.free_bc[st]);
             }
-        }
+            return ok;
+        });
         // no tensor-core operation may still run when the TMEM is released
         mma_commit_if(lead, &bar.fin);
         __all_sync(kFull, mbar_wait(&bar.fin, 0, kDrainNs));
-    } else if (warp < 4) {
-        // ---- weights and outputs: thread = token row of the tile
-        const int row = tid;
-        const uint32_t lanes = tm + ((uint32_t)(warp * 32) << 16);
-        bool ok = true;
-        for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
-            if (!unit_of(A, n, false, u)) continue;
+    } else if (warp < 8) {
+        // ---- weights and outputs: thread = token row of the tile, and half of the columns
+        const int rw = warp & 3, half = warp >> 2, row = tid & 127;
+        const uint32_t lanes = tm + ((uint32_t)(rw * 32) << 16);
+        each_unit([&](const Unit &u) {
+            bool ok = true;
             const DecayPass &p = A.pass[u.pass];
             const bool rev = p.rev;
-            const float g2 = decay_log2(decay_log(A.g.log_decay, u.h));
+            const Walk walk(u, rev);
+            const float g2 = decay_log2(u.gd), s_upd = p.s_upd, s_out = p.s_out;
+            const int vd = p.vd;
+            const CUtensorMap *out_map = &maps.o[u.pass];
             float y = 0.f;
-            const float l_upd = p.s_upd;
-            for (int i = 0; i < u.tiles; ++i, ++it) {
-                int64_t t;
-                int len;
-                tile_of(u, rev, i, t, len);
+            // lam^{|i-j|} over 16 columns before (after, reversed) the row = (its distance to the
+            // near end of them) x (a column's distance to it); the latter here, in pairs
+            uint64_t near[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                near[j] = rev ? two(exp2f(g2 * (float)(2 * j)), exp2f(g2 * (float)(2 * j + 1)))
+                              : two(exp2f(g2 * (float)(15 - 2 * j)), exp2f(g2 * (float)(14 - 2 * j)));
+            for (int i = 0; i < walk.tiles; ++i, ++it) {
+                const int len = walk.len(i);
                 // log2 of the row's f, and of the state's factor
                 const float lf = fmaxf(g2 * (float)(rev ? max(len - 1 - row, 0) : row + 1), -64.f) - y;
                 advance_exponent(y, g2, len);
                 if (!(ok = wait(&bar.s_full, it))) break;
                 tc_fence_after();
-                tmem_columns(lanes + kColS, 8, [&](int m, const uint32_t (&x)[16]) {
+                tmem_columns(lanes + kColS + 64 * half, 4, [&](int m, const uint32_t (&x)[16]) {
+                    const int c0 = 64 * half + 16 * m;
+                    const int d = rev ? c0 - row : row - c0;   // distance of column c0
                     uint32_t o[8];
-                    if (rev ? 16 * m + 15 < 32 * warp : 16 * m > 32 * warp + 31) {   // no pair of the warp's rows
+                    if (rev ? c0 + 15 < 32 * rw : c0 > 32 * rw + 31) {   // no pair of the warp's rows
 #pragma unroll
                         for (int j = 0; j < 8; ++j) o[j] = 0;
+                    } else if (rev ? c0 >= 32 * rw + 31 : c0 + 15 <= 32 * rw) {   // every pair
+                        const float far = s_upd * exp2_approx(fmaf(g2, (float)(rev ? d : d - 15), -lf));
+                        const uint64_t far2 = two(far, far);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            o[j] = pack2(mul2((uint64_t)x[2 * j + 1] << 32 | x[2 * j], mul2(near[j], far2)));
                     } else {
-                        // distance of column 16 m + j: d + j step
-                        const int d = rev ? 16 * m - row : row - 16 * m, step = rev ? 1 : -1;
                         const float l0 = fmaf(g2, (float)d, -lf), l1 = rev ? g2 : -g2;
+                        const int last = rev ? -d - 1 : d;   // columns up to it are the pairs, or those after it
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            float v[2];
+                            float v[2];   // selected, not branched around
 #pragma unroll
-                            for (int k = 0; k < 2; ++k)
-                                v[k] = d + (2 * j + k) * step >= 0
-                                           ? l_upd * __uint_as_float(x[2 * j + k]) * exp2_approx(fmaf((float)(2 * j + k), l1, l0))
-                                           : 0.f;
-                            o[j] = pack2(v[0], v[1]);
+                            for (int k = 0; k < 2; ++k) {
+                                v[k] = __uint_as_float(x[2 * j + k]) * exp2_approx(fmaf((float)(2 * j + k), l1, l0));
+                                v[k] = (2 * j + k <= last) != rev ? v[k] : 0.f;
+                            }
+                            o[j] = pack2(s_upd * v[0], s_upd * v[1]);
                         }
                     }
-                    tmem_st8(lanes + kColS + 8 * m, o);
+                    tmem_st8(lanes + kColS + 64 * half + 8 * m, o);
                 });
                 tmem_st_wait();
                 tc_fence_before();
@@ -523,54 +601,74 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 if (lane == 0) mbar_arrive(&bar.p_ready);
                 if (!(ok = wait(&bar.o_full, it))) break;
                 tc_fence_after();
-                const float f = p.s_out * exp2f(lf);
-                const bool wide = (uintptr_t)p.out % 32 == 0;
-                __nv_bfloat16 *dst = (__nv_bfloat16 *)p.out + ((t + row) * H + u.h) * (int64_t)p.vd;
-                tmem_columns(lanes + kColO, p.vd / 16, [&](int m, const uint32_t (&x)[16]) {
-                    if (row < len) {
-                        uint32_t o[8];
+                // O in bf16 goes through the tile's A (its products are complete): each warp
+                // writes its 32 rows and half of the columns there, swizzled as the store's
+                // box, and sends them on as one box -- or row by row at a sequence's end
+                const float f = s_out * exp2_approx(lf);
+                const uint64_t f2 = two(f, f);
+                uint8_t *buf = smem + (it & 1) * kStage + half * kBox + rw * 4096;
+                auto piece = [&](int r, int c) {   // 16 bytes: columns 8 c ..
+                    return (uint4 *)(buf + (vd == 128 ? r * 128 + ((c ^ (r & 7)) << 4)
+                                                      : r * 64 + ((c ^ ((r >> 1) & 3)) << 4)));
+                };
+                tmem_columns(lanes + kColO + half * (vd / 2), vd / 32, [&](int m, const uint32_t (&x)[16]) {
+                    uint32_t o[8];
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            o[j] = pack2(f * __uint_as_float(x[2 * j]), f * __uint_as_float(x[2 * j + 1]));
-                        store32(dst + 16 * m, o, wide);
-                    }
-                    __syncwarp();
+                    for (int j = 0; j < 8; ++j) o[j] = pack2(mul2((uint64_t)x[2 * j + 1] << 32 | x[2 * j], f2));
+                    *piece(lane, 2 * m) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *piece(lane, 2 * m + 1) = make_uint4(o[4], o[5], o[6], o[7]);
                 });
                 tc_fence_before();
+                fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.o_free);
+                if (lane == 0) {
+                    mbar_arrive(&bar.o_free);
+                    if (32 * rw + 32 <= len) {
+                        tma_store_3d(out_map, half * (vd / 2), u.h, (int)(walk.first(u, i) + 32 * rw), buf);
+                        bulk_commit();
+                        bulk_wait_read();
+                    }
+                }
+                __syncwarp();
+                if (32 * rw + 32 > len) {
+                    const int64_t row_step = (int64_t)H * vd;
+                    __nv_bfloat16 *dst = (__nv_bfloat16 *)p.out + (walk.first(u, i) + 32 * rw) * row_step +
+                                         u.h * vd + half * (vd / 2);
+                    for (int k = lane; k < 2 * vd; k += 32) {
+                        const int r = k / (vd / 16), c = k % (vd / 16);
+                        if (32 * rw + r < len) *(uint4 *)(dst + r * row_step + 8 * c) = *piece(r, c);
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.free_a[it & 1]);
             }
-        }
-    } else if (warp < 8) {
+            return ok;
+        });
+        bulk_wait();   // the block's shared memory goes with it
+    } else if (warp < 12) {
         // ---- state: thread = value index (TMEM lane)
-        const int e = tid - 128;
-        const uint32_t lanes = tm + ((uint32_t)((warp - 4) * 32) << 16);
+        const int e = tid & 127;
+        const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
         {
             const uint32_t zero[8] = {};
             tmem_st8(lanes + kColZero, zero);
             tmem_st_wait();   // the first h_ready publishes it
         }
-        bool ok = true;
-        for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
-            if (!unit_of(A, n, false, u)) continue;
+        each_unit([&](const Unit &u) {
+            bool ok = true;
             const DecayPass &p = A.pass[u.pass];
-            const float g2 = decay_log2(decay_log(A.g.log_decay, u.h));
+            const Walk walk(u, p.rev);
+            const float g2 = decay_log2(u.gd);
+            const int pieces = p.kd / 16;
             float y = 0.f;
-            const float *in = decay_state_in(p, u.seg, H, u.h);
-            float *to = decay_state_out(p, u.seg, H, u.h);
             if (u.tiles == 0) {   // an empty sequence: the state goes through
-                for (int d0 = 0; d0 < p.kd; d0 += 16) {
-                    uint32_t r[16];
-                    state_load(p, in, d0, e, r);
-                    state_store(p, to, d0, e, r);
-                }
-                continue;
+                if (u.to)
+                    for (int d = e; d < p.kd * p.vd; d += 128) u.to[d] = u.in ? u.in[d] : 0.f;
+                return true;
             }
-            for (int i = 0; i < u.tiles; ++i, ++it) {
-                int64_t t;
-                int len;
-                tile_of(u, p.rev, i, t, len);
-                advance_exponent(y, g2, len);
+            for (int i = 0; i < walk.tiles; ++i, ++it) {
+                advance_exponent(y, g2, walk.len(i));
                 // 16 columns of the entering state, to shared memory in bf16
                 auto take = [&](int m, const uint32_t (&r)[16]) {
 #pragma unroll
@@ -588,56 +686,56 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 tc_fence_after();
                 if (i == 0) {
 #pragma unroll 1
-                    for (int m = 0; m < p.kd / 16; ++m) {
+                    for (int m = 0; m < pieces; ++m) {
                         uint32_t r[16];
-                        state_load(p, in, 16 * m, e, r);
+                        state_load(p, u.in, 16 * m, e, r);
                         __syncwarp();
                         take(m, r);
                         tmem_st16(lanes + kColH + 16 * m, r);
                     }
                     tmem_st_wait();
                 } else {
-                    tmem_columns(lanes + kColH, p.kd / 16, take);
+                    tmem_columns(lanes + kColH, pieces, take);
                 }
                 fence_proxy_async_smem();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.h_ready);
             }
-            if (ok && to) {
-                if (!(ok = wait(&bar.kv_full, it - 1))) break;
+            if (ok && u.to) {
+                if (!(ok = wait(&bar.kv_full, it - 1))) return false;
                 tc_fence_after();
                 const float f = exp2f(-y);
-                tmem_columns(lanes + kColH, p.kd / 16, [&](int m, uint32_t (&r)[16]) {
+                tmem_columns(lanes + kColH, pieces, [&](int m, uint32_t (&r)[16]) {
 #pragma unroll
                     for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(f * __uint_as_float(r[j]));
-                    state_store(p, to, 16 * m, e, r);
+                    state_store(p, u.to, 16 * m, e, r);
                     __syncwarp();
                 });
             }
-        }
+            return ok;
+        });
     } else {
         // ---- weighted values: thread = value index (TMEM lane); group grp takes every other
         // 16 tokens, its token l = 16 a + j being the tile's 16 (2 a + grp) + j
-        const int grp = (warp - 8) >> 2, e = tid & 127;
+        const int grp = (warp - 12) >> 2, e = tid & 127;
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
-        float *w = (float *)(smem + kOffW) + (warp - 8) * (kC / 2);
-        bool ok = true;
-        for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
-            if (!unit_of(A, n, false, u)) continue;
+        float *w = (float *)(smem + kOffW) + (warp - 12) * (kC / 2);
+        each_unit([&](const Unit &u) {
+            bool ok = true;
             const DecayPass &p = A.pass[u.pass];
-            const float gd = decay_log(A.g.log_decay, u.h), g2 = decay_log2(gd);
+            const Walk walk(u, p.rev);
+            const float gd = u.gd, g2 = decay_log2(gd), s_upd = p.s_upd;
+            const bool any = e < p.vd;
             float y = 0.f, w0 = 0.f, w1 = 0.f;
             int wlen = -1;   // tokens of the tile that w0, w1 are for
-            for (int i = 0; i < u.tiles; ++i, ++it) {
+            for (int i = 0; i < walk.tiles; ++i, ++it) {
                 const uint32_t st = it & 1;
-                int64_t t;
-                int len;
-                tile_of(u, p.rev, i, t, len);
+                const int len = walk.len(i);
                 if (len != wlen) {
                     const int tok = 16 * (2 * (lane >> 4) + grp) + (lane & 15);
-                    w0 = token_weight(tok, len, p.rev, gd, p.s_upd, 0);
-                    w1 = token_weight(tok + 64, len, p.rev, gd, p.s_upd, 0);
+                    w0 = token_weight(tok, len, walk.rev, gd, s_upd, 0);
+                    w1 = token_weight(tok + 64, len, walk.rev, gd, s_upd, 0);
                     wlen = len;
                 }
                 advance_exponent(y, g2, len);
@@ -648,7 +746,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 __syncwarp();
                 if (!(ok = wait(&bar.full[st], it >> 1))) break;
                 uint8_t *ct = smem + st * kStage + 2 * kTile;
-                if (len < kC && e < p.vd) {
+                if (len < kC && any) {
                     // both groups write the same zeros; the product with P reads them too
                     zero_columns(ct, e & ~31, len, lane);
                     fence_proxy_async_smem();
@@ -659,7 +757,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                     const uint32_t part = it * kParts + 2 * a + grp, slot = part % kSlots, use = part / kSlots;
                     if (use && !(ok = wait(&bar.v_free[slot], use - 1))) break;
                     tc_fence_after();
-                    write_terms(lanes + kColV + slot * kSlotCols, ct, e, e < p.vd, 2 * a + grp, w + 16 * a);
+                    write_terms(lanes + kColV + slot * kSlotCols, ct, e, any, 2 * a + grp, w + 16 * a);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -667,7 +765,8 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 }
                 if (!ok) break;
             }
-        }
+            return ok;
+        });
     }
     tc_fence_before();
     __syncthreads();
@@ -688,11 +787,13 @@ constexpr int kLocStages = 3;
 constexpr uint32_t kLocStage = 2 * kTile;                    // B, C
 constexpr uint32_t kLocOffBar = kLocStages * kLocStage;
 constexpr uint32_t kLocOffW = kLocOffBar + 256;              // weights, a copy per warp
-constexpr uint32_t kSmemLocal = kLocOffW + 8 * kC * 4;
+constexpr uint32_t kLocOffRing = kLocOffW + 8 * kC * 4;
+constexpr uint32_t kSmemLocal = kLocOffRing + kRing * sizeof(Unit);
 constexpr uint32_t kLocColV = 128;                           // two buffers of a tile each
 static_assert(kLocColV + 2 * kParts * kSlotCols <= kTmemCols, "TMEM");
 
 struct LocalBars {
+    uint64_t u_full[kRing], u_free[kRing];   // a unit announced / done with (9 warps)
     uint64_t full[kLocStages], free[kLocStages];
     uint64_t v_ready[2], v_free[2];
     uint64_t h_full, h_free;   // a unit's sum complete / read
@@ -706,11 +807,15 @@ __global__ void __launch_bounds__(kLocThreads, 1)
 decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs A) {
     extern __shared__ __align__(1024) uint8_t smem[];
     LocalBars &bar = *(LocalBars *)(smem + kLocOffBar);
+    Unit *ring = (Unit *)(smem + kLocOffRing);
     volatile int *stop = &bar.stop;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int H = A.g.H;
     if (!GDR_INBOUNDS((smem_u32(smem) & 1023u) == 0)) return;   // swizzled tiles start on 1 KB
     if (tid == 0) {
+        for (uint32_t i = 0; i < kRing; ++i) {
+            mbar_init(&bar.u_full[i], 1);
+            mbar_init(&bar.u_free[i], 9);
+        }
         for (int i = 0; i < kLocStages; ++i) {
             mbar_init(&bar.full[i], 1);
             mbar_init(&bar.free[i], 1);
@@ -736,24 +841,43 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
     const uint32_t tm = bar.tmem;
     auto wait = [&](uint64_t *b, uint32_t use) { return wait_use(b, use, A.wait_ns, stop, A.status); };
     uint32_t it = 0, nu = 0;   // tiles and units so far
-    Unit u;
+    // Walks the announced units (every warp but the producer): f(unit) until the end or until
+    // it returns false.
+    auto each_unit = [&](auto &&f) {
+        for (uint32_t k = 0;; ++k) {
+            if (!wait(&bar.u_full[k % kRing], k / kRing)) return;
+            const Unit &u = ring[k % kRing];
+            if (u.tiles < 0 || !f(u)) return;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.u_free[k % kRing]);
+        }
+    };
 
     if (warp == kLocProducer) {
         bool ok = true;
-        for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
-            if (!unit_of(A, n, true, u) || u.tiles == 0) continue;
+        int64_t n = (int64_t)blockIdx.x - gridDim.x;
+        for (uint32_t k = 0; ok; ++k) {
+            Unit u;
+            if (!take_unit(A, true, n, u)) u.tiles = -1;
+            if (k >= kRing && !(ok = wait(&bar.u_free[k % kRing], k / kRing - 1))) break;
+            if (lane == 0) {
+                ring[k % kRing] = u;
+                mbar_arrive(&bar.u_full[k % kRing]);
+            }
+            __syncwarp();
+            if (u.tiles < 0) break;
             const DecayPass &p = A.pass[u.pass];
-            for (int i = 0; i < u.tiles; ++i, ++it) {
+            const Walk walk(u, p.rev);
+            const int kd = p.kd, vd = p.vd;
+            for (int i = 0; i < walk.tiles; ++i, ++it) {
                 const uint32_t st = it % kLocStages, use = it / kLocStages;
                 if (use && !(ok = wait(&bar.free[st], use - 1))) break;
                 if (lane == 0) {
-                    int64_t t;
-                    int len;
-                    tile_of(u, p.rev, i, t, len);
+                    const int64_t t = walk.first(u, i);
                     uint8_t *s = smem + st * kLocStage;
-                    mbar_arrive_expect_tx(&bar.full[st], (p.kd + p.vd) / 64 * kBox);
-                    load_tile(s, &maps.b[u.pass], p.kd, u.h, t, &bar.full[st]);
-                    load_tile(s + kTile, &maps.c[u.pass], p.vd, u.h, t, &bar.full[st]);
+                    mbar_arrive_expect_tx(&bar.full[st], (kd + vd) / 64 * kBox);
+                    load_tile(s, &maps.b[u.pass], kd, u.h, t, &bar.full[st]);
+                    load_tile(s + kTile, &maps.c[u.pass], vd, u.h, t, &bar.full[st]);
                 }
                 __syncwarp();
             }
@@ -763,20 +887,20 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
     } else if (warp == kLocIssuer) {
         const uint32_t s0 = smem_u32(smem);
         const bool lead = elect_one();
-        bool ok = true;
-        for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
-            if (!unit_of(A, n, true, u) || u.tiles == 0) continue;
+        each_unit([&](const Unit &u) {
+            bool ok = true;
+            if (u.tiles == 0) return true;
             const DecayPass &p = A.pass[u.pass];
-            const uint32_t id_h = instr_desc(kC, p.kd, 1, false, true);
-            if (nu && !(ok = wait(&bar.h_free, nu - 1))) break;
-            for (int i = 0; i < u.tiles; ++i, ++it) {
+            const Walk walk(u, p.rev);
+            const int kd = p.kd;
+            const uint32_t id_h = instr_desc(kC, kd, 1, false, true);
+            if (nu && !(ok = wait(&bar.h_free, nu - 1))) return false;
+            for (int i = 0; i < walk.tiles; ++i, ++it) {
                 const uint32_t st = it % kLocStages, buf = it & 1;
-                int64_t t;
-                int len;
-                tile_of(u, p.rev, i, t, len);
+                const int len = walk.len(i);
                 if (!(ok = wait(&bar.full[st], it / kLocStages))) break;
                 if (len < kC) {
-                    zero_rows(smem + st * kLocStage, p.kd, len, lane);
+                    zero_rows(smem + st * kLocStage, kd, len, lane);
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
@@ -793,67 +917,63 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                 }
                 mma_commit_if(lead, &bar.v_free[buf]);
                 mma_commit_if(lead, &bar.free[st]);
-                if (i == u.tiles - 1) mma_commit_if(lead, &bar.h_full);
+                if (i == walk.tiles - 1) mma_commit_if(lead, &bar.h_full);
             }
             ++nu;
-        }
+            return ok;
+        });
         mma_commit_if(lead, &bar.fin);
         __all_sync(kFull, mbar_wait(&bar.fin, 0, kDrainNs));
     } else {
         const int grp = warp >> 2, e = tid & 127;
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
         float *w = (float *)(smem + kLocOffW) + warp * kC;
-        bool ok = true;
-        for (int64_t n = blockIdx.x; n < A.units && ok; n += gridDim.x) {
-            if (!unit_of(A, n, true, u)) continue;
+        each_unit([&](const Unit &u) {
+            bool ok = true;
             const DecayPass &p = A.pass[u.pass];
             const bool rev = p.rev;
-            const float gd = decay_log(A.g.log_decay, u.h);
-            float *to = decay_state_out(p, u.seg, H, u.h);
+            const Walk walk(u, rev);
+            const float gd = u.gd, s_upd = p.s_upd;
+            const int64_t tokens = u.t1 - u.t0;
+            const bool any = e < p.vd;
             if (u.tiles == 0) {
                 if (grp == 0)
-                    for (int d0 = 0; d0 < p.kd; d0 += 16) {
-                        uint32_t r[16];
-                        state_load(p, nullptr, d0, e, r);
-                        state_store(p, to, d0, e, r);
-                    }
-                continue;
+                    for (int d = e; d < p.kd * p.vd; d += 128) u.to[d] = 0.f;
+                return true;
             }
-            for (int i = 0; i < u.tiles; ++i, ++it) {
+            for (int i = 0; i < walk.tiles; ++i, ++it) {
                 const uint32_t st = it % kLocStages, buf = it & 1;
                 if (buf != (uint32_t)grp) continue;
-                int64_t t;
-                int len;
-                tile_of(u, rev, i, t, len);
+                const int len = walk.len(i);
                 const uint32_t use = it >> 1;
                 // past the tile: its distance to the segment's end (its start, reversed)
-                const int64_t past = rev ? t - u.t0 : u.t1 - t - len;
+                const int64_t past = rev ? (int64_t)(walk.tiles - 1 - i) * kC : tokens - (int64_t)i * kC - len;
                 __syncwarp();   // the last tile's weights are read
 #pragma unroll
                 for (int k = 0; k < kC / 32; ++k)
-                    w[lane + 32 * k] = token_weight(lane + 32 * k, len, rev, gd, p.s_upd, past);
+                    w[lane + 32 * k] = token_weight(lane + 32 * k, len, rev, gd, s_upd, past);
                 __syncwarp();
                 if (!(ok = wait(&bar.full[st], it / kLocStages))) break;
                 if (use && !(ok = wait(&bar.v_free[buf], use - 1))) break;
                 tc_fence_after();
                 uint8_t *ct = smem + st * kLocStage + kTile;
-                if (len < kC && e < p.vd) {
+                if (len < kC && any) {
                     zero_columns(ct, e & ~31, len, lane);
                     __syncwarp();
                 }
 #pragma unroll 1
                 for (uint32_t k = 0; k < kParts; ++k)
-                    write_terms(lanes + kLocColV + (buf * kParts + k) * kSlotCols, ct, e, e < p.vd, k, w + 16 * k);
+                    write_terms(lanes + kLocColV + (buf * kParts + k) * kSlotCols, ct, e, any, k, w + 16 * k);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.v_ready[buf]);
             }
             if (ok && grp == 0) {
-                if (!(ok = wait(&bar.h_full, nu))) break;
+                if (!(ok = wait(&bar.h_full, nu))) return false;
                 tc_fence_after();
                 tmem_columns(lanes, p.kd / 16, [&](int m, const uint32_t (&r)[16]) {
-                    state_store(p, to, 16 * m, e, r);
+                    state_store(p, u.to, 16 * m, e, r);
                     __syncwarp();
                 });
                 tc_fence_before();
@@ -861,7 +981,8 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                 if (lane == 0) mbar_arrive(&bar.h_free);
             }
             ++nu;
-        }
+            return ok;
+        });
     }
     tc_fence_before();
     __syncthreads();
@@ -871,29 +992,27 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
     }
 }
 
-// [rows][H][width] bf16 viewed as (d, h, row), box (64, 1, 128), 128-byte swizzle.
-bool tile_map(CUtensorMap *map, const void *base, int width, int H, int64_t rows) {
-    return base && tc_make_tile_map(map, base, width, H, rows, kC);
-}
-
 }  // namespace
 
-cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, int sms, int *status,
-                            cudaStream_t stream) {
+cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, int sms, unsigned long long *next,
+                            int *status, cudaStream_t stream) {
     if (n < 1 || n > kMaxPasses) return cudaErrorInvalidValue;
     const bool local = passes[0].local;
     TcMaps maps{};
     TcArgs args{};
     for (int i = 0; i < n; ++i) {
         const DecayPass &p = passes[i];
-        if (!tile_map(&maps.b[i], p.b, p.kd, g.H, g.T_total) || !tile_map(&maps.c[i], p.c, p.vd, g.H, g.T_total) ||
-            (!local && !tile_map(&maps.a[i], p.a, p.kd, g.H, g.T_total)))
-            return cudaErrorNotSupported;
+        const bool ok = tc_make_tile_map(&maps.b[i], p.b, p.kd, g.H, g.T_total, kC, 64) &&
+                        tc_make_tile_map(&maps.c[i], p.c, p.vd, g.H, g.T_total, kC, 64) &&
+                        (local || (tc_make_tile_map(&maps.a[i], p.a, p.kd, g.H, g.T_total, kC, 64) &&
+                                   tc_make_tile_map(&maps.o[i], p.out, p.vd, g.H, g.T_total, 32, p.vd / 2)));
+        if (!ok) return cudaErrorNotSupported;
         args.pass[i] = p;
     }
     args.g = g;
     args.npass = n;
     args.units = g.max_segs * g.H * n;
+    args.next = next;
     args.status = status;
     args.wait_ns = kWaitNs;
     if (const char *w = std::getenv("GDR_TC_WAIT_NS")) {   // test hook: shorter pipeline waits
