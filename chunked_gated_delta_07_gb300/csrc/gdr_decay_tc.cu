@@ -30,9 +30,10 @@
 // of a tile run in different warps and overlap those of its neighbours:
 //   warps 0-7    Sc -> P (bf16, over Sc in TMEM); O -> out; half of the columns each group
 //   warps 8-11   S^^T -> bf16 (shared memory)
-//   warps 12-19  C' = weighted C -> TMEM, 16 tokens at a time, two groups in turn
+//   warps 12-19  C' = weighted C -> TMEM, 32 tokens at a time, half of them each group
 //   warp 20      TMA loads of A, B, C, two stages of 96 KB
 //   warp 21      issues every MMA (their order in the tensor pipe is the issue order)
+//   warp 22      TMA stores of the outputs, out of their tile's A
 //
 // Rounding.  The state is fp32 and so are its updates: C' has 24 significant bits, so it goes
 // in as the sum of three bf16 numbers that represent it exactly (three products instead of
@@ -238,8 +239,8 @@ __device__ __forceinline__ uint32_t pack2(uint64_t y) {
     return pack2(__uint_as_float((uint32_t)y), __uint_as_float((uint32_t)(y >> 32)));
 }
 
-// 16 tokens (from 16 k) of a tile's C'^T, row e, into three times 8 TMEM columns at `at` (a
-// whole warp): the weighted values x w as the bf16 terms hi + mid + lo = x w exactly, cut
+// 16 tokens (from 16 k) of a tile's C'^T, row e, into 8 TMEM columns at `at`, at + 16 and
+// at + 32 (a whole warp): the weighted values x w as the bf16 terms hi + mid + lo = x w exactly, cut
 // off the top of the fp32 product 8 significant bits at a time; a column holds two tokens.
 // w: the 16 weights.
 __device__ __forceinline__ void write_terms(uint32_t at, const uint8_t *tile, int e, bool any, int k,
@@ -273,8 +274,8 @@ __device__ __forceinline__ void write_terms(uint32_t at, const uint8_t *tile, in
     }
     __syncwarp();
     tmem_st8(at, hi);
-    tmem_st8(at + 8, mid);
-    tmem_st8(at + 16, lo);
+    tmem_st8(at + 16, mid);
+    tmem_st8(at + 32, lo);
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -334,13 +335,13 @@ template <typename F> __device__ __forceinline__ void tmem_columns(uint32_t at, 
 // ---------------------------------------------------------------------------
 // the output pass
 // ---------------------------------------------------------------------------
-constexpr int kOutThreads = 32 * 22, kOutProducer = 20, kOutIssuer = 21;   // warps
+constexpr int kOutThreads = 32 * 23, kOutProducer = 20, kOutIssuer = 21, kOutStore = 22;   // warps
 // TMEM columns
 constexpr uint32_t kColS = 0;      // Sc; P in the first 32 columns of each of its halves
 constexpr uint32_t kColO = 128;
 constexpr uint32_t kColH = 256;    // S^T
-constexpr uint32_t kColV = 384;    // C'^T: slots of 16 tokens x 3 terms
-constexpr uint32_t kSlotCols = 24, kSlots = 5, kParts = kC / 16;   // kParts uses of slots per tile
+constexpr uint32_t kColV = 384;    // C'^T: slots of 32 tokens x 3 terms
+constexpr uint32_t kSlotCols = 48, kSlots = 2, kParts = kC / 32;   // kParts uses of slots per tile
 constexpr uint32_t kColZero = kColV + kSlots * kSlotCols;          // 8 columns of zeros
 constexpr uint32_t kTmemCols = 512;
 static_assert(kColZero + 8 <= kTmemCols, "TMEM");
@@ -354,17 +355,18 @@ constexpr uint32_t kSmemOut = kOffRing + kRing * sizeof(Unit);
 static_assert(kSmemOut <= 232448, "shared memory");
 
 struct OutBars {
-    uint64_t u_full[kRing], u_free[kRing];   // a unit announced / done with (21 warps)
-    uint64_t full[2];      // a stage's tiles have arrived
-    uint64_t free_a[2];    // the stage's A is read, and the outputs that went through it (8 warps)
+    uint64_t u_full[kRing], u_free[kRing];   // a unit announced / done with (22 warps)
+    uint64_t full_a[2];    // a stage's A has arrived
+    uint64_t full_bc[2];   // ... its B and C
+    uint64_t free_a[2];    // the stage's A is read, and the outputs that went through it
     uint64_t free_bc[2];   // ... its B and C
     uint64_t s_full;       // Sc complete
     uint64_t p_ready;      // P written (8 warps)
     uint64_t o1_full;      // O = A S^ complete (the bf16 state is read)
     uint64_t o_full;       // O complete
-    uint64_t o_free;       // O read (8 warps)
+    uint64_t o_free;       // O read and in shared memory (8 warps)
     uint64_t h_ready;      // the bf16 state written (4 warps)
-    uint64_t v_ready[kSlots];   // a slot of C' written (4 warps)
+    uint64_t v_ready[kSlots];   // a slot of C' written (8 warps)
     uint64_t v_free[kSlots];    // ... read
     uint64_t kv_full;      // the tile's update of S^ complete
     uint64_t fin;          // every MMA of the block complete
@@ -386,15 +388,16 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
     if (tid == 0) {
         for (uint32_t i = 0; i < kRing; ++i) {
             mbar_init(&bar.u_full[i], 1);
-            mbar_init(&bar.u_free[i], 21);
+            mbar_init(&bar.u_free[i], 22);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar.full[i], 1);
-            mbar_init(&bar.free_a[i], 8);
+            mbar_init(&bar.full_a[i], 1);
+            mbar_init(&bar.full_bc[i], 1);
+            mbar_init(&bar.free_a[i], 1);
             mbar_init(&bar.free_bc[i], 1);
         }
         for (uint32_t i = 0; i < kSlots; ++i) {
-            mbar_init(&bar.v_ready[i], 4);
+            mbar_init(&bar.v_ready[i], 8);
             mbar_init(&bar.v_free[i], 1);
         }
         mbar_init(&bar.s_full, 1);
@@ -435,6 +438,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
     if (warp == kOutProducer) {
         bool ok = true;
         int64_t n = (int64_t)blockIdx.x - gridDim.x;
+        uint32_t nbc = 0;   // tiles whose B and C are on their way (`it`: whose A is too)
         for (uint32_t k = 0; ok; ++k) {
             Unit u;
             if (!take_unit(A, false, n, u)) u.tiles = -1;
@@ -450,22 +454,29 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             const int kd = p.kd, vd = p.vd;
             for (int i = 0; i < walk.tiles; ++i, ++it) {
                 const uint32_t st = it & 1;
-                if (it >= 2 && !((ok = wait(&bar.free_a[st], (it >> 1) - 1)) && (ok = wait(&bar.free_bc[st], (it >> 1) - 1))))
-                    break;
+                const int64_t t = walk.first(u, i);
+                uint8_t *s = smem + st * kStage;
+                if (it >= 2 && !(ok = wait(&bar.free_bc[st], (it >> 1) - 1))) break;
                 if (lane == 0) {
-                    const int64_t t = walk.first(u, i);
-                    uint8_t *s = smem + st * kStage;
-                    mbar_arrive_expect_tx(&bar.full[st], (2 * kd + vd) / 64 * kBox);
-                    load_tile(s, &maps.a[u.pass], kd, u.h, t, &bar.full[st]);
-                    load_tile(s + kTile, &maps.b[u.pass], kd, u.h, t, &bar.full[st]);
-                    load_tile(s + 2 * kTile, &maps.c[u.pass], vd, u.h, t, &bar.full[st]);
+                    mbar_arrive_expect_tx(&bar.full_bc[st], (kd + vd) / 64 * kBox);
+                    load_tile(s + kTile, &maps.b[u.pass], kd, u.h, t, &bar.full_bc[st]);
+                    load_tile(s + 2 * kTile, &maps.c[u.pass], vd, u.h, t, &bar.full_bc[st]);
+                }
+                __syncwarp();
+                ++nbc;
+                if (it >= 2 && !(ok = wait(&bar.free_a[st], (it >> 1) - 1))) break;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&bar.full_a[st], kd / 64 * kBox);
+                    load_tile(s, &maps.a[u.pass], kd, u.h, t, &bar.full_a[st]);
                 }
                 __syncwarp();
             }
         }
         // never leave with a copy in flight
         for (uint32_t k = it >= 2 ? it - 2 : 0; k < it; ++k)
-            __all_sync(kFull, mbar_wait(&bar.full[k & 1], (k >> 1) & 1u, kDrainNs));
+            __all_sync(kFull, mbar_wait(&bar.full_a[k & 1], (k >> 1) & 1u, kDrainNs));
+        for (uint32_t k = nbc >= 2 ? nbc - 2 : 0; k < nbc; ++k)
+            __all_sync(kFull, mbar_wait(&bar.full_bc[k & 1], (k >> 1) & 1u, kDrainNs));
     } else if (warp == kOutIssuer) {
         const uint32_t s0 = smem_u32(smem);
         const bool lead = elect_one();
@@ -486,7 +497,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 const int len = walk.len(i);
                 uint8_t *sp = smem + st * kStage;
                 const uint32_t sa = s0 + st * kStage, sb = sa + kTile, sc = sb + kTile;
-                if (!(ok = wait(&bar.full[st], it >> 1))) break;
+                if (!(ok = wait(&bar.full_bc[st], it >> 1)) || !(ok = wait(&bar.full_a[st], it >> 1))) break;
                 if (len < kC) {
                     zero_rows(sp + kTile, kd, len, lane);   // of C: by the warps that weigh it
                     fence_proxy_async_smem();
@@ -507,16 +518,17 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 const bool keep = down < 64;
                 for (; keep && down > 0; down -= 15)
                     mma_f16_ts_scaled_if(lead, tm + kColH, tm + kColZero, dBt, id_h, min(down, 15));
-#pragma unroll 1
+#pragma unroll
                 for (uint32_t k = 0; k < kParts; ++k) {
-                    const uint32_t part = it * kParts + k, slot = part % kSlots;
-                    if (!(ok = wait(&bar.v_ready[slot], part / kSlots))) break;
+                    const uint32_t slot = k % kSlots, av = tm + kColV + slot * kSlotCols;
+                    if (!(ok = wait(&bar.v_ready[slot], (it * kParts + k) / kSlots))) break;
                     tc_fence_after();
-                    const uint32_t av = tm + kColV + slot * kSlotCols;
-                    const uint64_t db = dBt + ((k * 2048) >> 4);
-                    mma_f16_ts_if(lead, tm + kColH, av, db, id_h, keep || k > 0);
-                    mma_f16_ts_if(lead, tm + kColH, av + 8, db, id_h, 1);
-                    mma_f16_ts_if(lead, tm + kColH, av + 16, db, id_h, 1);
+#pragma unroll
+                    for (uint32_t term = 0; term < 3; ++term)
+#pragma unroll
+                        for (uint32_t j = 0; j < 2; ++j)
+                            mma_f16_ts_if(lead, tm + kColH, av + term * 16 + j * 8, dBt + ((k * 4096 + j * 2048) >> 4),
+                                          id_h, keep || k + term + j > 0);
                     mma_commit_if(lead, &bar.v_free[slot]);
                 }
                 mma_commit_if(lead, &bar.kv_full);
@@ -550,7 +562,8 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             const Walk walk(u, rev);
             const float g2 = decay_log2(u.gd), s_upd = p.s_upd, s_out = p.s_out;
             const int vd = p.vd;
-            const CUtensorMap *out_map = &maps.o[u.pass];
+            // 15 steps of the decay on top of 1 / f stay in range
+            const bool gentle = g2 > -3.f;
             float y = 0.f;
             // lam^{|i-j|} over 16 columns before (after, reversed) the row = (its distance to the
             // near end of them) x (a column's distance to it); the latter here, in pairs
@@ -573,24 +586,36 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                     if (rev ? c0 + 15 < 32 * rw : c0 > 32 * rw + 31) {   // no pair of the warp's rows
 #pragma unroll
                         for (int j = 0; j < 8; ++j) o[j] = 0;
-                    } else if (rev ? c0 >= 32 * rw + 31 : c0 + 15 <= 32 * rw) {   // every pair
+                    } else if (gentle) {
+                        // the distance to the near end may be negative: then so is the column's
+                        // to what it is taken from, and their product is still a power >= 0
                         const float far = s_upd * exp2_approx(fmaf(g2, (float)(rev ? d : d - 15), -lf));
                         const uint64_t far2 = two(far, far);
+                        if (rev ? d >= 0 : d >= 15) {   // every pair
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            o[j] = pack2(mul2((uint64_t)x[2 * j + 1] << 32 | x[2 * j], mul2(near[j], far2)));
+                            for (int j = 0; j < 8; ++j)
+                                o[j] = pack2(mul2((uint64_t)x[2 * j + 1] << 32 | x[2 * j], mul2(near[j], far2)));
+                        } else {
+                            const int last = rev ? -d - 1 : d;   // columns up to it are the pairs, or those after it
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                const uint64_t v = mul2((uint64_t)x[2 * j + 1] << 32 | x[2 * j], mul2(near[j], far2));
+                                o[j] = pack2((2 * j <= last) != rev ? __uint_as_float((uint32_t)v) : 0.f,
+                                             (2 * j + 1 <= last) != rev ? __uint_as_float((uint32_t)(v >> 32)) : 0.f);
+                            }
+                        }
                     } else {
                         const float l0 = fmaf(g2, (float)d, -lf), l1 = rev ? g2 : -g2;
-                        const int last = rev ? -d - 1 : d;   // columns up to it are the pairs, or those after it
+                        const int last = rev ? -d - 1 : d;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
-                            float v[2];   // selected, not branched around
+                            float v[2];
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
                                 v[k] = __uint_as_float(x[2 * j + k]) * exp2_approx(fmaf((float)(2 * j + k), l1, l0));
-                                v[k] = (2 * j + k <= last) != rev ? v[k] : 0.f;
+                                v[k] = (2 * j + k <= last) != rev ? s_upd * v[k] : 0.f;
                             }
-                            o[j] = pack2(s_upd * v[0], s_upd * v[1]);
+                            o[j] = pack2(v[0], v[1]);
                         }
                     }
                     tmem_st8(lanes + kColS + 64 * half + 8 * m, o);
@@ -601,45 +626,54 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 if (lane == 0) mbar_arrive(&bar.p_ready);
                 if (!(ok = wait(&bar.o_full, it))) break;
                 tc_fence_after();
-                // O in bf16 goes through the tile's A (its products are complete): each warp
-                // writes its 32 rows and half of the columns there, swizzled as the store's
-                // box, and sends them on as one box -- or row by row at a sequence's end
+                // O in bf16 goes out through the tile's A (its products are complete), in the
+                // layout of the store's boxes
                 const float f = s_out * exp2_approx(lf);
                 const uint64_t f2 = two(f, f);
-                uint8_t *buf = smem + (it & 1) * kStage + half * kBox + rw * 4096;
-                auto piece = [&](int r, int c) {   // 16 bytes: columns 8 c ..
-                    return (uint4 *)(buf + (vd == 128 ? r * 128 + ((c ^ (r & 7)) << 4)
-                                                      : r * 64 + ((c ^ ((r >> 1) & 3)) << 4)));
-                };
+                uint8_t *buf = smem + (it & 1) * kStage;
                 tmem_columns(lanes + kColO + half * (vd / 2), vd / 32, [&](int m, const uint32_t (&x)[16]) {
                     uint32_t o[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) o[j] = pack2(mul2((uint64_t)x[2 * j + 1] << 32 | x[2 * j], f2));
-                    *piece(lane, 2 * m) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *piece(lane, 2 * m + 1) = make_uint4(o[4], o[5], o[6], o[7]);
+                    const int col = half * (vd / 2) + 16 * m;
+                    uint8_t *to = buf + (col >> 6) * kBox;
+                    *(uint4 *)(to + sw128_off(row, (col & 63) * 2)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *(uint4 *)(to + sw128_off(row, (col & 63) * 2 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
                 });
                 tc_fence_before();
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&bar.o_free);
-                    if (32 * rw + 32 <= len) {
-                        tma_store_3d(out_map, half * (vd / 2), u.h, (int)(walk.first(u, i) + 32 * rw), buf);
+                if (lane == 0) mbar_arrive(&bar.o_free);
+            }
+            return ok;
+        });
+    } else if (warp == kOutStore) {
+        // ---- outputs: a tile's as boxes of 64 columns, or row by row at a sequence's end
+        each_unit([&](const Unit &u) {
+            bool ok = true;
+            const DecayPass &p = A.pass[u.pass];
+            const Walk walk(u, p.rev);
+            const int vd = p.vd;
+            for (int i = 0; i < walk.tiles; ++i, ++it) {
+                const int len = walk.len(i);
+                const int64_t t = walk.first(u, i);
+                const uint8_t *buf = smem + (it & 1) * kStage;
+                if (!(ok = wait(&bar.o_free, it))) break;
+                if (len == kC) {
+                    if (lane == 0) {
+                        for (int b = 0; b < vd; b += 64)
+                            tma_store_3d(&maps.o[u.pass], b, u.h, (int)t, buf + (b >> 6) * kBox);
                         bulk_commit();
                         bulk_wait_read();
                     }
-                }
-                __syncwarp();
-                if (32 * rw + 32 > len) {
-                    const int64_t row_step = (int64_t)H * vd;
-                    __nv_bfloat16 *dst = (__nv_bfloat16 *)p.out + (walk.first(u, i) + 32 * rw) * row_step +
-                                         u.h * vd + half * (vd / 2);
-                    for (int k = lane; k < 2 * vd; k += 32) {
-                        const int r = k / (vd / 16), c = k % (vd / 16);
-                        if (32 * rw + r < len) *(uint4 *)(dst + r * row_step + 8 * c) = *piece(r, c);
+                } else {
+                    for (int k = lane; k < len * (vd / 8); k += 32) {
+                        const int r = k / (vd / 8), c = 8 * (k % (vd / 8));
+                        *(uint4 *)((__nv_bfloat16 *)p.out + ((t + r) * H + u.h) * (int64_t)vd + c) =
+                            *(const uint4 *)(buf + (c >> 6) * kBox + sw128_off(r, (c & 63) * 2));
                     }
+                    fence_proxy_async_smem();
                 }
-                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.free_a[it & 1]);
             }
@@ -717,7 +751,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
         });
     } else {
         // ---- weighted values: thread = value index (TMEM lane); group grp takes every other
-        // 16 tokens, its token l = 16 a + j being the tile's 16 (2 a + grp) + j
+        // 16 tokens, its token l = 16 k + j being the tile's 16 (2 k + grp) + j
         const int grp = (warp - 12) >> 2, e = tid & 127;
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
         float *w = (float *)(smem + kOffW) + (warp - 12) * (kC / 2);
@@ -744,7 +778,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 w[lane] = w0 * up;
                 w[lane + 32] = w1 * up;
                 __syncwarp();
-                if (!(ok = wait(&bar.full[st], it >> 1))) break;
+                if (!(ok = wait(&bar.full_bc[st], it >> 1))) break;
                 uint8_t *ct = smem + st * kStage + 2 * kTile;
                 if (len < kC && any) {
                     // both groups write the same zeros; the product with P reads them too
@@ -753,11 +787,11 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                     __syncwarp();
                 }
 #pragma unroll 1
-                for (int a = 0; a < 4; ++a) {
-                    const uint32_t part = it * kParts + 2 * a + grp, slot = part % kSlots, use = part / kSlots;
+                for (uint32_t k = 0; k < kParts; ++k) {
+                    const uint32_t slot = k % kSlots, use = (it * kParts + k) / kSlots;
                     if (use && !(ok = wait(&bar.v_free[slot], use - 1))) break;
                     tc_fence_after();
-                    write_terms(lanes + kColV + slot * kSlotCols, ct, e, any, 2 * a + grp, w + 16 * a);
+                    write_terms(lanes + kColV + slot * kSlotCols + 8 * grp, ct, e, any, 2 * k + grp, w + 16 * k);
                     tmem_st_wait();
                     tc_fence_before();
                     __syncwarp();
@@ -910,10 +944,12 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
 #pragma unroll 1
                 for (uint32_t k = 0; k < kParts; ++k) {
                     const uint32_t av = tm + kLocColV + (buf * kParts + k) * kSlotCols;
-                    const uint64_t db = dBt + ((k * 2048) >> 4);
-                    mma_f16_ts_if(lead, tm, av, db, id_h, i + k > 0);
-                    mma_f16_ts_if(lead, tm, av + 8, db, id_h, 1);
-                    mma_f16_ts_if(lead, tm, av + 16, db, id_h, 1);
+#pragma unroll
+                    for (uint32_t term = 0; term < 3; ++term)
+#pragma unroll
+                        for (uint32_t j = 0; j < 2; ++j)
+                            mma_f16_ts_if(lead, tm, av + term * 16 + j * 8, dBt + ((k * 4096 + j * 2048) >> 4), id_h,
+                                          i + k + term + j > 0);
                 }
                 mma_commit_if(lead, &bar.v_free[buf]);
                 mma_commit_if(lead, &bar.free[st]);
@@ -962,8 +998,9 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                     __syncwarp();
                 }
 #pragma unroll 1
-                for (uint32_t k = 0; k < kParts; ++k)
-                    write_terms(lanes + kLocColV + (buf * kParts + k) * kSlotCols, ct, e, any, k, w + 16 * k);
+                for (uint32_t k = 0; k < 2 * kParts; ++k)
+                    write_terms(lanes + kLocColV + (buf * kParts + k / 2) * kSlotCols + 8 * (k & 1), ct, e, any, k,
+                                w + 16 * k);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -1002,10 +1039,10 @@ cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, 
     TcArgs args{};
     for (int i = 0; i < n; ++i) {
         const DecayPass &p = passes[i];
-        const bool ok = tc_make_tile_map(&maps.b[i], p.b, p.kd, g.H, g.T_total, kC, 64) &&
-                        tc_make_tile_map(&maps.c[i], p.c, p.vd, g.H, g.T_total, kC, 64) &&
-                        (local || (tc_make_tile_map(&maps.a[i], p.a, p.kd, g.H, g.T_total, kC, 64) &&
-                                   tc_make_tile_map(&maps.o[i], p.out, p.vd, g.H, g.T_total, 32, p.vd / 2)));
+        const bool ok = tc_make_tile_map(&maps.b[i], p.b, p.kd, g.H, g.T_total, kC) &&
+                        tc_make_tile_map(&maps.c[i], p.c, p.vd, g.H, g.T_total, kC) &&
+                        (local || (tc_make_tile_map(&maps.a[i], p.a, p.kd, g.H, g.T_total, kC) &&
+                                   tc_make_tile_map(&maps.o[i], p.out, p.vd, g.H, g.T_total, kC)));
         if (!ok) return cudaErrorNotSupported;
         args.pass[i] = p;
     }

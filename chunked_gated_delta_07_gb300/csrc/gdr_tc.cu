@@ -987,19 +987,16 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
-// [rows][H][width] bf16 viewed as (d, h, row), box (box_cols, 1, box_rows) with box_cols 64
-// or 32, swizzled over the box's rows of 128 or 64 bytes.
-bool make_tile_map(CUtensorMap *map, const void *base, int width, int H, int64_t rows, int box_rows,
-                   int box_cols = 64) {
+// [rows][H][width] bf16 viewed as (d, h, row), box (64, 1, box_rows), 128-byte swizzle.
+bool make_tile_map(CUtensorMap *map, const void *base, int width, int H, int64_t rows, int box_rows) {
     auto fn = encode_fn();
     if (!fn || ((uintptr_t)base & 15)) return false;
     cuuint64_t dims[3] = {(cuuint64_t)width, (cuuint64_t)H, (cuuint64_t)std::max<int64_t>(rows, 1)};
     cuuint64_t strides[2] = {(cuuint64_t)width * 2, (cuuint64_t)width * 2 * H};
-    cuuint32_t box[3] = {(cuuint32_t)box_cols, 1, (cuuint32_t)box_rows};
+    cuuint32_t box[3] = {64, 1, (cuuint32_t)box_rows};
     cuuint32_t estr[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
-              estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -1036,9 +1033,8 @@ bool tc_make_map(CUtensorMap *map, const void *base, int H, int64_t rows) {
     return make_map(map, base, H, rows);
 }
 
-bool tc_make_tile_map(CUtensorMap *map, const void *base, int width, int H, int64_t rows, int box_rows,
-                      int box_cols) {
-    return make_tile_map(map, base, width, H, rows, box_rows, box_cols);
+bool tc_make_tile_map(CUtensorMap *map, const void *base, int width, int H, int64_t rows, int box_rows) {
+    return make_tile_map(map, base, width, H, rows, box_rows);
 }
 
 bool tc_supported(gdr_dtype_t dtype, int dk, int dv, int chunk) {

@@ -33,10 +33,8 @@ cudaError_t launch_tc_forward(const void *q, const void *k, const void *v, const
 // (128-byte swizzle); false when the driver entry point is missing or the base is
 // not 16-byte aligned.
 bool tc_make_map(CUtensorMap *map, const void *base, int H, int64_t rows);
-// The same for [rows][H][width] tensors and tiles of box_rows rows by box_cols columns (64, or
-// 32 with a 64-byte swizzle).
-bool tc_make_tile_map(CUtensorMap *map, const void *base, int width, int H, int64_t rows, int box_rows,
-                      int box_cols);
+// The same for [rows][H][width] tensors (width a multiple of 64) and box_rows-row tiles.
+bool tc_make_tile_map(CUtensorMap *map, const void *base, int width, int H, int64_t rows, int box_rows);
 
 // The per-channel decay forward on the tensor cores (gdr_tc_vec.cu): bf16, d = 128,
 // tiles of 16, bounded gate.  `warm` holds the warm-up of every (segment, head),
