@@ -116,11 +116,12 @@ constexpr uint32_t kRing = 4;   // units announced ahead
 
 // False where unit u has nothing to do.
 __device__ __forceinline__ bool unit_of(const TcArgs &A, int64_t u, bool local, Unit &o) {
-    o.pass = (int)(u % A.npass);
-    const int64_t sh = u / A.npass;
-    o.h = (int)(sh % A.g.H);
+    const uint32_t u32 = (uint32_t)u, sh = u32 / (uint32_t)A.npass;   // fewer than 2^31 units
+    o.pass = (int)(u32 - sh * (uint32_t)A.npass);
+    const uint32_t sg = sh / (uint32_t)A.g.H;
+    o.h = (int)(sh - sg * (uint32_t)A.g.H);
     DecaySeg seg;
-    if (!decay_segment(A.g, sh / A.g.H, seg)) return false;
+    if (!decay_segment(A.g, sg, seg)) return false;
     const DecayPass &p = A.pass[o.pass];
     o.gd = decay_log(A.g.log_decay, o.h);
     o.t0 = seg.t0;
@@ -174,12 +175,14 @@ __device__ __forceinline__ void load_tile(uint8_t *dst, const CUtensorMap *map, 
     if (width > 64) tma_load_3d(dst + kBox, map, 64, h, (int)t, bar);
 }
 
-// Zeroes the rows from n on of a tile in shared memory: tokens past the sequence's end,
-// which are another sequence's (one warp; made visible to the tensor cores).
-__device__ __forceinline__ void zero_rows(uint8_t *tile, int width, int n, int lane) {
-    for (int box = 0; box < width / 64; ++box)
-        for (int i = lane; i < (kC - n) * 8; i += 32)
-            *(uint4 *)(tile + box * kBox + sw128_off(n + i / 8, (i & 7) * 16)) = make_uint4(0, 0, 0, 0);
+// Zeroes the rows from n on of a tile in shared memory -- tokens past the sequence's end,
+// which are another sequence's -- as warp `part` of `parts`.  (A weight of 0 would not
+// silence a NaN.)
+__device__ __forceinline__ void zero_rows(uint8_t *tile, int width, int n, int part, int parts, int lane) {
+    for (int i = 32 * part + lane; i < (kC - n) * (width / 8); i += 32 * parts) {
+        const int r = n + i / (width / 8), c = i % (width / 8);
+        *(uint4 *)(tile + (c >> 3) * kBox + sw128_off(r, (c & 7) * 16)) = make_uint4(0, 0, 0, 0);
+    }
 }
 
 // log2 lam; below -200 every power but the zeroth is out of the range of fp32 and its
@@ -201,8 +204,7 @@ __device__ __forceinline__ float token_weight(int i, int len, bool rev, float gd
     return i < len ? s_upd * expf(gd * (float)(past + (rev ? i + 1 : len - 1 - i))) : 0.f;
 }
 
-// Zeroes the rows from n on of the 32 columns from e0 (one warp) of a tile: what a weight
-// of 0 would not silence.
+// Zeroes the rows from n on of the 32 columns from e0 (one warp) of a tile.
 __device__ __forceinline__ void zero_columns(uint8_t *tile, int e0, int n, int lane) {
     for (int i = lane; i < (kC - n) * 4; i += 32)
         *(uint4 *)(tile + (e0 >> 6) * kBox + sw128_off(n + i / 4, (e0 & 63) * 2 + (i & 3) * 16)) =
@@ -283,19 +285,22 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// 16 columns (d0 ..) of row e of a state in memory.
-__device__ __forceinline__ void state_load(const DecayPass &p, const float *in, int d0, int e, uint32_t (&r)[16]) {
+// 32 columns (d0 ..) of row e of a state in memory.
+__device__ __forceinline__ void state_load(const DecayPass &p, const float *in, int d0, int e, uint32_t (&r)[32]) {
 #pragma unroll
-    for (int j = 0; j < 16; ++j) r[j] = 0;
-    if (!in || e >= p.vd || d0 >= p.kd) return;
+    for (int j = 0; j < 32; ++j) r[j] = 0;
+    if (!in || e >= p.vd) return;
     if (p.transposed) {
+        const float *row = in + (int64_t)e * p.kd + d0;
 #pragma unroll
-        for (int j = 0; j < 16; j += 4) *(uint4 *)&r[j] = *(const uint4 *)&in[(int64_t)e * p.kd + d0 + j];
+        for (int j = 0; j < 32; j += 4) *(uint4 *)&r[j] = *(const uint4 *)&row[j];
     } else {
+        const float *col = in + (int64_t)d0 * p.vd + e;
 #pragma unroll
-        for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(in[(int64_t)(d0 + j) * p.vd + e]);
+        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(col[j * p.vd]);
     }
 }
+// 16 columns of it back.
 __device__ __forceinline__ void state_store(const DecayPass &p, float *to, int d0, int e, const uint32_t (&r)[16]) {
     if (!to || e >= p.vd || d0 >= p.kd) return;
     if (p.transposed) {
@@ -452,6 +457,10 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             const DecayPass &p = A.pass[u.pass];
             const Walk walk(u, p.rev);
             const int kd = p.kd, vd = p.vd;
+            // the entering state on its way into the L2, ahead of the warps that take it
+            if (u.in)
+                for (int i = 32 * lane; i < kd * vd; i += 1024)
+                    asm volatile("prefetch.global.L2 [%0];" ::"l"(u.in + i));
             for (int i = 0; i < walk.tiles; ++i, ++it) {
                 const uint32_t st = it & 1;
                 const int64_t t = walk.first(u, i);
@@ -495,14 +504,8 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             for (int i = 0; i < walk.tiles; ++i, ++it) {
                 const uint32_t st = it & 1;
                 const int len = walk.len(i);
-                uint8_t *sp = smem + st * kStage;
                 const uint32_t sa = s0 + st * kStage, sb = sa + kTile, sc = sb + kTile;
                 if (!(ok = wait(&bar.full_bc[st], it >> 1)) || !(ok = wait(&bar.full_a[st], it >> 1))) break;
-                if (len < kC) {
-                    zero_rows(sp + kTile, kd, len, lane);   // of C: by the warps that weigh it
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                }
                 tc_fence_after();
                 const uint64_t dA = smem_desc(sa, 16, 1024, kSw128), dB = smem_desc(sb, 16, 1024, kSw128);
                 const uint64_t dBt = smem_desc(sb, kBox, 1024, kSw128), dCt = smem_desc(sc, kBox, 1024, kSw128);
@@ -521,6 +524,15 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
 #pragma unroll
                 for (uint32_t k = 0; k < kParts; ++k) {
                     const uint32_t slot = k % kSlots, av = tm + kColV + slot * kSlotCols;
+                    if (k == kSlots) {   // while the slots are filled again
+                        if (it && !(ok = wait(&bar.o_free, it - 1))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (uint32_t j = 0; j < 8; ++j)
+                            if (j < kd16)
+                                mma_f16_ss_if(lead, tm + kColO, dA + k_major(j), dH + k_major(j), id_o1, j > 0);
+                        mma_commit_if(lead, &bar.o1_full);
+                    }
                     if (!(ok = wait(&bar.v_ready[slot], (it * kParts + k) / kSlots))) break;
                     tc_fence_after();
 #pragma unroll
@@ -532,13 +544,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                     mma_commit_if(lead, &bar.v_free[slot]);
                 }
                 mma_commit_if(lead, &bar.kv_full);
-                if (!ok || (it && !(ok = wait(&bar.o_free, it - 1)))) break;
-                tc_fence_after();
-#pragma unroll
-                for (uint32_t k = 0; k < 8; ++k)
-                    if (k < kd16) mma_f16_ss_if(lead, tm + kColO, dA + k_major(k), dH + k_major(k), id_o1, k > 0);
-                mma_commit_if(lead, &bar.o1_full);
-                if (!(ok = wait(&bar.p_ready, it))) break;
+                if (!ok || !(ok = wait(&bar.p_ready, it))) break;
                 tc_fence_after();
 #pragma unroll
                 for (uint32_t k = 0; k < kC / 16; ++k)
@@ -583,7 +589,9 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                     const int c0 = 64 * half + 16 * m;
                     const int d = rev ? c0 - row : row - c0;   // distance of column c0
                     uint32_t o[8];
-                    if (rev ? c0 + 15 < 32 * rw : c0 > 32 * rw + 31) {   // no pair of the warp's rows
+                    // the row's pairs among the block's columns: from lo to hi - 1
+                    const int lo = rev ? -d : 0, hi = rev ? len - c0 : d + 1;
+                    if (rev ? c0 + 15 < 32 * rw || hi <= 0 : c0 > 32 * rw + 31) {   // none of the warp's rows has any
 #pragma unroll
                         for (int j = 0; j < 8; ++j) o[j] = 0;
                     } else if (gentle) {
@@ -591,31 +599,25 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                         // to what it is taken from, and their product is still a power >= 0
                         const float far = s_upd * exp2_approx(fmaf(g2, (float)(rev ? d : d - 15), -lf));
                         const uint64_t far2 = two(far, far);
-                        if (rev ? d >= 0 : d >= 15) {   // every pair
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            o[j] = pack2(mul2((uint64_t)x[2 * j + 1] << 32 | x[2 * j], mul2(near[j], far2)));
+                        if (!__all_sync(kFull, lo <= 0 && hi >= 16))
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
-                                o[j] = pack2(mul2((uint64_t)x[2 * j + 1] << 32 | x[2 * j], mul2(near[j], far2)));
-                        } else {
-                            const int last = rev ? -d - 1 : d;   // columns up to it are the pairs, or those after it
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                const uint64_t v = mul2((uint64_t)x[2 * j + 1] << 32 | x[2 * j], mul2(near[j], far2));
-                                o[j] = pack2((2 * j <= last) != rev ? __uint_as_float((uint32_t)v) : 0.f,
-                                             (2 * j + 1 <= last) != rev ? __uint_as_float((uint32_t)(v >> 32)) : 0.f);
-                            }
-                        }
+                                o[j] &= (2 * j >= lo && 2 * j < hi ? 0xffffu : 0u) |
+                                        (2 * j + 1 >= lo && 2 * j + 1 < hi ? 0xffff0000u : 0u);
                     } else {
                         const float l0 = fmaf(g2, (float)d, -lf), l1 = rev ? g2 : -g2;
-                        const int last = rev ? -d - 1 : d;
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             float v[2];
 #pragma unroll
-                            for (int k = 0; k < 2; ++k) {
-                                v[k] = __uint_as_float(x[2 * j + k]) * exp2_approx(fmaf((float)(2 * j + k), l1, l0));
-                                v[k] = (2 * j + k <= last) != rev ? s_upd * v[k] : 0.f;
-                            }
-                            o[j] = pack2(v[0], v[1]);
+                            for (int k = 0; k < 2; ++k)
+                                v[k] = s_upd * __uint_as_float(x[2 * j + k]) *
+                                       exp2_approx(fmaf((float)(2 * j + k), l1, l0));
+                            o[j] = pack2(v[0], v[1]) & ((2 * j >= lo && 2 * j < hi ? 0xffffu : 0u) |
+                                                        (2 * j + 1 >= lo && 2 * j + 1 < hi ? 0xffff0000u : 0u));
                         }
                     }
                     tmem_st8(lanes + kColS + 64 * half + 8 * m, o);
@@ -667,6 +669,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                         bulk_wait_read();
                     }
                 } else {
+#pragma unroll 4
                     for (int k = lane; k < len * (vd / 8); k += 32) {
                         const int r = k / (vd / 8), c = 8 * (k % (vd / 8));
                         *(uint4 *)((__nv_bfloat16 *)p.out + ((t + r) * H + u.h) * (int64_t)vd + c) =
@@ -720,12 +723,16 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 tc_fence_after();
                 if (i == 0) {
 #pragma unroll 1
-                    for (int m = 0; m < pieces; ++m) {
-                        uint32_t r[16];
+                    for (int m = 0; m < pieces; m += 2) {
+                        uint32_t r[32];
                         state_load(p, u.in, 16 * m, e, r);
                         __syncwarp();
-                        take(m, r);
-                        tmem_st16(lanes + kColH + 16 * m, r);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t(&half)[16] = *(uint32_t(*)[16])&r[16 * k];
+                            take(m + k, half);
+                            tmem_st16(lanes + kColH + 16 * (m + k), half);
+                        }
                     }
                     tmem_st_wait();
                 } else {
@@ -780,9 +787,9 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 __syncwarp();
                 if (!(ok = wait(&bar.full_bc[st], it >> 1))) break;
                 uint8_t *ct = smem + st * kStage + 2 * kTile;
-                if (len < kC && any) {
-                    // both groups write the same zeros; the product with P reads them too
-                    zero_columns(ct, e & ~31, len, lane);
+                if (len < kC) {   // the products with P and with S^ read these rows too
+                    if (any) zero_columns(ct, e & ~31, len, lane);   // both groups the same zeros
+                    zero_rows(ct - kTile, p.kd, len, warp - 12, 8, lane);
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
@@ -934,7 +941,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                 const int len = walk.len(i);
                 if (!(ok = wait(&bar.full[st], it / kLocStages))) break;
                 if (len < kC) {
-                    zero_rows(smem + st * kLocStage, kd, len, lane);
+                    zero_rows(smem + st * kLocStage, kd, len, 0, 1, lane);
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
@@ -1057,6 +1064,7 @@ cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, 
         if (x >= 0 && (uint64_t)x < kWaitNs) args.wait_ns = (uint64_t)x;
     }
     if (args.units == 0) return cudaSuccess;
+    if (args.units > 0x7fffffff) return cudaErrorInvalidValue;
     auto kern = local ? decay_local_kernel : decay_out_kernel;
     const int bytes = (int)(local ? kSmemLocal : kSmemOut);
     const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
