@@ -533,8 +533,8 @@ gdr_status_t validate_forward(const void *q, const void *k, const void *v, const
 // ---------------------------------------------------------------------------
 namespace {
 
-// Scratch of one call, every region 256-byte aligned: the plan and two unit counters (packed
-// input), the boundary states of the forward chain and, for the backward pass, of the reversed one.
+// Scratch of one call, every region 256-byte aligned: the plan (packed
+// input), two unit counters, the boundary states of the forward chain and, for the backward pass, of the reversed one.
 struct DecayLayout {
     size_t plan = 0, next = 0, slots = 0, slots_rev = 0, copy = 0, total = 0;
 };
@@ -553,7 +553,7 @@ constexpr int64_t kDecayStepTokens = 8;   // most tokens that decay_step_kernel 
 //     ceil(units N s / slots) (ceil(tiles / s) + fixed) + (s - 1) / s * local
 // in tiles: whole rounds of the machine, a start-up per segment, and the local pass over
 // the inner segments, which reads half of what the output pass moves.  Packed sequences
-// (lengths unknown on the host) are cut into even shares of all tiles, six per slot, so
+// (lengths unknown on the host) are cut into even shares of all tiles, three per slot, so
 // that one long sequence among short ones is cut too and the slots end together.
 // GDR_DECAY_SEG_TILES=n cuts into n tiles per segment whatever the sizes (the parity tests
 // run many short segments).
@@ -587,7 +587,7 @@ DecayGeom decay_geom(const DecayShape &s, int64_t units, int64_t slots, int64_t 
         g.max_slots = g.max_segs - s.N;
     } else {
         const int64_t tiles = (s.T_total + kDecayTile - 1) / kDecayTile;
-        const int64_t even = std::max(min_tiles, (tiles * units + 6 * slots - 1) / (6 * slots));
+        const int64_t even = std::max(min_tiles, (tiles * units + 3 * slots - 1) / (3 * slots));
         const int64_t seg = std::min<int64_t>(set > 0 ? set : even, 1 << 24);
         g.seg_tokens = seg * kDecayTile;
         // a sequence of len tokens has ceil(len / seg) segments, at least one
@@ -637,8 +637,8 @@ DecayLayout decay_layout(const DecayShape &s, const DecayGeom &g, bool backward)
         off += align_up(bytes);
         return at;
     };
-    L.plan = take(s.varlen ? 3 * sizeof(int64_t) * (size_t)(s.N + 1) : 0);
-    L.next = take(s.varlen ? 2 * sizeof(unsigned long long) : 0);
+    L.plan = take(s.varlen ? 2 * sizeof(int64_t) * (size_t)(s.N + 1) : 0);
+    L.next = take(s.varlen || g.max_slots ? 2 * sizeof(unsigned long long) : 0);
     L.slots = take(st * g.max_slots);
     L.slots_rev = take(backward ? st * g.max_slots : 0);
     // forward in place (hT = h0) with segments: the entering states' copy
@@ -647,18 +647,20 @@ DecayLayout decay_layout(const DecayShape &s, const DecayGeom &g, bool backward)
     return L;
 }
 
-// The plan of packed input, and the geometry completed with it.
+// The plan of packed input and the geometry completed with it; the unit counters zeroed.
 gdr_status_t decay_plan(DecayGeom *g, const int32_t *cu, const float *log_decay, char *ws, const DecayLayout &L,
                         int *status, cudaStream_t stream) {
     g->log_decay = log_decay;
-    if (g->dense) return GDR_OK;
-    int64_t *seq_start = (int64_t *)(ws + L.plan);
-    g->p = Plan{g->N, kDecayTile, (int)(g->seg_tokens / kDecayTile), seq_start, seq_start + (g->N + 1),
-                seq_start + 2 * (g->N + 1)};
-    return launch_plan(cu, g->N, 0, g->T_total, kDecayTile, g->p.seg_chunks, seq_start, seq_start + (g->N + 1),
-                       seq_start + 2 * (g->N + 1), status, stream) == cudaSuccess
-               ? GDR_OK
-               : GDR_ERR_CUDA;
+    unsigned long long *next = (unsigned long long *)(ws + L.next);
+    cudaError_t err = cudaSuccess;
+    if (!g->dense) {
+        int64_t *seq_start = (int64_t *)(ws + L.plan), *seg_base = seq_start + (g->N + 1);
+        g->p = Plan{g->N, kDecayTile, (int)(g->seg_tokens / kDecayTile), seq_start, nullptr, seg_base};
+        err = launch_decay_plan(cu, *g, seq_start, seg_base, next, status, stream);
+    } else if (g->max_slots > 0) {
+        err = cudaMemsetAsync(next, 0, 2 * sizeof(*next), stream);
+    }
+    return err == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
 }
 
 // Runs passes that are independent of each other, after the boundary states of those
@@ -666,22 +668,16 @@ gdr_status_t decay_plan(DecayGeom *g, const int32_t *cu, const float *log_decay,
 cudaError_t decay_run(const DecayGeom &g, const DecayPass *chains, int nchains, const DecayPass *passes, int n,
                       gdr_dtype_t dtype, bool tc, DeviceCtx *ctx, char *ws, const DecayLayout &L,
                       cudaStream_t stream) {
-    unsigned long long *next = g.dense ? nullptr : (unsigned long long *)(ws + L.next);
-    if (tc && next) {
-        const cudaError_t err = cudaMemsetAsync(next, 0, 2 * sizeof(*next), stream);
-        if (err != cudaSuccess) return err;
-    }
+    unsigned long long *next =
+        !g.dense || g.max_slots > 0 ? (unsigned long long *)(ws + L.next) : nullptr;
     auto run = [&](const DecayPass *p, int k) {
-        if (tc)
-            return launch_decay_tc(g, p, k, ctx->sms, next ? next + (p->local ? 1 : 0) : nullptr, ctx->d_status,
-                                   stream);
-        cudaError_t err = cudaSuccess;
-        for (int i = 0; i < k && err == cudaSuccess; ++i) err = launch_decay_rec(g, p[i], dtype, stream);
-        return err;
+        return tc ? launch_decay_tc(g, p, k, ctx->sms, next ? next + (p->local ? 1 : 0) : nullptr, ctx->d_status,
+                                    stream)
+                  : launch_decay_rec(g, p, k, dtype, stream);
     };
     if (g.max_slots > 0) {
         cudaError_t err = run(chains, nchains);
-        for (int i = 0; i < nchains && err == cudaSuccess; ++i) err = launch_decay_combine(g, chains[i], stream);
+        if (err == cudaSuccess) err = launch_decay_combine(g, chains, nchains, stream);
         if (err != cudaSuccess) return err;
     }
     return run(passes, n);
@@ -1222,7 +1218,7 @@ gdr_status_t gdr_decay_recurrent_fwd(const void *q, const void *k, const void *v
     g.max_segs = N;
     g.log_decay = log_decay;
     const DecayPass pass{q, k, v, out, state, state, nullptr, dk, dv, false, false, false, 1.f, scale};
-    return launch_decay_rec(g, pass, dtype, (cudaStream_t)stream) == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+    return launch_decay_rec(g, &pass, 1, dtype, (cudaStream_t)stream) == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
 }
 
 gdr_status_t gdr_layer_norm_fwd(const void *x, const float *weight, const float *bias, void *y, float *mean,

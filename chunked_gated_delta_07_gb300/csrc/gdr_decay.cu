@@ -9,6 +9,7 @@
 // that share columns.  The arithmetic is fp32 throughout; the pass is bound by the CUDA
 // cores (2 kd vd fused multiply-adds per token and head against 2 kd + 2 vd elements moved).
 #include <algorithm>
+#include <type_traits>
 
 #include "gdr_decay.cuh"
 
@@ -18,141 +19,227 @@ GDR_DEBUG_TU()
 
 namespace {
 
+// Exclusive sums of the sequences' segments (at least one each) over 1024 threads, each
+// with a run of sequences; 32 sums of warps in one more.
+__global__ void __launch_bounds__(1024)
+decay_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_total, int64_t seg_tokens,
+                  int64_t *__restrict__ seq_start, int64_t *__restrict__ seg_base, unsigned long long *next,
+                  int *status) {
+    __shared__ int64_t sums[32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (N + 1023) / 1024, n0 = min(N, tid * per), n1 = min(N, n0 + per);
+    auto segments = [&](int64_t len) { return len > seg_tokens ? (len + seg_tokens - 1) / seg_tokens : 1; };
+    int64_t mine = 0;
+    bool bad = tid == 0 && (cu[0] != 0 || (int64_t)cu[N] != T_total);
+    for (int n = n0; n < n1; ++n) {
+        const int64_t len = (int64_t)cu[n + 1] - cu[n];
+        bad |= len < 0;
+        mine += segments(len);
+    }
+    int64_t at = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += x;
+    }
+    if (lane == 31) sums[warp] = at;
+    bad = __syncthreads_or(bad);
+    int64_t before = lane < warp ? sums[lane] : 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+    at += before - mine;
+    if (tid < 2) next[tid] = 0;
+    // bad offsets: an empty plan, every sequence without tokens or segments
+    for (int n = n0; n < n1; ++n) {
+        seq_start[n] = bad ? 0 : cu[n];
+        seg_base[n] = bad ? 0 : at;
+        at += segments((int64_t)cu[n + 1] - cu[n]);
+    }
+    if (tid == 1023) {
+        seq_start[N] = bad ? 0 : T_total;
+        seg_base[N] = bad ? 0 : at;
+    }
+    if (tid == 0 && bad) set_status(status, GDR_ERR_BAD_SEQLENS);
+}
+
+// Passes of one launch; blockIdx.y says which.
+struct Passes {
+    DecayPass p[kDecayMaxPasses];
+};
+
 constexpr int kTb = 16;     // tokens per staged tile
 constexpr int kCols = 64;   // state columns per block
 
-template <typename T, int KD, bool REV, bool OUT>
-__global__ void __launch_bounds__(KD)
-decay_rec_kernel(const DecayGeom g, const DecayPass p) {
-    constexpr int kLanes = KD / 8;   // threads along kd; 8 threads along the columns
+template <typename T, int KD, bool OUT>
+__global__ void __launch_bounds__(2 * KD)
+decay_rec_kernel(const DecayGeom g, const __grid_constant__ Passes passes) {
+    const DecayPass &p = passes.p[blockIdx.y];
+    constexpr int kThreads = 2 * KD;
+    constexpr int kLanes = KD / 4;   // threads along kd, 4 rows each; 8 threads along the columns
     constexpr unsigned kFull = 0xffffffffu;
     __shared__ __align__(16) float bs[kTb][KD];
     __shared__ __align__(16) float as[OUT ? kTb : 1][KD];
     __shared__ __align__(16) float cs[kTb][kCols];
     __shared__ float os[OUT ? kTb : 1][kCols];
     __shared__ float pw[kTb][2];   // lam^j, lam^-j
-    const int slices = p.vd / kCols;
+    const int vd = p.vd, slices = vd / kCols, H = g.H;
+    if (blockIdx.x >= g.max_segs * H * slices) return;   // of a wider pass
     const int e0 = (int)(blockIdx.x % slices) * kCols;
     const int64_t sh = blockIdx.x / slices;
-    const int h = (int)(sh % g.H);
+    const int h = (int)(sh % H);
+    const bool rev = p.rev;
     DecaySeg seg;
-    if (!decay_segment(g, sh / g.H, seg)) return;
-    if (!OUT && (REV ? seg.first : seg.last)) return;   // no boundary behind it
+    if (!decay_segment(g, sh / H, seg)) return;
+    if (!OUT && (rev ? seg.first : seg.last)) return;   // no boundary behind it
     if (!GDR_INBOUNDS(seg.t0 >= 0 && seg.t1 <= g.T_total && (!p.slots || seg.slot <= g.max_slots))) return;
     const float gd = decay_log(g.log_decay, h);
     int64_t t0 = seg.t0, t1 = seg.t1;
     if (!OUT) {
         const int64_t reach = decay_reach(gd, t1 - t0);
-        if (REV) t1 = t0 + reach; else t0 = t1 - reach;
+        if (rev) t1 = t0 + reach; else t0 = t1 - reach;
     }
     const int64_t ntok = t1 - t0;
     // Inside a block of nb tokens the state is kept without its decay: with j tokens of the
     // block behind it, S = lam^j S^, S^ += lam^-j b c^T and out = (lam^j a)^T S^, and lam^nb
     // enters the state once per block.  That saves a third of the instructions and keeps the
     // powers exact: lam itself rounds to 24 bits, an error that a product of n of them
-    // multiplies by n.  Blocks are
-    // whole tiles while lam^-15 stays in range, else single tokens.  A forward pass decays the
-    // state before its first token too, a reversed one after its last.
+    // multiplies by n.  Blocks are whole tiles while lam^-15 stays in range, else single
+    // tokens.  A forward pass decays the state before its first token too, a reversed one
+    // after its last.
     const int nb = gd >= -4.f ? kTb : 1;
     const DecayFactor step(gd * (float)nb);
     const int tid = threadIdx.x, dl = tid % kLanes, eg = tid / kLanes;
-    // the thread's elements: kd index 4 dl + (u & 3) + (u >> 2) KD / 2, column e0 + 8 eg + j
-    float s[8][8];
-    const float *in = decay_state_in(p, seg, g.H, h);
+    // the thread's elements: row 4 dl + u of kd, column e0 + 8 eg + j
+    float s[4][8];
+    const float *in = decay_state_in(p, seg, H, h);
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        const int d = 4 * dl + (u & 3) + (u >> 2) * (KD / 2);
+    for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int e = e0 + 8 * eg + j;
-            s[u][j] = in ? in[p.transposed ? (int64_t)e * KD + d : (int64_t)d * p.vd + e] : 0.f;
+            const int d = 4 * dl + u, e = e0 + 8 * eg + j;
+            s[u][j] = in ? in[p.transposed ? e * KD + d : d * vd + e] : 0.f;
         }
-    }
     auto decay = [&](const DecayFactor &f) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
+        for (int u = 0; u < 4; ++u)
 #pragma unroll
             for (int j = 0; j < 8; ++j) s[u][j] = f(s[u][j]);
     };
-    if (!REV && ntok > 0) decay(DecayFactor(gd));
+    if (!rev && ntok > 0) decay(DecayFactor(gd));
     if (tid < kTb) {
         const float e = nb > 1 ? gd * (float)tid : 0.f;
         pw[tid][0] = expf(e);
         pw[tid][1] = expf(-e);
     }
-    __syncthreads();
+    // A tile's tokens in the order of the pass, as loaded: the next tile's are on their way
+    // while one is computed
+    constexpr int kPerB = kTb * KD / kThreads, kPerC = kTb * kCols / kThreads;
     const T *A = (const T *)p.a, *B = (const T *)p.b, *C = (const T *)p.c;
     T *O = (T *)p.out;
+    T ra[OUT ? kPerB : 1], rb[kPerB], rc[kPerC];
+    auto row_of = [&](int64_t n) { return (rev ? t1 - 1 - n : t0 + n) * H + h; };   // n-th token's row
+    auto load = [&](int64_t tb) {
+#pragma unroll
+        for (int k = 0; k < kPerB; ++k) {
+            const int i = tid + k * kThreads;
+            const int64_t n = tb + i / KD;
+            const bool on = n < ntok;
+            const int64_t at = on ? row_of(n) * KD + i % KD : 0;
+            rb[k] = on ? B[at] : from_f32<T>(0.f);
+            if (OUT) ra[k] = on ? A[at] : from_f32<T>(0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < kPerC; ++k) {
+            const int i = tid + k * kThreads;
+            const int64_t n = tb + i / kCols;
+            rc[k] = n < ntok ? C[row_of(n) * vd + e0 + i % kCols] : from_f32<T>(0.f);
+        }
+    };
+    load(0);
+    __syncthreads();
     for (int64_t tb = 0; tb < ntok; tb += kTb) {
         const int nr = (int)min((int64_t)kTb, ntok - tb);
         if (tb && nb > 1) decay(step);
-        // token of the tile's row r, in the order of the pass
-        auto row_of = [&](int r) { return (REV ? t1 - 1 - (tb + r) : t0 + tb + r) * g.H + h; };
-        for (int i = tid; i < nr * KD; i += KD) {
-            const int64_t at = row_of(i / KD) * KD + i % KD;
-            bs[i / KD][i % KD] = to_f32(B[at]);
-            if (OUT) as[i / KD][i % KD] = to_f32(A[at]) * (p.s_out * pw[i / KD][0]);
+#pragma unroll
+        for (int k = 0; k < kPerB; ++k) {
+            const int i = tid + k * kThreads;
+            bs[i / KD][i % KD] = to_f32(rb[k]);
+            if (OUT) as[i / KD][i % KD] = to_f32(ra[k]) * (p.s_out * pw[i / KD][0]);
         }
-        for (int i = tid; i < nr * kCols; i += KD)
-            cs[i / kCols][i % kCols] = to_f32(C[row_of(i / kCols) * p.vd + e0 + i % kCols]) * (p.s_upd * pw[i / kCols][1]);
+#pragma unroll
+        for (int k = 0; k < kPerC; ++k) {
+            const int i = tid + k * kThreads;
+            cs[i / kCols][i % kCols] = to_f32(rc[k]) * (p.s_upd * pw[i / kCols][1]);
+        }
         __syncthreads();
-#pragma unroll 2
-        for (int r = 0; r < nr; ++r) {
-            if (nb == 1 && tb + r) decay(step);
-            float bv[8], cv[8], av[8], o[8];
-            *(float4 *)&bv[0] = *(const float4 *)&bs[r][4 * dl];
-            *(float4 *)&bv[4] = *(const float4 *)&bs[r][4 * dl + KD / 2];
-            *(float4 *)&cv[0] = *(const float4 *)&cs[r][8 * eg];
-            *(float4 *)&cv[4] = *(const float4 *)&cs[r][8 * eg + 4];
-            if (OUT) {
-                *(float4 *)&av[0] = *(const float4 *)&as[r][4 * dl];
-                *(float4 *)&av[4] = *(const float4 *)&as[r][4 * dl + KD / 2];
+        if (tb + kTb < ntok) load(tb + kTb);
+        // kU tokens at a time: their sums over the lanes are independent of each other, and
+        // the state's chain is one multiply-add per token
+        auto tokens = [&](int r0, auto count) {
+            constexpr int kU = decltype(count)::value;
+            float o[kU][8];
+#pragma unroll
+            for (int q = 0; q < kU; ++q) {
+                const int r = r0 + q;
+                if (nb == 1 && tb + r) decay(step);
+                float bv[4], cv[8], av[4];
+                *(float4 *)&bv[0] = *(const float4 *)&bs[r][4 * dl];
+                *(float4 *)&cv[0] = *(const float4 *)&cs[r][8 * eg];
+                *(float4 *)&cv[4] = *(const float4 *)&cs[r][8 * eg + 4];
+                if (OUT) *(float4 *)&av[0] = *(const float4 *)&as[r][4 * dl];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[q][j] = 0.f;
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        s[u][j] = fmaf(bv[u], cv[j], s[u][j]);
+                        if (OUT) o[q][j] = fmaf(av[u], s[u][j], o[q][j]);
+                    }
             }
+            if (!OUT) return;
+            // sum over the kLanes threads of the columns: each exchange halves the columns a
+            // thread carries until it has one; lane bits give which
+            int col = 0, lanes = kLanes;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = 0.f;
+            for (int n = 4; n; n >>= 1) {
+                lanes >>= 1;
+                const bool up = dl & lanes;
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    s[u][j] = fmaf(bv[u], cv[j], s[u][j]);
-                    if (OUT) o[j] = fmaf(av[u], s[u][j], o[j]);
-                }
-            if (OUT) {
-                // sum over the kLanes threads of the columns: each exchange halves the
-                // columns a thread carries; lane bits give the column it ends with
-                int col = 0, lanes = kLanes;
-#pragma unroll
-                for (int n = 4; n; n >>= 1) {
-                    lanes >>= 1;
-                    const bool up = dl & lanes;
+                for (int q = 0; q < kU; ++q)
 #pragma unroll
                     for (int j = 0; j < n; ++j) {
-                        const float send = up ? o[j] : o[j + n];
-                        o[j] = (up ? o[j + n] : o[j]) + __shfl_xor_sync(kFull, send, lanes);
+                        const float send = up ? o[q][j] : o[q][j + n];
+                        o[q][j] = (up ? o[q][j + n] : o[q][j]) + __shfl_xor_sync(kFull, send, lanes);
                     }
-                    if (up) col += n;
-                }
-                if (kLanes == 16) o[0] += __shfl_xor_sync(kFull, o[0], 1);
-                if (kLanes == 8 || !(dl & 1)) os[r][8 * eg + col] = o[0];
+                if (up) col += n;
             }
-        }
+#pragma unroll
+            for (int q = 0; q < kU; ++q) {
+#pragma unroll
+                for (int n = kLanes / 16; n; n >>= 1) o[q][0] += __shfl_xor_sync(kFull, o[q][0], n);
+                if (dl % (kLanes / 8) == 0) os[r0 + q][8 * eg + col] = o[q][0];
+            }
+        };
+        int r = 0;
+#pragma unroll 1
+        for (; r + 2 <= nr; r += 2) tokens(r, std::integral_constant<int, 2>{});
+        if (r < nr) tokens(r, std::integral_constant<int, 1>{});
         __syncthreads();
         if (OUT)
-            for (int i = tid; i < nr * kCols; i += KD)
-                O[row_of(i / kCols) * p.vd + e0 + i % kCols] = from_f32<T>(os[i / kCols][i % kCols]);
+            for (int i = tid; i < nr * kCols; i += kThreads)
+                O[row_of(tb + i / kCols) * vd + e0 + i % kCols] = from_f32<T>(os[i / kCols][i % kCols]);
     }
-    float *to = decay_state_out(p, seg, g.H, h);
+    float *to = decay_state_out(p, seg, H, h);
     if (!to) return;
-    if (ntok > 0) decay(DecayFactor(gd * (float)((nb > 1 ? (ntok - 1) % kTb : 0) + (REV ? 1 : 0))));
+    if (ntok > 0) decay(DecayFactor(gd * (float)((nb > 1 ? (ntok - 1) % kTb : 0) + (rev ? 1 : 0))));
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-        const int d = 4 * dl + (u & 3) + (u >> 2) * (KD / 2);
+    for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int e = e0 + 8 * eg + j;
-            to[p.transposed ? (int64_t)e * KD + d : (int64_t)d * p.vd + e] = s[u][j];
+            const int d = 4 * dl + u, e = e0 + 8 * eg + j;
+            to[p.transposed ? e * KD + d : d * vd + e] = s[u][j];
         }
-    }
 }
 
 // A few tokens of every sequence, the state updated in place.  A block owns 64 columns of
@@ -221,7 +308,8 @@ decay_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
 // state that enters the next segment, written over the sum.  A block takes 1024 elements
 // of one (sequence, head).
 __global__ void __launch_bounds__(256)
-decay_combine_kernel(const DecayGeom g, const DecayPass p) {
+decay_combine_kernel(const DecayGeom g, const __grid_constant__ Passes passes) {
+    const DecayPass &p = passes.p[blockIdx.y];
     const int64_t st = (int64_t)p.kd * p.vd;
     const int parts = (int)(st / 1024);
     const int64_t at = (blockIdx.x % parts) * 1024 + 4 * threadIdx.x;
@@ -253,22 +341,35 @@ decay_combine_kernel(const DecayGeom g, const DecayPass p) {
     }
 }
 
+Passes packed(const DecayPass *p, int n) {
+    Passes a{};
+    std::copy(p, p + n, a.p);
+    return a;
+}
+
+// One launch per key width among the passes.
 template <typename T, int KD>
-cudaError_t rec_t(const DecayGeom &g, const DecayPass &p, cudaStream_t stream) {
-    const int64_t blocks = g.max_segs * g.H * (p.vd / kCols);
+cudaError_t rec_t(const DecayGeom &g, const DecayPass *p, int n, cudaStream_t stream) {
+    DecayPass mine[kDecayMaxPasses];
+    int k = 0, vd = 0;
+    for (int i = 0; i < n; ++i)
+        if (p[i].kd == KD) {
+            mine[k++] = p[i];
+            vd = std::max(vd, p[i].vd);
+        }
+    const int64_t blocks = g.max_segs * g.H * (vd / kCols);
+    if (k == 0 || blocks == 0) return cudaSuccess;
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
-    if (blocks == 0) return cudaSuccess;
-    ProfScope prof(stream, p.local ? "decay_rec_kernel (local)" : "decay_rec_kernel");
-    const unsigned n = (unsigned)blocks;
-    if (!p.local) {
-        if (p.rev) decay_rec_kernel<T, KD, true, true><<<n, KD, 0, stream>>>(g, p);
-        else decay_rec_kernel<T, KD, false, true><<<n, KD, 0, stream>>>(g, p);
-    } else {
-        if (p.rev) decay_rec_kernel<T, KD, true, false><<<n, KD, 0, stream>>>(g, p);
-        else decay_rec_kernel<T, KD, false, false><<<n, KD, 0, stream>>>(g, p);
-    }
+    ProfScope prof(stream, p[0].local ? "decay_rec_kernel (local)" : "decay_rec_kernel");
+    auto kern = p[0].local ? decay_rec_kernel<T, KD, false> : decay_rec_kernel<T, KD, true>;
+    kern<<<dim3((unsigned)blocks, (unsigned)k), 2 * KD, 0, stream>>>(g, packed(mine, k));
     count_launch();
     return cudaGetLastError();
+}
+template <typename T>
+cudaError_t rec_all(const DecayGeom &g, const DecayPass *p, int n, cudaStream_t stream) {
+    const cudaError_t err = rec_t<T, 128>(g, p, n, stream);
+    return err == cudaSuccess ? rec_t<T, 64>(g, p, n, stream) : err;
 }
 
 template <typename T>
@@ -293,17 +394,26 @@ cudaError_t launch_decay_step(const void *q, const void *k, const void *v, const
                              : step_t<float>(q, k, v, log_decay, state, out, N, T, H, dk, dv, scale, stream);
 }
 
-cudaError_t launch_decay_rec(const DecayGeom &g, const DecayPass &p, gdr_dtype_t dtype, cudaStream_t stream) {
-    if (dtype == GDR_BF16)
-        return p.kd == 128 ? rec_t<__nv_bfloat16, 128>(g, p, stream) : rec_t<__nv_bfloat16, 64>(g, p, stream);
-    return p.kd == 128 ? rec_t<float, 128>(g, p, stream) : rec_t<float, 64>(g, p, stream);
+cudaError_t launch_decay_rec(const DecayGeom &g, const DecayPass *passes, int n, gdr_dtype_t dtype,
+                             cudaStream_t stream) {
+    if (n < 1 || n > kDecayMaxPasses) return cudaErrorInvalidValue;
+    return dtype == GDR_BF16 ? rec_all<__nv_bfloat16>(g, passes, n, stream) : rec_all<float>(g, passes, n, stream);
 }
 
-cudaError_t launch_decay_combine(const DecayGeom &g, const DecayPass &p, cudaStream_t stream) {
-    const int64_t blocks = (int64_t)g.N * g.H * ((int64_t)p.kd * p.vd / 1024);
-    if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+cudaError_t launch_decay_combine(const DecayGeom &g, const DecayPass *passes, int n, cudaStream_t stream) {
+    const int64_t blocks = (int64_t)g.N * g.H * ((int64_t)passes[0].kd * passes[0].vd / 1024);
+    if (blocks > 0x7fffffff || n < 1 || n > kDecayMaxPasses) return cudaErrorInvalidValue;
     ProfScope prof(stream, "decay_combine_kernel");
-    decay_combine_kernel<<<(unsigned)blocks, 256, 0, stream>>>(g, p);
+    decay_combine_kernel<<<dim3((unsigned)blocks, (unsigned)n), 256, 0, stream>>>(g, packed(passes, n));
+    count_launch();
+    return cudaGetLastError();
+}
+
+cudaError_t launch_decay_plan(const int32_t *cu_seqlens, const DecayGeom &g, int64_t *seq_start, int64_t *seg_base,
+                              unsigned long long *next, int *status, cudaStream_t stream) {
+    ProfScope prof(stream, "decay_plan_kernel");
+    decay_plan_kernel<<<1, 1024, 0, stream>>>(cu_seqlens, g.N, g.T_total, g.seg_tokens, seq_start, seg_base, next,
+                                              status);
     count_launch();
     return cudaGetLastError();
 }

@@ -129,18 +129,26 @@ __device__ __forceinline__ float *decay_state_out(const DecayPass &p, const Deca
 }
 #endif
 
-// Token by token on the CUDA cores (gdr_decay.cu): any dtype, kd and vd in {64, 128}.
-cudaError_t launch_decay_rec(const DecayGeom &g, const DecayPass &p, gdr_dtype_t dtype, cudaStream_t stream);
+constexpr int kDecayMaxPasses = 3;
+
+// The plan of packed input: seq_start and seg_base of g.p (N + 1 each) from the offsets,
+// which it validates, and the two unit counters zeroed (gdr_decay.cu).
+cudaError_t launch_decay_plan(const int32_t *cu_seqlens, const DecayGeom &g, int64_t *seq_start, int64_t *seg_base,
+                              unsigned long long *next, int *status, cudaStream_t stream);
+// Token by token on the CUDA cores (gdr_decay.cu): any dtype, kd and vd in {64, 128}; n
+// independent passes, all local or all not.
+cudaError_t launch_decay_rec(const DecayGeom &g, const DecayPass *passes, int n, gdr_dtype_t dtype,
+                             cudaStream_t stream);
 // T tokens of N sequences, the state [N, H, dk, dv] updated in place (gdr_decay.cu).
 cudaError_t launch_decay_step(const void *q, const void *k, const void *v, const float *log_decay, float *state,
                               void *out, gdr_dtype_t dtype, int N, int64_t T, int H, int dk, int dv, float scale,
                               cudaStream_t stream);
 // On the tensor cores (gdr_decay_tc.cu): bf16, token tensors 16-byte aligned, fewer than
 // 2^31 - 128 token rows.  Passes of one launch are independent and all local or all not.
-// `next`: a zeroed counter that hands out the units, or null (units of equal length).
+// `next`: a zeroed counter that hands out the units, or null (few units of equal length).
 cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, int sms, unsigned long long *next,
                             int *status, cudaStream_t stream);
-// Chains the local sums in `slots` into boundary states, from s0 (null: zero).
-cudaError_t launch_decay_combine(const DecayGeom &g, const DecayPass &p, cudaStream_t stream);
+// Chains the local sums in `slots` of n passes into boundary states, from s0 (null: zero).
+cudaError_t launch_decay_combine(const DecayGeom &g, const DecayPass *passes, int n, cudaStream_t stream);
 
 }  // namespace gdr

@@ -64,7 +64,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kC = kDecayTile;
-constexpr int kMaxPasses = 3;
+constexpr int kMaxPasses = kDecayMaxPasses;
 constexpr uint32_t kBox = kC * 128;        // 64 columns x 128 tokens, 128-byte rows, swizzled
 constexpr uint32_t kTile = 2 * kBox;       // one tensor's tile: up to two boxes
 constexpr unsigned kFull = 0xffffffffu;
@@ -80,6 +80,7 @@ struct TcArgs {
     int npass;
     int64_t units;      // max_segs * H * npass
     unsigned long long *next;   // the next unit to take, or null: units by stride
+    bool long_first;            // the counter runs over all units twice
     int *status;
     uint64_t wait_ns;
 };
@@ -137,20 +138,28 @@ __device__ __forceinline__ bool unit_of(const TcArgs &A, int64_t u, bool local, 
     o.to = decay_state_out(p, seg, A.g.H, o.h);
     return GDR_INBOUNDS(seg.t0 >= 0 && seg.t1 <= A.g.T_total && seg.slot <= A.g.max_slots);
 }
-// The block's next unit (one warp): those of its stride, or whatever comes next; false at
-// the end.  `n`: the last one (blockIdx.x - gridDim.x at the start).
+// The block's next unit (one warp): those of its stride, or from the counter.  Where there are
+// not very many the counter runs over all twice -- those of more than half a segment's tiles
+// first, then the others, so that the blocks end together.  False at the end.  `n`: the last one (blockIdx.x -
+// gridDim.x at the start).
 __device__ __forceinline__ bool take_unit(const TcArgs &A, bool local, int64_t &n, Unit &u) {
-    do {
+    while (true) {
+        bool want_long = false;
+        int64_t i;
         if (A.next) {
             unsigned long long x = 0;
             if ((threadIdx.x & 31) == 0) x = atomicAdd(A.next, 1ull);
-            n = (int64_t)__shfl_sync(kFull, x, 0);
+            i = (int64_t)__shfl_sync(kFull, x, 0);
+            want_long = A.long_first && i < A.units;
+            if (A.long_first && !want_long) i -= A.units;
         } else {
-            n += gridDim.x;
+            i = n += gridDim.x;
         }
-        if (n >= A.units) return false;
-    } while (!unit_of(A, n, local, u));
-    return true;
+        if (i >= A.units) return false;
+        if (unit_of(A, i, local, u) &&
+            (!A.long_first || (2 * (int64_t)u.tiles * kC > A.g.seg_tokens) == want_long))
+            return true;
+    }
 }
 // The tiles of a unit in the order of its pass, in registers: a role's loop reads neither
 // shared memory nor parameters for its bookkeeping.
@@ -821,28 +830,28 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
 // the local pass: each segment's own writes, decayed to its end
 // ---------------------------------------------------------------------------
 // Every write's weight is its distance to the segment's end, so the accumulator needs no
-// decay on the way: the tensor cores sum C'^T B over all tiles.  The two groups of four
-// warps take the tiles in turn, each with its own buffer of C' in TMEM.
-constexpr int kLocThreads = 32 * 10, kLocProducer = 8, kLocIssuer = 9;     // warps
+// decay on the way: the tensor cores sum C'^T B over all tiles.  Four groups of four warps
+// take 32 tokens of a tile each, with slots of C' in TMEM for two tiles.
+constexpr int kLocThreads = 32 * 18, kLocProducer = 16, kLocIssuer = 17;   // warps
 constexpr int kLocStages = 3;
 constexpr uint32_t kLocStage = 2 * kTile;                    // B, C
 constexpr uint32_t kLocOffBar = kLocStages * kLocStage;
-constexpr uint32_t kLocOffW = kLocOffBar + 256;              // weights, a copy per warp
-constexpr uint32_t kLocOffRing = kLocOffW + 8 * kC * 4;
+constexpr uint32_t kLocOffW = kLocOffBar + 320;              // weights, a copy per warp
+constexpr uint32_t kLocOffRing = kLocOffW + 16 * 32 * 4;
 constexpr uint32_t kSmemLocal = kLocOffRing + kRing * sizeof(Unit);
-constexpr uint32_t kLocColV = 128;                           // two buffers of a tile each
+constexpr uint32_t kLocColV = 128;                           // a tile's slots, twice
 static_assert(kLocColV + 2 * kParts * kSlotCols <= kTmemCols, "TMEM");
 
 struct LocalBars {
-    uint64_t u_full[kRing], u_free[kRing];   // a unit announced / done with (9 warps)
+    uint64_t u_full[kRing], u_free[kRing];   // a unit announced / done with (17 warps)
     uint64_t full[kLocStages], free[kLocStages];
-    uint64_t v_ready[2], v_free[2];
+    uint64_t v_ready[2 * kParts], v_free[2 * kParts];
     uint64_t h_full, h_free;   // a unit's sum complete / read
     uint64_t fin;
     uint32_t tmem;
     int stop;
 };
-static_assert(sizeof(LocalBars) <= 256, "barriers");
+static_assert(sizeof(LocalBars) <= 320, "barriers");
 
 __global__ void __launch_bounds__(kLocThreads, 1)
 decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs A) {
@@ -855,13 +864,13 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
     if (tid == 0) {
         for (uint32_t i = 0; i < kRing; ++i) {
             mbar_init(&bar.u_full[i], 1);
-            mbar_init(&bar.u_free[i], 9);
+            mbar_init(&bar.u_free[i], 17);
         }
         for (int i = 0; i < kLocStages; ++i) {
             mbar_init(&bar.full[i], 1);
             mbar_init(&bar.free[i], 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (uint32_t i = 0; i < 2 * kParts; ++i) {
             mbar_init(&bar.v_ready[i], 4);
             mbar_init(&bar.v_free[i], 1);
         }
@@ -945,20 +954,22 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
-                if (!(ok = wait(&bar.v_ready[buf], it >> 1))) break;
                 tc_fence_after();
                 const uint64_t dBt = smem_desc(s0 + st * kLocStage, kBox, 1024, kSw128);
-#pragma unroll 1
+#pragma unroll
                 for (uint32_t k = 0; k < kParts; ++k) {
-                    const uint32_t av = tm + kLocColV + (buf * kParts + k) * kSlotCols;
+                    const uint32_t slot = buf * kParts + k, av = tm + kLocColV + slot * kSlotCols;
+                    if (!(ok = wait(&bar.v_ready[slot], it >> 1))) break;
+                    tc_fence_after();
 #pragma unroll
                     for (uint32_t term = 0; term < 3; ++term)
 #pragma unroll
                         for (uint32_t j = 0; j < 2; ++j)
                             mma_f16_ts_if(lead, tm, av + term * 16 + j * 8, dBt + ((k * 4096 + j * 2048) >> 4), id_h,
                                           i + k + term + j > 0);
+                    mma_commit_if(lead, &bar.v_free[slot]);
                 }
-                mma_commit_if(lead, &bar.v_free[buf]);
+                if (!ok) break;
                 mma_commit_if(lead, &bar.free[st]);
                 if (i == walk.tiles - 1) mma_commit_if(lead, &bar.h_full);
             }
@@ -970,7 +981,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
     } else {
         const int grp = warp >> 2, e = tid & 127;
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
-        float *w = (float *)(smem + kLocOffW) + warp * kC;
+        float *w = (float *)(smem + kLocOffW) + warp * 32;
         each_unit([&](const Unit &u) {
             bool ok = true;
             const DecayPass &p = A.pass[u.pass];
@@ -986,32 +997,29 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
             }
             for (int i = 0; i < walk.tiles; ++i, ++it) {
                 const uint32_t st = it % kLocStages, buf = it & 1;
-                if (buf != (uint32_t)grp) continue;
+                const uint32_t slot = buf * kParts + grp;
                 const int len = walk.len(i);
                 const uint32_t use = it >> 1;
                 // past the tile: its distance to the segment's end (its start, reversed)
                 const int64_t past = rev ? (int64_t)(walk.tiles - 1 - i) * kC : tokens - (int64_t)i * kC - len;
                 __syncwarp();   // the last tile's weights are read
-#pragma unroll
-                for (int k = 0; k < kC / 32; ++k)
-                    w[lane + 32 * k] = token_weight(lane + 32 * k, len, rev, gd, s_upd, past);
+                w[lane] = token_weight(32 * grp + lane, len, rev, gd, s_upd, past);
                 __syncwarp();
                 if (!(ok = wait(&bar.full[st], it / kLocStages))) break;
-                if (use && !(ok = wait(&bar.v_free[buf], use - 1))) break;
+                if (use && !(ok = wait(&bar.v_free[slot], use - 1))) break;
                 tc_fence_after();
                 uint8_t *ct = smem + st * kLocStage + kTile;
-                if (len < kC && any) {
+                if (len < kC && any) {   // all groups the same zeros
                     zero_columns(ct, e & ~31, len, lane);
                     __syncwarp();
                 }
 #pragma unroll 1
-                for (uint32_t k = 0; k < 2 * kParts; ++k)
-                    write_terms(lanes + kLocColV + (buf * kParts + k / 2) * kSlotCols + 8 * (k & 1), ct, e, any, k,
-                                w + 16 * k);
+                for (uint32_t k = 0; k < 2; ++k)
+                    write_terms(lanes + kLocColV + slot * kSlotCols + 8 * k, ct, e, any, 2 * grp + k, w + 16 * k);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.v_ready[buf]);
+                if (lane == 0) mbar_arrive(&bar.v_ready[slot]);
             }
             if (ok && grp == 0) {
                 if (!(ok = wait(&bar.h_full, nu))) return false;
@@ -1057,6 +1065,7 @@ cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, 
     args.npass = n;
     args.units = g.max_segs * g.H * n;
     args.next = next;
+    args.long_first = next && args.units <= 64 * (int64_t)sms;   // a look at a unit costs some 0.3 us
     args.status = status;
     args.wait_ns = kWaitNs;
     if (const char *w = std::getenv("GDR_TC_WAIT_NS")) {   // test hook: shorter pipeline waits
