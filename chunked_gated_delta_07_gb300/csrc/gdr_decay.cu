@@ -245,7 +245,9 @@ decay_rec_kernel(const DecayGeom g, const __grid_constant__ Passes passes) {
 // A few tokens of every sequence, the state updated in place.  A block owns 64 columns of
 // one (sequence, head)'s state: 256 threads hold kd / 16 rows x 4 columns each as float4,
 // all loaded before anything else (32 KB a block in flight at kd = 128), so that the
-// pass is bound by the state's traffic, 2 x 4 kd vd bytes.  Sums over kd: a shuffle, then
+// pass is bound by the state's traffic, 2 x 4 kd vd bytes.  The states go back with the
+// evict-first policy: 256 sequences' of 16 heads are twice the L2, and plain stores push out
+// lines that are still to be read (98.8 us against 80.8).  Sums over kd: a shuffle, then
 // the 8 warps' partial sums through shared memory.
 template <typename T, int KD>
 __global__ void __launch_bounds__(256)
@@ -288,7 +290,7 @@ decay_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
         }
         if (t == Tn - 1)
 #pragma unroll
-            for (int u = 0; u < kRows; ++u) S[(int64_t)4 * u * vd] = s[u];
+            for (int u = 0; u < kRows; ++u) __stcs(&S[(int64_t)4 * u * vd], s[u]);
         o.x += __shfl_xor_sync(0xffffffffu, o.x, 16);
         o.y += __shfl_xor_sync(0xffffffffu, o.y, 16);
         o.z += __shfl_xor_sync(0xffffffffu, o.z, 16);
