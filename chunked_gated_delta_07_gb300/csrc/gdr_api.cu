@@ -670,17 +670,17 @@ cudaError_t decay_run(const DecayGeom &g, const DecayPass *chains, int nchains, 
                       cudaStream_t stream) {
     unsigned long long *next =
         !g.dense || g.max_slots > 0 ? (unsigned long long *)(ws + L.next) : nullptr;
-    auto run = [&](const DecayPass *p, int k) {
-        return tc ? launch_decay_tc(g, p, k, ctx->sms, next ? next + (p->local ? 1 : 0) : nullptr, ctx->d_status,
-                                    stream)
-                  : launch_decay_rec(g, p, k, dtype, stream);
+    auto run = [&](const DecayPass *p, int k, bool early) {
+        return tc ? launch_decay_tc(g, p, k, ctx->sms, next ? next + (p->local ? 1 : 0) : nullptr, early,
+                                    ctx->d_status, stream)
+                  : launch_decay_rec(g, p, k, dtype, early, stream);
     };
     if (g.max_slots > 0) {
-        cudaError_t err = run(chains, nchains);
+        cudaError_t err = run(chains, nchains, !g.dense);
         if (err == cudaSuccess) err = launch_decay_combine(g, chains, nchains, stream);
         if (err != cudaSuccess) return err;
     }
-    return run(passes, n);
+    return run(passes, n, !g.dense || g.max_slots > 0);
 }
 
 // Scratch of a call: the caller's workspace, or the internal cache grown to size.
@@ -1126,13 +1126,13 @@ gdr_status_t gdr_decay_fwd(const void *q, const void *k, const void *v, const fl
     const DecayLayout L = decay_layout(s, g, false);
     char *ws;
     if ((st = take_workspace(ctx, workspace, workspace_bytes, L.total, &ws)) != GDR_OK) return st;
-    if ((st = decay_plan(&g, cu_seqlens, log_decay, ws, L, ctx->d_status, stream)) != GDR_OK) return st;
     if (hT && hT == h0 && g.max_slots > 0) {
         // one CTA may read a sequence's entering state after another has written its last
         if (cudaMemcpyAsync(ws + L.copy, h0, nst, cudaMemcpyDeviceToDevice, stream) != cudaSuccess)
             return GDR_ERR_CUDA;
         h0 = (const float *)(ws + L.copy);
     }
+    if ((st = decay_plan(&g, cu_seqlens, log_decay, ws, L, ctx->d_status, stream)) != GDR_OK) return st;
     float *slots = (float *)(ws + L.slots);
     const DecayPass chain{nullptr, k, v, nullptr, h0, nullptr, slots, dk, dv, false, false, true, 1.f, 1.f};
     const DecayPass pass{q, k, v, out, h0, hT, slots, dk, dv, false, false, false, 1.f, scale};
@@ -1218,7 +1218,7 @@ gdr_status_t gdr_decay_recurrent_fwd(const void *q, const void *k, const void *v
     g.max_segs = N;
     g.log_decay = log_decay;
     const DecayPass pass{q, k, v, out, state, state, nullptr, dk, dv, false, false, false, 1.f, scale};
-    return launch_decay_rec(g, &pass, 1, dtype, (cudaStream_t)stream) == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+    return launch_decay_rec(g, &pass, 1, dtype, false, (cudaStream_t)stream) == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
 }
 
 gdr_status_t gdr_layer_norm_fwd(const void *x, const float *weight, const float *bias, void *y, float *mean,

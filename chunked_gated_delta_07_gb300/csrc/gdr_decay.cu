@@ -26,6 +26,7 @@ decay_plan_kernel(const int32_t *__restrict__ cu, int N, int64_t T_total, int64_
                   int64_t *__restrict__ seq_start, int64_t *__restrict__ seg_base, unsigned long long *next,
                   int *status) {
     __shared__ int64_t sums[32];
+    let_next_start();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (N + 1023) / 1024, n0 = min(N, tid * per), n1 = min(N, n0 + per);
     auto segments = [&](int64_t len) { return len > seg_tokens ? (len + seg_tokens - 1) / seg_tokens : 1; };
@@ -82,6 +83,8 @@ decay_rec_kernel(const DecayGeom g, const __grid_constant__ Passes passes) {
     __shared__ __align__(16) float cs[kTb][kCols];
     __shared__ float os[OUT ? kTb : 1][kCols];
     __shared__ float pw[kTb][2];   // lam^j, lam^-j
+    let_next_start();
+    after_previous();
     const int vd = p.vd, slices = vd / kCols, H = g.H;
     if (blockIdx.x >= g.max_segs * H * slices) return;   // of a wider pass
     const int e0 = (int)(blockIdx.x % slices) * kCols;
@@ -311,6 +314,8 @@ decay_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
 // of one (sequence, head).
 __global__ void __launch_bounds__(256)
 decay_combine_kernel(const DecayGeom g, const __grid_constant__ Passes passes) {
+    let_next_start();
+    after_previous();
     const DecayPass &p = passes.p[blockIdx.y];
     const int64_t st = (int64_t)p.kd * p.vd;
     const int parts = (int)(st / 1024);
@@ -351,7 +356,7 @@ Passes packed(const DecayPass *p, int n) {
 
 // One launch per key width among the passes.
 template <typename T, int KD>
-cudaError_t rec_t(const DecayGeom &g, const DecayPass *p, int n, cudaStream_t stream) {
+cudaError_t rec_t(const DecayGeom &g, const DecayPass *p, int n, bool early, cudaStream_t stream) {
     DecayPass mine[kDecayMaxPasses];
     int k = 0, vd = 0;
     for (int i = 0; i < n; ++i)
@@ -364,14 +369,17 @@ cudaError_t rec_t(const DecayGeom &g, const DecayPass *p, int n, cudaStream_t st
     if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
     ProfScope prof(stream, p[0].local ? "decay_rec_kernel (local)" : "decay_rec_kernel");
     auto kern = p[0].local ? decay_rec_kernel<T, KD, false> : decay_rec_kernel<T, KD, true>;
-    kern<<<dim3((unsigned)blocks, (unsigned)k), 2 * KD, 0, stream>>>(g, packed(mine, k));
+    const cudaError_t err = launch_early(early, kern, dim3((unsigned)blocks, (unsigned)k), 2 * KD, 0, stream, g,
+                                         packed(mine, k));
     count_launch();
-    return cudaGetLastError();
+    return err;
 }
 template <typename T>
-cudaError_t rec_all(const DecayGeom &g, const DecayPass *p, int n, cudaStream_t stream) {
-    const cudaError_t err = rec_t<T, 128>(g, p, n, stream);
-    return err == cudaSuccess ? rec_t<T, 64>(g, p, n, stream) : err;
+cudaError_t rec_all(const DecayGeom &g, const DecayPass *p, int n, bool early, cudaStream_t stream) {
+    // a call's two launches are independent, but the next kernel waits for the second one only
+    const bool both = std::any_of(p, p + n, [&](const DecayPass &q) { return q.kd != p[0].kd; });
+    const cudaError_t err = rec_t<T, 128>(g, p, n, early, stream);
+    return err == cudaSuccess ? rec_t<T, 64>(g, p, n, early && !both, stream) : err;
 }
 
 template <typename T>
@@ -396,19 +404,21 @@ cudaError_t launch_decay_step(const void *q, const void *k, const void *v, const
                              : step_t<float>(q, k, v, log_decay, state, out, N, T, H, dk, dv, scale, stream);
 }
 
-cudaError_t launch_decay_rec(const DecayGeom &g, const DecayPass *passes, int n, gdr_dtype_t dtype,
+cudaError_t launch_decay_rec(const DecayGeom &g, const DecayPass *passes, int n, gdr_dtype_t dtype, bool early,
                              cudaStream_t stream) {
     if (n < 1 || n > kDecayMaxPasses) return cudaErrorInvalidValue;
-    return dtype == GDR_BF16 ? rec_all<__nv_bfloat16>(g, passes, n, stream) : rec_all<float>(g, passes, n, stream);
+    return dtype == GDR_BF16 ? rec_all<__nv_bfloat16>(g, passes, n, early, stream)
+                             : rec_all<float>(g, passes, n, early, stream);
 }
 
 cudaError_t launch_decay_combine(const DecayGeom &g, const DecayPass *passes, int n, cudaStream_t stream) {
     const int64_t blocks = (int64_t)g.N * g.H * ((int64_t)passes[0].kd * passes[0].vd / 1024);
     if (blocks > 0x7fffffff || n < 1 || n > kDecayMaxPasses) return cudaErrorInvalidValue;
     ProfScope prof(stream, "decay_combine_kernel");
-    decay_combine_kernel<<<dim3((unsigned)blocks, (unsigned)n), 256, 0, stream>>>(g, packed(passes, n));
+    const cudaError_t err = launch_early(true, decay_combine_kernel, dim3((unsigned)blocks, (unsigned)n), 256, 0,
+                                         stream, g, packed(passes, n));
     count_launch();
-    return cudaGetLastError();
+    return err;
 }
 
 cudaError_t launch_decay_plan(const int32_t *cu_seqlens, const DecayGeom &g, int64_t *seq_start, int64_t *seg_base,

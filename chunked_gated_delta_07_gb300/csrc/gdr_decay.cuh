@@ -136,8 +136,9 @@ constexpr int kDecayMaxPasses = 3;
 cudaError_t launch_decay_plan(const int32_t *cu_seqlens, const DecayGeom &g, int64_t *seq_start, int64_t *seg_base,
                               unsigned long long *next, int *status, cudaStream_t stream);
 // Token by token on the CUDA cores (gdr_decay.cu): any dtype, kd and vd in {64, 128}; n
-// independent passes, all local or all not.
-cudaError_t launch_decay_rec(const DecayGeom &g, const DecayPass *passes, int n, gdr_dtype_t dtype,
+// independent passes, all local or all not.  `early`: the kernel before it in the stream is
+// the same call's.
+cudaError_t launch_decay_rec(const DecayGeom &g, const DecayPass *passes, int n, gdr_dtype_t dtype, bool early,
                              cudaStream_t stream);
 // T tokens of N sequences, the state [N, H, dk, dv] updated in place (gdr_decay.cu).
 cudaError_t launch_decay_step(const void *q, const void *k, const void *v, const float *log_decay, float *state,
@@ -147,7 +148,7 @@ cudaError_t launch_decay_step(const void *q, const void *k, const void *v, const
 // 2^31 - 128 token rows.  Passes of one launch are independent and all local or all not.
 // `next`: a zeroed counter that hands out the units, or null (few units of equal length).
 cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, int sms, unsigned long long *next,
-                            int *status, cudaStream_t stream);
+                            bool early, int *status, cudaStream_t stream);
 // Chains the local sums in `slots` of n passes into boundary states, from s0 (null: zero).
 cudaError_t launch_decay_combine(const DecayGeom &g, const DecayPass *passes, int n, cudaStream_t stream);
 

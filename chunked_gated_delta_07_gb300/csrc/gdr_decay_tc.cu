@@ -399,6 +399,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
     const int H = A.g.H;
     if (!GDR_INBOUNDS((smem_u32(smem) & 1023u) == 0)) return;   // swizzled tiles start on 1 KB
 
+    let_next_start();
     if (tid == 0) {
         for (uint32_t i = 0; i < kRing; ++i) {
             mbar_init(&bar.u_full[i], 1);
@@ -433,6 +434,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    after_previous();
     const uint32_t tm = bar.tmem;
 
     auto wait = [&](uint64_t *b, uint32_t use) { return wait_use(b, use, A.wait_ns, stop, A.status); };
@@ -861,6 +863,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
     volatile int *stop = &bar.stop;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (!GDR_INBOUNDS((smem_u32(smem) & 1023u) == 0)) return;   // swizzled tiles start on 1 KB
+    let_next_start();
     if (tid == 0) {
         for (uint32_t i = 0; i < kRing; ++i) {
             mbar_init(&bar.u_full[i], 1);
@@ -888,6 +891,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    after_previous();
     const uint32_t tm = bar.tmem;
     auto wait = [&](uint64_t *b, uint32_t use) { return wait_use(b, use, A.wait_ns, stop, A.status); };
     uint32_t it = 0, nu = 0;   // tiles and units so far
@@ -1047,7 +1051,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
 }  // namespace
 
 cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, int sms, unsigned long long *next,
-                            int *status, cudaStream_t stream) {
+                            bool early, int *status, cudaStream_t stream) {
     if (n < 1 || n > kMaxPasses) return cudaErrorInvalidValue;
     const bool local = passes[0].local;
     TcMaps maps{};
@@ -1079,9 +1083,10 @@ cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, 
     const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (err != cudaSuccess) return err;
     ProfScope prof(stream, local ? "decay_local_kernel" : "decay_out_kernel");
-    kern<<<(unsigned)std::min<int64_t>(args.units, sms), local ? kLocThreads : kOutThreads, bytes, stream>>>(maps, args);
+    const cudaError_t run = launch_early(early, kern, dim3((unsigned)std::min<int64_t>(args.units, sms)),
+                                         local ? kLocThreads : kOutThreads, (size_t)bytes, stream, maps, args);
     count_launch();
-    return cudaGetLastError();
+    return run;
 }
 
 }  // namespace gdr

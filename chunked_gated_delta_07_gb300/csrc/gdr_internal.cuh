@@ -194,6 +194,28 @@ cudaError_t launch_router_topk(const void *logits, const float *bias, int32_t *i
 cudaError_t launch_router_update(const int64_t *load, float *bias, double *thr, int E, int mode,
                                  double q_lo, double q_hi, float eta, cudaStream_t stream);
 
+// Kernels of one call that follow each other may be launched early: the next one's blocks
+// start once every block of the one before has called let_next_start() (or ended), and wait
+// in after_previous() until that one is complete and its writes visible.  A kernel launched
+// early calls after_previous() in every thread before anything else it could end by.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_early(bool early, void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t stream,
+                         A... args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // layer norm over the last axis (gdr_norm.cu); `sms` sizes the grids
 constexpr int kNormMaxD = 16384;
 size_t norm_bwd_scratch_bytes(int64_t rows, int G, int D, gdr_dtype_t dtype, int sms);

@@ -230,7 +230,7 @@ norm_fwd_kernel(const T *x, const float *__restrict__ w, const float *__restrict
                 if ((v * TPR + lane) * VEC < s.D) sq[0] = fmaf(xv[v][i], xv[v][i], sq[0]);
             }
         row_sum<TPR, 1>(sq, red, turn);
-        const float rs = 1.f / sqrtf(sq[0] * s.inv_d + s.eps);
+        const float rs = rsqrtf(sq[0] * s.inv_d + s.eps);   // within 2^-22 of its value
         if (on) {
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
@@ -255,6 +255,7 @@ norm_bwd_kernel(const T *dy, const T *x, const float *__restrict__ mean, const f
                 const float *__restrict__ w, T *dx, float *__restrict__ part, NormShape s) {
     constexpr int kThreads = bwd_threads<TPR>();
     __shared__ float red[2][2][32];
+    let_next_start();
     int turn = 0;
     const int sub = threadIdx.x / TPR, lane = threadIdx.x % TPR;
     const int gi = sub % s.gpb, ri = sub / s.gpb;
@@ -379,6 +380,7 @@ __global__ void __launch_bounds__(1024)
 norm_sum_kernel(const float *__restrict__ part, float *__restrict__ dw, float *__restrict__ db, int nb,
                 int64_t gd) {
     __shared__ float sm[32][33];
+    after_previous();
     float *out = blockIdx.y ? db : dw;
     if (!out) return;
     const int col = threadIdx.x & 31, sl = threadIdx.x >> 5;
@@ -509,9 +511,10 @@ cudaError_t bwd_t(const void *dy, const void *x, const float *mean, const float 
     if (err != cudaSuccess || !part) return err;
     const int64_t gd = (int64_t)G * D;
     ProfScope prof(stream, "norm_sum_kernel");
-    norm_sum_kernel<<<dim3((unsigned)((gd + 31) / 32), 2), 1024, 0, stream>>>(part, dw, db, (int)n.grid.x, gd);
+    const cudaError_t sum = launch_early(true, norm_sum_kernel, dim3((unsigned)((gd + 31) / 32), 2), 1024, 0, stream,
+                                         (const float *)part, dw, db, (int)n.grid.x, gd);
     count_launch();
-    return cudaGetLastError();
+    return sum;
 }
 
 }  // namespace
