@@ -254,36 +254,29 @@ __device__ __forceinline__ uint32_t pack2(uint64_t y) {
 // at + 32 (a whole warp): the weighted values x w as the bf16 terms hi + mid + lo = x w exactly, cut
 // off the top of the fp32 product 8 significant bits at a time; a column holds two tokens.
 // w: the 16 weights.
-__device__ __forceinline__ void write_terms(uint32_t at, const uint8_t *tile, int e, bool any, int k,
-                                            const float *w) {
+__device__ __forceinline__ void write_terms(uint32_t at, const uint8_t *tile, int e, int k, const float *w) {
     uint32_t hi[8], mid[8], lo[8];
-    if (any) {
-        const uint8_t *col = tile + (e >> 6) * kBox + (e & 7) * 2 + k * 2048;
-        const uint32_t chunk = (e & 63) >> 3;
+    const uint8_t *col = tile + (e >> 6) * kBox + (e & 7) * 2 + k * 2048;
+    const uint32_t chunk = (e & 63) >> 3;
 #pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-            const ulonglong2 w4 = *(const ulonglong2 *)&w[2 * i];
+    for (int i = 0; i < 8; i += 2) {
+        const ulonglong2 w4 = *(const ulonglong2 *)&w[2 * i];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                uint32_t x[2];
+        for (int j = 0; j < 2; ++j) {
+            uint32_t x[2];
 #pragma unroll
-                for (int l = 0; l < 2; ++l) {
-                    const int r = 2 * (i + j) + l;
-                    const uint32_t at16 = (r >> 3) * 1024 + (r & 7) * 128 + ((chunk ^ (r & 7)) << 4);
-                    x[l] = (uint32_t)*(const uint16_t *)(col + at16) << 16;
-                }
-                uint64_t y = mul2((uint64_t)x[1] << 32 | x[0], j ? w4.y : w4.x);
-                hi[i + j] = tops(y);
-                y = rest(y);
-                mid[i + j] = tops(y);
-                lo[i + j] = tops(rest(y));
+            for (int l = 0; l < 2; ++l) {
+                const int r = 2 * (i + j) + l;
+                const uint32_t at16 = (r >> 3) * 1024 + (r & 7) * 128 + ((chunk ^ (r & 7)) << 4);
+                x[l] = (uint32_t)*(const uint16_t *)(col + at16) << 16;
             }
+            uint64_t y = mul2((uint64_t)x[1] << 32 | x[0], j ? w4.y : w4.x);
+            hi[i + j] = tops(y);
+            y = rest(y);
+            mid[i + j] = tops(y);
+            lo[i + j] = tops(rest(y));
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) hi[j] = mid[j] = lo[j] = 0;
     }
-    __syncwarp();
     tmem_st8(at, hi);
     tmem_st8(at + 16, mid);
     tmem_st8(at + 32, lo);
@@ -708,7 +701,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             const DecayPass &p = A.pass[u.pass];
             const Walk walk(u, p.rev);
             const float g2 = decay_log2(u.gd);
-            const int pieces = p.kd / 16;
+            const int pieces = e < p.vd ? p.kd / 16 : 0;   // (by warps; the other lanes' sums are nobody's)
             float y = 0.f;
             if (u.tiles == 0) {   // an empty sequence: the state goes through
                 if (u.to)
@@ -746,7 +739,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                         }
                     }
                     tmem_st_wait();
-                } else {
+                } else if (pieces) {
                     tmem_columns(lanes + kColH, pieces, take);
                 }
                 fence_proxy_async_smem();
@@ -754,7 +747,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.h_ready);
             }
-            if (ok && u.to) {
+            if (ok && u.to && pieces) {
                 if (!(ok = wait(&bar.kv_full, it - 1))) return false;
                 tc_fence_after();
                 const float f = exp2f(-y);
@@ -778,7 +771,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             const DecayPass &p = A.pass[u.pass];
             const Walk walk(u, p.rev);
             const float gd = u.gd, g2 = decay_log2(gd), s_upd = p.s_upd;
-            const bool any = e < p.vd;
+            const bool any = e < p.vd;   // (by warps; the other lanes' sums are nobody's)
             float y = 0.f, w0 = 0.f, w1 = 0.f;
             int wlen = -1;   // tokens of the tile that w0, w1 are for
             for (int i = 0; i < walk.tiles; ++i, ++it) {
@@ -809,8 +802,10 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                     const uint32_t slot = k % kSlots, use = (it * kParts + k) / kSlots;
                     if (use && !(ok = wait(&bar.v_free[slot], use - 1))) break;
                     tc_fence_after();
-                    write_terms(lanes + kColV + slot * kSlotCols + 8 * grp, ct, e, any, 2 * k + grp, w + 16 * k);
-                    tmem_st_wait();
+                    if (any) {
+                        write_terms(lanes + kColV + slot * kSlotCols + 8 * grp, ct, e, 2 * k + grp, w + 16 * k);
+                        tmem_st_wait();
+                    }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.v_ready[slot]);
@@ -993,7 +988,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
             const Walk walk(u, rev);
             const float gd = u.gd, s_upd = p.s_upd;
             const int64_t tokens = u.t1 - u.t0;
-            const bool any = e < p.vd;
+            const bool any = e < p.vd;   // (by warps; the other lanes' sums are nobody's)
             if (u.tiles == 0) {
                 if (grp == 0)
                     for (int d = e; d < p.kd * p.vd; d += 128) u.to[d] = 0.f;
@@ -1019,7 +1014,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                 }
 #pragma unroll 1
                 for (uint32_t k = 0; k < 2; ++k)
-                    write_terms(lanes + kLocColV + slot * kSlotCols + 8 * k, ct, e, any, 2 * grp + k, w + 16 * k);
+                    if (any) write_terms(lanes + kLocColV + slot * kSlotCols + 8 * k, ct, e, 2 * grp + k, w + 16 * k);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
@@ -1028,10 +1023,11 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
             if (ok && grp == 0) {
                 if (!(ok = wait(&bar.h_full, nu))) return false;
                 tc_fence_after();
-                tmem_columns(lanes, p.kd / 16, [&](int m, const uint32_t (&r)[16]) {
-                    state_store(p, u.to, 16 * m, e, r);
-                    __syncwarp();
-                });
+                if (any)
+                    tmem_columns(lanes, p.kd / 16, [&](int m, const uint32_t (&r)[16]) {
+                        state_store(p, u.to, 16 * m, e, r);
+                        __syncwarp();
+                    });
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.h_free);
