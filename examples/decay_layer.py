@@ -118,7 +118,8 @@ def main():
     losses = train(layer)
     print(f"loss {losses[0]:.4f} -> {losses[-1]:.4f} after {len(losses)} steps")
     x = torch.randn(2, 300, 512, device="cuda").bfloat16()
-    whole = layer(x)
+    with torch.no_grad():
+        whole = layer(x)
     y, state = layer.prefill(x[:, :290].contiguous())
     rows = [y] + [layer.step(x[:, t:t + 1].contiguous(), state) for t in range(290, 300)]
     far = (torch.cat(rows, 1).float() - whole.float()).norm() / whole.float().norm()

@@ -285,3 +285,22 @@ def test_bad_offsets_are_reported_and_write_nothing(offsets, path):
     assert gdr.gdr_get_status() == gdr.GDR_ERR_BAD_SEQLENS
     assert (out == 7.0).all() and (hT == 7.0).all()
     ok()   # the status was cleared
+
+
+@pytest.mark.parametrize("seg_tiles", [0, 2], indirect=True)
+@pytest.mark.parametrize("lens", [None, [300, 0, 129, 500]])
+def test_waits_that_run_out_report_a_timeout_and_unwind(seg_tiles, lens, monkeypatch):
+    """Every wait of the tensor-core kernels is bounded.  With the limit at 0 each looks once: the
+    first one not yet satisfied sets the status and the block unwinds (its copies drained, its
+    tensor memory freed), so the next call at the default limit is right."""
+    x = inputs(2, 600, 3, 128, 128, "bf16", 600, lens=lens)
+    ok()
+    monkeypatch.setenv("GDR_TC_WAIT_NS", "0")
+    gdr.decay_fwd(x["q"], x["k"], x["v"], x["g"], h0=x["h0"], cu_seqlens=x["cu"])
+    assert gdr.gdr_get_status() == gdr.GDR_ERR_TIMEOUT
+    gdr.decay_bwd(x["q"], x["k"], x["v"], x["g"], x["dout"], dhT=x["dhT"], h0=x["h0"], cu_seqlens=x["cu"])
+    assert gdr.gdr_get_status() == gdr.GDR_ERR_TIMEOUT
+    monkeypatch.delenv("GDR_TC_WAIT_NS")
+    for _ in range(2):
+        check_fwd(x)
+        check_bwd(x)
