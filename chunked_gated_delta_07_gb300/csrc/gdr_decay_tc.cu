@@ -13,33 +13,38 @@
 // one accumulator; the floor of f keeps P in range for any decay, and what it adds is the
 // state's part taken at 2^-64 where lam^{i+1} is below that.
 //
-// The state is kept as S = 2^-y S^ with y in [0, 1).  A tile's decay lam^n = 2^-x moves
-// y + x: its whole part scales S^ by a power of two, which the tensor cores do as they read
-// the accumulator, and the rest becomes the next y, which goes into the weights.  So no warp
-// ever rewrites the state.  (A whole part of 64 or more: the old state is left out of the sum.)
+// Four warps keep the state, 128 fp32 numbers a thread, and add each tile's part to it, which
+// the tensor cores leave in the tensor memory (TMEM).  (A state that stayed there as the
+// accumulator of every tile lost up to 1e-5 of itself where the decay is weak: the tensor cores
+// cut a sum off where it leaves fp32 instead of rounding it, 24 times a tile and always
+// towards zero.  Registers: 4e-7 and no more over 65536 tokens.)
 //
-// All four products run on the tensor cores with fp32 accumulators in the tensor memory
-// (TMEM), 128 x 128 each:
+// All four products run on the tensor cores with fp32 accumulators in TMEM, 128 x 128 each:
 //     Sc = A B^T                     lanes = query tokens i
-//     S^^T <- 2^-k S^^T + C'^T B     lanes = value index e: the resident state
-//     O  = A S^                      lanes = query tokens i; S^ from shared memory in bf16
-//     O  += P C                      P in TMEM in bf16
-// in this order.  A tile of one head is 128 KB of HBM traffic (3 loads, 1 store; 2.9 us of an
-// SM's share of the measured bandwidth) and 25 MFLOP (2.0 us of an SM's share of the bf16
-// rate), so the pass can be bound by HBM if its other work stays out of the way.  The stages
-// of a tile run in different warps and overlap those of its neighbours:
+//     U  = C'^T B                    lanes = value index e: the tile's part of the new S^T
+//     O  = A S                       lanes = query tokens i; S from shared memory in bf16
+//     O += P C                       P in TMEM in bf16
+// in this order, O = A S in the middle of U's parts.  A tile of one head is 128 KB of HBM traffic
+// (3 loads, 1 store; 2.9 us of an SM's share of the measured bandwidth) and 25 MFLOP (2.0 us of
+// an SM's share of the bf16 rate), so the pass can be bound by HBM if its other work stays out
+// of the way.  The stages of a tile run in different warps and overlap those of its neighbours:
 //   warps 0-7    Sc -> P (bf16, over Sc in TMEM); O -> out; half of the columns each group
-//   warps 8-11   S^^T -> bf16 (shared memory)
+//   warps 8-11   S <- lam^n S + U, in bf16 to shared memory
 //   warps 12-19  C' = weighted C -> TMEM, 32 tokens at a time, half of them each group
 //   warp 20      TMA loads of A, B, C, two stages of 96 KB
 //   warp 21      issues every MMA (their order in the tensor pipe is the issue order)
 //   warp 22      TMA stores of the outputs, out of their tile's A
+// What is left of the bound (8 x 4096 tokens of 16 heads, 128 units on 152 SMs: 116 us, 3.6 us a
+// tile; 262144 tokens: 82% of the measured bandwidth): a tile's chain through its A -- load, Sc,
+// P, O, store -- takes some 14000 cycles, with two tiles in flight.
 //
 // Rounding.  The state is fp32 and so are its updates: C' has 24 significant bits, so it goes
 // in as the sum of three bf16 numbers that represent it exactly (three products instead of
-// one; two would leave 2^-17 in hT and dh0).  P and the state as a factor of O are rounded to
-// bf16: each adds an error of at most 2^-8 of its part of an output that is itself rounded
-// to bf16 (2.3e-3 in the mean square over the outputs against 1.7e-3 for their rounding alone).
+// one; two would leave 2^-17 in hT and dh0).  Small terms go first and the tile's tokens in the
+// order of growing weights, so that little is cut off.  P and the state as a factor of O are
+// rounded to bf16: each adds an error of at most 2^-8 of its part of an output that is itself
+// rounded to bf16 (2.3e-3 in the mean square over the outputs against 1.7e-3 for their rounding
+// alone).
 //
 // A block is persistent: it walks the units (segment, head, pass) with a stride of the grid
 // (equal sequences) or takes the next one from a counter (packed ones), and its pipeline
@@ -86,9 +91,9 @@ struct TcArgs {
 };
 
 // The rest of a wait that its first look did not end.  The warp sleeps meanwhile, in pieces
-// of up to 0.1 ms.
-__device__ __noinline__ bool wait_long(uint64_t *b, uint32_t parity, uint64_t limit_ns, volatile int *stop,
-                                       int *status) {
+// of up to 0.1 ms.  (Inline: a call would have the callers save the state's registers.)
+__device__ __forceinline__ bool wait_long(uint64_t *b, uint32_t parity, uint64_t limit_ns, volatile int *stop,
+                                          int *status) {
     const uint64_t t0 = globaltimer_ns();
     while (__all_sync(kFull, !*stop && globaltimer_ns() - t0 < limit_ns))
         if (__all_sync(kFull, mbar_try_wait_for(b, parity, 100000))) return true;
@@ -198,15 +203,6 @@ __device__ __forceinline__ void zero_rows(uint8_t *tile, int width, int n, int p
 // reciprocals, whatever lam is, and differences of multiples stay exact enough.
 __device__ __forceinline__ float decay_log2(float gd) { return fmaxf(gd * 1.4426950408889634f, -200.f); }
 
-// The exponent y of the state S = 2^-y S^ after a tile of len tokens; returns the whole part,
-// the power of two that S^ is scaled down by (0 for a growing state).
-__device__ __forceinline__ int advance_exponent(float &y, float g2, int len) {
-    y = fmaf(-g2, (float)len, y);
-    const float whole = fmaxf(floorf(y), 0.f);
-    y -= whole;
-    return (int)whole;
-}
-
 // A token's weight in the update of the state: s_upd lam^{len - 1 - i + past} (forward) or
 // s_upd lam^{i + 1 + past}; rows from len on are not the sequence's and have 0.
 __device__ __forceinline__ float token_weight(int i, int len, bool rev, float gd, float s_upd, int64_t past) {
@@ -233,6 +229,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     uint64_t r;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
 __device__ __forceinline__ uint32_t tops(uint64_t y) {   // the upper 16 bits of both
@@ -287,33 +288,11 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// 32 columns (d0 ..) of row e of a state in memory.
-__device__ __forceinline__ void state_load(const DecayPass &p, const float *in, int d0, int e, uint32_t (&r)[32]) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) r[j] = 0;
-    if (!in || e >= p.vd) return;
-    if (p.transposed) {
-        const float *row = in + (int64_t)e * p.kd + d0;
-#pragma unroll
-        for (int j = 0; j < 32; j += 4) *(uint4 *)&r[j] = *(const uint4 *)&row[j];
-    } else {
-        const float *col = in + (int64_t)d0 * p.vd + e;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(col[j * p.vd]);
-    }
+// A thread's registers from here on (all warps of a warpgroup).
+template <int kRegs, bool kMore> __device__ __forceinline__ void set_registers() {
+    if (kMore) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
-// 16 columns of it back.
-__device__ __forceinline__ void state_store(const DecayPass &p, float *to, int d0, int e, const uint32_t (&r)[16]) {
-    if (!to || e >= p.vd || d0 >= p.kd) return;
-    if (p.transposed) {
-#pragma unroll
-        for (int j = 0; j < 16; j += 4) *(uint4 *)&to[(int64_t)e * p.kd + d0 + j] = *(const uint4 *)&r[j];
-    } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) to[(int64_t)(d0 + j) * p.vd + e] = __uint_as_float(r[j]);
-    }
-}
-
 // Waits for the warp's TMEM loads; names the registers of one of them, so that no use of
 // those moves above the wait.
 __device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16]) {
@@ -323,6 +302,86 @@ __device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16]) {
                  :
                  : "memory");
 }
+// Row e of S^T in registers, s[j] = (S[2j][e], S[2j+1][e]): from memory (zeros past the
+// widths and for a null `in`), back, and in bf16 to shared memory as a K-major tile's row.
+using StateRow = uint64_t[kC / 2];
+template <int kVd>
+__device__ __forceinline__ void state_load(const DecayPass &p, const float *in, int e, StateRow &s) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (64 * h >= p.kd) break;
+        if (p.transposed) {
+            const ulonglong2 *row = (const ulonglong2 *)(in + e * p.kd + 64 * h);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                const ulonglong2 x = row[j];
+                s[32 * h + 2 * j] = x.x;
+                s[32 * h + 2 * j + 1] = x.y;
+            }
+        } else {
+            const float *col = in + 64 * h * kVd + e;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[32 * h + j] = two(col[2 * j * kVd], col[(2 * j + 1) * kVd]);
+        }
+    }
+}
+__device__ __forceinline__ void state_load(const DecayPass &p, const float *in, int e, StateRow &s) {
+#pragma unroll
+    for (int j = 0; j < kC / 2; ++j) s[j] = 0;
+    if (!in || e >= p.vd) return;
+    if (p.vd == 64) state_load<64>(p, in, e, s);
+    else state_load<128>(p, in, e, s);
+}
+template <int kVd> __device__ __forceinline__ void state_store(const DecayPass &p, float *to, int e, const StateRow &s) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (64 * h >= p.kd) break;
+        if (p.transposed) {
+            ulonglong2 *row = (ulonglong2 *)(to + e * p.kd + 64 * h);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) row[j] = make_ulonglong2(s[32 * h + 2 * j], s[32 * h + 2 * j + 1]);
+        } else {
+            float *col = to + 64 * h * kVd + e;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                col[2 * j * kVd] = __uint_as_float((uint32_t)s[32 * h + j]);
+                col[(2 * j + 1) * kVd] = __uint_as_float((uint32_t)(s[32 * h + j] >> 32));
+            }
+        }
+    }
+}
+__device__ __forceinline__ void state_store(const DecayPass &p, float *to, int e, const StateRow &s) {
+    if (e >= p.vd) return;
+    if (p.vd == 64) state_store<64>(p, to, e, s);
+    else state_store<128>(p, to, e, s);
+}
+__device__ __forceinline__ void state_to_bf16(const StateRow &s, uint8_t *tile, int e, int kd) {
+#pragma unroll
+    for (int j = 0; j < kC / 8; ++j) {
+        if (8 * j == 64 && kd == 64) break;
+        *(uint4 *)(tile + (j >> 3) * kBox + sw128_off(e, (j & 7) * 16)) =
+            make_uint4(pack2(s[4 * j]), pack2(s[4 * j + 1]), pack2(s[4 * j + 2]), pack2(s[4 * j + 3]));
+    }
+}
+// s <- s fa + s fb + the kd TMEM columns from `at` on, in fp32 (a whole warp); the factors, in
+// pairs, are (1, lam^n - 1) near 1 and (lam^n, 0) otherwise.  Without kDecay s is only added to.
+template <bool kDecay>
+__device__ __forceinline__ void state_add(StateRow &s, uint32_t at, int kd, uint64_t fa, uint64_t fb) {
+#pragma unroll
+    for (int m = 0; m < kC / 16; ++m) {
+        if (m == 4 && kd == 64) break;
+        uint32_t r[16];
+        tmem_ld16(at + 16 * m, r);
+        tmem_arrived(r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            uint64_t &x = s[8 * m + j];
+            const uint64_t u = (uint64_t)r[2 * j + 1] << 32 | r[2 * j];
+            x = kDecay ? fma2(x, fa, fma2(x, fb, u)) : add2(x, u);
+        }
+    }
+}
+
 // f(m, r) for 16 columns at a time from `at`, the next ones on their way meanwhile.  One
 // copy of f: the warps of a block run six different programs, which have to stay in the
 // instruction caches together.
@@ -339,40 +398,18 @@ template <typename F> __device__ __forceinline__ void tmem_columns(uint32_t at, 
     }
 }
 
-// The same, 32 columns at a time with nothing on its way meanwhile.  A load and its wait take
-// some 170 cycles, and hardly more for 32 columns than for 8: the state's warps, whose work on
-// a column is short, gain (8 x 4096 tokens 133 -> 127 us); those of P and O do not (with O
-// 129 us, with both 130 us).
-template <typename F> __device__ __forceinline__ void tmem_columns32(uint32_t at, int pieces, F &&f) {
-#pragma unroll 1
-    for (int m = 0; m < pieces; m += 2) {
-        uint32_t r[32];
-        tmem_ld32(at + 16 * m, r);
-        asm volatile("tcgen05.wait::ld.sync.aligned;"
-                     : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                       "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                       "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-                       "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
-                     :
-                     : "memory");
-#pragma unroll
-        for (int k = 0; k < 2; ++k) f(m + k, *(uint32_t(*)[16])&r[16 * k]);
-    }
-}
-
 // ---------------------------------------------------------------------------
 // the output pass
 // ---------------------------------------------------------------------------
-constexpr int kOutThreads = 32 * 23, kOutProducer = 20, kOutIssuer = 21, kOutStore = 22;   // warps
+constexpr int kOutThreads = 32 * 24, kOutProducer = 20, kOutIssuer = 21, kOutStore = 22;   // warps
 // TMEM columns
 constexpr uint32_t kColS = 0;      // Sc; P in the first 32 columns of each of its halves
 constexpr uint32_t kColO = 128;
-constexpr uint32_t kColH = 256;    // S^T
+constexpr uint32_t kColU = 256;    // the tile's part of the new S^T
 constexpr uint32_t kColV = 384;    // C'^T: slots of 32 tokens x 3 terms
 constexpr uint32_t kSlotCols = 48, kSlots = 2, kParts = kC / 32;   // kParts uses of slots per tile
-constexpr uint32_t kColZero = kColV + kSlots * kSlotCols;          // 8 columns of zeros
 constexpr uint32_t kTmemCols = 512;
-static_assert(kColZero + 8 <= kTmemCols, "TMEM");
+static_assert(kColV + kSlots * kSlotCols <= kTmemCols, "TMEM");
 // shared memory
 constexpr uint32_t kStage = 3 * kTile;               // A, B, C
 constexpr uint32_t kOffH = 2 * kStage;               // the state in bf16, [e][d], K-major
@@ -381,6 +418,10 @@ constexpr uint32_t kOffW = kOffBar + 320;            // weights of a group's 64 
 constexpr uint32_t kOffRing = kOffW + 8 * (kC / 2) * 4;
 constexpr uint32_t kSmemOut = kOffRing + kRing * sizeof(Unit);
 static_assert(kSmemOut <= 232448, "shared memory");
+// Registers of a thread at launch (what 768 threads may have) and from then on, by role: the
+// increase draws on the registers that the block was launched with.
+constexpr int kRegsLaunch = 80, kRegsOut = 64, kRegsState = 168, kRegsV = 64, kRegsOther = 56;
+static_assert(2 * kRegsOut + kRegsState + 2 * kRegsV + kRegsOther <= 6 * kRegsLaunch, "registers");
 
 struct OutBars {
     uint64_t u_full[kRing], u_free[kRing];   // a unit announced / done with (22 warps)
@@ -390,13 +431,13 @@ struct OutBars {
     uint64_t free_bc[2];   // ... its B and C
     uint64_t s_full;       // Sc complete
     uint64_t p_ready;      // P written (8 warps)
-    uint64_t o1_full;      // O = A S^ complete (the bf16 state is read)
     uint64_t o_full;       // O complete
     uint64_t o_free;       // O read and in shared memory (8 warps)
+    uint64_t s_free;       // U read (4 warps)
     uint64_t h_ready;      // the bf16 state written (4 warps)
     uint64_t v_ready[kSlots];   // a slot of C' written (8 warps)
     uint64_t v_free[kSlots];    // ... read
-    uint64_t kv_full;      // the tile's update of S^ complete
+    uint64_t kv_full;      // U complete, and the bf16 state read
     uint64_t fin;          // every MMA of the block complete
     uint32_t tmem;
     int stop;
@@ -431,9 +472,9 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
         }
         mbar_init(&bar.s_full, 1);
         mbar_init(&bar.p_ready, 8);
-        mbar_init(&bar.o1_full, 1);
         mbar_init(&bar.o_full, 1);
         mbar_init(&bar.o_free, 8);
+        mbar_init(&bar.s_free, 4);
         mbar_init(&bar.h_ready, 4);
         mbar_init(&bar.kv_full, 1);
         mbar_init(&bar.fin, 1);
@@ -465,125 +506,155 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
         }
     };
 
-    if (warp == kOutProducer) {
-        bool ok = true;
-        int64_t n = (int64_t)blockIdx.x - gridDim.x;
-        uint32_t nbc = 0;   // tiles whose B and C are on their way (`it`: whose A is too)
-        for (uint32_t k = 0; ok; ++k) {
-            Unit u;
-            if (!take_unit(A, false, n, u)) u.tiles = -1;
-            if (k >= kRing && !(ok = wait(&bar.u_free[k % kRing], k / kRing - 1))) break;
-            if (lane == 0) {
-                ring[k % kRing] = u;
-                mbar_arrive(&bar.u_full[k % kRing]);
-            }
-            __syncwarp();
-            if (u.tiles < 0) break;
-            const DecayPass &p = A.pass[u.pass];
-            const Walk walk(u, p.rev);
-            const int kd = p.kd, vd = p.vd;
-            // the entering state on its way into the L2, ahead of the warps that take it
-            if (u.in)
-                for (int i = 32 * lane; i < kd * vd; i += 1024)
-                    asm volatile("prefetch.global.L2 [%0];" ::"l"(u.in + i));
-            for (int i = 0; i < walk.tiles; ++i, ++it) {
-                const uint32_t st = it & 1;
-                const int64_t t = walk.first(u, i);
-                uint8_t *s = smem + st * kStage;
-                if (it >= 2 && !(ok = wait(&bar.free_bc[st], (it >> 1) - 1))) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&bar.full_bc[st], (kd + vd) / 64 * kBox);
-                    load_tile(s + kTile, &maps.b[u.pass], kd, u.h, t, &bar.full_bc[st]);
-                    load_tile(s + 2 * kTile, &maps.c[u.pass], vd, u.h, t, &bar.full_bc[st]);
-                }
-                __syncwarp();
-                ++nbc;
-                if (it >= 2 && !(ok = wait(&bar.free_a[st], (it >> 1) - 1))) break;
-                if (lane == 0) {
-                    mbar_arrive_expect_tx(&bar.full_a[st], kd / 64 * kBox);
-                    load_tile(s, &maps.a[u.pass], kd, u.h, t, &bar.full_a[st]);
-                }
-                __syncwarp();
-            }
-        }
-        // never leave with a copy in flight
-        for (uint32_t k = it >= 2 ? it - 2 : 0; k < it; ++k)
-            __all_sync(kFull, mbar_wait(&bar.full_a[k & 1], (k >> 1) & 1u, kDrainNs));
-        for (uint32_t k = nbc >= 2 ? nbc - 2 : 0; k < nbc; ++k)
-            __all_sync(kFull, mbar_wait(&bar.full_bc[k & 1], (k >> 1) & 1u, kDrainNs));
-    } else if (warp == kOutIssuer) {
-        const uint32_t s0 = smem_u32(smem);
-        const bool lead = elect_one();
-        each_unit([&](const Unit &u) {
+    if (warp >= kOutProducer) {
+        set_registers<kRegsOther, false>();
+        if (warp == kOutProducer) {
             bool ok = true;
-            const DecayPass &p = A.pass[u.pass];
-            const Walk walk(u, p.rev);
-            const int kd = p.kd;
-            const uint32_t kd16 = (uint32_t)kd / 16;
-            const uint32_t id_s = instr_desc(kC, kC, 1, false, false);
-            const uint32_t id_o1 = instr_desc(kC, p.vd, 1, false, false);
-            const uint32_t id_o2 = instr_desc(kC, p.vd, 1, false, true);
-            const uint32_t id_h = instr_desc(kC, kd, 1, false, true);
-            const float g2 = decay_log2(u.gd);
-            float y = 0.f;
-            for (int i = 0; i < walk.tiles; ++i, ++it) {
-                const uint32_t st = it & 1;
-                const int len = walk.len(i);
-                const uint32_t sa = s0 + st * kStage, sb = sa + kTile, sc = sb + kTile;
-                if (!(ok = wait(&bar.full_bc[st], it >> 1)) || !(ok = wait(&bar.full_a[st], it >> 1))) break;
-                tc_fence_after();
-                const uint64_t dA = smem_desc(sa, 16, 1024, kSw128), dB = smem_desc(sb, 16, 1024, kSw128);
-                const uint64_t dBt = smem_desc(sb, kBox, 1024, kSw128), dCt = smem_desc(sc, kBox, 1024, kSw128);
-                const uint64_t dH = smem_desc(s0 + kOffH, 16, 1024, kSw128);
-                // the previous tile's P is read: its product precedes this one in the pipe
-#pragma unroll
-                for (uint32_t k = 0; k < 8; ++k)
-                    if (k < kd16) mma_f16_ss_if(lead, tm + kColS, dA + k_major(k), dB + k_major(k), id_s, k > 0);
-                mma_commit_if(lead, &bar.s_full);
-                if (!(ok = wait(&bar.h_ready, it))) break;
-                // the state's power of two, on products with zeros
-                int down = advance_exponent(y, g2, len);
-                const bool keep = down < 64;
-                for (; keep && down > 0; down -= 15)
-                    mma_f16_ts_scaled_if(lead, tm + kColH, tm + kColZero, dBt, id_h, min(down, 15));
-#pragma unroll
-                for (uint32_t k = 0; k < kParts; ++k) {
-                    const uint32_t slot = k % kSlots, av = tm + kColV + slot * kSlotCols;
-                    if (k == kSlots) {   // while the slots are filled again
-                        if (it && !(ok = wait(&bar.o_free, it - 1))) break;
-                        tc_fence_after();
-#pragma unroll
-                        for (uint32_t j = 0; j < 8; ++j)
-                            if (j < kd16)
-                                mma_f16_ss_if(lead, tm + kColO, dA + k_major(j), dH + k_major(j), id_o1, j > 0);
-                        mma_commit_if(lead, &bar.o1_full);
+            int64_t n = (int64_t)blockIdx.x - gridDim.x;
+            uint32_t nbc = 0;   // tiles whose B and C are on their way (`it`: whose A is too)
+            for (uint32_t k = 0; ok; ++k) {
+                Unit u;
+                if (!take_unit(A, false, n, u)) u.tiles = -1;
+                if (k >= kRing && !(ok = wait(&bar.u_free[k % kRing], k / kRing - 1))) break;
+                if (lane == 0) {
+                    ring[k % kRing] = u;
+                    mbar_arrive(&bar.u_full[k % kRing]);
+                }
+                __syncwarp();
+                if (u.tiles < 0) break;
+                const DecayPass &p = A.pass[u.pass];
+                const Walk walk(u, p.rev);
+                const int kd = p.kd, vd = p.vd;
+                // the entering state on its way into the L2, ahead of the warps that take it
+                if (u.in)
+                    for (int i = 32 * lane; i < kd * vd; i += 1024)
+                        asm volatile("prefetch.global.L2 [%0];" ::"l"(u.in + i));
+                for (int i = 0; i < walk.tiles; ++i, ++it) {
+                    const uint32_t st = it & 1;
+                    const int64_t t = walk.first(u, i);
+                    uint8_t *s = smem + st * kStage;
+                    if (it >= 2 && !(ok = wait(&bar.free_bc[st], (it >> 1) - 1))) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bar.full_bc[st], (kd + vd) / 64 * kBox);
+                        load_tile(s + kTile, &maps.b[u.pass], kd, u.h, t, &bar.full_bc[st]);
+                        load_tile(s + 2 * kTile, &maps.c[u.pass], vd, u.h, t, &bar.full_bc[st]);
                     }
-                    if (!(ok = wait(&bar.v_ready[slot], (it * kParts + k) / kSlots))) break;
+                    __syncwarp();
+                    ++nbc;
+                    if (it >= 2 && !(ok = wait(&bar.free_a[st], (it >> 1) - 1))) break;
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&bar.full_a[st], kd / 64 * kBox);
+                        load_tile(s, &maps.a[u.pass], kd, u.h, t, &bar.full_a[st]);
+                    }
+                    __syncwarp();
+                }
+            }
+            // never leave with a copy in flight
+            for (uint32_t k = it >= 2 ? it - 2 : 0; k < it; ++k)
+                __all_sync(kFull, mbar_wait(&bar.full_a[k & 1], (k >> 1) & 1u, kDrainNs));
+            for (uint32_t k = nbc >= 2 ? nbc - 2 : 0; k < nbc; ++k)
+                __all_sync(kFull, mbar_wait(&bar.full_bc[k & 1], (k >> 1) & 1u, kDrainNs));
+        } else if (warp == kOutIssuer) {
+            const uint32_t s0 = smem_u32(smem);
+            const bool lead = elect_one();
+            each_unit([&](const Unit &u) {
+                bool ok = true;
+                const DecayPass &p = A.pass[u.pass];
+                const Walk walk(u, p.rev);
+                const int kd = p.kd;
+                const uint32_t kd16 = (uint32_t)kd / 16;
+                const uint32_t id_s = instr_desc(kC, kC, 1, false, false);
+                const uint32_t id_o1 = instr_desc(kC, p.vd, 1, false, false);
+                const uint32_t id_o2 = instr_desc(kC, p.vd, 1, false, true);
+                const uint32_t id_h = instr_desc(kC, kd, 1, false, true);
+                for (int i = 0; i < walk.tiles; ++i, ++it) {
+                    const uint32_t st = it & 1;
+                    const uint32_t sa = s0 + st * kStage, sb = sa + kTile, sc = sb + kTile;
+                    if (!(ok = wait(&bar.full_bc[st], it >> 1)) || !(ok = wait(&bar.full_a[st], it >> 1))) break;
+                    tc_fence_after();
+                    const uint64_t dA = smem_desc(sa, 16, 1024, kSw128), dB = smem_desc(sb, 16, 1024, kSw128);
+                    const uint64_t dBt = smem_desc(sb, kBox, 1024, kSw128), dCt = smem_desc(sc, kBox, 1024, kSw128);
+                    const uint64_t dH = smem_desc(s0 + kOffH, 16, 1024, kSw128);
+                    // the previous tile's P is read: its product precedes this one in the pipe
+#pragma unroll
+                    for (uint32_t k = 0; k < 8; ++k)
+                        if (k < kd16) mma_f16_ss_if(lead, tm + kColS, dA + k_major(k), dB + k_major(k), id_s, k > 0);
+                    mma_commit_if(lead, &bar.s_full);
+                    if (!(ok = wait(&bar.s_free, it))) break;
+#pragma unroll
+                    for (uint32_t k = 0; k < kParts; ++k) {
+                        const uint32_t slot = k % kSlots, av = tm + kColV + slot * kSlotCols;
+                        if (k == kSlots) {   // while the slots are filled again
+                            if (!(ok = wait(&bar.h_ready, it)) || (it && !(ok = wait(&bar.o_free, it - 1)))) break;
+                            tc_fence_after();
+#pragma unroll
+                            for (uint32_t j = 0; j < 8; ++j)
+                                if (j < kd16)
+                                    mma_f16_ss_if(lead, tm + kColO, dA + k_major(j), dH + k_major(j), id_o1, j > 0);
+                        }
+                        if (!(ok = wait(&bar.v_ready[slot], (it * kParts + k) / kSlots))) break;
+                        tc_fence_after();
+                        const uint64_t dPart = dBt + (((p.rev ? kParts - 1 - k : k) * 4096) >> 4);
+#pragma unroll
+                        for (uint32_t term = 0; term < 3; ++term)
+#pragma unroll
+                            for (uint32_t j = 0; j < 2; ++j)
+                                mma_f16_ts_if(lead, tm + kColU, av + (2 - term) * 16 + j * 8, dPart + ((j * 2048) >> 4),
+                                              id_h, k + term + j > 0);
+                        mma_commit_if(lead, &bar.v_free[slot]);
+                    }
+                    mma_commit_if(lead, &bar.kv_full);
+                    if (!ok || !(ok = wait(&bar.p_ready, it))) break;
                     tc_fence_after();
 #pragma unroll
-                    for (uint32_t term = 0; term < 3; ++term)
-#pragma unroll
-                        for (uint32_t j = 0; j < 2; ++j)
-                            mma_f16_ts_if(lead, tm + kColH, av + term * 16 + j * 8, dBt + ((k * 4096 + j * 2048) >> 4),
-                                          id_h, keep || k + term + j > 0);
-                    mma_commit_if(lead, &bar.v_free[slot]);
+                    for (uint32_t k = 0; k < kC / 16; ++k)
+                        mma_f16_ts_if(lead, tm + kColO, tm + kColS + (k >> 2) * 64 + (k & 3) * 8, dCt + ((k * 2048) >> 4), id_o2, 1);
+                    mma_commit_if(lead, &bar.o_full);
+                    mma_commit_if(lead, &bar.free_bc[st]);
                 }
-                mma_commit_if(lead, &bar.kv_full);
-                if (!ok || !(ok = wait(&bar.p_ready, it))) break;
-                tc_fence_after();
-#pragma unroll
-                for (uint32_t k = 0; k < kC / 16; ++k)
-                    mma_f16_ts_if(lead, tm + kColO, tm + kColS + (k >> 2) * 64 + (k & 3) * 8, dCt + ((k * 2048) >> 4), id_o2, 1);
-                mma_commit_if(lead, &bar.o_full);
-                mma_commit_if(lead, &bar.free_bc[st]);
-            }
-            return ok;
-        });
-        // no tensor-core operation may still run when the TMEM is released
-        mma_commit_if(lead, &bar.fin);
-        __all_sync(kFull, mbar_wait(&bar.fin, 0, kDrainNs));
+                return ok;
+            });
+            // no tensor-core operation may still run when the TMEM is released
+            mma_commit_if(lead, &bar.fin);
+            __all_sync(kFull, mbar_wait(&bar.fin, 0, kDrainNs));
+        } else if (warp == kOutStore) {
+            // ---- outputs: a tile's as boxes of 64 columns, or row by row at a sequence's end
+            each_unit([&](const Unit &u) {
+                bool ok = true;
+                const DecayPass &p = A.pass[u.pass];
+                const Walk walk(u, p.rev);
+                const int vd = p.vd;
+                for (int i = 0; i < walk.tiles; ++i, ++it) {
+                    const int len = walk.len(i);
+                    const int64_t t = walk.first(u, i);
+                    const uint8_t *buf = smem + (it & 1) * kStage;
+                    if (!(ok = wait(&bar.o_free, it))) break;
+                    if (len == kC) {
+                        if (lane == 0) {
+                            for (int b = 0; b < vd; b += 64)
+                                tma_store_3d(&maps.o[u.pass], b, u.h, (int)t, buf + (b >> 6) * kBox);
+                            bulk_commit();
+                            bulk_wait_read();
+                        }
+                    } else {
+#pragma unroll 4
+                        for (int k = lane; k < len * (vd / 8); k += 32) {
+                            const int r = k / (vd / 8), c = 8 * (k % (vd / 8));
+                            *(uint4 *)((__nv_bfloat16 *)p.out + ((t + r) * H + u.h) * (int64_t)vd + c) =
+                                *(const uint4 *)(buf + (c >> 6) * kBox + sw128_off(r, (c & 63) * 2));
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.free_a[it & 1]);
+                }
+                return ok;
+            });
+            bulk_wait();   // the block's shared memory goes with it
+        }
     } else if (warp < 8) {
         // ---- weights and outputs: thread = token row of the tile, and half of the columns
+        set_registers<kRegsOut, false>();
         const int rw = warp & 3, half = warp >> 2, row = tid & 127;
         const uint32_t lanes = tm + ((uint32_t)(rw * 32) << 16);
         each_unit([&](const Unit &u) {
@@ -593,21 +664,19 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             const Walk walk(u, rev);
             const float g2 = decay_log2(u.gd), s_upd = p.s_upd, s_out = p.s_out;
             const int vd = p.vd;
-            // 15 steps of the decay on top of 1 / f stay in range
-            const bool gentle = g2 > -3.f;
-            float y = 0.f;
-            // lam^{|i-j|} over 16 columns before (after, reversed) the row = (its distance to the
+            // 7 steps of the decay on top of 1 / f stay in range
+            const bool gentle = g2 > -6.f;
+            // lam^{|i-j|} over 8 columns before (after, reversed) the row = (its distance to the
             // near end of them) x (a column's distance to it); the latter here, in pairs
-            uint64_t near[8];
+            uint64_t near[4];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int j = 0; j < 4; ++j)
                 near[j] = rev ? two(exp2f(g2 * (float)(2 * j)), exp2f(g2 * (float)(2 * j + 1)))
-                              : two(exp2f(g2 * (float)(15 - 2 * j)), exp2f(g2 * (float)(14 - 2 * j)));
+                              : two(exp2f(g2 * (float)(7 - 2 * j)), exp2f(g2 * (float)(6 - 2 * j)));
             for (int i = 0; i < walk.tiles; ++i, ++it) {
                 const int len = walk.len(i);
-                // log2 of the row's f, and of the state's factor
-                const float lf = fmaxf(g2 * (float)(rev ? max(len - 1 - row, 0) : row + 1), -64.f) - y;
-                advance_exponent(y, g2, len);
+                // log2 of the row's f
+                const float lf = fmaxf(g2 * (float)(rev ? max(len - 1 - row, 0) : row + 1), -64.f);
                 if (!(ok = wait(&bar.s_full, it))) break;
                 tc_fence_after();
                 tmem_columns(lanes + kColS + 64 * half, 4, [&](int m, const uint32_t (&x)[16]) {
@@ -622,11 +691,14 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                     } else if (gentle) {
                         // the distance to the near end may be negative: then so is the column's
                         // to what it is taken from, and their product is still a power >= 0
-                        const float far = s_upd * exp2_approx(fmaf(g2, (float)(rev ? d : d - 15), -lf));
-                        const uint64_t far2 = two(far, far);
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            o[j] = pack2(mul2((uint64_t)x[2 * j + 1] << 32 | x[2 * j], mul2(near[j], far2)));
+                        for (int k = 0; k < 2; ++k) {
+                            const float far = s_upd * exp2_approx(fmaf(g2, (float)(rev ? d + 8 * k : d - 7 - 8 * k), -lf));
+                            const uint64_t far2 = two(far, far);
+#pragma unroll
+                            for (int j = 4 * k; j < 4 * k + 4; ++j)
+                                o[j] = pack2(mul2((uint64_t)x[2 * j + 1] << 32 | x[2 * j], mul2(near[j & 3], far2)));
+                        }
                         if (!__all_sync(kFull, lo <= 0 && hi >= 16))
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
@@ -674,116 +746,61 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             }
             return ok;
         });
-    } else if (warp == kOutStore) {
-        // ---- outputs: a tile's as boxes of 64 columns, or row by row at a sequence's end
-        each_unit([&](const Unit &u) {
-            bool ok = true;
-            const DecayPass &p = A.pass[u.pass];
-            const Walk walk(u, p.rev);
-            const int vd = p.vd;
-            for (int i = 0; i < walk.tiles; ++i, ++it) {
-                const int len = walk.len(i);
-                const int64_t t = walk.first(u, i);
-                const uint8_t *buf = smem + (it & 1) * kStage;
-                if (!(ok = wait(&bar.o_free, it))) break;
-                if (len == kC) {
-                    if (lane == 0) {
-                        for (int b = 0; b < vd; b += 64)
-                            tma_store_3d(&maps.o[u.pass], b, u.h, (int)t, buf + (b >> 6) * kBox);
-                        bulk_commit();
-                        bulk_wait_read();
-                    }
-                } else {
-#pragma unroll 4
-                    for (int k = lane; k < len * (vd / 8); k += 32) {
-                        const int r = k / (vd / 8), c = 8 * (k % (vd / 8));
-                        *(uint4 *)((__nv_bfloat16 *)p.out + ((t + r) * H + u.h) * (int64_t)vd + c) =
-                            *(const uint4 *)(buf + (c >> 6) * kBox + sw128_off(r, (c & 63) * 2));
-                    }
-                    fence_proxy_async_smem();
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.free_a[it & 1]);
-            }
-            return ok;
-        });
-        bulk_wait();   // the block's shared memory goes with it
     } else if (warp < 12) {
-        // ---- state: thread = value index (TMEM lane)
+        // ---- state: thread = value index (TMEM lane), whose row of S^T it keeps in registers
+        set_registers<kRegsState, true>();
         const int e = tid & 127;
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
-        {
-            const uint32_t zero[8] = {};
-            tmem_st8(lanes + kColZero, zero);
-            tmem_st_wait();   // the first h_ready publishes it
-        }
         each_unit([&](const Unit &u) {
             bool ok = true;
             const DecayPass &p = A.pass[u.pass];
             const Walk walk(u, p.rev);
-            const float g2 = decay_log2(u.gd);
-            const int pieces = e < p.vd ? p.kd / 16 : 0;   // (by warps; the other lanes' sums are nobody's)
-            float y = 0.f;
+            const float gd = u.gd;
+            const int kd = p.kd;
+            const bool any = e < p.vd;   // (by warps; the other lanes' sums are nobody's)
             if (u.tiles == 0) {   // an empty sequence: the state goes through
                 if (u.to)
-                    for (int d = e; d < p.kd * p.vd; d += 128) u.to[d] = u.in ? u.in[d] : 0.f;
+                    for (int d = e; d < kd * p.vd; d += 128) u.to[d] = u.in ? u.in[d] : 0.f;
                 return true;
             }
-            for (int i = 0; i < walk.tiles; ++i, ++it) {
-                advance_exponent(y, g2, walk.len(i));
-                // 16 columns of the entering state, to shared memory in bf16
-                auto take = [&](int m, const uint32_t (&r)[16]) {
-#pragma unroll
-                    for (int j = 0; j < 16; j += 8) {
-                        uint32_t o[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            o[k] = pack2(__uint_as_float(r[j + 2 * k]), __uint_as_float(r[j + 2 * k + 1]));
-                        *(uint4 *)(smem + kOffH + (m >> 2) * kBox + sw128_off(e, (16 * (m & 3) + j) * 2)) =
-                            make_uint4(o[0], o[1], o[2], o[3]);
-                    }
-                };
-                // the update of S^ is complete, and the bf16 state read
-                if (it && !((ok = wait(&bar.kv_full, it - 1)) && (ok = wait(&bar.o1_full, it - 1)))) break;
-                tc_fence_after();
-                if (i == 0) {
-#pragma unroll 1
-                    for (int m = 0; m < pieces; m += 2) {
-                        uint32_t r[32];
-                        state_load(p, u.in, 16 * m, e, r);
-                        __syncwarp();
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            uint32_t(&half)[16] = *(uint32_t(*)[16])&r[16 * k];
-                            take(m + k, half);
-                            tmem_st16(lanes + kColH + 16 * (m + k), half);
-                        }
-                    }
-                    tmem_st_wait();
-                } else if (pieces) {
-                    tmem_columns32(lanes + kColH, pieces, take);
+            StateRow s;
+            state_load(p, u.in, e, s);
+            uint64_t fa = 0, fb = 0;   // factors of s over flen tokens: s fa + s fb
+            int flen = -1;
+            // the update of tile i (whose number is n): kv_full says it is complete
+            auto update = [&](int i) {
+                if (walk.len(i) != flen) {
+                    flen = walk.len(i);
+                    const DecayFactor f(gd * (float)flen);
+                    fa = f.near1 ? two(1.f, 1.f) : two(f.f, f.f);
+                    fb = f.near1 ? two(f.f, f.f) : 0;
                 }
-                fence_proxy_async_smem();
+                if (any) state_add<true>(s, lanes + kColU, kd, fa, fb);
+            };
+            for (int i = 0; i < walk.tiles; ++i, ++it) {
+                if (it && !(ok = wait(&bar.kv_full, it - 1))) break;
+                tc_fence_after();
+                if (i) update(i - 1);
                 tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.s_free);
+                if (any) state_to_bf16(s, smem + kOffH, e, kd);
+                fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.h_ready);
             }
-            if (ok && u.to && pieces) {
+            if (ok && u.to) {
                 if (!(ok = wait(&bar.kv_full, it - 1))) return false;
                 tc_fence_after();
-                const float f = exp2f(-y);
-                tmem_columns32(lanes + kColH, pieces, [&](int m, uint32_t (&r)[16]) {
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(f * __uint_as_float(r[j]));
-                    state_store(p, u.to, 16 * m, e, r);
-                    __syncwarp();
-                });
+                update(walk.tiles - 1);
+                state_store(p, u.to, e, s);
             }
             return ok;
         });
     } else {
         // ---- weighted values: thread = value index (TMEM lane); group grp takes every other
         // 16 tokens, its token l = 16 k + j being the tile's 16 (2 k + grp) + j
+        set_registers<kRegsV, false>();
         const int grp = (warp - 12) >> 2, e = tid & 127;
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
         float *w = (float *)(smem + kOffW) + (warp - 12) * (kC / 2);
@@ -791,25 +808,20 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             bool ok = true;
             const DecayPass &p = A.pass[u.pass];
             const Walk walk(u, p.rev);
-            const float gd = u.gd, g2 = decay_log2(gd), s_upd = p.s_upd;
+            const float gd = u.gd, s_upd = p.s_upd;
             const bool any = e < p.vd;   // (by warps; the other lanes' sums are nobody's)
-            float y = 0.f, w0 = 0.f, w1 = 0.f;
-            int wlen = -1;   // tokens of the tile that w0, w1 are for
+            int wlen = -1;   // tokens of the tile that the weights are for
             for (int i = 0; i < walk.tiles; ++i, ++it) {
                 const uint32_t st = it & 1;
                 const int len = walk.len(i);
                 if (len != wlen) {
+                    __syncwarp();   // the last tile's weights are read
                     const int tok = 16 * (2 * (lane >> 4) + grp) + (lane & 15);
-                    w0 = token_weight(tok, len, walk.rev, gd, s_upd, 0);
-                    w1 = token_weight(tok + 64, len, walk.rev, gd, s_upd, 0);
+                    w[lane] = token_weight(tok, len, walk.rev, gd, s_upd, 0);
+                    w[lane + 32] = token_weight(tok + 64, len, walk.rev, gd, s_upd, 0);
+                    __syncwarp();
                     wlen = len;
                 }
-                advance_exponent(y, g2, len);
-                const float up = exp2f(y);   // into S^ after the tile
-                __syncwarp();                // the last tile's weights are read
-                w[lane] = w0 * up;
-                w[lane + 32] = w1 * up;
-                __syncwarp();
                 if (!(ok = wait(&bar.full_bc[st], it >> 1))) break;
                 uint8_t *ct = smem + st * kStage + 2 * kTile;
                 if (len < kC) {   // the products with P and with S^ read these rows too
@@ -821,10 +833,11 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
 #pragma unroll 1
                 for (uint32_t k = 0; k < kParts; ++k) {
                     const uint32_t slot = k % kSlots, use = (it * kParts + k) / kSlots;
+                    const uint32_t part = walk.rev ? kParts - 1 - k : k;
                     if (use && !(ok = wait(&bar.v_free[slot], use - 1))) break;
                     tc_fence_after();
                     if (any) {
-                        write_terms(lanes + kColV + slot * kSlotCols + 8 * grp, ct, e, 2 * k + grp, w + 16 * k);
+                        write_terms(lanes + kColV + slot * kSlotCols + 8 * grp, ct, e, 2 * part + grp, w + 16 * part);
                         tmem_st_wait();
                     }
                     tc_fence_before();
@@ -847,24 +860,28 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
 // ---------------------------------------------------------------------------
 // the local pass: each segment's own writes, decayed to its end
 // ---------------------------------------------------------------------------
-// Every write's weight is its distance to the segment's end, so the accumulator needs no
-// decay on the way: the tensor cores sum C'^T B over all tiles.  Four groups of four warps
-// take 32 tokens of a tile each, with slots of C' in TMEM for two tiles.
-constexpr int kLocThreads = 32 * 18, kLocProducer = 16, kLocIssuer = 17;   // warps
+// Every write's weight is its distance to the segment's end, so the sum of C'^T B over the tiles
+// needs no decay on the way.  Four groups of four warps take 32 tokens of a tile each, through
+// five slots of C' in TMEM; four more add a tile's product to the sum, which they keep in
+// registers, while the next one's runs in the other accumulator.  262144 tokens of 16 heads:
+// 199 us, 0.93 us a tile, of which the tensor cores' 24 products take 0.8.
+constexpr int kLocThreads = 32 * 24, kLocProducer = 20, kLocIssuer = 21;   // warps
 constexpr int kLocStages = 3;
 constexpr uint32_t kLocStage = 2 * kTile;                    // B, C
 constexpr uint32_t kLocOffBar = kLocStages * kLocStage;
 constexpr uint32_t kLocOffW = kLocOffBar + 320;              // weights, a copy per warp
 constexpr uint32_t kLocOffRing = kLocOffW + 16 * 32 * 4;
 constexpr uint32_t kSmemLocal = kLocOffRing + kRing * sizeof(Unit);
-constexpr uint32_t kLocColV = 128;                           // a tile's slots, twice
-static_assert(kLocColV + 2 * kParts * kSlotCols <= kTmemCols, "TMEM");
+constexpr uint32_t kLocColV = 2 * kC, kLocSlots = 5;         // after two accumulators
+constexpr int kLocRegsV = 64, kLocRegsState = 176, kLocRegsOther = 48;
+static_assert(4 * kLocRegsV + kLocRegsState + kLocRegsOther <= 6 * kRegsLaunch, "registers");
+static_assert(kLocColV + kLocSlots * kSlotCols <= kTmemCols, "TMEM");
 
 struct LocalBars {
-    uint64_t u_full[kRing], u_free[kRing];   // a unit announced / done with (17 warps)
+    uint64_t u_full[kRing], u_free[kRing];   // a unit announced / done with (21 warps)
     uint64_t full[kLocStages], free[kLocStages];
-    uint64_t v_ready[2 * kParts], v_free[2 * kParts];
-    uint64_t h_full, h_free;   // a unit's sum complete / read
+    uint64_t v_ready[kLocSlots], v_free[kLocSlots];
+    uint64_t sum_full[2], sum_free[2];   // a tile's sum complete / read (4 warps)
     uint64_t fin;
     uint32_t tmem;
     int stop;
@@ -883,18 +900,20 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
     if (tid == 0) {
         for (uint32_t i = 0; i < kRing; ++i) {
             mbar_init(&bar.u_full[i], 1);
-            mbar_init(&bar.u_free[i], 17);
+            mbar_init(&bar.u_free[i], 21);
         }
         for (int i = 0; i < kLocStages; ++i) {
             mbar_init(&bar.full[i], 1);
             mbar_init(&bar.free[i], 1);
         }
-        for (uint32_t i = 0; i < 2 * kParts; ++i) {
+        for (uint32_t i = 0; i < kLocSlots; ++i) {
             mbar_init(&bar.v_ready[i], 4);
             mbar_init(&bar.v_free[i], 1);
         }
-        mbar_init(&bar.h_full, 1);
-        mbar_init(&bar.h_free, 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.sum_full[i], 1);
+            mbar_init(&bar.sum_free[i], 4);
+        }
         mbar_init(&bar.fin, 1);
         *stop = 0;
         fence_mbar_init();
@@ -910,7 +929,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
     after_previous();
     const uint32_t tm = bar.tmem;
     auto wait = [&](uint64_t *b, uint32_t use) { return wait_use(b, use, A.wait_ns, stop, A.status); };
-    uint32_t it = 0, nu = 0;   // tiles and units so far
+    uint32_t it = 0;   // tiles so far
     // Walks the announced units (every warp but the producer): f(unit) until the end or until
     // it returns false.
     auto each_unit = [&](auto &&f) {
@@ -923,82 +942,87 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
         }
     };
 
-    if (warp == kLocProducer) {
-        bool ok = true;
-        int64_t n = (int64_t)blockIdx.x - gridDim.x;
-        for (uint32_t k = 0; ok; ++k) {
-            Unit u;
-            if (!take_unit(A, true, n, u)) u.tiles = -1;
-            if (k >= kRing && !(ok = wait(&bar.u_free[k % kRing], k / kRing - 1))) break;
-            if (lane == 0) {
-                ring[k % kRing] = u;
-                mbar_arrive(&bar.u_full[k % kRing]);
-            }
-            __syncwarp();
-            if (u.tiles < 0) break;
-            const DecayPass &p = A.pass[u.pass];
-            const Walk walk(u, p.rev);
-            const int kd = p.kd, vd = p.vd;
-            for (int i = 0; i < walk.tiles; ++i, ++it) {
-                const uint32_t st = it % kLocStages, use = it / kLocStages;
-                if (use && !(ok = wait(&bar.free[st], use - 1))) break;
+    if (warp >= kLocProducer) {
+        set_registers<kLocRegsOther, false>();
+        if (warp == kLocProducer) {
+            bool ok = true;
+            int64_t n = (int64_t)blockIdx.x - gridDim.x;
+            for (uint32_t k = 0; ok; ++k) {
+                Unit u;
+                if (!take_unit(A, true, n, u)) u.tiles = -1;
+                if (k >= kRing && !(ok = wait(&bar.u_free[k % kRing], k / kRing - 1))) break;
                 if (lane == 0) {
-                    const int64_t t = walk.first(u, i);
-                    uint8_t *s = smem + st * kLocStage;
-                    mbar_arrive_expect_tx(&bar.full[st], (kd + vd) / 64 * kBox);
-                    load_tile(s, &maps.b[u.pass], kd, u.h, t, &bar.full[st]);
-                    load_tile(s + kTile, &maps.c[u.pass], vd, u.h, t, &bar.full[st]);
+                    ring[k % kRing] = u;
+                    mbar_arrive(&bar.u_full[k % kRing]);
                 }
                 __syncwarp();
-            }
-        }
-        for (uint32_t k = it >= kLocStages ? it - kLocStages : 0; k < it; ++k)
-            __all_sync(kFull, mbar_wait(&bar.full[k % kLocStages], (k / kLocStages) & 1u, kDrainNs));
-    } else if (warp == kLocIssuer) {
-        const uint32_t s0 = smem_u32(smem);
-        const bool lead = elect_one();
-        each_unit([&](const Unit &u) {
-            bool ok = true;
-            if (u.tiles == 0) return true;
-            const DecayPass &p = A.pass[u.pass];
-            const Walk walk(u, p.rev);
-            const int kd = p.kd;
-            const uint32_t id_h = instr_desc(kC, kd, 1, false, true);
-            if (nu && !(ok = wait(&bar.h_free, nu - 1))) return false;
-            for (int i = 0; i < walk.tiles; ++i, ++it) {
-                const uint32_t st = it % kLocStages, buf = it & 1;
-                const int len = walk.len(i);
-                if (!(ok = wait(&bar.full[st], it / kLocStages))) break;
-                if (len < kC) {
-                    zero_rows(smem + st * kLocStage, kd, len, 0, 1, lane);
-                    fence_proxy_async_smem();
+                if (u.tiles < 0) break;
+                const DecayPass &p = A.pass[u.pass];
+                const Walk walk(u, p.rev);
+                const int kd = p.kd, vd = p.vd;
+                for (int i = 0; i < walk.tiles; ++i, ++it) {
+                    const uint32_t st = it % kLocStages, use = it / kLocStages;
+                    if (use && !(ok = wait(&bar.free[st], use - 1))) break;
+                    if (lane == 0) {
+                        const int64_t t = walk.first(u, i);
+                        uint8_t *s = smem + st * kLocStage;
+                        mbar_arrive_expect_tx(&bar.full[st], (kd + vd) / 64 * kBox);
+                        load_tile(s, &maps.b[u.pass], kd, u.h, t, &bar.full[st]);
+                        load_tile(s + kTile, &maps.c[u.pass], vd, u.h, t, &bar.full[st]);
+                    }
                     __syncwarp();
                 }
-                tc_fence_after();
-                const uint64_t dBt = smem_desc(s0 + st * kLocStage, kBox, 1024, kSw128);
-#pragma unroll
-                for (uint32_t k = 0; k < kParts; ++k) {
-                    const uint32_t slot = buf * kParts + k, av = tm + kLocColV + slot * kSlotCols;
-                    if (!(ok = wait(&bar.v_ready[slot], it >> 1))) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (uint32_t term = 0; term < 3; ++term)
-#pragma unroll
-                        for (uint32_t j = 0; j < 2; ++j)
-                            mma_f16_ts_if(lead, tm, av + term * 16 + j * 8, dBt + ((k * 4096 + j * 2048) >> 4), id_h,
-                                          i + k + term + j > 0);
-                    mma_commit_if(lead, &bar.v_free[slot]);
-                }
-                if (!ok) break;
-                mma_commit_if(lead, &bar.free[st]);
-                if (i == walk.tiles - 1) mma_commit_if(lead, &bar.h_full);
             }
-            ++nu;
-            return ok;
-        });
-        mma_commit_if(lead, &bar.fin);
-        __all_sync(kFull, mbar_wait(&bar.fin, 0, kDrainNs));
-    } else {
+            for (uint32_t k = it >= kLocStages ? it - kLocStages : 0; k < it; ++k)
+                __all_sync(kFull, mbar_wait(&bar.full[k % kLocStages], (k / kLocStages) & 1u, kDrainNs));
+        } else if (warp == kLocIssuer) {
+            const uint32_t s0 = smem_u32(smem);
+            const bool lead = elect_one();
+            each_unit([&](const Unit &u) {
+                bool ok = true;
+                if (u.tiles == 0) return true;
+                const DecayPass &p = A.pass[u.pass];
+                const Walk walk(u, p.rev);
+                const int kd = p.kd;
+                const uint32_t id_h = instr_desc(kC, kd, 1, false, true);
+                for (int i = 0; i < walk.tiles; ++i, ++it) {
+                    const uint32_t st = it % kLocStages, buf = it & 1;
+                    const int len = walk.len(i);
+                    if (!(ok = wait(&bar.full[st], it / kLocStages))) break;
+                    if (len < kC) {
+                        zero_rows(smem + st * kLocStage, kd, len, 0, 1, lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (it >= 2 && !(ok = wait(&bar.sum_free[buf], (it >> 1) - 1))) break;
+                    tc_fence_after();
+                    const uint64_t dBt = smem_desc(s0 + st * kLocStage, kBox, 1024, kSw128);
+#pragma unroll
+                    for (uint32_t k = 0; k < kParts; ++k) {
+                        const uint32_t n = it * kParts + k, slot = n % kLocSlots, av = tm + kLocColV + slot * kSlotCols;
+                        const uint64_t dPart = dBt + (((p.rev ? kParts - 1 - k : k) * 4096) >> 4);
+                        if (!(ok = wait(&bar.v_ready[slot], n / kLocSlots))) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (uint32_t term = 0; term < 3; ++term)
+#pragma unroll
+                            for (uint32_t j = 0; j < 2; ++j)
+                                mma_f16_ts_if(lead, tm + buf * kC, av + (2 - term) * 16 + j * 8, dPart + ((j * 2048) >> 4),
+                                              id_h, k + term + j > 0);
+                        mma_commit_if(lead, &bar.v_free[slot]);
+                    }
+                    if (!ok) break;
+                    mma_commit_if(lead, &bar.free[st]);
+                    mma_commit_if(lead, &bar.sum_full[buf]);
+                }
+                return ok;
+            });
+            mma_commit_if(lead, &bar.fin);
+            __all_sync(kFull, mbar_wait(&bar.fin, 0, kDrainNs));
+        }
+    } else if (warp < 16) {
+        // ---- weighted values: thread = value index (TMEM lane), group grp 32 tokens of the tile
+        set_registers<kLocRegsV, false>();
         const int grp = warp >> 2, e = tid & 127;
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
         float *w = (float *)(smem + kLocOffW) + warp * 32;
@@ -1010,16 +1034,11 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
             const float gd = u.gd, s_upd = p.s_upd;
             const int64_t tokens = u.t1 - u.t0;
             const bool any = e < p.vd;   // (by warps; the other lanes' sums are nobody's)
-            if (u.tiles == 0) {
-                if (grp == 0)
-                    for (int d = e; d < p.kd * p.vd; d += 128) u.to[d] = 0.f;
-                return true;
-            }
             for (int i = 0; i < walk.tiles; ++i, ++it) {
-                const uint32_t st = it % kLocStages, buf = it & 1;
-                const uint32_t slot = buf * kParts + grp;
+                const uint32_t st = it % kLocStages;
+                const uint32_t n = it * kParts + (rev ? kParts - 1 - grp : grp);   // in the issuer's order
+                const uint32_t slot = n % kLocSlots, use = n / kLocSlots;
                 const int len = walk.len(i);
-                const uint32_t use = it >> 1;
                 // past the tile: its distance to the segment's end (its start, reversed)
                 const int64_t past = rev ? (int64_t)(walk.tiles - 1 - i) * kC : tokens - (int64_t)i * kC - len;
                 __syncwarp();   // the last tile's weights are read
@@ -1041,20 +1060,30 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.v_ready[slot]);
             }
-            if (ok && grp == 0) {
-                if (!(ok = wait(&bar.h_full, nu))) return false;
+            return ok;
+        });
+    } else {
+        // ---- sums: thread = value index (TMEM lane), whose row it keeps in registers
+        set_registers<kLocRegsState, true>();
+        const int e = tid & 127;
+        const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
+        each_unit([&](const Unit &u) {
+            const DecayPass &p = A.pass[u.pass];
+            const bool any = e < p.vd;   // (by warps; the other lanes' sums are nobody's)
+            StateRow s;
+#pragma unroll
+            for (int j = 0; j < kC / 2; ++j) s[j] = 0;
+            for (int i = 0; i < u.tiles; ++i, ++it) {
+                const uint32_t buf = it & 1;
+                if (!wait(&bar.sum_full[buf], it >> 1)) return false;
                 tc_fence_after();
-                if (any)
-                    tmem_columns(lanes, p.kd / 16, [&](int m, const uint32_t (&r)[16]) {
-                        state_store(p, u.to, 16 * m, e, r);
-                        __syncwarp();
-                    });
+                if (any) state_add<false>(s, lanes + buf * kC, p.kd, 0, 0);
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.h_free);
+                if (lane == 0) mbar_arrive(&bar.sum_free[buf]);
             }
-            ++nu;
-            return ok;
+            state_store(p, u.to, e, s);
+            return true;
         });
     }
     tc_fence_before();
@@ -1097,6 +1126,13 @@ cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, 
     if (args.units > 0x7fffffff) return cudaErrorInvalidValue;
     auto kern = local ? decay_local_kernel : decay_out_kernel;
     const int bytes = (int)(local ? kSmemLocal : kSmemOut);
+    // the kernels' split of the registers is made for this many a thread
+    static const bool split = [] {
+        cudaFuncAttributes a{}, b{};
+        return cudaFuncGetAttributes(&a, decay_local_kernel) == cudaSuccess && a.numRegs >= kRegsLaunch &&
+               cudaFuncGetAttributes(&b, decay_out_kernel) == cudaSuccess && b.numRegs >= kRegsLaunch;
+    }();
+    if (!split) return cudaErrorInvalidConfiguration;
     const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (err != cudaSuccess) return err;
     ProfScope prof(stream, local ? "decay_local_kernel" : "decay_out_kernel");

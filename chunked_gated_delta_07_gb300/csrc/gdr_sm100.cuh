@@ -249,38 +249,6 @@ __device__ __forceinline__ void mma_f16_ts_if(bool lead, uint32_t d, uint32_t a,
         "r"(a), "l"(b), "r"(idesc), "r"(accum), "r"((uint32_t)lead)
         : "memory");
 }
-// D[tmem] = A[tmem] * B[smem] + 2^-S * D[tmem]; S in [0, 15] is an immediate.
-template <int S>
-__device__ __forceinline__ void mma_f16_ts_scale_if(bool lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc) {
-    static_assert(S >= 0 && S <= 15, "scale-input-d range");
-    asm volatile(
-        "{ .reg .pred p, l; setp.ne.b32 p, 1, 0; setp.ne.b32 l, %4, 0;"
-        " @l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p, %5; }" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)lead), "n"(S)
-        : "memory");
-}
-// The same with a run-time S (one branch per value).
-__device__ __forceinline__ void mma_f16_ts_scaled_if(bool lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
-                                                     int s) {
-    switch (s) {
-        case 0: mma_f16_ts_scale_if<0>(lead, d, a, b, idesc); break;
-        case 1: mma_f16_ts_scale_if<1>(lead, d, a, b, idesc); break;
-        case 2: mma_f16_ts_scale_if<2>(lead, d, a, b, idesc); break;
-        case 3: mma_f16_ts_scale_if<3>(lead, d, a, b, idesc); break;
-        case 4: mma_f16_ts_scale_if<4>(lead, d, a, b, idesc); break;
-        case 5: mma_f16_ts_scale_if<5>(lead, d, a, b, idesc); break;
-        case 6: mma_f16_ts_scale_if<6>(lead, d, a, b, idesc); break;
-        case 7: mma_f16_ts_scale_if<7>(lead, d, a, b, idesc); break;
-        case 8: mma_f16_ts_scale_if<8>(lead, d, a, b, idesc); break;
-        case 9: mma_f16_ts_scale_if<9>(lead, d, a, b, idesc); break;
-        case 10: mma_f16_ts_scale_if<10>(lead, d, a, b, idesc); break;
-        case 11: mma_f16_ts_scale_if<11>(lead, d, a, b, idesc); break;
-        case 12: mma_f16_ts_scale_if<12>(lead, d, a, b, idesc); break;
-        case 13: mma_f16_ts_scale_if<13>(lead, d, a, b, idesc); break;
-        case 14: mma_f16_ts_scale_if<14>(lead, d, a, b, idesc); break;
-        default: mma_f16_ts_scale_if<15>(lead, d, a, b, idesc); break;
-    }
-}
 __device__ __forceinline__ void mma_commit_if(bool lead, uint64_t *bar) {
     asm volatile(
         "{ .reg .pred l; setp.ne.b32 l, %1, 0;"

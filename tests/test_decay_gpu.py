@@ -148,6 +148,23 @@ def test_extreme_decays(dtype, path):
     assert ref.rel(hT, last) <= BOUND32
 
 
+@pytest.mark.parametrize("seg_tiles", [0, 8], indirect=True)
+@pytest.mark.parametrize("g", [0.0, -1e-4, -2e-3])
+def test_weak_decays_keep_states_in_full_precision(g, seg_tiles):
+    """States that remember thousands of tokens.  The tensor cores add a tile's products 16 tokens
+    and one of three terms at a time, 24 sums that are cut off and not rounded: half a unit in the
+    last place (2^-24) each on average, always towards zero, 24 * 2^-24 = 1.4e-6 for the tile's
+    part.  Adding the parts up must not add to that but what rounding does, 2^-24 at random."""
+    x = inputs(1, 4096, 2, 128, 128, "bf16", 140, slopes=[-g, -g])
+    bound = 1.5e-6
+    _, hT = gdr.decay_fwd(x["q"], x["k"], x["v"], x["g"], h0=x["h0"])
+    dh0 = gdr.decay_bwd(x["q"], x["k"], x["v"], x["g"], x["dout"], dhT=x["dhT"], h0=x["h0"])[3]
+    ok()
+    far = ref.rel(hT, ref.decay_fwd(x["q"], x["k"], x["v"], x["g"], x["h0"], None)[1])
+    far0 = ref.rel(dh0, ref.decay_bwd(x["q"], x["k"], x["v"], x["g"], x["dout"], x["dhT"], x["h0"], None)[3])
+    assert far <= bound and far0 <= bound, (far, far0)
+
+
 @pytest.mark.parametrize("path", ["auto", "simt"])
 def test_unaligned_pointers_take_the_general_path(path):
     """Tensors one element past a 16-byte boundary."""
