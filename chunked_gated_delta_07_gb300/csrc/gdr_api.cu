@@ -545,7 +545,16 @@ struct DecayShape {
     bool varlen;
 };
 
-constexpr int64_t kDecayStepTokens = 8;   // most tokens that decay_step_kernel takes
+// Most tokens that decay_step_kernel takes, which moves the state at HBM's rate but spends a
+// block-wide sum on every token; decay_rec_kernel's start costs more and its tokens less.  256
+// sequences of 16 heads, step against rec: 1 token 83 against 200 us, 4 tokens 123 against 229,
+// 8 tokens 236 against 273, 12 tokens 359 against 305; one sequence: 8 tokens 12.8 against 12.1 us.
+constexpr int64_t kDecayStepTokens = 8;
+// Sequences of at most this many tokens (packed: this many in all) run on the CUDA cores, whose
+// kernel has the shorter start: 16 heads, 4 tokens 9.4 us against the tensor cores' 14.1, 8 tokens
+// 10.5 against 13.9, 24 tokens 15.2 against 15.6, 64 tokens 26 against 16; 64 sequences, 4 tokens
+// 47 against 50, 8 tokens 58 against 50 (backward 125 against 136).
+constexpr int64_t kDecayShortTokens = 8;
 
 // Segments of a call.  A pass runs one block (tensor cores) or one column slice (CUDA
 // cores) per (segment, head): `units` per segment and sequence, `slots` at a time.  Equal
@@ -557,9 +566,9 @@ constexpr int64_t kDecayStepTokens = 8;   // most tokens that decay_step_kernel 
 // that one long sequence among short ones is cut too and the slots end together.
 // GDR_DECAY_SEG_TILES=n cuts into n tiles per segment whatever the sizes (the parity tests
 // run many short segments).
-DecayGeom decay_geom(const DecayShape &s, int64_t units, int64_t slots, int64_t min_tiles, double fixed) {
+DecayGeom decay_geom(const DecayShape &s, int64_t units, int64_t slots, int tile, int64_t min_tiles, double fixed) {
     const char *env = std::getenv("GDR_DECAY_SEG_TILES");
-    const int64_t set = env ? std::atoll(env) : 0;
+    const int64_t set = env ? std::atoll(env) * (kDecayTile / tile) : 0;
     DecayGeom g{};
     g.dense = !s.varlen;
     g.N = s.N;
@@ -567,7 +576,7 @@ DecayGeom decay_geom(const DecayShape &s, int64_t units, int64_t slots, int64_t 
     g.T_per = s.T_per;
     g.T_total = s.T_total;
     if (g.dense) {
-        const int64_t tiles = std::max<int64_t>(1, (s.T_per + kDecayTile - 1) / kDecayTile);
+        const int64_t tiles = std::max<int64_t>(1, (s.T_per + tile - 1) / tile);
         int64_t best = 1;
         double least = 0;
         for (int64_t c = 1; c <= 4 * slots && (c == 1 || c * min_tiles <= tiles); ++c) {
@@ -581,15 +590,15 @@ DecayGeom decay_geom(const DecayShape &s, int64_t units, int64_t slots, int64_t 
             if (rounds > 8) break;   // enough blocks to even out
         }
         const int64_t seg = set > 0 ? set : (tiles + best - 1) / best;
-        g.seg_tokens = seg * kDecayTile;
+        g.seg_tokens = seg * tile;
         g.segs_per_seq = (tiles + seg - 1) / seg;
         g.max_segs = g.segs_per_seq * s.N;
         g.max_slots = g.max_segs - s.N;
     } else {
-        const int64_t tiles = (s.T_total + kDecayTile - 1) / kDecayTile;
+        const int64_t tiles = (s.T_total + tile - 1) / tile;
         const int64_t even = std::max(min_tiles, (tiles * units + 3 * slots - 1) / (3 * slots));
         const int64_t seg = std::min<int64_t>(set > 0 ? set : even, 1 << 24);
-        g.seg_tokens = seg * kDecayTile;
+        g.seg_tokens = seg * tile;
         // a sequence of len tokens has ceil(len / seg) segments, at least one
         g.max_slots = s.T_total / g.seg_tokens;
         g.max_segs = g.max_slots + s.N;
@@ -621,11 +630,22 @@ bool decay_tc_ok(gdr_dtype_t dtype, const DecayShape &s, std::initializer_list<c
     return true;
 }
 
+// Whether the call runs on the tensor cores.
+bool decay_use_tc(bool can, gdr_path_t path, const DecayShape &s) {
+    const int64_t longest = s.varlen ? s.T_total : s.T_per;
+    return can && (path == GDR_PATH_TC || (path != GDR_PATH_SIMT && longest > kDecayShortTokens));
+}
+
+// Segments on the CUDA cores are cut this fine: a block takes 0.3 us a token, and a call of few
+// tokens has blocks to spare (7 packed sequences, 5003 tokens of 2 heads x 64 in fp32, backward:
+// 83 us with 128, 62 with 64, 63 with 32, where chaining the states takes over).
+constexpr int kSimtTile = 64;
+
 DecayGeom decay_call_geom(const DecayShape &s, bool tc, bool backward, int sms) {
     const int passes = backward ? 3 : 1;
-    if (tc) return decay_geom(s, (int64_t)s.H * passes, sms, 4, 2.0);
+    if (tc) return decay_geom(s, (int64_t)s.H * passes, sms, kDecayTile, 4, 2.0);
     // CUDA cores: four resident blocks of 64 columns per SM; passes run one by one
-    return decay_geom(s, (int64_t)s.H * (std::max(s.dk, s.dv) / 64), 4 * (int64_t)sms, 1, 0.1);
+    return decay_geom(s, (int64_t)s.H * (std::max(s.dk, s.dv) / 64), 4 * (int64_t)sms, kSimtTile, 1, 0.1);
 }
 
 DecayLayout decay_layout(const DecayShape &s, const DecayGeom &g, bool backward) {
@@ -655,7 +675,7 @@ gdr_status_t decay_plan(DecayGeom *g, const int32_t *cu, const float *log_decay,
     cudaError_t err = cudaSuccess;
     if (!g->dense) {
         int64_t *seq_start = (int64_t *)(ws + L.plan), *seg_base = seq_start + (g->N + 1);
-        g->p = Plan{g->N, kDecayTile, (int)(g->seg_tokens / kDecayTile), seq_start, nullptr, seg_base};
+        g->p = Plan{g->N, 0, 0, seq_start, nullptr, seg_base};
         err = launch_decay_plan(cu, *g, seq_start, seg_base, next, status, stream);
     } else if (g->max_slots > 0) {
         err = cudaMemsetAsync(next, 0, 2 * sizeof(*next), stream);
@@ -1112,7 +1132,7 @@ gdr_status_t gdr_decay_fwd(const void *q, const void *k, const void *v, const fl
         return GDR_ERR_INVALID_ARG;
     const bool can_tc = decay_tc_ok(dtype, s, {q, k, v, out});
     if (path == GDR_PATH_TC && !can_tc) return GDR_ERR_UNSUPPORTED;
-    const bool tc = can_tc && path != GDR_PATH_SIMT;
+    const bool tc = decay_use_tc(can_tc, path, s);
     cudaStream_t stream = (cudaStream_t)stream_;
     if (s.T_total == 0 && !s.varlen) {   // no tokens: hT = h0
         if (!hT || hT == h0) return GDR_OK;
@@ -1158,7 +1178,7 @@ gdr_status_t gdr_decay_bwd(const void *q, const void *k, const void *v, const fl
         return GDR_ERR_INVALID_ARG;
     const bool can_tc = decay_tc_ok(dtype, s, {q, k, v, dout, dq, dk_out, dv_out});
     if (path == GDR_PATH_TC && !can_tc) return GDR_ERR_UNSUPPORTED;
-    const bool tc = can_tc && path != GDR_PATH_SIMT;
+    const bool tc = decay_use_tc(can_tc, path, s);
     cudaStream_t stream = (cudaStream_t)stream_;
     if (s.T_total == 0 && !s.varlen) {   // no tokens: dh0 = dhT
         if (!dh0) return GDR_OK;

@@ -3,11 +3,15 @@
 //
 // decay_rec_kernel runs one pass (gdr_decay.cuh) in its recurrent form.  The columns of
 // the state S (kd x vd) are independent, so a block owns one (segment, head, 64-column
-// slice) and keeps it in registers, 8 x 8 elements per thread, while the tokens stream
-// through shared memory in tiles of 16.  Per token a thread does 64 updates and 64
-// products for out = S^T a, whose sum over kd is a halving exchange over the kd / 8 lanes
-// that share columns.  The arithmetic is fp32 throughout; the pass is bound by the CUDA
-// cores (2 kd vd fused multiply-adds per token and head against 2 kd + 2 vd elements moved).
+// slice) and keeps it in registers, 4 x 8 elements per thread, while the tokens stream
+// through shared memory in tiles of 16, the next tile's loads on their way.  Per token a thread
+// does 32 updates and 32 products for out = S^T a, whose sum over kd is a halving exchange over
+// the kd / 4 lanes that share columns.  The arithmetic is fp32 throughout.  Few blocks: bound by
+// a token's chain of exchanges, 0.3 us a token (7 packed sequences, 5003 tokens of 2 heads x 64 in
+// fp32, backward: 62 us in all).  Many: by issue slots, a quarter of the multiply-adds' rate
+// (8 x 4096 tokens of 16 heads x 128 in fp32, forward: 2.2 ms, the local pass 0.41 of it).  8 x 8
+// elements halve the exchanges, but the threads too: the packed call took 238 us with them and 86
+// with 4 x 8.
 #include <algorithm>
 #include <type_traits>
 
@@ -115,13 +119,24 @@ decay_rec_kernel(const DecayGeom g, const __grid_constant__ Passes passes) {
     // the thread's elements: row 4 dl + u of kd, column e0 + 8 eg + j
     float s[4][8];
     const float *in = decay_state_in(p, seg, H, h);
+    if (!in) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) s[u][j] = 0.f;
+    } else if (p.transposed) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int d = 4 * dl + u, e = e0 + 8 * eg + j;
-            s[u][j] = in ? in[p.transposed ? e * KD + d : d * vd + e] : 0.f;
+            const float4 x = *(const float4 *)&in[(e0 + 8 * eg + j) * KD + 4 * dl];
+            s[0][j] = x.x, s[1][j] = x.y, s[2][j] = x.z, s[3][j] = x.w;
         }
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int j = 0; j < 8; j += 4)
+                *(float4 *)&s[u][j] = *(const float4 *)&in[(4 * dl + u) * vd + e0 + 8 * eg + j];
+    }
     auto decay = [&](const DecayFactor &f) {
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -236,13 +251,17 @@ decay_rec_kernel(const DecayGeom g, const __grid_constant__ Passes passes) {
     float *to = decay_state_out(p, seg, H, h);
     if (!to) return;
     if (ntok > 0) decay(DecayFactor(gd * (float)((nb > 1 ? (ntok - 1) % kTb : 0) + (rev ? 1 : 0))));
+    if (p.transposed) {
 #pragma unroll
-    for (int u = 0; u < 4; ++u)
+        for (int j = 0; j < 8; ++j)
+            *(float4 *)&to[(e0 + 8 * eg + j) * KD + 4 * dl] = make_float4(s[0][j], s[1][j], s[2][j], s[3][j]);
+    } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int d = 4 * dl + u, e = e0 + 8 * eg + j;
-            to[p.transposed ? e * KD + d : d * vd + e] = s[u][j];
-        }
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int j = 0; j < 8; j += 4)
+                *(float4 *)&to[(4 * dl + u) * vd + e0 + 8 * eg + j] = *(const float4 *)&s[u][j];
+    }
 }
 
 // A few tokens of every sequence, the state updated in place.  A block owns 64 columns of
@@ -337,14 +356,23 @@ decay_combine_kernel(const DecayGeom g, const __grid_constant__ Passes passes) {
     const DecayFactor full(gd * (float)g.seg_tokens);
     float4 cur = p.s0 ? *(const float4 *)&p.s0[nh * st + at] : make_float4(0.f, 0.f, 0.f, 0.f);
     float *slots = p.slots + ((base - n) * g.H + h) * st + at;
-#pragma unroll 4
-    for (int64_t i = 0; i < cnt - 1; ++i) {
-        // reversed: the last segment, which may be short, comes first
-        const DecayFactor f = p.rev && i == 0 ? DecayFactor(gd * (float)(len - (cnt - 1) * g.seg_tokens)) : full;
-        float4 *sp = (float4 *)&slots[(p.rev ? cnt - 2 - i : i) * g.H * st];
-        const float4 x = *sp;
-        cur = make_float4(f(cur.x) + x.x, f(cur.y) + x.y, f(cur.z) + x.z, f(cur.w) + x.w);
-        *sp = cur;
+    // kAhead sums on their way at a time: the stores would keep later loads behind them
+    constexpr int kAhead = 4;
+    for (int64_t i0 = 0; i0 < cnt - 1; i0 += kAhead) {
+        float4 x[kAhead];
+        auto slot = [&](int64_t i) { return (float4 *)&slots[(p.rev ? cnt - 2 - i : i) * g.H * st]; };
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (i0 + k < cnt - 1) x[k] = *slot(i0 + k);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int64_t i = i0 + k;
+            if (i >= cnt - 1) break;
+            // reversed: the last segment, which may be short, comes first
+            const DecayFactor f = p.rev && i == 0 ? DecayFactor(gd * (float)(len - (cnt - 1) * g.seg_tokens)) : full;
+            cur = make_float4(f(cur.x) + x[k].x, f(cur.y) + x[k].y, f(cur.z) + x[k].z, f(cur.w) + x[k].w);
+            *slot(i) = cur;
+        }
     }
 }
 

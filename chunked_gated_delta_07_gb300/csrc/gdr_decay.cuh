@@ -26,11 +26,11 @@ namespace gdr {
 constexpr int kDecayTile = 128;   // tokens per tile
 
 struct DecayGeom {
-    Plan p;                  // packed input only (tiles of kDecayTile)
+    Plan p;                  // packed input only (no tiles)
     bool dense;
     int N, H;
     int64_t T_per, T_total;  // tokens per sequence (dense) / over all sequences
-    int64_t seg_tokens;      // tokens per segment (a multiple of kDecayTile)
+    int64_t seg_tokens;      // tokens per segment (tensor cores: a multiple of kDecayTile)
     int64_t segs_per_seq;    // dense: segments of a sequence
     int64_t max_segs;        // upper bound on the segments of all sequences
     int64_t max_slots;       // upper bound on the segment boundaries inside sequences

@@ -390,8 +390,9 @@ GDR_API gdr_status_t gdr_chunk_bwd(const void *q, const void *k, const void *v, 
  *              may be h0 (carried in place)
  *   scale      finite; multiplies the outputs only, not the state
  *   path       GDR_PATH_AUTO: the tcgen05 kernel for bf16 tensors that are 16-byte
- *              aligned, else the fp32 CUDA-core kernel; GDR_PATH_TC refuses
- *              (GDR_ERR_UNSUPPORTED) what the former does not take
+ *              aligned, else (and for sequences of at most 8 tokens; packed: 8 in all) the
+ *              fp32 CUDA-core kernel; GDR_PATH_TC refuses (GDR_ERR_UNSUPPORTED) what the
+ *              former cannot take
  *   workspace  16-byte aligned device scratch of gdr_decay_workspace_size(...) bytes, or
  *              NULL: the internal per-device cache (calls that share it must not
  *              overlap on the GPU)

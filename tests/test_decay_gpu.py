@@ -98,6 +98,15 @@ def test_backward_lengths(T, dtype, path):
     check_bwd(inputs(2, T, 2, 128, 128, dtype, 40 + T), path)
 
 
+@pytest.mark.parametrize("T", [1, 2, 7, 8, 9])
+@pytest.mark.parametrize("path", ["auto", "tc"])
+def test_short_sequences_on_either_path(T, path):
+    """At most 8 tokens run on the CUDA cores unless the tensor cores are asked for."""
+    x = inputs(3, T, 2, 128, 64, "bf16", 60 + T)
+    check_fwd(x, path)
+    check_bwd(x, path)
+
+
 @pytest.mark.parametrize("dk,dv", [(64, 64), (64, 128), (128, 64)])
 @pytest.mark.parametrize("dtype,path", [("bf16", "auto"), ("bf16", "simt"), ("f32", "auto")])
 def test_widths(dk, dv, dtype, path):
