@@ -105,11 +105,11 @@ struct DecayFactor {
     __device__ __forceinline__ float operator()(float x) const { return fmaf(x, f, near1 ? x : 0.f); }
 };
 
-// Tokens after which exp(n g) rounds to zero in fp32 (its smallest positive value is
-// e^-103.3): what a local pass need not read.
+// Tokens after which exp(n g) is below fp32's smallest normal number, e^-87.3: what a local
+// pass need not read.
 __device__ __forceinline__ int64_t decay_reach(float g, int64_t n) {
     if (!(g < 0.f)) return n;
-    const float r = 104.f / -g;
+    const float r = 88.f / -g;
     return r < (float)n ? min(n, (int64_t)r + 1) : n;
 }
 
