@@ -19,6 +19,12 @@
 // sums dw and db in registers; the block adds its groups in a fixed order through shared
 // memory and writes one partial sum per (block, column), and a second kernel adds those.
 // No atomics: the result is the same on every run.
+//
+// Measured (bf16): 524288 rows x 128 with 16 weight rows forward 47.7 us, 5.7 TB/s, 84% of a
+// copy's; backward 71.7 us, 5.7 TB/s.  8191 rows x 2048 backward 29.2 us, 3.5 TB/s: with 14 pairs
+// of rows to a block, the first loads, the last stores and the sum of 304 partials weigh as much
+// as the rows between them.  16 elements a thread, which halves the threads of a row's exchanges,
+// gave 48.4, 167 and 65 us.
 #include <algorithm>
 #include <initializer_list>
 #include <type_traits>
@@ -82,7 +88,9 @@ template <typename T, int VEC> __device__ __forceinline__ void store_n(T *p, con
 // backward pass, whose blocks each write a partial sum of the weights' gradients.
 template <int TPR> constexpr int fwd_threads() { return TPR > 256 ? TPR : 256; }
 template <int TPR> constexpr int bwd_threads() { return TPR > 512 ? TPR : 512; }
-constexpr int kThreadsPerSm = 1024;   // of either pass, as its registers allow
+// Of either pass on an SM, as its registers allow (1536 in the forward pass: 60 us for the first
+// call above against 48).
+constexpr int kThreadsPerSm = 1024;
 
 // Rows under way per thread: loads of 16-byte pieces go through a ring in shared memory
 // (asynchronous copies, each thread reading back its own: no barrier), 4 rows deep where the
@@ -375,7 +383,8 @@ norm_bwd_kernel(const T *dy, const T *x, const float *__restrict__ mean, const f
 }
 
 // out[c] = sum over the nb partial sums of column c, in a fixed order: 32 columns x 32
-// slices of the partials per block.
+// slices of the partials per block.  Bound by its start and the loads' latency: 6 us for
+// 5 MB of partials out of the L2, 2 to 3 of them behind the end of the pass (launched early).
 __global__ void __launch_bounds__(1024)
 norm_sum_kernel(const float *__restrict__ part, float *__restrict__ dw, float *__restrict__ db, int nb,
                 int64_t gd) {
