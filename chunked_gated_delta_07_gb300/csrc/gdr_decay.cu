@@ -330,11 +330,11 @@ decay_step_kernel(const T *__restrict__ q, const T *__restrict__ k, const T *__r
     }
 }
 
-// cur = s0; per segment in the order of the pass: cur = lam^len cur + its local sum, the
-// state that enters the next segment, written over the sum.  A block takes 1024 elements
-// of one (sequence, head).  Bound by the sums' latency, four on their way at a time: 18 boundaries
+// cur = s0; per segment in the order of the pass: cur = lam^len cur + its local sum (of its
+// parts, in order), the state that enters the next segment, written over the sum.  A block
+// takes 1024 elements of one (sequence, head).  Bound by the sums' latency, four on their way at a time: 18 boundaries
 // of 16 heads x 128 x 128 12 us (one at a time 16.5; eight 12.3, and 14.5 against 12.4 where there
-// are many short sequences).
+// are many short sequences), 16 with the slow heads' sums in three parts.
 __global__ void __launch_bounds__(256)
 decay_combine_kernel(const DecayGeom g, const __grid_constant__ Passes passes) {
     let_next_start();
@@ -358,6 +358,8 @@ decay_combine_kernel(const DecayGeom g, const __grid_constant__ Passes passes) {
     if (cnt < 2 || !GDR_INBOUNDS(base - n + cnt - 1 <= g.max_slots)) return;
     const float gd = decay_log(g.log_decay, h);
     const DecayFactor full(gd * (float)g.seg_tokens);
+    const int sums = decay_parts(g, gd);
+    const int64_t part_step = g.max_slots * g.H * st / 4;   // in float4
     float4 cur = p.s0 ? *(const float4 *)&p.s0[nh * st + at] : make_float4(0.f, 0.f, 0.f, 0.f);
     float *slots = p.slots + ((base - n) * g.H + h) * st + at;
     // (the stores would keep later loads behind them)
@@ -368,6 +370,16 @@ decay_combine_kernel(const DecayGeom g, const __grid_constant__ Passes passes) {
 #pragma unroll
         for (int k = 0; k < kAhead; ++k)
             if (i0 + k < cnt - 1) x[k] = *slot(i0 + k);
+        for (int j = 1; j < sums; ++j) {
+            float4 y[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (i0 + k < cnt - 1) y[k] = slot(i0 + k)[j * part_step];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (i0 + k < cnt - 1)
+                    x[k] = make_float4(x[k].x + y[k].x, x[k].y + y[k].y, x[k].z + y[k].z, x[k].w + y[k].w);
+        }
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const int64_t i = i0 + k;

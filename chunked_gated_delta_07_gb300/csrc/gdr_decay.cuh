@@ -34,6 +34,8 @@ struct DecayGeom {
     int64_t segs_per_seq;    // dense: segments of a sequence
     int64_t max_segs;        // upper bound on the segments of all sequences
     int64_t max_slots;       // upper bound on the segment boundaries inside sequences
+    int parts;               // pieces that a local pass cuts a segment into at most ...
+    int64_t part_tokens;     // ... of this many tokens each, counted from where its sum ends
     const float *log_decay;  // [H]
 };
 
@@ -42,7 +44,8 @@ struct DecayPass {
     void *out;               // [rows][H][vd]
     const float *s0;         // entering states [N][H][...] or null (zero)
     float *sT;               // leaving states [N][H][...] or null
-    float *slots;            // boundary states [max_slots][H][...] or null (no segments)
+    float *slots;            // boundary states [max_slots][H][...] or null (no segments); as
+                             // many again for the sums of each further part
     int kd, vd;
     // the states in memory are [kd][vd], or [vd][kd] (the pass's state transposed)
     bool transposed;
@@ -111,6 +114,12 @@ __device__ __forceinline__ int64_t decay_reach(float g, int64_t n) {
     if (!(g < 0.f)) return n;
     const float r = 88.f / -g;
     return r < (float)n ? min(n, (int64_t)r + 1) : n;
+}
+
+// Parts of a segment that the local pass sums for a head with log-decay g, and combine adds.
+__device__ __forceinline__ int decay_parts(const DecayGeom &geom, float g) {
+    const int64_t reach = decay_reach(g, geom.seg_tokens);
+    return (int)min((int64_t)geom.parts, (reach + geom.part_tokens - 1) / geom.part_tokens);
 }
 
 // Where a pass's segment finds its entering state and leaves its last one (null: zero, or

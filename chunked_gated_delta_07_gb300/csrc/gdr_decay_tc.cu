@@ -83,7 +83,7 @@ struct TcArgs {
     DecayGeom g;
     DecayPass pass[kMaxPasses];
     int npass;
-    int64_t units;      // max_segs * H * npass
+    int64_t units;      // max_segs * H * npass, and times the parts in a local pass
     unsigned long long *next;   // the next unit to take, or null: units by stride
     bool long_first;            // the counter runs over all units twice
     int *status;
@@ -113,8 +113,11 @@ __device__ __forceinline__ bool wait_use(uint64_t *b, uint32_t use, uint64_t lim
 // One unit of a block's walk, put into shared memory by the producer for all warps.
 struct Unit {
     int64_t t0, t1;    // tokens it runs (a local pass: those that reach the segment's end)
-    const float *in;   // entering state (null: zero) and where to leave the last one (or null)
-    float *to;
+    union {
+        const float *in;   // entering state (null: zero)
+        int64_t past;      // a local pass's: tokens between it and where its sum ends
+    };
+    float *to;         // where to leave the last state (or null)
     float gd;          // the head's log-decay
     int pass, h, tiles;   // tiles < 0: no more units
 };
@@ -122,8 +125,13 @@ constexpr uint32_t kRing = 4;   // units announced ahead
 
 // False where unit u has nothing to do.
 __device__ __forceinline__ bool unit_of(const TcArgs &A, int64_t u, bool local, Unit &o) {
-    const uint32_t u32 = (uint32_t)u, sh = u32 / (uint32_t)A.npass;   // fewer than 2^31 units
-    o.pass = (int)(u32 - sh * (uint32_t)A.npass);
+    uint32_t sh = (uint32_t)u, part = 0;   // fewer than 2^31 units
+    o.pass = (int)(sh % (uint32_t)A.npass);
+    sh /= (uint32_t)A.npass;
+    if (local) {
+        part = sh % (uint32_t)A.g.parts;
+        sh /= (uint32_t)A.g.parts;
+    }
     const uint32_t sg = sh / (uint32_t)A.g.H;
     o.h = (int)(sh - sg * (uint32_t)A.g.H);
     DecaySeg seg;
@@ -134,17 +142,27 @@ __device__ __forceinline__ bool unit_of(const TcArgs &A, int64_t u, bool local, 
     o.t1 = seg.t1;
     if (local) {
         if (p.rev ? seg.first : seg.last) return false;   // no boundary behind it
+        if ((int)part >= decay_parts(A.g, o.gd)) return false;
         // whole tiles: the segment is one (reversed: but for its sequence's last tile)
         const int64_t reach = (decay_reach(o.gd, o.t1 - o.t0) + kC - 1) / kC * kC;
-        if (p.rev) o.t1 = min(o.t1, o.t0 + reach); else o.t0 = max(o.t0, o.t1 - reach);
+        const int64_t past = part * A.g.part_tokens, end = min(reach, past + A.g.part_tokens);
+        if (p.rev) {
+            o.t1 = min(o.t1, o.t0 + end);
+            o.t0 = min(o.t1, o.t0 + past);
+        } else {
+            o.t0 = max(o.t0, o.t1 - end);
+            o.t1 = max(o.t0, o.t1 - past);
+        }
     }
     o.tiles = (int)((o.t1 - o.t0 + kC - 1) / kC);
-    o.in = decay_state_in(p, seg, A.g.H, o.h);
+    if (local) o.past = part * A.g.part_tokens;
+    else o.in = decay_state_in(p, seg, A.g.H, o.h);
     o.to = decay_state_out(p, seg, A.g.H, o.h);
+    if (local) o.to += (int64_t)part * A.g.max_slots * A.g.H * p.kd * p.vd;
     return GDR_INBOUNDS(seg.t0 >= 0 && seg.t1 <= A.g.T_total && seg.slot <= A.g.max_slots);
 }
 // The block's next unit (one warp): those of its stride, or from the counter.  Where there are
-// not very many the counter runs over all twice -- those of more than half a segment's tiles
+// not very many the counter runs over all twice -- those of more than half the most tiles
 // first, then the others, so that the blocks end together.  False at the end.  `n`: the last one (blockIdx.x -
 // gridDim.x at the start).
 __device__ __forceinline__ bool take_unit(const TcArgs &A, bool local, int64_t &n, Unit &u) {
@@ -162,7 +180,7 @@ __device__ __forceinline__ bool take_unit(const TcArgs &A, bool local, int64_t &
         }
         if (i >= A.units) return false;
         if (unit_of(A, i, local, u) &&
-            (!A.long_first || (2 * (int64_t)u.tiles * kC > A.g.seg_tokens) == want_long))
+            (!A.long_first || (2 * (int64_t)u.tiles * kC > (local ? A.g.part_tokens : A.g.seg_tokens)) == want_long))
             return true;
     }
 }
@@ -863,8 +881,9 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
 // Every write's weight is its distance to the segment's end, so the sum of C'^T B over the tiles
 // needs no decay on the way.  Four groups of four warps take 32 tokens of a tile each, through
 // five slots of C' in TMEM; four more add a tile's product to the sum, which they keep in
-// registers, while the next one's runs in the other accumulator.  262144 tokens of 16 heads:
-// 199 us, 0.93 us a tile, of which the tensor cores' 24 products take 0.8.
+// registers, while the next one's runs in the other accumulator.  262144 tokens of 16 heads, 19
+// segments in up to 3 parts: 150 us, 4.1 TB/s.  A tile takes an SM 1.9 us, near the 1.6 that its
+// copies need for 64 KB; the rest is units that do not come out even.
 constexpr int kLocThreads = 32 * 24, kLocProducer = 20, kLocIssuer = 21;   // warps
 constexpr int kLocStages = 3;
 constexpr uint32_t kLocStage = 2 * kTile;                    // B, C
@@ -1040,7 +1059,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                 const uint32_t slot = n % kLocSlots, use = n / kLocSlots;
                 const int len = walk.len(i);
                 // past the tile: its distance to the segment's end (its start, reversed)
-                const int64_t past = rev ? (int64_t)(walk.tiles - 1 - i) * kC : tokens - (int64_t)i * kC - len;
+                const int64_t past = u.past + (rev ? (int64_t)(walk.tiles - 1 - i) * kC : tokens - (int64_t)i * kC - len);
                 __syncwarp();   // the last tile's weights are read
                 w[lane] = token_weight(32 * grp + lane, len, rev, gd, s_upd, past);
                 __syncwarp();
@@ -1113,7 +1132,7 @@ cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, 
     }
     args.g = g;
     args.npass = n;
-    args.units = g.max_segs * g.H * n;
+    args.units = g.max_segs * g.H * n * (local ? g.parts : 1);
     args.next = next;
     args.long_first = next && args.units <= 64 * (int64_t)sms;   // a look at a unit costs some 0.3 us
     args.status = status;

@@ -134,6 +134,16 @@ def test_segments(seg_tiles, lens, dtype, path):
     check_bwd(x, path)
 
 
+@pytest.mark.parametrize("seg_tiles", [8, 11, 12], indirect=True)
+@pytest.mark.parametrize("B,T", [(1, 5000), (2, 3333)])
+def test_segments_summed_in_parts(seg_tiles, B, T):
+    """Segments of 8 tiles or more are summed in parts, for the heads that remember that far:
+    memories of all parts, some of them and the last few tokens alone."""
+    x = inputs(B, T, 5, 64, 128, "bf16", 160 + seg_tiles, slopes=[0.0, 0.002, 0.1, 0.2, 3.0])
+    check_fwd(x)
+    check_bwd(x)
+
+
 @pytest.mark.parametrize("path", ["auto", "simt"])
 def test_long_sequence_uses_segments(path):
     x = inputs(1, 9000, 1, 128, 128, "bf16", 130, slopes=[0.004])
