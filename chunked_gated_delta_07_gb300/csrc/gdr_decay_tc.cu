@@ -34,6 +34,9 @@
 //   warp 20      TMA loads of A, B, C, two stages of 96 KB
 //   warp 21      issues every MMA (their order in the tensor pipe is the issue order)
 //   warp 22      TMA stores of the outputs, out of their tile's A
+// Where both widths are 64 (kNarrow) there is room for more: four stages of 48 KB, a whole tile's
+// C' in TMEM, and, as the state takes half the registers, four warps of their own (20-23) for
+// O -> out (65536 tokens of 32 heads x 64 in 37 sequences: 391 us against 400).
 // What is left of the bound (8 x 4096 tokens of 16 heads, 128 units on 152 SMs: 116 us, 3.6 us a
 // tile; 262144 tokens: 82% of the measured bandwidth): a tile's chain through its A -- load, Sc,
 // P, O, store -- takes some 14000 cycles, with two tiles in flight.
@@ -72,6 +75,7 @@ constexpr int kC = kDecayTile;
 constexpr int kMaxPasses = kDecayMaxPasses;
 constexpr uint32_t kBox = kC * 128;        // 64 columns x 128 tokens, 128-byte rows, swizzled
 constexpr uint32_t kTile = 2 * kBox;       // one tensor's tile: up to two boxes
+constexpr uint32_t kBarBytes = 384;        // of a block's barriers
 constexpr unsigned kFull = 0xffffffffu;
 constexpr uint64_t kWaitNs = 2000000000ull;   // pipeline wait limit: 2 s
 constexpr uint64_t kDrainNs = 2000000000ull;  // drains before exit
@@ -322,11 +326,11 @@ __device__ __forceinline__ void tmem_arrived(uint32_t (&r)[16]) {
 }
 // Row e of S^T in registers, s[j] = (S[2j][e], S[2j+1][e]): from memory (zeros past the
 // widths and for a null `in`), back, and in bf16 to shared memory as a K-major tile's row.
-using StateRow = uint64_t[kC / 2];
-template <int kVd>
-__device__ __forceinline__ void state_load(const DecayPass &p, const float *in, int e, StateRow &s) {
+template <int kKd> using StateRow = uint64_t[kKd / 2];   // kKd: the widest kd
+template <int kVd, int kKd>
+__device__ __forceinline__ void state_load_from(const DecayPass &p, const float *in, int e, StateRow<kKd> &s) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kKd / 64; ++h) {
         if (64 * h >= p.kd) break;
         if (p.transposed) {
             const ulonglong2 *row = (const ulonglong2 *)(in + e * p.kd + 64 * h);
@@ -343,16 +347,18 @@ __device__ __forceinline__ void state_load(const DecayPass &p, const float *in, 
         }
     }
 }
-__device__ __forceinline__ void state_load(const DecayPass &p, const float *in, int e, StateRow &s) {
+template <int kKd>
+__device__ __forceinline__ void state_load(const DecayPass &p, const float *in, int e, StateRow<kKd> &s) {
 #pragma unroll
-    for (int j = 0; j < kC / 2; ++j) s[j] = 0;
+    for (int j = 0; j < kKd / 2; ++j) s[j] = 0;
     if (!in || e >= p.vd) return;
-    if (p.vd == 64) state_load<64>(p, in, e, s);
-    else state_load<128>(p, in, e, s);
+    if (p.vd == 64) state_load_from<64, kKd>(p, in, e, s);
+    else state_load_from<128, kKd>(p, in, e, s);
 }
-template <int kVd> __device__ __forceinline__ void state_store(const DecayPass &p, float *to, int e, const StateRow &s) {
+template <int kVd, int kKd>
+__device__ __forceinline__ void state_store_to(const DecayPass &p, float *to, int e, const StateRow<kKd> &s) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kKd / 64; ++h) {
         if (64 * h >= p.kd) break;
         if (p.transposed) {
             ulonglong2 *row = (ulonglong2 *)(to + e * p.kd + 64 * h);
@@ -368,14 +374,16 @@ template <int kVd> __device__ __forceinline__ void state_store(const DecayPass &
         }
     }
 }
-__device__ __forceinline__ void state_store(const DecayPass &p, float *to, int e, const StateRow &s) {
+template <int kKd>
+__device__ __forceinline__ void state_store(const DecayPass &p, float *to, int e, const StateRow<kKd> &s) {
     if (e >= p.vd) return;
-    if (p.vd == 64) state_store<64>(p, to, e, s);
-    else state_store<128>(p, to, e, s);
+    if (p.vd == 64) state_store_to<64, kKd>(p, to, e, s);
+    else state_store_to<128, kKd>(p, to, e, s);
 }
-__device__ __forceinline__ void state_to_bf16(const StateRow &s, uint8_t *tile, int e, int kd) {
+template <int kKd>
+__device__ __forceinline__ void state_to_bf16(const StateRow<kKd> &s, uint8_t *tile, int e, int kd) {
 #pragma unroll
-    for (int j = 0; j < kC / 8; ++j) {
+    for (int j = 0; j < kKd / 8; ++j) {
         if (8 * j == 64 && kd == 64) break;
         *(uint4 *)(tile + (j >> 3) * kBox + sw128_off(e, (j & 7) * 16)) =
             make_uint4(pack2(s[4 * j]), pack2(s[4 * j + 1]), pack2(s[4 * j + 2]), pack2(s[4 * j + 3]));
@@ -383,10 +391,10 @@ __device__ __forceinline__ void state_to_bf16(const StateRow &s, uint8_t *tile, 
 }
 // s <- s fa + s fb + the kd TMEM columns from `at` on, in fp32 (a whole warp); the factors, in
 // pairs, are (1, lam^n - 1) near 1 and (lam^n, 0) otherwise.  Without kDecay s is only added to.
-template <bool kDecay>
-__device__ __forceinline__ void state_add(StateRow &s, uint32_t at, int kd, uint64_t fa, uint64_t fb) {
+template <bool kDecay, int kKd>
+__device__ __forceinline__ void state_add(StateRow<kKd> &s, uint32_t at, int kd, uint64_t fa, uint64_t fb) {
 #pragma unroll
-    for (int m = 0; m < kC / 16; ++m) {
+    for (int m = 0; m < kKd / 16; ++m) {
         if (m == 4 && kd == 64) break;
         uint32_t r[16];
         tmem_ld16(at + 16 * m, r);
@@ -419,51 +427,66 @@ template <typename F> __device__ __forceinline__ void tmem_columns(uint32_t at, 
 // ---------------------------------------------------------------------------
 // the output pass
 // ---------------------------------------------------------------------------
-constexpr int kOutThreads = 32 * 24, kOutProducer = 20, kOutIssuer = 21, kOutStore = 22;   // warps
+// (one warp, the last, fills up its warpgroup and has nothing to do)
+constexpr int kOutWarps = 24, kOutWarpsNarrow = 28;
 // TMEM columns
 constexpr uint32_t kColS = 0;      // Sc; P in the first 32 columns of each of its halves
 constexpr uint32_t kColO = 128;
-constexpr uint32_t kColU = 256;    // the tile's part of the new S^T
-constexpr uint32_t kColV = 384;    // C'^T: slots of 32 tokens x 3 terms
-constexpr uint32_t kSlotCols = 48, kSlots = 2, kParts = kC / 32;   // kParts uses of slots per tile
+// then U, the tile's part of the new S^T, and slots of C'^T, 32 tokens x 3 terms each: 2 of them,
+// or a tile's 4 where both widths are 64 (kNarrow)
+constexpr uint32_t kSlotCols = 48, kMaxSlots = 4, kParts = kC / 32;   // kParts uses of slots per tile
 constexpr uint32_t kTmemCols = 512;
-static_assert(kColV + kSlots * kSlotCols <= kTmemCols, "TMEM");
 // shared memory
-constexpr uint32_t kStage = 3 * kTile;               // A, B, C
-constexpr uint32_t kOffH = 2 * kStage;               // the state in bf16, [e][d], K-major
+constexpr uint32_t kMaxStages = 4;                   // tiles in flight: 2 of 96 KB, or 4 of 48 (kNarrow)
+constexpr uint32_t kOffH = 2 * 3 * kTile;            // the state in bf16, [e][d], K-major
 constexpr uint32_t kOffBar = kOffH + kTile;
-constexpr uint32_t kOffW = kOffBar + 320;            // weights of a group's 64 tokens, a copy per warp
+constexpr uint32_t kOffW = kOffBar + kBarBytes;            // weights of a group's 64 tokens, a copy per warp
 constexpr uint32_t kOffRing = kOffW + 8 * (kC / 2) * 4;
 constexpr uint32_t kSmemOut = kOffRing + kRing * sizeof(Unit);
 static_assert(kSmemOut <= 232448, "shared memory");
-// Registers of a thread at launch (what 768 threads may have) and from then on, by role: the
-// increase draws on the registers that the block was launched with.
-constexpr int kRegsLaunch = 80, kRegsOut = 64, kRegsState = 168, kRegsV = 64, kRegsOther = 56;
-static_assert(2 * kRegsOut + kRegsState + 2 * kRegsV + kRegsOther <= 6 * kRegsLaunch, "registers");
+// Registers of a thread at launch (what 768, or narrow 896, threads may have); by role from then
+// on, where the increase draws on the registers that the block was launched with.
+constexpr int kRegsLaunch = 80, kRegsLaunchNarrow = 72;
 
 struct OutBars {
-    uint64_t u_full[kRing], u_free[kRing];   // a unit announced / done with (22 warps)
-    uint64_t full_a[2];    // a stage's A has arrived
-    uint64_t full_bc[2];   // ... its B and C
-    uint64_t free_a[2];    // the stage's A is read, and the outputs that went through it
-    uint64_t free_bc[2];   // ... its B and C
+    uint64_t u_full[kRing], u_free[kRing];   // a unit announced / done with (every warp that takes units)
+    uint64_t full_a[kMaxStages];    // a stage's A has arrived
+    uint64_t full_bc[kMaxStages];   // ... its B and C
+    uint64_t free_a[kMaxStages];    // the stage's A is read, and the outputs that went through it
+    uint64_t free_bc[kMaxStages];   // ... its B and C
     uint64_t s_full;       // Sc complete
     uint64_t p_ready;      // P written (8 warps)
     uint64_t o_full;       // O complete
-    uint64_t o_free;       // O read and in shared memory (8 warps)
+    uint64_t o_free;       // O read (8 warps; narrow: 4)
+    // ... and in shared memory.  One per stage: the stores, which wait for every one, may be a
+    // tile late, and a barrier that had moved on twice would look as if it had not moved.
+    uint64_t staged[kMaxStages];
     uint64_t s_free;       // U read (4 warps)
     uint64_t h_ready;      // the bf16 state written (4 warps)
-    uint64_t v_ready[kSlots];   // a slot of C' written (8 warps)
-    uint64_t v_free[kSlots];    // ... read
+    uint64_t v_ready[kMaxSlots];   // a slot of C' written (8 warps)
+    uint64_t v_free[kMaxSlots];    // ... read
     uint64_t kv_full;      // U complete, and the bf16 state read
     uint64_t fin;          // every MMA of the block complete
     uint32_t tmem;
     int stop;
 };
-static_assert(sizeof(OutBars) <= 320, "barriers");
+static_assert(sizeof(OutBars) <= kBarBytes, "barriers");
 
-__global__ void __launch_bounds__(kOutThreads, 1)
+template <bool kNarrow>
+__global__ void __launch_bounds__(32 * (kNarrow ? kOutWarpsNarrow : kOutWarps), 1)
 decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs A) {
+    constexpr uint32_t kColU = kColO + (kNarrow ? 64 : kC), kColV = kColU + (kNarrow ? 64 : kC);
+    constexpr int kOutProducer = (kNarrow ? kOutWarpsNarrow : kOutWarps) - 4, kOutIssuer = kOutProducer + 1;
+    constexpr int kOutStore = kOutProducer + 2;
+    constexpr uint32_t kSlots = kNarrow ? 4 : 2;
+    constexpr uint32_t kTileBytes = kNarrow ? kBox : kTile, kStageBytes = 3 * kTileBytes;   // A, B, C
+    constexpr uint32_t kStages = kNarrow ? kMaxStages : 2;
+    static_assert(kStages * kStageBytes <= kOffH, "stages");
+    constexpr int kKd = kNarrow ? 64 : kC;
+    constexpr int kRegsOut = 64, kRegsState = kNarrow ? 136 : 168, kRegsV = 64;
+    constexpr int kRegsO = kNarrow ? 48 : 0, kRegsOther = kNarrow ? 64 : 56;
+    static_assert(2 * kRegsOut + kRegsState + 2 * kRegsV + kRegsO + kRegsOther <=
+                      (kNarrow ? 7 * kRegsLaunchNarrow : 6 * kRegsLaunch), "registers");
     extern __shared__ __align__(1024) uint8_t smem[];
     OutBars &bar = *(OutBars *)(smem + kOffBar);
     Unit *ring = (Unit *)(smem + kOffRing);
@@ -476,12 +499,13 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
     if (tid == 0) {
         for (uint32_t i = 0; i < kRing; ++i) {
             mbar_init(&bar.u_full[i], 1);
-            mbar_init(&bar.u_free[i], 22);
+            mbar_init(&bar.u_free[i], kNarrow ? 26 : 22);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (uint32_t i = 0; i < kStages; ++i) {
             mbar_init(&bar.full_a[i], 1);
             mbar_init(&bar.full_bc[i], 1);
             mbar_init(&bar.free_a[i], 1);
+            mbar_init(&bar.staged[i], kNarrow ? 4 : 8);
             mbar_init(&bar.free_bc[i], 1);
         }
         for (uint32_t i = 0; i < kSlots; ++i) {
@@ -491,7 +515,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
         mbar_init(&bar.s_full, 1);
         mbar_init(&bar.p_ready, 8);
         mbar_init(&bar.o_full, 1);
-        mbar_init(&bar.o_free, 8);
+        mbar_init(&bar.o_free, kNarrow ? 4 : 8);
         mbar_init(&bar.s_free, 4);
         mbar_init(&bar.h_ready, 4);
         mbar_init(&bar.kv_full, 1);
@@ -524,6 +548,32 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
         }
     };
 
+    // O of tile n out through its A (whose products are complete), in bf16 in the layout of the
+    // store's boxes: 16 m columns from c0 of the thread's row, times f.
+    auto take_o = [&](uint32_t n, int row, int c0, int pieces, uint32_t lanes, float f) {
+        if (!wait(&bar.o_full, n)) return false;
+        tc_fence_after();
+        const uint64_t f2 = two(f, f);
+        uint8_t *buf = smem + (n % kStages) * kStageBytes;
+        tmem_columns(lanes + kColO + c0, pieces, [&](int m, const uint32_t (&x)[16]) {
+            uint32_t o[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = pack2(mul2((uint64_t)x[2 * j + 1] << 32 | x[2 * j], f2));
+            const int col = c0 + 16 * m;
+            uint8_t *to = buf + (col >> 6) * kBox;
+            *(uint4 *)(to + sw128_off(row, (col & 63) * 2)) = make_uint4(o[0], o[1], o[2], o[3]);
+            *(uint4 *)(to + sw128_off(row, (col & 63) * 2 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
+        });
+        tc_fence_before();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+            mbar_arrive(&bar.o_free);
+            mbar_arrive(&bar.staged[n % kStages]);
+        }
+        return true;
+    };
+
     if (warp >= kOutProducer) {
         set_registers<kRegsOther, false>();
         if (warp == kOutProducer) {
@@ -548,18 +598,18 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                     for (int i = 32 * lane; i < kd * vd; i += 1024)
                         asm volatile("prefetch.global.L2 [%0];" ::"l"(u.in + i));
                 for (int i = 0; i < walk.tiles; ++i, ++it) {
-                    const uint32_t st = it & 1;
+                    const uint32_t st = it % kStages;
                     const int64_t t = walk.first(u, i);
-                    uint8_t *s = smem + st * kStage;
-                    if (it >= 2 && !(ok = wait(&bar.free_bc[st], (it >> 1) - 1))) break;
+                    uint8_t *s = smem + st * kStageBytes;
+                    if (it >= kStages && !(ok = wait(&bar.free_bc[st], (it / kStages) - 1))) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&bar.full_bc[st], (kd + vd) / 64 * kBox);
-                        load_tile(s + kTile, &maps.b[u.pass], kd, u.h, t, &bar.full_bc[st]);
-                        load_tile(s + 2 * kTile, &maps.c[u.pass], vd, u.h, t, &bar.full_bc[st]);
+                        load_tile(s + kTileBytes, &maps.b[u.pass], kd, u.h, t, &bar.full_bc[st]);
+                        load_tile(s + 2 * kTileBytes, &maps.c[u.pass], vd, u.h, t, &bar.full_bc[st]);
                     }
                     __syncwarp();
                     ++nbc;
-                    if (it >= 2 && !(ok = wait(&bar.free_a[st], (it >> 1) - 1))) break;
+                    if (it >= kStages && !(ok = wait(&bar.free_a[st], (it / kStages) - 1))) break;
                     if (lane == 0) {
                         mbar_arrive_expect_tx(&bar.full_a[st], kd / 64 * kBox);
                         load_tile(s, &maps.a[u.pass], kd, u.h, t, &bar.full_a[st]);
@@ -568,10 +618,10 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 }
             }
             // never leave with a copy in flight
-            for (uint32_t k = it >= 2 ? it - 2 : 0; k < it; ++k)
-                __all_sync(kFull, mbar_wait(&bar.full_a[k & 1], (k >> 1) & 1u, kDrainNs));
-            for (uint32_t k = nbc >= 2 ? nbc - 2 : 0; k < nbc; ++k)
-                __all_sync(kFull, mbar_wait(&bar.full_bc[k & 1], (k >> 1) & 1u, kDrainNs));
+            for (uint32_t k = it >= kStages ? it - kStages : 0; k < it; ++k)
+                __all_sync(kFull, mbar_wait(&bar.full_a[k % kStages], (k / kStages) & 1u, kDrainNs));
+            for (uint32_t k = nbc >= kStages ? nbc - kStages : 0; k < nbc; ++k)
+                __all_sync(kFull, mbar_wait(&bar.full_bc[k % kStages], (k / kStages) & 1u, kDrainNs));
         } else if (warp == kOutIssuer) {
             const uint32_t s0 = smem_u32(smem);
             const bool lead = elect_one();
@@ -586,9 +636,9 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 const uint32_t id_o2 = instr_desc(kC, p.vd, 1, false, true);
                 const uint32_t id_h = instr_desc(kC, kd, 1, false, true);
                 for (int i = 0; i < walk.tiles; ++i, ++it) {
-                    const uint32_t st = it & 1;
-                    const uint32_t sa = s0 + st * kStage, sb = sa + kTile, sc = sb + kTile;
-                    if (!(ok = wait(&bar.full_bc[st], it >> 1)) || !(ok = wait(&bar.full_a[st], it >> 1))) break;
+                    const uint32_t st = it % kStages;
+                    const uint32_t sa = s0 + st * kStageBytes, sb = sa + kTileBytes, sc = sb + kTileBytes;
+                    if (!(ok = wait(&bar.full_bc[st], it / kStages)) || !(ok = wait(&bar.full_a[st], it / kStages))) break;
                     tc_fence_after();
                     const uint64_t dA = smem_desc(sa, 16, 1024, kSw128), dB = smem_desc(sb, 16, 1024, kSw128);
                     const uint64_t dBt = smem_desc(sb, kBox, 1024, kSw128), dCt = smem_desc(sc, kBox, 1024, kSw128);
@@ -602,7 +652,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
 #pragma unroll
                     for (uint32_t k = 0; k < kParts; ++k) {
                         const uint32_t slot = k % kSlots, av = tm + kColV + slot * kSlotCols;
-                        if (k == kSlots) {   // while the slots are filled again
+                        if (k == kParts / 2) {   // while the slots are filled again
                             if (!(ok = wait(&bar.h_ready, it)) || (it && !(ok = wait(&bar.o_free, it - 1)))) break;
                             tc_fence_after();
 #pragma unroll
@@ -645,8 +695,8 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 for (int i = 0; i < walk.tiles; ++i, ++it) {
                     const int len = walk.len(i);
                     const int64_t t = walk.first(u, i);
-                    const uint8_t *buf = smem + (it & 1) * kStage;
-                    if (!(ok = wait(&bar.o_free, it))) break;
+                    const uint8_t *buf = smem + (it % kStages) * kStageBytes;
+                    if (!(ok = wait(&bar.staged[it % kStages], it / kStages))) break;
                     if (len == kC) {
                         if (lane == 0) {
                             for (int b = 0; b < vd; b += 64)
@@ -664,7 +714,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                         fence_proxy_async_smem();
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.free_a[it & 1]);
+                    if (lane == 0) mbar_arrive(&bar.free_a[it % kStages]);
                 }
                 return ok;
             });
@@ -741,28 +791,27 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.p_ready);
-                if (!(ok = wait(&bar.o_full, it))) break;
-                tc_fence_after();
-                // O in bf16 goes out through the tile's A (its products are complete), in the
-                // layout of the store's boxes
-                const float f = s_out * exp2_approx(lf);
-                const uint64_t f2 = two(f, f);
-                uint8_t *buf = smem + (it & 1) * kStage;
-                tmem_columns(lanes + kColO + half * (vd / 2), vd / 32, [&](int m, const uint32_t (&x)[16]) {
-                    uint32_t o[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) o[j] = pack2(mul2((uint64_t)x[2 * j + 1] << 32 | x[2 * j], f2));
-                    const int col = half * (vd / 2) + 16 * m;
-                    uint8_t *to = buf + (col >> 6) * kBox;
-                    *(uint4 *)(to + sw128_off(row, (col & 63) * 2)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *(uint4 *)(to + sw128_off(row, (col & 63) * 2 + 16)) = make_uint4(o[4], o[5], o[6], o[7]);
-                });
-                tc_fence_before();
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.o_free);
+                if constexpr (!kNarrow) {
+                    const float f = s_out * exp2_approx(lf);
+                    if (!(ok = take_o(it, row, half * (vd / 2), vd / 32, lanes, f))) break;
+                }
             }
             return ok;
+        });
+    } else if (kNarrow && warp >= 20) {
+        // ---- outputs: thread = token row of the tile
+        set_registers<kNarrow ? kRegsO : kRegsOther, false>();
+        const int row = tid & 127;
+        const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
+        each_unit([&](const Unit &u) {
+            const DecayPass &p = A.pass[u.pass];
+            const Walk walk(u, p.rev);
+            const float g2 = decay_log2(u.gd);
+            for (int i = 0; i < walk.tiles; ++i, ++it) {
+                const float lf = fmaxf(g2 * (float)(walk.rev ? max(walk.len(i) - 1 - row, 0) : row + 1), -64.f);
+                if (!take_o(it, row, 0, 4, lanes, p.s_out * exp2_approx(lf))) return false;
+            }
+            return true;
         });
     } else if (warp < 12) {
         // ---- state: thread = value index (TMEM lane), whose row of S^T it keeps in registers
@@ -781,8 +830,8 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                     for (int d = e; d < kd * p.vd; d += 128) u.to[d] = u.in ? u.in[d] : 0.f;
                 return true;
             }
-            StateRow s;
-            state_load(p, u.in, e, s);
+            StateRow<kKd> s;
+            state_load<kKd>(p, u.in, e, s);
             uint64_t fa = 0, fb = 0;   // factors of s over flen tokens: s fa + s fb
             int flen = -1;
             // the update of tile i (whose number is n): kv_full says it is complete
@@ -793,7 +842,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                     fa = f.near1 ? two(1.f, 1.f) : two(f.f, f.f);
                     fb = f.near1 ? two(f.f, f.f) : 0;
                 }
-                if (any) state_add<true>(s, lanes + kColU, kd, fa, fb);
+                if (any) state_add<true, kKd>(s, lanes + kColU, kd, fa, fb);
             };
             for (int i = 0; i < walk.tiles; ++i, ++it) {
                 if (it && !(ok = wait(&bar.kv_full, it - 1))) break;
@@ -802,7 +851,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.s_free);
-                if (any) state_to_bf16(s, smem + kOffH, e, kd);
+                if (any) state_to_bf16<kKd>(s, smem + kOffH, e, kd);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.h_ready);
@@ -811,7 +860,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                 if (!(ok = wait(&bar.kv_full, it - 1))) return false;
                 tc_fence_after();
                 update(walk.tiles - 1);
-                state_store(p, u.to, e, s);
+                state_store<kKd>(p, u.to, e, s);
             }
             return ok;
         });
@@ -830,7 +879,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             const bool any = e < p.vd;   // (by warps; the other lanes' sums are nobody's)
             int wlen = -1;   // tokens of the tile that the weights are for
             for (int i = 0; i < walk.tiles; ++i, ++it) {
-                const uint32_t st = it & 1;
+                const uint32_t st = it % kStages;
                 const int len = walk.len(i);
                 if (len != wlen) {
                     __syncwarp();   // the last tile's weights are read
@@ -840,11 +889,11 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
                     __syncwarp();
                     wlen = len;
                 }
-                if (!(ok = wait(&bar.full_bc[st], it >> 1))) break;
-                uint8_t *ct = smem + st * kStage + 2 * kTile;
+                if (!(ok = wait(&bar.full_bc[st], it / kStages))) break;
+                uint8_t *ct = smem + st * kStageBytes + 2 * kTileBytes;
                 if (len < kC) {   // the products with P and with S^ read these rows too
                     if (any) zero_columns(ct, e & ~31, len, lane);   // both groups the same zeros
-                    zero_rows(ct - kTile, p.kd, len, warp - 12, 8, lane);
+                    zero_rows(ct - kTileBytes, p.kd, len, warp - 12, 8, lane);
                     fence_proxy_async_smem();
                     __syncwarp();
                 }
@@ -885,30 +934,35 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
 // segments in up to 3 parts: 150 us, 4.1 TB/s.  A tile takes an SM 1.9 us, near the 1.6 that its
 // copies need for 64 KB; the rest is units that do not come out even.
 constexpr int kLocThreads = 32 * 24, kLocProducer = 20, kLocIssuer = 21;   // warps
-constexpr int kLocStages = 3;
-constexpr uint32_t kLocStage = 2 * kTile;                    // B, C
-constexpr uint32_t kLocOffBar = kLocStages * kLocStage;
-constexpr uint32_t kLocOffW = kLocOffBar + 320;              // weights, a copy per warp
+constexpr int kLocMaxStages = 6;                             // 3 of 64 KB, or 6 of 32 (kNarrow)
+constexpr uint32_t kLocOffBar = 3 * 2 * kTile;
+constexpr uint32_t kLocOffW = kLocOffBar + kBarBytes;              // weights, a copy per warp
 constexpr uint32_t kLocOffRing = kLocOffW + 16 * 32 * 4;
 constexpr uint32_t kSmemLocal = kLocOffRing + kRing * sizeof(Unit);
-constexpr uint32_t kLocColV = 2 * kC, kLocSlots = 5;         // after two accumulators
-constexpr int kLocRegsV = 64, kLocRegsState = 176, kLocRegsOther = 48;
-static_assert(4 * kLocRegsV + kLocRegsState + kLocRegsOther <= 6 * kRegsLaunch, "registers");
-static_assert(kLocColV + kLocSlots * kSlotCols <= kTmemCols, "TMEM");
-
+constexpr uint32_t kLocMaxSlots = 8;
 struct LocalBars {
     uint64_t u_full[kRing], u_free[kRing];   // a unit announced / done with (21 warps)
-    uint64_t full[kLocStages], free[kLocStages];
-    uint64_t v_ready[kLocSlots], v_free[kLocSlots];
+    uint64_t full[kLocMaxStages], free[kLocMaxStages];
+    uint64_t v_ready[kLocMaxSlots], v_free[kLocMaxSlots];
     uint64_t sum_full[2], sum_free[2];   // a tile's sum complete / read (4 warps)
     uint64_t fin;
     uint32_t tmem;
     int stop;
 };
-static_assert(sizeof(LocalBars) <= 320, "barriers");
+static_assert(sizeof(LocalBars) <= kBarBytes, "barriers");
 
+template <bool kNarrow>
 __global__ void __launch_bounds__(kLocThreads, 1)
 decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs A) {
+    // TMEM columns: two accumulators, and slots of C'^T
+    constexpr uint32_t kAcc = kNarrow ? 64 : kC, kLocColV = 2 * kAcc, kLocSlots = kNarrow ? 8 : 5;
+    constexpr uint32_t kTileBytes = kNarrow ? kBox : kTile, kStageBytes = 2 * kTileBytes;   // B, C
+    constexpr int kLocStages = kNarrow ? kLocMaxStages : 3;
+    static_assert(kLocStages * kStageBytes <= kLocOffBar, "stages");
+    constexpr int kKd = kNarrow ? 64 : kC;
+    constexpr int kLocRegsV = kNarrow ? 72 : 64, kLocRegsState = kNarrow ? 120 : 176, kLocRegsOther = kNarrow ? 72 : 48;
+    static_assert(4 * kLocRegsV + kLocRegsState + kLocRegsOther <= 6 * kRegsLaunch, "registers");
+    static_assert(kLocSlots <= kLocMaxSlots && kLocColV + kLocSlots * kSlotCols <= kTmemCols, "TMEM");
     extern __shared__ __align__(1024) uint8_t smem[];
     LocalBars &bar = *(LocalBars *)(smem + kLocOffBar);
     Unit *ring = (Unit *)(smem + kLocOffRing);
@@ -984,10 +1038,10 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                     if (use && !(ok = wait(&bar.free[st], use - 1))) break;
                     if (lane == 0) {
                         const int64_t t = walk.first(u, i);
-                        uint8_t *s = smem + st * kLocStage;
+                        uint8_t *s = smem + st * kStageBytes;
                         mbar_arrive_expect_tx(&bar.full[st], (kd + vd) / 64 * kBox);
                         load_tile(s, &maps.b[u.pass], kd, u.h, t, &bar.full[st]);
-                        load_tile(s + kTile, &maps.c[u.pass], vd, u.h, t, &bar.full[st]);
+                        load_tile(s + kTileBytes, &maps.c[u.pass], vd, u.h, t, &bar.full[st]);
                     }
                     __syncwarp();
                 }
@@ -1009,13 +1063,13 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                     const int len = walk.len(i);
                     if (!(ok = wait(&bar.full[st], it / kLocStages))) break;
                     if (len < kC) {
-                        zero_rows(smem + st * kLocStage, kd, len, 0, 1, lane);
+                        zero_rows(smem + st * kStageBytes, kd, len, 0, 1, lane);
                         fence_proxy_async_smem();
                         __syncwarp();
                     }
                     if (it >= 2 && !(ok = wait(&bar.sum_free[buf], (it >> 1) - 1))) break;
                     tc_fence_after();
-                    const uint64_t dBt = smem_desc(s0 + st * kLocStage, kBox, 1024, kSw128);
+                    const uint64_t dBt = smem_desc(s0 + st * kStageBytes, kBox, 1024, kSw128);
 #pragma unroll
                     for (uint32_t k = 0; k < kParts; ++k) {
                         const uint32_t n = it * kParts + k, slot = n % kLocSlots, av = tm + kLocColV + slot * kSlotCols;
@@ -1026,7 +1080,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                         for (uint32_t term = 0; term < 3; ++term)
 #pragma unroll
                             for (uint32_t j = 0; j < 2; ++j)
-                                mma_f16_ts_if(lead, tm + buf * kC, av + (2 - term) * 16 + j * 8, dPart + ((j * 2048) >> 4),
+                                mma_f16_ts_if(lead, tm + buf * kAcc, av + (2 - term) * 16 + j * 8, dPart + ((j * 2048) >> 4),
                                               id_h, k + term + j > 0);
                         mma_commit_if(lead, &bar.v_free[slot]);
                     }
@@ -1066,7 +1120,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                 if (!(ok = wait(&bar.full[st], it / kLocStages))) break;
                 if (use && !(ok = wait(&bar.v_free[slot], use - 1))) break;
                 tc_fence_after();
-                uint8_t *ct = smem + st * kLocStage + kTile;
+                uint8_t *ct = smem + st * kStageBytes + kTileBytes;
                 if (len < kC && any) {   // all groups the same zeros
                     zero_columns(ct, e & ~31, len, lane);
                     __syncwarp();
@@ -1089,19 +1143,19 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
         each_unit([&](const Unit &u) {
             const DecayPass &p = A.pass[u.pass];
             const bool any = e < p.vd;   // (by warps; the other lanes' sums are nobody's)
-            StateRow s;
+            StateRow<kKd> s;
 #pragma unroll
-            for (int j = 0; j < kC / 2; ++j) s[j] = 0;
+            for (int j = 0; j < kKd / 2; ++j) s[j] = 0;
             for (int i = 0; i < u.tiles; ++i, ++it) {
                 const uint32_t buf = it & 1;
                 if (!wait(&bar.sum_full[buf], it >> 1)) return false;
                 tc_fence_after();
-                if (any) state_add<false>(s, lanes + buf * kC, p.kd, 0, 0);
+                if (any) state_add<false, kKd>(s, lanes + buf * kAcc, p.kd, 0, 0);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.sum_free[buf]);
             }
-            state_store(p, u.to, e, s);
+            state_store<kKd>(p, u.to, e, s);
             return true;
         });
     }
@@ -1143,20 +1197,26 @@ cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, 
     }
     if (args.units == 0) return cudaSuccess;
     if (args.units > 0x7fffffff) return cudaErrorInvalidValue;
-    auto kern = local ? decay_local_kernel : decay_out_kernel;
+    bool narrow = true;
+    for (int i = 0; i < n; ++i) narrow &= passes[i].kd == 64 && passes[i].vd == 64;
+    auto kern = local ? (narrow ? decay_local_kernel<true> : decay_local_kernel<false>)
+                      : (narrow ? decay_out_kernel<true> : decay_out_kernel<false>);
     const int bytes = (int)(local ? kSmemLocal : kSmemOut);
     // the kernels' split of the registers is made for this many a thread
     static const bool split = [] {
-        cudaFuncAttributes a{}, b{};
-        return cudaFuncGetAttributes(&a, decay_local_kernel) == cudaSuccess && a.numRegs >= kRegsLaunch &&
-               cudaFuncGetAttributes(&b, decay_out_kernel) == cudaSuccess && b.numRegs >= kRegsLaunch;
+        auto has = [](auto kern, int regs) {
+            cudaFuncAttributes a{};
+            return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs >= regs;
+        };
+        return has(decay_local_kernel<false>, kRegsLaunch) && has(decay_local_kernel<true>, kRegsLaunch) &&
+               has(decay_out_kernel<false>, kRegsLaunch) && has(decay_out_kernel<true>, kRegsLaunchNarrow);
     }();
     if (!split) return cudaErrorInvalidConfiguration;
     const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (err != cudaSuccess) return err;
     ProfScope prof(stream, local ? "decay_local_kernel" : "decay_out_kernel");
     const cudaError_t run = launch_early(early, kern, dim3((unsigned)std::min<int64_t>(args.units, sms)),
-                                         local ? kLocThreads : kOutThreads, (size_t)bytes, stream, maps, args);
+                                         local ? kLocThreads : 32 * (narrow ? kOutWarpsNarrow : kOutWarps), (size_t)bytes, stream, maps, args);
     count_launch();
     return run;
 }

@@ -250,6 +250,19 @@ def test_deterministic_and_on_another_stream(path):
     assert all(torch.equal(p, r) for p, r in zip(a, b))
 
 
+@pytest.mark.parametrize("d,H", [(64, 32), (128, 16)])
+def test_many_calls_neither_stall_nor_differ(d, H):
+    """Packed sequences with many short last tiles, whose rows are stored one by one while the next
+    tiles are under way: no call may run into a wait's limit or give another result."""
+    lens = [1 + (37 * i) % 300 for i in range(60)] + [2000, 3000]
+    x = inputs(1, 0, H, d, d, "bf16", 700, lens=lens)
+    out, hT = check_fwd(x)
+    for _ in range(300):
+        o, h = gdr.decay_fwd(x["q"], x["k"], x["v"], x["g"], h0=x["h0"], cu_seqlens=x["cu"], scale=0.5)
+    ok()
+    assert torch.equal(o, out) and torch.equal(h, hT)
+
+
 def test_gradients_against_differences():
     """The gradients along a random direction against central differences of the fp64 forward:
     bilinear in each input, so a difference in one input is exact up to rounding."""
