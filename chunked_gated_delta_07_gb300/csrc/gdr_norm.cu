@@ -257,8 +257,11 @@ norm_fwd_kernel(const T *x, const float *__restrict__ w, const float *__restrict
 }
 
 // part: [2][gridDim.x][G][D] partial sums of dw, then db (null where neither is wanted).
+// Rows in single elements get twice the registers, one block of 512 threads at a time: with two,
+// 8 elements' sums, weights and addresses do not fit (65537 rows x 999 bf16 208 us, with one 110;
+// 200000 x 125 137 and 66).  Rows in 16-byte pieces fit.
 template <typename T, int TPR, int NV, int VEC>
-__global__ void __launch_bounds__(bwd_threads<TPR>(), kThreadsPerSm / bwd_threads<TPR>())
+__global__ void __launch_bounds__(bwd_threads<TPR>(), VEC > 1 ? kThreadsPerSm / bwd_threads<TPR>() : 1)
 norm_bwd_kernel(const T *dy, const T *x, const float *__restrict__ mean, const float *__restrict__ rstd,
                 const float *__restrict__ w, T *dx, float *__restrict__ part, NormShape s) {
     constexpr int kThreads = bwd_threads<TPR>();
@@ -414,12 +417,14 @@ struct NormPick {
 };
 
 // The smallest group of threads that holds a row at 8 elements a thread (16 beyond 8192
-// columns): in 16-byte pieces where every row can be read that way, else in single elements.
+// columns): in 16-byte pieces where every row can be read that way, else in single elements, of
+// which 512 threads take 16 (20000 rows x 6001 fp32 backward 307 us, 1024 threads with 8 370;
+// 4097 bf16 forward 138 and 170).
 NormPick pick_layout(int D, size_t es, bool pieces) {
     const int vec = pieces ? (int)(16 / es) : 1, nv = 8 / vec;
     for (int tpr = 8; tpr <= 1024; tpr *= pieces ? 2 : 4)
         if (tpr * 8 >= D) return {tpr, nv, vec};
-    return {1024, D <= 8192 ? nv : 2 * nv, vec};
+    return {!pieces && D <= 8192 ? 512 : 1024, 2 * nv, vec};
 }
 
 struct NormGrid {
@@ -467,7 +472,7 @@ template <typename T, typename F> cudaError_t with_layout(const NormPick &p, F &
     GDR_NORM_CASE(32, 8, 1)
     GDR_NORM_CASE(128, 8, 1)
     GDR_NORM_CASE(512, 8, 1)
-    GDR_NORM_CASE(1024, 8, 1)
+    GDR_NORM_CASE(512, 16, 1)
     GDR_NORM_CASE(1024, 16, 1)
 #undef GDR_NORM_CASE
     return cudaErrorInvalidValue;
