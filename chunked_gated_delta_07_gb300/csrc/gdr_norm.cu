@@ -349,6 +349,9 @@ norm_bwd_kernel(const T *dy, const T *x, const float *__restrict__ mean, const f
         mu = mu1;
         rs = rs1;
     }
+    // no copy of this thread's may still be on its way into the ring: those asked for past the
+    // last row fill it with zeros, and its memory is taken for the groups' sums below
+    copies_wait<0>();
     if (!part) return;
     // the block's partial sums, its row sets added in order through shared memory
     const int64_t gd = (int64_t)s.G * s.D;
