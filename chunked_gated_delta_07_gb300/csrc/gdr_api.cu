@@ -622,7 +622,8 @@ gdr_status_t check_decay(const float *log_decay, int B, int64_t T, int H, int dk
     const int64_t T_total = varlen ? T : (int64_t)B * T;
     if ((T_total > 0 && (int64_t)H > ((int64_t)1 << 40) / T_total) || (int64_t)H * B > (1 << 26))
         return GDR_ERR_UNSUPPORTED;
-    if (T_total > 0 && !log_decay) return GDR_ERR_INVALID_ARG;
+    // packed calls launch even for no tokens, to pass the states on, and read the decays
+    if ((T_total > 0 || varlen) && !log_decay) return GDR_ERR_INVALID_ARG;
     *s = DecayShape{B, H, dk, dv, varlen ? 0 : T, T_total, varlen};
     return GDR_OK;
 }
