@@ -929,7 +929,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
 // ---------------------------------------------------------------------------
 // Every write's weight is its distance to the segment's end, so the sum of C'^T B over the tiles
 // needs no decay on the way.  Four groups of four warps take 32 tokens of a tile each, through
-// five slots of C' in TMEM; four more add a tile's product to the sum, which they keep in
+// slots of C' in TMEM of their own, one each or two (kNarrow); four more add a tile's product to the sum, which they keep in
 // registers, while the next one's runs in the other accumulator.  262144 tokens of 16 heads, 19
 // segments in up to 3 parts: 150 us, 4.1 TB/s.  A tile takes an SM 1.9 us, near the 1.6 that its
 // copies need for 64 KB; the rest is units that do not come out even.
@@ -955,13 +955,16 @@ template <bool kNarrow>
 __global__ void __launch_bounds__(kLocThreads, 1)
 decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs A) {
     // TMEM columns: two accumulators, and slots of C'^T
-    constexpr uint32_t kAcc = kNarrow ? 64 : kC, kLocColV = 2 * kAcc, kLocSlots = kNarrow ? 8 : 5;
+    constexpr uint32_t kAcc = kNarrow ? 64 : kC, kLocColV = 2 * kAcc, kLocSlots = kNarrow ? 8 : 4;
     constexpr uint32_t kTileBytes = kNarrow ? kBox : kTile, kStageBytes = 2 * kTileBytes;   // B, C
     constexpr int kLocStages = kNarrow ? kLocMaxStages : 3;
     static_assert(kLocStages * kStageBytes <= kLocOffBar, "stages");
     constexpr int kKd = kNarrow ? 64 : kC;
     constexpr int kLocRegsV = kNarrow ? 72 : 64, kLocRegsState = kNarrow ? 120 : 176, kLocRegsOther = kNarrow ? 72 : 48;
     static_assert(4 * kLocRegsV + kLocRegsState + kLocRegsOther <= 6 * kRegsLaunch, "registers");
+    // a group waits for every use of its slots: a parity tells one use from the one before, no further
+    // (five slots between them were no faster)
+    static_assert(kLocSlots % kParts == 0, "slots of one group each");
     static_assert(kLocSlots <= kLocMaxSlots && kLocColV + kLocSlots * kSlotCols <= kTmemCols, "TMEM");
     extern __shared__ __align__(1024) uint8_t smem[];
     LocalBars &bar = *(LocalBars *)(smem + kLocOffBar);
@@ -1094,7 +1097,9 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
             __all_sync(kFull, mbar_wait(&bar.fin, 0, kDrainNs));
         }
     } else if (warp < 16) {
-        // ---- weighted values: thread = value index (TMEM lane), group grp 32 tokens of the tile
+        // ---- weighted values: thread = value index (TMEM lane), group grp the tile's 32 tokens that
+        // the issuer takes as its grp-th part: forward and reversed units alike, so that its slots
+        // stay its own
         set_registers<kLocRegsV, false>();
         const int grp = warp >> 2, e = tid & 127;
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
@@ -1104,18 +1109,19 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
             const DecayPass &p = A.pass[u.pass];
             const bool rev = p.rev;
             const Walk walk(u, rev);
+            const int part = rev ? (int)kParts - 1 - grp : grp;   // from token 32 part on
             const float gd = u.gd, s_upd = p.s_upd;
             const int64_t tokens = u.t1 - u.t0;
             const bool any = e < p.vd;   // (by warps; the other lanes' sums are nobody's)
             for (int i = 0; i < walk.tiles; ++i, ++it) {
                 const uint32_t st = it % kLocStages;
-                const uint32_t n = it * kParts + (rev ? kParts - 1 - grp : grp);   // in the issuer's order
+                const uint32_t n = it * kParts + grp;   // in the issuer's order
                 const uint32_t slot = n % kLocSlots, use = n / kLocSlots;
                 const int len = walk.len(i);
                 // past the tile: its distance to the segment's end (its start, reversed)
                 const int64_t past = u.past + (rev ? (int64_t)(walk.tiles - 1 - i) * kC : tokens - (int64_t)i * kC - len);
                 __syncwarp();   // the last tile's weights are read
-                w[lane] = token_weight(32 * grp + lane, len, rev, gd, s_upd, past);
+                w[lane] = token_weight(32 * part + lane, len, rev, gd, s_upd, past);
                 __syncwarp();
                 if (!(ok = wait(&bar.full[st], it / kLocStages))) break;
                 if (use && !(ok = wait(&bar.v_free[slot], use - 1))) break;
@@ -1127,7 +1133,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                 }
 #pragma unroll 1
                 for (uint32_t k = 0; k < 2; ++k)
-                    if (any) write_terms(lanes + kLocColV + slot * kSlotCols + 8 * k, ct, e, 2 * grp + k, w + 16 * k);
+                    if (any) write_terms(lanes + kLocColV + slot * kSlotCols + 8 * k, ct, e, 2 * part + k, w + 16 * k);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
