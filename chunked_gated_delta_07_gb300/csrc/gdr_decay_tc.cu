@@ -1129,6 +1129,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
                 uint8_t *ct = smem + st * kStageBytes + kTileBytes;
                 if (len < kC && any) {   // all groups the same zeros
                     zero_columns(ct, e & ~31, len, lane);
+                    fence_proxy_async_smem();   // before the stage's next tile is copied over them
                     __syncwarp();
                 }
 #pragma unroll 1
