@@ -41,3 +41,32 @@ def test_every_backward_call_gives_the_same(seg_tiles, dk, dv, H, lens):  # noqa
     call = lambda: gdr.decay_bwd(x["q"], x["k"], x["v"], x["g"], x["dout"], dhT=x["dhT"], h0=x["h0"],  # noqa: E731
                                  cu_seqlens=x["cu"], scale=0.5)
     assert differing(call, call(), 200) == 0
+
+
+@pytest.mark.parametrize("seg_tiles", [0, 1, 3], indirect=True)
+@pytest.mark.parametrize("dk,dv,H,lens", [(64, 64, 32, LENS), (128, 128, 16, LENS), (64, 128, 16, LENS),
+                                          (128, 128, 16, None), (64, 64, 16, None)])
+def test_every_forward_call_gives_the_same(seg_tiles, dk, dv, H, lens):  # noqa: F811
+    x = inputs(2, 3001, H, dk, dv, "bf16", 720, lens=lens)
+    call = lambda: gdr.decay_fwd(x["q"], x["k"], x["v"], x["g"], h0=x["h0"], cu_seqlens=x["cu"], scale=0.5)  # noqa: E731
+    assert differing(call, call(), 500) == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [LENS, None])
+def test_every_call_on_the_cuda_cores_gives_the_same(dtype, lens):
+    x = inputs(2, 1001, 3, 128, 64, dtype, 730, lens=lens)
+    call = lambda: gdr.decay_bwd(x["q"], x["k"], x["v"], x["g"], x["dout"], dhT=x["dhT"], h0=x["h0"],  # noqa: E731
+                                 cu_seqlens=x["cu"], scale=0.5, path="simt")
+    assert differing(call, call(), 100) == 0
+
+
+@pytest.mark.parametrize("T", [1, 5, 20])
+def test_every_decoding_call_gives_the_same(T):
+    x = inputs(64, T, 16, 128, 128, "bf16", 740)
+
+    def call():
+        state = x["h0"].clone()
+        return gdr.decay_recurrent_fwd(x["q"], x["k"], x["v"], x["g"], state, scale=0.5), state
+
+    assert differing(call, call(), 200) == 0
