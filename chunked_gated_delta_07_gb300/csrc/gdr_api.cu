@@ -718,7 +718,10 @@ cudaError_t decay_run(const DecayGeom &g, const DecayPass *chains, int nchains, 
         if (err == cudaSuccess) err = launch_decay_combine(g, chains, nchains, stream);
         if (err != cudaSuccess) return err;
     }
-    return run(passes, n, !g.dense || g.max_slots > 0);
+    cudaError_t err = run(passes, n, !g.dense || g.max_slots > 0);
+    if (err == cudaSuccess && tc && g.max_slots > 0)
+        err = launch_decay_tc(g, passes, n, ctx->sms, nullptr, true, ctx->d_status, stream, true);
+    return err;
 }
 
 // Scratch of a call: the caller's workspace, or the internal cache grown to size.

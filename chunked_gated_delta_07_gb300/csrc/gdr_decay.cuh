@@ -15,7 +15,10 @@
 // A long sequence is cut into segments of seg_tiles tiles.  A local pass sums each
 // segment's own writes, decayed to its end (its start, reversed), combine chains the sums
 // into the states that cross the segments' boundaries, and the output pass runs every
-// segment from its entering state.  Boundary b of sequence n lies between its segments b
+// segment from its entering state.  On the tensor cores the local pass skips the tokens that
+// the decay leaves nothing of; only of a NaN or an infinity it leaves a NaN.  The output pass
+// meets those tokens, and where it did a launch behind it runs the sequence's head again, uncut.
+// Boundary b of sequence n lies between its segments b
 // and b + 1 and has the slot seg_base[n] - n + b.
 #pragma once
 
@@ -109,7 +112,7 @@ struct DecayFactor {
 };
 
 // Tokens after which exp(n g) is below fp32's smallest normal number, e^-87.3: what a local
-// pass need not read.
+// pass on the tensor cores need not read.
 __device__ __forceinline__ int64_t decay_reach(float g, int64_t n) {
     if (!(g < 0.f)) return n;
     const float r = 88.f / -g;
@@ -156,8 +159,10 @@ cudaError_t launch_decay_step(const void *q, const void *k, const void *v, const
 // On the tensor cores (gdr_decay_tc.cu): bf16, token tensors 16-byte aligned, fewer than
 // 2^31 - 128 token rows.  Passes of one launch are independent and all local or all not.
 // `next`: a zeroed counter that hands out the units, or null (few units of equal length).
+// `again`: runs, uncut, every (sequence, head, pass) of cut sequences whose outputs, by the launch
+// before, show a value that is not finite and that a local sum may have skipped.
 cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, int sms, unsigned long long *next,
-                            bool early, int *status, cudaStream_t stream);
+                            bool early, int *status, cudaStream_t stream, bool again = false);
 // Chains the local sums in `slots` of n passes into boundary states, from s0 (null: zero).
 cudaError_t launch_decay_combine(const DecayGeom &g, const DecayPass *passes, int n, cudaStream_t stream);
 

@@ -127,8 +127,38 @@ struct Unit {
 };
 constexpr uint32_t kRing = 4;   // units announced ahead
 
+// The output pass, its second run of the sequences that need one, and the local pass.
+enum Kind { kOut, kAgain, kLocal };
+
+// Whether outputs of sequence n in unit o's head and pass show a value that is not finite and that
+// a local sum may have skipped; if so the sequence as one segment (one warp).  Such a value is in the
+// state before the last tile of the segment that it is in, so the outputs of the segment's last
+// token, all of them or those of a column, are not finite either.
+__device__ __forceinline__ bool whole_sequence(const TcArgs &A, int64_t n, const Unit &o, DecaySeg &seg) {
+    const DecayGeom &g = A.g;
+    if (n >= g.N) return false;
+    const DecayPass &p = A.pass[o.pass];
+    const int64_t cuts = (g.dense ? g.segs_per_seq : g.p.seg_base[n + 1] - g.p.seg_base[n]) - 1;
+    if (cuts < 1 || decay_reach(decay_log(g.log_decay, o.h), g.seg_tokens) > g.seg_tokens - kC) return false;
+    seg.t0 = g.dense ? n * g.T_per : g.p.seq_start[n];
+    seg.t1 = g.dense ? seg.t0 + g.T_per : g.p.seq_start[n + 1];
+    const int lanes = p.vd / 8, per = 32 / lanes, lane = threadIdx.x & 31;   // of a row; rows at a time
+    bool bad = false;
+#pragma unroll 4
+    for (int64_t i = lane / lanes; i < cuts; i += per) {
+        const int64_t t = seg.t0 + (i + 1) * g.seg_tokens - (p.rev ? 0 : 1);
+        const uint4 x = *(const uint4 *)((const __nv_bfloat16 *)p.out + (t * g.H + o.h) * p.vd + 8 * (lane % lanes));
+        for (uint32_t w : {x.x, x.y, x.z, x.w}) bad |= (~w & 0x7f80u) == 0 || (~w & 0x7f800000u) == 0;
+    }
+    seg.n = (int)n;
+    seg.slot = 0;
+    seg.first = seg.last = true;
+    return __any_sync(kFull, bad);
+}
+
 // False where unit u has nothing to do.
-__device__ __forceinline__ bool unit_of(const TcArgs &A, int64_t u, bool local, Unit &o) {
+template <Kind kKind> __device__ __forceinline__ bool unit_of(const TcArgs &A, int64_t u, Unit &o) {
+    constexpr bool local = kKind == kLocal;
     uint32_t sh = (uint32_t)u, part = 0;   // fewer than 2^31 units
     o.pass = (int)(sh % (uint32_t)A.npass);
     sh /= (uint32_t)A.npass;
@@ -139,7 +169,7 @@ __device__ __forceinline__ bool unit_of(const TcArgs &A, int64_t u, bool local, 
     const uint32_t sg = sh / (uint32_t)A.g.H;
     o.h = (int)(sh - sg * (uint32_t)A.g.H);
     DecaySeg seg;
-    if (!decay_segment(A.g, sg, seg)) return false;
+    if (!(kKind == kAgain ? whole_sequence(A, sg, o, seg) : decay_segment(A.g, sg, seg))) return false;
     const DecayPass &p = A.pass[o.pass];
     o.gd = decay_log(A.g.log_decay, o.h);
     o.t0 = seg.t0;
@@ -169,7 +199,8 @@ __device__ __forceinline__ bool unit_of(const TcArgs &A, int64_t u, bool local, 
 // not very many the counter runs over all twice -- those of more than half the most tiles
 // first, then the others, so that the blocks end together.  False at the end.  `n`: the last one (blockIdx.x -
 // gridDim.x at the start).
-__device__ __forceinline__ bool take_unit(const TcArgs &A, bool local, int64_t &n, Unit &u) {
+template <Kind kKind> __device__ __forceinline__ bool take_unit(const TcArgs &A, int64_t &n, Unit &u) {
+    constexpr bool local = kKind == kLocal;
     while (true) {
         bool want_long = false;
         int64_t i;
@@ -183,7 +214,7 @@ __device__ __forceinline__ bool take_unit(const TcArgs &A, bool local, int64_t &
             i = n += gridDim.x;
         }
         if (i >= A.units) return false;
-        if (unit_of(A, i, local, u) &&
+        if (unit_of<kKind>(A, i, u) &&
             (!A.long_first || (2 * (int64_t)u.tiles * kC > (local ? A.g.part_tokens : A.g.seg_tokens)) == want_long))
             return true;
     }
@@ -472,7 +503,7 @@ struct OutBars {
 };
 static_assert(sizeof(OutBars) <= kBarBytes, "barriers");
 
-template <bool kNarrow>
+template <bool kNarrow, Kind kKind>
 __global__ void __launch_bounds__(32 * (kNarrow ? kOutWarpsNarrow : kOutWarps), 1)
 decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ TcArgs A) {
     constexpr uint32_t kColU = kColO + (kNarrow ? 64 : kC), kColV = kColU + (kNarrow ? 64 : kC);
@@ -496,6 +527,15 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
     if (!GDR_INBOUNDS((smem_u32(smem) & 1023u) == 0)) return;   // swizzled tiles start on 1 KB
 
     let_next_start();
+    if constexpr (kKind == kAgain) {   // only if the block has a unit
+        after_previous();
+        bool any = false;
+        for (int64_t u = blockIdx.x + (int64_t)warp * gridDim.x; u < A.units; u += (int64_t)(blockDim.x / 32) * gridDim.x) {
+            Unit o;
+            any |= unit_of<kAgain>(A, u, o);
+        }
+        if (!__syncthreads_or(any)) return;
+    }
     if (tid == 0) {
         for (uint32_t i = 0; i < kRing; ++i) {
             mbar_init(&bar.u_full[i], 1);
@@ -582,7 +622,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
             uint32_t nbc = 0;   // tiles whose B and C are on their way (`it`: whose A is too)
             for (uint32_t k = 0; ok; ++k) {
                 Unit u;
-                if (!take_unit(A, false, n, u)) u.tiles = -1;
+                if (!take_unit<kKind>(A, n, u)) u.tiles = -1;
                 if (k >= kRing && !(ok = wait(&bar.u_free[k % kRing], k / kRing - 1))) break;
                 if (lane == 0) {
                     ring[k % kRing] = u;
@@ -1025,7 +1065,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
             int64_t n = (int64_t)blockIdx.x - gridDim.x;
             for (uint32_t k = 0; ok; ++k) {
                 Unit u;
-                if (!take_unit(A, true, n, u)) u.tiles = -1;
+                if (!take_unit<kLocal>(A, n, u)) u.tiles = -1;
                 if (k >= kRing && !(ok = wait(&bar.u_free[k % kRing], k / kRing - 1))) break;
                 if (lane == 0) {
                     ring[k % kRing] = u;
@@ -1177,7 +1217,7 @@ decay_local_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ 
 }  // namespace
 
 cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, int sms, unsigned long long *next,
-                            bool early, int *status, cudaStream_t stream) {
+                            bool early, int *status, cudaStream_t stream, bool again) {
     if (n < 1 || n > kMaxPasses) return cudaErrorInvalidValue;
     const bool local = passes[0].local;
     TcMaps maps{};
@@ -1193,7 +1233,7 @@ cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, 
     }
     args.g = g;
     args.npass = n;
-    args.units = g.max_segs * g.H * n * (local ? g.parts : 1);
+    args.units = (again ? g.N : g.max_segs) * g.H * n * (local ? g.parts : 1);
     args.next = next;
     args.long_first = next && args.units <= 64 * (int64_t)sms;   // a look at a unit costs some 0.3 us
     args.status = status;
@@ -1206,22 +1246,27 @@ cudaError_t launch_decay_tc(const DecayGeom &g, const DecayPass *passes, int n, 
     if (args.units > 0x7fffffff) return cudaErrorInvalidValue;
     bool narrow = true;
     for (int i = 0; i < n; ++i) narrow &= passes[i].kd == 64 && passes[i].vd == 64;
-    auto kern = local ? (narrow ? decay_local_kernel<true> : decay_local_kernel<false>)
-                      : (narrow ? decay_out_kernel<true> : decay_out_kernel<false>);
+    using Kernel = void (*)(TcMaps, TcArgs);
+    static constexpr Kernel kernels[2][3] = {
+        {decay_out_kernel<false, kOut>, decay_out_kernel<false, kAgain>, decay_local_kernel<false>},
+        {decay_out_kernel<true, kOut>, decay_out_kernel<true, kAgain>, decay_local_kernel<true>}};
+    const Kernel kern = kernels[narrow][local ? kLocal : again ? kAgain : kOut];
     const int bytes = (int)(local ? kSmemLocal : kSmemOut);
     // the kernels' split of the registers is made for this many a thread
     static const bool split = [] {
-        auto has = [](auto kern, int regs) {
-            cudaFuncAttributes a{};
-            return cudaFuncGetAttributes(&a, kern) == cudaSuccess && a.numRegs >= regs;
-        };
-        return has(decay_local_kernel<false>, kRegsLaunch) && has(decay_local_kernel<true>, kRegsLaunch) &&
-               has(decay_out_kernel<false>, kRegsLaunch) && has(decay_out_kernel<true>, kRegsLaunchNarrow);
+        bool all = true;
+        for (int n = 0; n < 2; ++n)
+            for (int k = 0; k < 3; ++k) {
+                cudaFuncAttributes a{};
+                all &= cudaFuncGetAttributes(&a, kernels[n][k]) == cudaSuccess &&
+                       a.numRegs >= (n && k != kLocal ? kRegsLaunchNarrow : kRegsLaunch);
+            }
+        return all;
     }();
     if (!split) return cudaErrorInvalidConfiguration;
     const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (err != cudaSuccess) return err;
-    ProfScope prof(stream, local ? "decay_local_kernel" : "decay_out_kernel");
+    ProfScope prof(stream, local ? "decay_local_kernel" : again ? "decay_out_kernel (again)" : "decay_out_kernel");
     const cudaError_t run = launch_early(early, kern, dim3((unsigned)std::min<int64_t>(args.units, sms)),
                                          local ? kLocThreads : 32 * (narrow ? kOutWarpsNarrow : kOutWarps), (size_t)bytes, stream, maps, args);
     count_launch();

@@ -399,9 +399,11 @@ GDR_API gdr_status_t gdr_chunk_bwd(const void *q, const void *k, const void *v, 
  * dk, dv in {64, 128}; B, H >= 1; T >= 0; sequences of no tokens pass h0 on to hT.
  * States are accumulated in fp32; on the tensor cores the writes enter them with 24
  * significant bits, while the in-tile weights and the state are rounded to bf16 where
- * they are multiplied for a (bf16) output.  A NaN or infinity in a token reaches, besides
- * the outputs after it, those of its own 128-token tile; other sequences never.  Outputs
- * must not overlap inputs.  Bad offsets: GDR_ERR_BAD_SEQLENS in the status word,
+ * they are multiplied for a (bf16) output.  A NaN or infinity in a token stays in the state,
+ * however fast the head forgets: it reaches the outputs after it and hT (on the tensor
+ * cores as a NaN, and also the outputs of its own 128-token tile; a call whose cut
+ * sequence has one that the decay leaves nothing of runs that sequence's head twice);
+ * other heads and sequences never.  Outputs must not overlap inputs.  Bad offsets: GDR_ERR_BAD_SEQLENS in the status word,
  * nothing is written.  Asynchronous on `stream`; deterministic.
  */
 GDR_API gdr_status_t gdr_decay_fwd(const void *q, const void *k, const void *v, const float *log_decay,
