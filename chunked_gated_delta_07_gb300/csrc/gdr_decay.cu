@@ -107,10 +107,10 @@ decay_rec_kernel(const DecayGeom g, const __grid_constant__ Passes passes) {
     // block behind it, S = lam^j S^, S^ += lam^-j b c^T and out = (lam^j a)^T S^, and lam^nb
     // enters the state once per block.  That saves a third of the instructions and keeps the
     // powers exact: lam itself rounds to 24 bits, an error that a product of n of them
-    // multiplies by n.  Blocks are whole tiles while lam^-15 stays in range, else single
-    // tokens.  A forward pass decays the state before its first token too, a reversed one
+    // multiplies by n.  Blocks are whole tiles while lam^-15 costs no more than 2^22 of fp32's
+    // range, else single tokens (8 x 4096 tokens of 16 heads, all so fast: 3.0 ms against 2.2).  A forward pass decays the state before its first token too, a reversed one
     // after its last.
-    const int nb = gd >= -4.f ? kTb : 1;
+    const int nb = gd >= -1.f ? kTb : 1;
     const DecayFactor step(gd * (float)nb);
     const int tid = threadIdx.x, dl = tid % kLanes, eg = tid / kLanes;
     // the thread's elements: row 4 dl + u of kd, column e0 + 8 eg + j

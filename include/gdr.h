@@ -397,6 +397,10 @@ GDR_API gdr_status_t gdr_chunk_bwd(const void *q, const void *k, const void *v, 
  *              NULL: the internal per-device cache (calls that share it must not
  *              overlap on the GPU)
  * dk, dv in {64, 128}; B, H >= 1; T >= 0; sequences of no tokens pass h0 on to hT.
+ * Magnitudes.  On the CUDA cores products scale k v below 2^104 and outputs above 2^-104
+ * keep clear of fp32's limits.  On the tensor cores |scale q.k| and |out / scale| have to stay
+ * below 2^62 (in gdr_decay_bwd |scale v.dout| and the gradients too), and an output takes 2^-64
+ * of the entering state's part where the decay leaves less of it than that.
  * States are accumulated in fp32; on the tensor cores the writes enter them with 24
  * significant bits, while the in-tile weights and the state are rounded to bf16 where
  * they are multiplied for a (bf16) output.  A NaN or infinity in a token stays in the state,
