@@ -253,8 +253,12 @@ __device__ __forceinline__ void zero_rows(uint8_t *tile, int width, int n, int p
 }
 
 // log2 lam; below -200 every power but the zeroth is out of the range of fp32 and its
-// reciprocals, whatever lam is, and differences of multiples stay exact enough.
-__device__ __forceinline__ float decay_log2(float gd) { return fmaxf(gd * 1.4426950408889634f, -200.f); }
+// reciprocals, whatever lam is, and differences of multiples stay exact enough.  A NaN stays one.
+__device__ __forceinline__ float decay_log2(float gd) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(gd * 1.4426950408889634f), "f"(-200.f));
+    return y;
+}
 
 // A token's weight in the update of the state: s_upd lam^{len - 1 - i + past} (forward) or
 // s_upd lam^{i + 1 + past}; rows from len on are not the sequence's and have 0.

@@ -145,3 +145,24 @@ def test_other_widths(seg_tiles, dk, dv, lens):  # noqa: F811
     assert dq[0, AT:2500, 0].isnan().all() and dq[0, :TILE].isfinite().all() and dq[0, :2500, 1:].isfinite().all()
     assert dk_[0, :2500 - AT, 0, 9].isnan().all() and dv_[0, :2500 - AT, 0].isnan().all()
     assert dh0[0, 0, 9].isnan().all() and dh0[0, 1:].isfinite().all() and dh0[1:].isfinite().all()
+
+
+@pytest.mark.parametrize("T", [1, 5, 40, 300])
+@pytest.mark.parametrize("dtype,path", [("bf16", "auto"), ("bf16", "tc"), ("bf16", "simt"), ("f32", "auto")])
+def test_log_decay_that_is_no_number(T, dtype, path):
+    """Every output and state of its head is NaN, from the first token on; other heads are untouched."""
+    x = inputs(2, T, 3, 128, 128, dtype, 850)
+    g = x["g"].clone()
+    g[1] = NAN
+    for h0 in (x["h0"], None):
+        out, hT = gdr.decay_fwd(x["q"], x["k"], x["v"], x["g"], h0=h0, path=path)
+        bad, hbad = gdr.decay_fwd(x["q"], x["k"], x["v"], g, h0=h0, path=path)
+        dq = gdr.decay_bwd(x["q"], x["k"], x["v"], g, x["dout"], h0=h0, path=path)[0]
+        ok()
+        assert bad[:, :, 1].isnan().all() and hbad[:, 1].isnan().all() and dq[:, :, 1].isnan().all()
+        assert torch.equal(bad[:, :, ::2], out[:, :, ::2]) and torch.equal(hbad[:, ::2], hT[:, ::2])
+        assert dq[:, :, ::2].isfinite().all()
+    state = x["h0"].clone()
+    out = gdr.decay_recurrent_fwd(x["q"], x["k"], x["v"], g, state)
+    ok()
+    assert out[:, :, 1].isnan().all() and state[:, 1].isnan().all() and out[:, :, ::2].isfinite().all()
