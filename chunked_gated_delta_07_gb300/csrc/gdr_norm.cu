@@ -183,12 +183,12 @@ norm_fwd_kernel(const T *x, const float *__restrict__ w, const float *__restrict
     int turn = 0;
     const int sub = threadIdx.x / TPR, lane = threadIdx.x % TPR;
     const int gi = sub % s.gpb, ri = sub / s.gpb;
-    const int g = blockIdx.y * s.gpb + gi;
+    const int g = blockIdx.x * s.gpb + gi;
     const bool mine = ri < s.rpb && g < s.G;
     constexpr int kDepth = VEC > 1 ? ring_depth<NV, 1>() : 2;
     extern __shared__ uint4 ring[];
-    const int64_t step = (int64_t)gridDim.x * s.rpb, row_step = step * s.G;
-    int64_t m = (int64_t)blockIdx.x * s.rpb + ri, row = m * s.G + g;
+    const int64_t step = (int64_t)gridDim.y * s.rpb, row_step = step * s.G;
+    int64_t m = (int64_t)blockIdx.y * s.rpb + ri, row = m * s.G + g;
     RowStream<T, fwd_threads<TPR>(), TPR, NV, VEC> xs{};
     xs.p = x + row * s.D + lane * VEC;
     xs.step = row_step * s.D;
@@ -256,7 +256,7 @@ norm_fwd_kernel(const T *x, const float *__restrict__ w, const float *__restrict
     }
 }
 
-// part: [2][gridDim.x][G][D] partial sums of dw, then db (null where neither is wanted).
+// part: [2][gridDim.y][G][D] partial sums of dw, then db (null where neither is wanted).
 // Rows in single elements get twice the registers, one block of 512 threads at a time: with two,
 // 8 elements' sums, weights and addresses do not fit (65537 rows x 999 bf16 208 us, with one 110;
 // 200000 x 125 137 and 66).  Rows in 16-byte pieces fit.
@@ -270,10 +270,10 @@ norm_bwd_kernel(const T *dy, const T *x, const float *__restrict__ mean, const f
     int turn = 0;
     const int sub = threadIdx.x / TPR, lane = threadIdx.x % TPR;
     const int gi = sub % s.gpb, ri = sub / s.gpb;
-    const int g = blockIdx.y * s.gpb + gi;
+    const int g = blockIdx.x * s.gpb + gi;
     const bool mine = ri < s.rpb && g < s.G;
-    const int64_t step = (int64_t)gridDim.x * s.rpb, row_step = step * s.G;
-    int64_t m = (int64_t)blockIdx.x * s.rpb + ri, row = m * s.G + g;
+    const int64_t step = (int64_t)gridDim.y * s.rpb, row_step = step * s.G;
+    int64_t m = (int64_t)blockIdx.y * s.rpb + ri, row = m * s.G + g;
     constexpr int kDepth = VEC > 1 ? ring_depth<NV, 2>() : 2;
     extern __shared__ uint4 ring[];
     RowStream<T, kThreads, TPR, NV, VEC> xs{}, ds{};
@@ -372,7 +372,7 @@ norm_bwd_kernel(const T *dy, const T *x, const float *__restrict__ mean, const f
                         a[k / VEC][k % VEC] += comb[k * kThreads + r * s.gpb * TPR + first];
         }
         if (!mine || ri != 0) continue;
-        float *dst = part + ((int64_t)which * gridDim.x + blockIdx.x) * gd + (int64_t)g * s.D;
+        float *dst = part + ((int64_t)which * gridDim.y + blockIdx.y) * gd + (int64_t)g * s.D;
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + lane) * VEC;
@@ -431,7 +431,7 @@ NormPick pick_layout(int D, size_t es, bool pieces) {
 }
 
 struct NormGrid {
-    dim3 grid;
+    dim3 grid;   // groups of weight rows (up to 2^20) x blocks along the row sets
     int threads;
     NormShape s;
 };
@@ -450,7 +450,7 @@ NormGrid norm_grid(const NormPick &p, int64_t rows, int G, int D, float eps, int
     const int64_t by = (G + o.s.gpb - 1) / o.s.gpb;
     const int64_t want = (o.s.sets + o.s.rpb - 1) / o.s.rpb;
     const int64_t most = std::max<int64_t>(1, (int64_t)sms * (kThreadsPerSm / o.threads) / by);
-    o.grid = dim3((unsigned)std::min(want, most), (unsigned)by);
+    o.grid = dim3((unsigned)by, (unsigned)std::min(want, most));
     return o;
 }
 
@@ -529,7 +529,7 @@ cudaError_t bwd_t(const void *dy, const void *x, const float *mean, const float 
     const int64_t gd = (int64_t)G * D;
     ProfScope prof(stream, "norm_sum_kernel");
     const cudaError_t sum = launch_early(true, norm_sum_kernel, dim3((unsigned)((gd + 31) / 32), 2), 1024, 0, stream,
-                                         (const float *)part, dw, db, (int)n.grid.x, gd);
+                                         (const float *)part, dw, db, (int)n.grid.y, gd);
     count_launch();
     return sum;
 }
@@ -540,7 +540,7 @@ size_t norm_bwd_scratch_bytes(int64_t rows, int G, int D, gdr_dtype_t dtype, int
     const size_t es = dtype == GDR_BF16 ? 2 : 4;
     size_t need = 0;   // whichever layout the pointers' alignment allows
     for (bool pieces : {true, false})
-        need = std::max(need, sizeof(float) * 2 * norm_grid(pick_layout(D, es, pieces), rows, G, D, 0.f, sms, 512).grid.x *
+        need = std::max(need, sizeof(float) * 2 * norm_grid(pick_layout(D, es, pieces), rows, G, D, 0.f, sms, 512).grid.y *
                                   (size_t)G * D);
     return need;
 }
