@@ -32,7 +32,7 @@ EXPORTS = ("gdr_chunk_fwd", "gdr_chunk_fwd_ex", "gdr_chunk_fwd_workspace_size",
            "gdr_profile_read", "gdr_profile_select", "gdr_chunk_fwd_noalloc", "gdr_recurrent_fwd", "gdr_chunk_bwd", "gdr_chunk_fwd_vec",
            "gdr_router_topk", "gdr_router_bias_update", "gdr_chunk_bwd_vec",
            "gdr_decay_fwd", "gdr_decay_bwd", "gdr_decay_workspace_size", "gdr_decay_recurrent_fwd",
-           "gdr_layer_norm_fwd", "gdr_layer_norm_bwd")
+           "gdr_layer_norm_fwd", "gdr_layer_norm_bwd", "gdr_layer_norm_bwd_ex", "gdr_layer_norm_bwd_workspace_size")
 
 _lock = threading.Lock()
 _lib = None
@@ -65,6 +65,8 @@ _SIGS = {
     "gdr_decay_recurrent_fwd": (_I, [_P] * 6 + [_I, _I64, _I, _I, _I, _F, _I, _P]),
     "gdr_layer_norm_fwd": (_I, [_P] * 6 + [_I64, _I, _I, _F, _I, _P]),
     "gdr_layer_norm_bwd": (_I, [_P] * 8 + [_I64, _I, _I, _I, _P]),
+    "gdr_layer_norm_bwd_ex": (_I, [_P] * 8 + [_I64, _I, _I, _I, _P, _SZ, _P]),
+    "gdr_layer_norm_bwd_workspace_size": (_SZ, [_I64, _I, _I, _I]),
 }
 
 
@@ -366,7 +368,7 @@ def _workspace_bytes(workspace, device):
         return 0
     _require_cuda(workspace, "workspace")
     if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on q's device")
+        raise ValueError("workspace must be a contiguous tensor on the device of the first input")
     return workspace.numel() * workspace.element_size()
 
 
@@ -440,6 +442,17 @@ def gdr_layer_norm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, rows, G, D
                                     _ptr(dweight), _ptr(dbias), rows, G, D, dtype, _stream(stream))
 
 
+def gdr_layer_norm_bwd_ex(dy, x, mean, rstd, weight, dx, dweight, dbias, rows, G, D, dtype, workspace=None,
+                          workspace_bytes=0, stream=None) -> int:
+    return lib().gdr_layer_norm_bwd_ex(_ptr(dy), _ptr(x), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dx),
+                                       _ptr(dweight), _ptr(dbias), rows, G, D, dtype, _ptr(workspace),
+                                       workspace_bytes, _stream(stream))
+
+
+def gdr_layer_norm_bwd_workspace_size(rows, G, D, dtype=GDR_BF16) -> int:
+    return int(lib().gdr_layer_norm_bwd_workspace_size(rows, G, D, dtype))
+
+
 def check_norm_inputs(x, weight=None, bias=None, dy=None, mean=None, rstd=None, out=None):
     """Check the tensors of a layer-norm call against x [.., D]: weight and bias fp32 of shape [D] or
     of x's last two axes [G, D] (one weight per head), dy and out like x, mean and rstd fp32 [..].
@@ -492,10 +505,11 @@ def layer_norm_fwd(x, weight=None, bias=None, eps=1e-5, out=None, want_stats=Tru
 
 
 def layer_norm_bwd(dy, x, mean, rstd, weight=None, per_head=False, want_dweight=True, want_dbias=True,
-                   stream=None):
+                   stream=None, workspace=None):
     """Backward of layer_norm_fwd from its mean and rstd: returns (dx, dweight, dbias), the latter
     two fp32 with weight's shape (without a weight: [D], or [G, D] if per_head), None where not
-    wanted."""
+    wanted.  On a stream beside other calls it is given a workspace of its own
+    (gdr_layer_norm_bwd_workspace_size bytes)."""
     import torch
     if dy is None or mean is None or rstd is None:
         raise ValueError("dy, mean and rstd are required")
@@ -509,9 +523,10 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, per_head=False, want_dweight=
     dx = torch.empty_like(x)
     dw = torch.empty(shape, dtype=torch.float32, device=x.device) if want_dweight else None
     db = torch.empty(shape, dtype=torch.float32, device=x.device) if want_dbias else None
-    rc = gdr_layer_norm_bwd(dy, x, mean, rstd, weight, dx, dw, db, rows, G, D, dtype_code(x), stream)
+    rc = gdr_layer_norm_bwd_ex(dy, x, mean, rstd, weight, dx, dw, db, rows, G, D, dtype_code(x), workspace,
+                               _workspace_bytes(workspace, x.device), stream)
     if rc != GDR_OK:
-        raise GdrError(rc, "gdr_layer_norm_bwd")
+        raise GdrError(rc, "gdr_layer_norm_bwd_ex")
     return dx, dw, db
 
 

@@ -1285,12 +1285,27 @@ gdr_status_t gdr_layer_norm_fwd(const void *x, const float *weight, const float 
                : GDR_ERR_CUDA;
 }
 
+size_t gdr_layer_norm_bwd_workspace_size(int64_t rows, int G, int D, gdr_dtype_t dtype) {
+    if ((dtype != GDR_BF16 && dtype != GDR_F32) || rows < 1 || G < 1 || D < 1 || rows % G != 0) return 0;
+    if (D > kNormMaxD || G > (1 << 20) || rows > ((int64_t)1 << 40)) return 0;
+    DeviceCtx *ctx = device_ctx();
+    return norm_bwd_scratch_bytes(rows, G, D, dtype, ctx ? ctx->sms : 152);
+}
+
 gdr_status_t gdr_layer_norm_bwd(const void *dy, const void *x, const float *mean, const float *rstd,
                                 const float *weight, void *dx, float *dweight, float *dbias, int64_t rows,
-                                int G, int D, gdr_dtype_t dtype, gdr_stream_t stream_) {
+                                int G, int D, gdr_dtype_t dtype, gdr_stream_t stream) {
+    return gdr_layer_norm_bwd_ex(dy, x, mean, rstd, weight, dx, dweight, dbias, rows, G, D, dtype, nullptr, 0, stream);
+}
+
+gdr_status_t gdr_layer_norm_bwd_ex(const void *dy, const void *x, const float *mean, const float *rstd,
+                                   const float *weight, void *dx, float *dweight, float *dbias, int64_t rows,
+                                   int G, int D, gdr_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                                   gdr_stream_t stream_) {
     if (dtype != GDR_BF16 && dtype != GDR_F32) return GDR_ERR_INVALID_ARG;
     if (rows < 0 || G < 1 || D < 1 || rows % G != 0) return GDR_ERR_INVALID_ARG;
     if (D > kNormMaxD || G > (1 << 20) || rows > ((int64_t)1 << 40)) return GDR_ERR_UNSUPPORTED;
+    if (!al16(workspace)) return GDR_ERR_INVALID_ARG;
     const size_t xb = (size_t)rows * D * (dtype == GDR_BF16 ? 2 : 4), sb = sizeof(float) * (size_t)rows;
     const size_t wb = sizeof(float) * (size_t)G * D;
     cudaStream_t stream = (cudaStream_t)stream_;
@@ -1309,7 +1324,7 @@ gdr_status_t gdr_layer_norm_bwd(const void *dy, const void *x, const float *mean
     if (!ctx) return GDR_ERR_CUDA;
     char *ws;
     const size_t need = dweight || dbias ? norm_bwd_scratch_bytes(rows, G, D, dtype, ctx->sms) : 0;
-    const gdr_status_t st = take_workspace(ctx, nullptr, 0, need, &ws);
+    const gdr_status_t st = take_workspace(ctx, workspace, workspace_bytes, need, &ws);
     if (st != GDR_OK) return st;
     return launch_norm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, rows, G, D, dtype, ctx->sms,
                            (float *)ws, stream) == cudaSuccess

@@ -56,7 +56,9 @@
  * else from a cache the library keeps per device (grown with cudaMalloc,
  * freed by gdr_release).  Calls that share the internal cache must not
  * overlap on the GPU: issue them on one stream, or pass each stream its own
- * workspace.
+ * workspace.  Nor may several host threads issue them at once, since the first
+ * call that needs more scratch than any before it replaces the cache's buffer;
+ * a call captured into a graph, which keeps its pointers, is given a workspace.
  *
  * Errors.  Arguments are checked before anything is launched: unsupported
  * sizes return GDR_ERR_UNSUPPORTED, malformed ones GDR_ERR_INVALID_ARG.  A
@@ -475,12 +477,28 @@ GDR_API gdr_status_t gdr_layer_norm_fwd(const void *x, const float *weight, cons
  *   dy, x, dx [rows, D] in dtype (dx may be dy or x); weight [G, D] fp32 or NULL (1)
  *   dweight, dbias [G, D] fp32, or NULL (not wanted)
  * The sums over rows are fp32 in a fixed order (no atomics).  Scratch comes from the
- * internal per-device cache.  Sizes and errors as above; asynchronous on `stream`.
+ * internal per-device cache: calls that share it must not overlap on the GPU.  Sizes and
+ * errors as above; asynchronous on `stream`.
  */
 GDR_API gdr_status_t gdr_layer_norm_bwd(const void *dy, const void *x, const float *mean,
                                 const float *rstd, const float *weight, void *dx, float *dweight,
                                 float *dbias, int64_t rows, int G, int D, gdr_dtype_t dtype,
                                 gdr_stream_t stream);
+
+/*
+ * The same with the caller's scratch: 16-byte aligned device memory of
+ * gdr_layer_norm_bwd_workspace_size(...) bytes (GDR_ERR_NO_WORKSPACE if it is less), or NULL
+ * for the cache.  A call on a stream of its own, beside other calls that need scratch, is
+ * given one.
+ */
+GDR_API gdr_status_t gdr_layer_norm_bwd_ex(const void *dy, const void *x, const float *mean,
+                                const float *rstd, const float *weight, void *dx, float *dweight,
+                                float *dbias, int64_t rows, int G, int D, gdr_dtype_t dtype,
+                                void *workspace, size_t workspace_bytes, gdr_stream_t stream);
+
+/* Scratch bytes of gdr_layer_norm_bwd for these sizes (none where neither dweight nor dbias
+ * is wanted); 0 on invalid sizes. */
+GDR_API size_t gdr_layer_norm_bwd_workspace_size(int64_t rows, int G, int D, gdr_dtype_t dtype);
 
 /* Synchronise `stream`, then read and clear the current device's status word.
  * Returns GDR_OK, GDR_ERR_BAD_SEQLENS, GDR_ERR_TIMEOUT or GDR_ERR_CUDA. */
