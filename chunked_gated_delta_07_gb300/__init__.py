@@ -513,6 +513,8 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, per_head=False, want_dweight=
     import torch
     if dy is None or mean is None or rstd is None:
         raise ValueError("dy, mean and rstd are required")
+    if per_head and x is not None and x.dim() < 2:
+        raise ValueError("per_head: x must be [.., G, D]")
     rows, G, D = check_norm_inputs(x, weight, dy=dy, mean=mean, rstd=rstd)
     _require_cuda(x, "x")
     if weight is not None:
