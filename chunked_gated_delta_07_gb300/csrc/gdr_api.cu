@@ -631,16 +631,16 @@ gdr_status_t check_decay(const float *log_decay, int B, int64_t T, int H, int dk
 // True when the tensor-core kernel takes this call: bf16 and every token tensor readable
 // as TMA tiles and writable in 16-byte pieces.
 bool decay_tc_ok(gdr_dtype_t dtype, const DecayShape &s, std::initializer_list<const void *> tensors) {
-    if (dtype != GDR_BF16 || s.T_total == 0 || s.T_total > 0x7fffffff - kDecayTile) return false;
+    if (dtype != GDR_BF16 || s.T_total > 0x7fffffff - kDecayTile) return false;
     for (const void *t : tensors)
         if (!al16(t)) return false;
     return true;
 }
 
-// Whether the call runs on the tensor cores.
+// Whether the call runs on the tensor cores (not for no tokens: a tensor map has rows).
 bool decay_use_tc(bool can, gdr_path_t path, const DecayShape &s) {
     const int64_t longest = s.varlen ? s.T_total : s.T_per;
-    return can && (path == GDR_PATH_TC || (path != GDR_PATH_SIMT && longest > kDecayShortTokens));
+    return can && s.T_total > 0 && (path == GDR_PATH_TC || (path != GDR_PATH_SIMT && longest > kDecayShortTokens));
 }
 
 // Segments on the CUDA cores are cut this fine: a block takes 0.3 us a token, and a call of few

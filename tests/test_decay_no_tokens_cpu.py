@@ -22,3 +22,10 @@ def test_packed_call_without_tokens_needs_the_decays(call, dtype):
 def test_dense_call_without_tokens_does_not(call):
     # nothing to pass on either: the call returns before it needs a device
     assert call(T=0, log_decay=None) == gdr.GDR_OK
+
+
+@pytest.mark.parametrize("call", [fwd, bwd])
+def test_tensor_core_path_takes_no_tokens(call):
+    """As the other calls' does: there is nothing that it could not run."""
+    assert call(T=0, path=gdr.GDR_PATH_TC) == gdr.GDR_OK
+    assert call(T=0, path=gdr.GDR_PATH_TC, dtype=gdr.GDR_F32) == gdr.GDR_ERR_UNSUPPORTED
