@@ -75,3 +75,12 @@ def test_single_tokens(dtype):
         # the same numbers in other units: roundings differ where 1e30 is not a power of two
         assert float((out.double() / 1e30 - want.double()).norm() / want.double().norm()) <= 1e-2
         assert float((state.double() / 1e30 - small.double()).norm() / small.double().norm()) <= 1e-2
+
+
+@pytest.mark.parametrize("seg_tiles", [0, 1], indirect=True)
+@pytest.mark.parametrize("dtype,path", [("bf16", "auto"), ("bf16", "simt"), ("f32", "auto")])
+def test_heads_that_grow(seg_tiles, dtype, path):  # noqa: F811
+    """Log-decays above 0: 200 tokens take the state to e^2, e^20 and e^80 of itself."""
+    x = inputs(2, 200, 3, 128, 64, dtype, 540, slopes=[-0.01, -0.1, -0.4])
+    check_fwd(x, path)
+    check_bwd(x, path)
