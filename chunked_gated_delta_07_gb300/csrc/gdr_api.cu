@@ -553,7 +553,9 @@ constexpr int64_t kDecayStepTokens = 8;
 // Sequences of at most this many tokens (packed: this many in all) run on the CUDA cores, whose
 // kernel has the shorter start: 16 heads, 4 tokens 9.4 us against the tensor cores' 14.1, 8 tokens
 // 10.5 against 13.9, 24 tokens 15.2 against 15.6, 64 tokens 26 against 16; 64 sequences, 4 tokens
-// 47 against 50, 8 tokens 58 against 50 (backward 125 against 136).
+// 47 against 50, 8 tokens 58 against 50 (backward 125 against 136).  The better side depends on the
+// number of sequences and heads too, which the rule leaves out: it loses those 8 of 58, and 4 of 14.7
+// with one sequence of 12 tokens.
 constexpr int64_t kDecayShortTokens = 8;
 
 // Segments of a call.  A pass runs one block (tensor cores) or one column slice (CUDA

@@ -9,7 +9,7 @@
 // the kd / 4 lanes that share columns.  The arithmetic is fp32 throughout.  Few blocks: bound by
 // a token's chain of exchanges, 0.3 us a token (7 packed sequences, 5003 tokens of 2 heads x 64 in
 // fp32, backward: 62 us in all).  Many: by issue slots, a quarter of the multiply-adds' rate
-// (8 x 4096 tokens of 16 heads x 128 in fp32, forward: 2.2 ms, the local pass 0.41 of it).  8 x 8
+// (8 x 4096 tokens of 16 heads x 128 in fp32, forward: 2.2 ms, 0.41 of them the local pass).  8 x 8
 // elements halve the exchanges, but the threads too: the packed call took 238 us with them and 86
 // with 4 x 8.
 #include <algorithm>
@@ -108,8 +108,8 @@ decay_rec_kernel(const DecayGeom g, const __grid_constant__ Passes passes) {
     // enters the state once per block.  That saves a third of the instructions and keeps the
     // powers exact: lam itself rounds to 24 bits, an error that a product of n of them
     // multiplies by n.  Blocks are whole tiles while lam^-15 costs no more than 2^22 of fp32's
-    // range, else single tokens (8 x 4096 tokens of 16 heads, all so fast: 3.0 ms against 2.2).  A forward pass decays the state before its first token too, a reversed one
-    // after its last.
+    // range, else single tokens (8 x 4096 tokens of 16 heads, all so fast: 3.0 ms against 2.2).  A
+    // forward pass decays the state before its first token too, a reversed one after its last.
     const int nb = gd >= -1.f ? kTb : 1;
     const DecayFactor step(gd * (float)nb);
     const int tid = threadIdx.x, dl = tid % kLanes, eg = tid / kLanes;

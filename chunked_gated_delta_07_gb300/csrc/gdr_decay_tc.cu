@@ -38,7 +38,7 @@
 // C' in TMEM, and, as the state takes half the registers, four warps of their own (20-23) for
 // O -> out (65536 tokens of 32 heads x 64 in 37 sequences: 391 us against 400).
 // What is left of the bound (8 x 4096 tokens of 16 heads, 128 units on 152 SMs: 116 us, 3.6 us a
-// tile; 262144 tokens: 82% of the measured bandwidth): a tile's chain through its A -- load, Sc,
+// tile; 262144 tokens: 84% of the measured bandwidth): a tile's chain through its A -- load, Sc,
 // P, O, store -- takes some 14000 cycles, with two tiles in flight.
 //
 // Rounding.  The state is fp32 and so are its updates: C' has 24 significant bits, so it goes
@@ -975,7 +975,7 @@ decay_out_kernel(const __grid_constant__ TcMaps maps, const __grid_constant__ Tc
 // needs no decay on the way.  Four groups of four warps take 32 tokens of a tile each, through
 // slots of C' in TMEM of their own, one each or two (kNarrow); four more add a tile's product to the sum, which they keep in
 // registers, while the next one's runs in the other accumulator.  262144 tokens of 16 heads, 19
-// segments in up to 3 parts: 150 us, 4.1 TB/s.  A tile takes an SM 1.9 us, near the 1.6 that its
+// segments in up to 3 parts: 142 us, 4.4 TB/s.  A tile takes an SM 1.8 us, near the 1.6 that its
 // copies need for 64 KB; the rest is units that do not come out even.
 constexpr int kLocThreads = 32 * 24, kLocProducer = 20, kLocIssuer = 21;   // warps
 constexpr int kLocMaxStages = 6;                             // 3 of 64 KB, or 6 of 32 (kNarrow)

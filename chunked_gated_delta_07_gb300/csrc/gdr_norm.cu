@@ -20,8 +20,8 @@
 // memory and writes one partial sum per (block, column), and a second kernel adds those.
 // No atomics: the result is the same on every run.
 //
-// Measured (bf16): 524288 rows x 128 with 16 weight rows forward 47.7 us, 5.7 TB/s, 84% of a
-// copy's; backward 71.7 us, 5.7 TB/s.  8191 rows x 2048 backward 29.2 us, 3.5 TB/s: with 14 pairs
+// Measured (bf16): 524288 rows x 128 with 16 weight rows forward 47.6 us, 5.7 TB/s, 84% of a
+// copy's; backward 71.5 us, 5.7 TB/s.  8191 rows x 2048 backward 29.0 us, 3.5 TB/s: with 14 pairs
 // of rows to a block, the first loads, the last stores and the sum of 304 partials weigh as much
 // as the rows between them.  16 elements a thread, which halves the threads of a row's exchanges,
 // gave 48.4, 167 and 65 us.
@@ -258,8 +258,8 @@ norm_fwd_kernel(const T *x, const float *__restrict__ w, const float *__restrict
 
 // part: [2][gridDim.y][G][D] partial sums of dw, then db (null where neither is wanted).
 // Rows in single elements get twice the registers, one block of 512 threads at a time: with two,
-// 8 elements' sums, weights and addresses do not fit (65537 rows x 999 bf16 208 us, with one 110;
-// 200000 x 125 137 and 66).  Rows in 16-byte pieces fit.
+// 8 elements' sums, weights and addresses do not fit (the kernel alone, with dy = x: 65537 rows x
+// 999 bf16 208 us, with one 110; 200000 x 125 137 and 66).  Rows in 16-byte pieces fit.
 template <typename T, int TPR, int NV, int VEC>
 __global__ void __launch_bounds__(bwd_threads<TPR>(), VEC > 1 ? kThreadsPerSm / bwd_threads<TPR>() : 1)
 norm_bwd_kernel(const T *dy, const T *x, const float *__restrict__ mean, const float *__restrict__ rstd,
@@ -421,8 +421,8 @@ struct NormPick {
 
 // The smallest group of threads that holds a row at 8 elements a thread (16 beyond 8192
 // columns): in 16-byte pieces where every row can be read that way, else in single elements, of
-// which 512 threads take 16 (20000 rows x 6001 fp32 backward 307 us, 1024 threads with 8 370;
-// 4097 bf16 forward 138 and 170).
+// which 512 threads take 16 (the kernel alone: 20000 rows x 6001 fp32 backward, dy = x, 307 us, 1024
+// threads with 8 370; 4097 bf16 forward 138 and 170).
 NormPick pick_layout(int D, size_t es, bool pieces) {
     const int vec = pieces ? (int)(16 / es) : 1, nv = 8 / vec;
     for (int tpr = 8; tpr <= 1024; tpr *= pieces ? 2 : 4)
