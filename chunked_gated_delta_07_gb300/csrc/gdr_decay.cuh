@@ -16,10 +16,10 @@
 // segment's own writes, decayed to its end (its start, reversed), combine chains the sums
 // into the states that cross the segments' boundaries, and the output pass runs every
 // segment from its entering state.  On the tensor cores the local pass skips the tokens that
-// the decay leaves nothing of; only of a NaN or an infinity it leaves a NaN.  The output pass
-// meets those tokens, and where it did a launch behind it runs the sequence's head again, uncut.
-// Boundary b of sequence n lies between its segments b
-// and b + 1 and has the slot seg_base[n] - n + b.
+// the decay leaves nothing of.  It does leave a NaN of a NaN or an infinity; the output pass
+// reads all tokens, and where its outputs show such a value, a launch behind it runs the
+// sequence's head again, uncut.  Boundary b of sequence n lies between its segments b and
+// b + 1 and has the slot seg_base[n] - n + b.
 #pragma once
 
 #include "gdr_internal.cuh"

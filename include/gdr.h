@@ -409,8 +409,9 @@ GDR_API gdr_status_t gdr_chunk_bwd(const void *q, const void *k, const void *v, 
  * however fast the head forgets: it reaches the outputs after it and hT (on the tensor
  * cores as a NaN, and also the outputs of its own 128-token tile; a call whose cut
  * sequence has one that the decay leaves nothing of runs that sequence's head twice);
- * other heads and sequences never.  Outputs must not overlap inputs.  Bad offsets: GDR_ERR_BAD_SEQLENS in the status word,
- * nothing is written.  Asynchronous on `stream`; deterministic.
+ * other heads and sequences never.  Outputs must not overlap inputs.  Bad offsets:
+ * GDR_ERR_BAD_SEQLENS in the status word, nothing is written.  Asynchronous on `stream`;
+ * deterministic.
  */
 GDR_API gdr_status_t gdr_decay_fwd(const void *q, const void *k, const void *v, const float *log_decay,
                            const float *h0, void *out, float *hT, const int32_t *cu_seqlens, int B,
