@@ -32,7 +32,8 @@ EXPORTS = ("gdr_chunk_fwd", "gdr_chunk_fwd_ex", "gdr_chunk_fwd_workspace_size",
            "gdr_profile_read", "gdr_profile_select", "gdr_chunk_fwd_noalloc", "gdr_recurrent_fwd", "gdr_chunk_bwd", "gdr_chunk_fwd_vec",
            "gdr_router_topk", "gdr_router_bias_update", "gdr_chunk_bwd_vec",
            "gdr_decay_fwd", "gdr_decay_bwd", "gdr_decay_workspace_size", "gdr_decay_recurrent_fwd",
-           "gdr_layer_norm_fwd", "gdr_layer_norm_bwd", "gdr_layer_norm_bwd_ex", "gdr_layer_norm_bwd_workspace_size")
+           "gdr_layer_norm_fwd", "gdr_layer_norm_bwd", "gdr_layer_norm_bwd_ex", "gdr_layer_norm_bwd_workspace_size",
+           "gdr_gated_scan_fwd", "gdr_gated_scan_bwd", "gdr_gated_scan_bwd_workspace_size", "gdr_gated_scan_recurrent_fwd")
 
 _lock = threading.Lock()
 _lib = None
@@ -67,6 +68,10 @@ _SIGS = {
     "gdr_layer_norm_bwd": (_I, [_P] * 8 + [_I64, _I, _I, _I, _P]),
     "gdr_layer_norm_bwd_ex": (_I, [_P] * 8 + [_I64, _I, _I, _I, _P, _SZ, _P]),
     "gdr_layer_norm_bwd_workspace_size": (_SZ, [_I64, _I, _I, _I]),
+    "gdr_gated_scan_fwd": (_I, [_P] * 7 + [_I, _I64, _I, _F, _I, _I, _I, _P]),
+    "gdr_gated_scan_bwd": (_I, [_P] * 10 + [_I, _I64, _I, _F, _I, _I, _I, _P, _SZ, _P]),
+    "gdr_gated_scan_bwd_workspace_size": (_SZ, [_I, _I64, _I, _I]),
+    "gdr_gated_scan_recurrent_fwd": (_I, [_P] * 4 + [_I, _I64, _I, _F, _I, _I, _I, _P]),
 }
 
 
@@ -534,6 +539,133 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, per_head=False, want_dweight=
     if rc != GDR_OK:
         raise GdrError(rc, "gdr_layer_norm_bwd_ex")
     return dx, dw, db
+
+
+# ---- gated scan: one decay per token and channel -----------------------------------------
+GDR_SOURCE_PLAIN, GDR_SOURCE_CONVEX, GDR_SOURCE_VARIANCE = 0, 1, 2
+_SOURCES = {"plain": GDR_SOURCE_PLAIN, "convex": GDR_SOURCE_CONVEX, "variance": GDR_SOURCE_VARIANCE}
+GDR_SCAN_INTERVAL = 128   # tokens from one kept state to the next
+
+
+def gdr_gated_scan_fwd(x, a, h0, out, hT, states, cu_seqlens, B, T, D, b, dtype, gate, source, stream=None) -> int:
+    return lib().gdr_gated_scan_fwd(_ptr(x), _ptr(a), _ptr(h0), _ptr(out), _ptr(hT), _ptr(states), _ptr(cu_seqlens),
+                                    B, T, D, float(b), dtype, gate, source, _stream(stream))
+
+
+def gdr_gated_scan_bwd(x, a, h0, states, dout, dhT, dx, da, dh0, cu_seqlens, B, T, D, b, dtype, gate, source,
+                       workspace=None, workspace_bytes=0, stream=None) -> int:
+    return lib().gdr_gated_scan_bwd(_ptr(x), _ptr(a), _ptr(h0), _ptr(states), _ptr(dout), _ptr(dhT), _ptr(dx),
+                                    _ptr(da), _ptr(dh0), _ptr(cu_seqlens), B, T, D, float(b), dtype, gate, source,
+                                    _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def gdr_gated_scan_bwd_workspace_size(B, T, D, packed=False) -> int:
+    return int(lib().gdr_gated_scan_bwd_workspace_size(B, T, D, int(packed)))
+
+
+def gdr_gated_scan_recurrent_fwd(x, a, state, out, N, T, D, b, dtype, gate, source, stream=None) -> int:
+    return lib().gdr_gated_scan_recurrent_fwd(_ptr(x), _ptr(a), _ptr(state), _ptr(out), N, T, D, float(b), dtype,
+                                              gate, source, _stream(stream))
+
+
+def check_scan_inputs(x, a, h0=None, cu_seqlens=None, dout=None, dhT=None, out=None, hT=None, states=None):
+    """Check the tensors of a gated scan against x [B, T, D], as check_sequence_inputs does; states
+    fp32 [B T // 128, D].  Returns (T, D, N)."""
+    import torch
+    if x is None or x.dim() != 3:
+        raise ValueError("x must be [B, T, D]")
+    dt, dev = x.dtype, x.device
+    if dt not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"x: dtype {dt}, expected bfloat16 or float32")
+    B, T, D = x.shape
+    _expect("x", x, x.shape, dt, dev)
+    _expect("a", a, x.shape, dt, dev)
+    N = B
+    if cu_seqlens is not None:
+        if B != 1:
+            raise ValueError("with cu_seqlens the token tensors are [1, T_total, D]")
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be [N + 1] with N >= 1")
+        _expect("cu_seqlens", cu_seqlens, cu_seqlens.shape, torch.int32, dev)
+        N = cu_seqlens.numel() - 1
+    for name, t in (("h0", h0), ("hT", hT), ("dhT", dhT)):
+        if t is not None:
+            _expect(name, t, (N, D), torch.float32, dev)
+    for name, t in (("out", out), ("dout", dout)):
+        if t is not None:
+            _expect(name, t, x.shape, dt, dev)
+    if states is not None:
+        _expect("states", states, (B * T // GDR_SCAN_INTERVAL, D), torch.float32, dev)
+    return T, D, N
+
+
+def _scan_form(gate, source):
+    for what, name, known in (("gate", gate, _GATES), ("source", source, _SOURCES)):
+        if name not in known:
+            raise ValueError(f"{what} must be one of {sorted(known)}")
+    return _GATES[gate], _SOURCES[source]
+
+
+def gated_scan_fwd(x, a, h0=None, cu_seqlens=None, b=2.0, gate="bounded", source="plain", out=None, hT=None,
+                   states=None, want_state=True, want_states=False, stream=None):
+    """h_t = alpha_t h_{t-1} + w x_t per channel, alpha_t = exp(g(a_t)); returns (out, hT, states).
+
+    x, a [B,T,D] on one CUDA device, of one dtype (bf16 or fp32); with cu_seqlens (int32, N+1) B
+    must be 1; h0, hT [N,D] fp32 (hT may be h0).  g is the gate ("bounded": -b sigmoid(a), "softplus":
+    -softplus(a)); source is w: "plain" 1, "convex" 1 - alpha, "variance" sqrt(1 - alpha^2).
+    states [B T // 128, D] fp32 (None unless wanted) are what gated_scan_bwd starts from: the state
+    behind every 128th token of the B T tokens."""
+    import torch
+    T, D, N = check_scan_inputs(x, a, h0, cu_seqlens, out=out, hT=hT, states=states)
+    _require_cuda(x, "x")
+    g, w = _scan_form(gate, source)
+    if out is None:
+        out = torch.empty_like(x)
+    if hT is None and want_state:
+        hT = torch.empty((N, D), dtype=torch.float32, device=x.device)
+    if states is None and want_states:
+        states = torch.empty((x.shape[0] * T // GDR_SCAN_INTERVAL, D), dtype=torch.float32, device=x.device)
+    rc = gdr_gated_scan_fwd(x, a, h0, out, hT, states, cu_seqlens, N, T, D, b, dtype_code(x), g, w, stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_gated_scan_fwd")
+    return out, hT, states
+
+
+def gated_scan_bwd(x, a, dout, dhT=None, h0=None, states=None, cu_seqlens=None, b=2.0, gate="bounded",
+                   source="plain", want_dh0=True, stream=None, workspace=None):
+    """Gradients of <dout, out> + <dhT, hT> of gated_scan_fwd: returns (dx, da, dh0).  Without the
+    forward's states (of the same inputs) they are computed again: into the workspace
+    (gdr_gated_scan_bwd_workspace_size bytes), which a call beside others on its own stream is given."""
+    import torch
+    if dout is None:
+        raise ValueError("dout is required")
+    T, D, N = check_scan_inputs(x, a, h0, cu_seqlens, dout=dout, dhT=dhT, states=states)
+    _require_cuda(x, "x")
+    g, w = _scan_form(gate, source)
+    dx, da = torch.empty_like(x), torch.empty_like(a)
+    dh0 = torch.empty((N, D), dtype=torch.float32, device=x.device) if want_dh0 else None
+    rc = gdr_gated_scan_bwd(x, a, h0, states, dout, dhT, dx, da, dh0, cu_seqlens, N, T, D, b, dtype_code(x), g, w,
+                            workspace, _workspace_bytes(workspace, x.device), stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_gated_scan_bwd")
+    return dx, da, dh0
+
+
+def gated_scan_recurrent_fwd(x, a, state, b=2.0, gate="bounded", source="plain", out=None, stream=None):
+    """Decode T tokens of the gated scan: x, a [N,T,D], state [N,D] fp32 updated in place; returns
+    out [N,T,D]."""
+    import torch
+    if state is None:
+        raise ValueError("state is required")
+    T, D, N = check_scan_inputs(x, a, h0=state, out=out)
+    _require_cuda(x, "x")
+    g, w = _scan_form(gate, source)
+    if out is None:
+        out = torch.empty_like(x)
+    rc = gdr_gated_scan_recurrent_fwd(x, a, state, out, N, T, D, b, dtype_code(x), g, w, stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_gated_scan_recurrent_fwd")
+    return out
 
 
 def gdr_gate_cumsum(a, G, cu_seqlens, B, T, H, chunk, b, dtype, gate, stream=None) -> int:

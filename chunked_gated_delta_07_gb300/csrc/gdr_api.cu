@@ -15,6 +15,7 @@
 
 #include "gdr_decay.cuh"
 #include "gdr_internal.cuh"
+#include "gdr_scan.cuh"
 #include "gdr_tc.cuh"
 
 namespace gdr {
@@ -736,6 +737,28 @@ gdr_status_t take_workspace(DeviceCtx *ctx, void *workspace, size_t workspace_by
     return GDR_OK;
 }
 
+gdr_status_t check_scan(int B, int64_t T, int D, float b, gdr_dtype_t dtype, gdr_gate_t gate, gdr_source_t source,
+                        const int32_t *cu, bool packed, ScanShape *s) {
+    if (dtype != GDR_BF16 && dtype != GDR_F32) return GDR_ERR_INVALID_ARG;
+    if (gate != GDR_GATE_BOUNDED && gate != GDR_GATE_SOFTPLUS) return GDR_ERR_INVALID_ARG;
+    if (source != GDR_SOURCE_PLAIN && source != GDR_SOURCE_CONVEX && source != GDR_SOURCE_VARIANCE)
+        return GDR_ERR_INVALID_ARG;
+    if (B < 1 || T < 0 || D < 1) return GDR_ERR_INVALID_ARG;
+    if (gate == GDR_GATE_BOUNDED && !(b > 0.f && std::isfinite(b))) return GDR_ERR_INVALID_ARG;
+    if (T > kScanMaxTokens || (!packed && (int64_t)B * T > kScanMaxTokens)) return GDR_ERR_UNSUPPORTED;
+    const int64_t total = packed ? T : (int64_t)B * T;
+    if (std::max<int64_t>(total, B) > ((int64_t)1 << 40) / D) return GDR_ERR_UNSUPPORTED;
+    *s = ScanShape{};
+    s->cu = cu;
+    s->N = B;
+    s->T_per = packed ? 0 : (int)T;
+    s->total = (int)total;
+    s->D = D;
+    s->b = b;
+    return GDR_OK;
+}
+inline size_t scan_states_bytes(const ScanShape &s) { return sizeof(float) * (size_t)(s.total / kScanTile) * s.D; }
+
 // No output may overlap an input or another output.
 bool outputs_clear(std::initializer_list<std::pair<const void *, size_t>> outs,
                    std::initializer_list<std::pair<const void *, size_t>> ins) {
@@ -1330,6 +1353,95 @@ gdr_status_t gdr_layer_norm_bwd_ex(const void *dy, const void *x, const float *m
     if (st != GDR_OK) return st;
     return launch_norm_bwd(dy, x, mean, rstd, weight, dx, dweight, dbias, rows, G, D, dtype, ctx->sms,
                            (float *)ws, stream) == cudaSuccess
+               ? GDR_OK
+               : GDR_ERR_CUDA;
+}
+
+gdr_status_t gdr_gated_scan_fwd(const void *x, const void *a, const float *h0, void *out, float *hT,
+                                float *states, const int32_t *cu_seqlens, int B, int64_t T, int D, float b,
+                                gdr_dtype_t dtype, gdr_gate_t gate, gdr_source_t source, gdr_stream_t stream_) {
+    ScanShape s;
+    const gdr_status_t st = check_scan(B, T, D, b, dtype, gate, source, cu_seqlens, cu_seqlens != nullptr, &s);
+    if (st != GDR_OK) return st;
+    if (s.total > 0 && (!x || !a || !out)) return GDR_ERR_INVALID_ARG;
+    const size_t xb = (size_t)s.total * D * (dtype == GDR_BF16 ? 2 : 4), hb = sizeof(float) * (size_t)B * D;
+    const size_t kb = scan_states_bytes(s), cb = sizeof(int32_t) * ((size_t)B + 1);
+    if (!outputs_clear({{out, xb}, {hT, hb}, {states, kb}}, {{x, xb}, {a, xb}, {cu_seqlens, cb}}) ||
+        !outputs_clear({{out, xb}, {states, kb}}, {{h0, hb}}) || (hT != h0 && overlaps(hT, hb, h0, hb)))
+        return GDR_ERR_INVALID_ARG;
+    cudaStream_t stream = (cudaStream_t)stream_;
+    if (s.total == 0 && !cu_seqlens) {   // no tokens: hT = h0
+        if (!hT || hT == h0) return GDR_OK;
+        const cudaError_t e = h0 ? cudaMemcpyAsync(hT, h0, hb, cudaMemcpyDeviceToDevice, stream)
+                                 : cudaMemsetAsync(hT, 0, hb, stream);
+        return e == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+    }
+    DeviceCtx *ctx = device_ctx();
+    if (!ctx) return GDR_ERR_CUDA;
+    return launch_scan_fwd(ScanFwd{x, a, h0, out, hT, states}, s, dtype, gate, source, ctx->sms, ctx->d_status,
+                           stream) == cudaSuccess
+               ? GDR_OK
+               : GDR_ERR_CUDA;
+}
+
+size_t gdr_gated_scan_bwd_workspace_size(int B, int64_t T, int D, int packed) {
+    ScanShape s;
+    if (check_scan(B, T, D, 1.f, GDR_F32, GDR_GATE_BOUNDED, GDR_SOURCE_PLAIN, nullptr, packed != 0, &s) != GDR_OK)
+        return 0;
+    return scan_states_bytes(s);
+}
+
+gdr_status_t gdr_gated_scan_bwd(const void *x, const void *a, const float *h0, const float *states,
+                                const void *dout, const float *dhT, void *dx, void *da, float *dh0,
+                                const int32_t *cu_seqlens, int B, int64_t T, int D, float b, gdr_dtype_t dtype,
+                                gdr_gate_t gate, gdr_source_t source, void *workspace, size_t workspace_bytes,
+                                gdr_stream_t stream_) {
+    ScanShape s;
+    gdr_status_t st = check_scan(B, T, D, b, dtype, gate, source, cu_seqlens, cu_seqlens != nullptr, &s);
+    if (st != GDR_OK) return st;
+    if (s.total > 0 && (!x || !a || !dout || !dx || !da)) return GDR_ERR_INVALID_ARG;
+    if (!al16(workspace)) return GDR_ERR_INVALID_ARG;
+    const size_t xb = (size_t)s.total * D * (dtype == GDR_BF16 ? 2 : 4), hb = sizeof(float) * (size_t)B * D;
+    const size_t kb = scan_states_bytes(s), cb = sizeof(int32_t) * ((size_t)B + 1);
+    if (!outputs_clear({{dx, xb}, {da, xb}, {dh0, hb}},
+                       {{x, xb}, {a, xb}, {dout, xb}, {h0, hb}, {dhT, hb}, {states, kb}, {cu_seqlens, cb}}))
+        return GDR_ERR_INVALID_ARG;
+    cudaStream_t stream = (cudaStream_t)stream_;
+    if (s.total == 0 && !cu_seqlens) {   // no tokens: dh0 = dhT
+        if (!dh0) return GDR_OK;
+        const cudaError_t e = dhT ? cudaMemcpyAsync(dh0, dhT, hb, cudaMemcpyDeviceToDevice, stream)
+                                  : cudaMemsetAsync(dh0, 0, hb, stream);
+        return e == cudaSuccess ? GDR_OK : GDR_ERR_CUDA;
+    }
+    DeviceCtx *ctx = device_ctx();
+    if (!ctx) return GDR_ERR_CUDA;
+    if (!states && kb > 0) {   // the states that the forward pass would have kept
+        char *ws;
+        if ((st = take_workspace(ctx, workspace, workspace_bytes, kb, &ws)) != GDR_OK) return st;
+        if (launch_scan_fwd(ScanFwd{x, a, h0, nullptr, nullptr, (float *)ws}, s, dtype, gate, source, ctx->sms,
+                            ctx->d_status, stream) != cudaSuccess)
+            return GDR_ERR_CUDA;
+        states = (const float *)ws;
+    }
+    return launch_scan_bwd(ScanBwd{x, a, dout, h0, dhT, states, dx, da, dh0}, s, dtype, gate, source, ctx->sms,
+                           ctx->d_status, stream) == cudaSuccess
+               ? GDR_OK
+               : GDR_ERR_CUDA;
+}
+
+gdr_status_t gdr_gated_scan_recurrent_fwd(const void *x, const void *a, float *state, void *out, int N, int64_t T,
+                                          int D, float b, gdr_dtype_t dtype, gdr_gate_t gate, gdr_source_t source,
+                                          gdr_stream_t stream) {
+    ScanShape s;
+    const gdr_status_t st = check_scan(N, T, D, b, dtype, gate, source, nullptr, false, &s);
+    if (st != GDR_OK) return st;
+    if (T == 0) return GDR_OK;
+    if (!x || !a || !state || !out) return GDR_ERR_INVALID_ARG;
+    if ((int64_t)N * D > (int64_t)1 << 38) return GDR_ERR_UNSUPPORTED;   // the grid's limit
+    const size_t xb = (size_t)s.total * D * (dtype == GDR_BF16 ? 2 : 4), hb = sizeof(float) * (size_t)N * D;
+    if (!outputs_clear({{out, xb}, {state, hb}}, {{x, xb}, {a, xb}})) return GDR_ERR_INVALID_ARG;
+    return launch_scan_step(x, a, state, out, N, (int)T, D, b, dtype, gate, source, (cudaStream_t)stream) ==
+                   cudaSuccess
                ? GDR_OK
                : GDR_ERR_CUDA;
 }

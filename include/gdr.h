@@ -501,6 +501,70 @@ GDR_API gdr_status_t gdr_layer_norm_bwd_ex(const void *dy, const void *x, const 
  * is wanted); 0 on invalid sizes. */
 GDR_API size_t gdr_layer_norm_bwd_workspace_size(int64_t rows, int G, int D, gdr_dtype_t dtype);
 
+/* What weighs the inputs of the gated scan. */
+typedef enum {
+    GDR_SOURCE_PLAIN = 0,   /* 1                                                     */
+    GDR_SOURCE_CONVEX = 1,  /* 1 - alpha: the state is a weighted mean of its inputs */
+    GDR_SOURCE_VARIANCE = 2 /* sqrt(1 - alpha^2): unit inputs leave a unit state     */
+} gdr_source_t;
+
+/*
+ * Gated scan, one decay per token and channel: the recurrence of a layer whose state is a
+ * vector, with the library's gates.  Per (sequence, channel)
+ *     alpha_t = exp(g(a_t)),   h_t = alpha_t h_{t-1} + w(alpha_t) x_t
+ * from h0 to hT; every h_t is an output.  The bounded gate is that of the incremental
+ * linear-attention layer ("Deep Dive: The Next Generation of Ultra-Long Context Sparse MoE
+ * LLMs", §3.3), whose decay here acts on a diagonal state.
+ *   x, a, out  [B, T, D] in dtype (packed: [1, T, D], cu_seqlens with B + 1 offsets, T in all)
+ *   h0, hT     [N, D] fp32, or NULL (zero / not written); hT may be h0 (carried in place)
+ *   states     [total / 128, D] fp32, or NULL: row i is the state behind token 128 i + 127 of
+ *              the token axis (all B T tokens one after the other), which the backward pass
+ *              starts from.  total / 128 is rounded down.
+ *   b          bound of the bounded gate, > 0 and finite (not looked at for softplus)
+ * D >= 1; B >= 1; T >= 0; at most 2^31 - 2304 tokens in all and 2^40 elements; sequences of no
+ * tokens pass h0 on to hT.  Element alignment is enough (16-byte pointers with D a multiple of
+ * 16 bytes are read fastest).  fp32 inside.  A NaN or an infinity stays in its channel's state
+ * to the end of the sequence (an infinity may become a NaN); other channels and sequences
+ * never see it.  Outputs must not overlap inputs.  Bad offsets: GDR_ERR_BAD_SEQLENS in the
+ * status word, nothing is written.  No scratch; asynchronous on `stream`; deterministic.
+ */
+GDR_API gdr_status_t gdr_gated_scan_fwd(const void *x, const void *a, const float *h0, void *out, float *hT,
+                                float *states, const int32_t *cu_seqlens, int B, int64_t T, int D, float b,
+                                gdr_dtype_t dtype, gdr_gate_t gate, gdr_source_t source,
+                                gdr_stream_t stream);
+
+/*
+ * The gradients of <dout, out> + <dhT, hT> of gdr_gated_scan_fwd with respect to x, a and h0.
+ * With l_t the gradient of h_t,
+ *     l_t = dout_t + alpha_{t+1} l_{t+1} (the last token's holds dhT too)
+ *     dx_t = w l_t,  da_t = l_t (alpha_t h_{t-1} + w'(g_t) x_t) g'(a_t),  dh0 = alpha_1 l_1
+ *   dout, dx, da [.., D] (dtype);  dhT [N, D] fp32 or NULL (zero);  dh0 [N, D] fp32 or NULL
+ *   states       as the forward pass wrote them for the same inputs, or NULL: they are computed
+ *                again, into the workspace
+ *   workspace    device scratch of gdr_gated_scan_bwd_workspace_size(...) bytes, 16-byte
+ *                aligned, or NULL: the internal per-device cache (calls that share it must not
+ *                overlap on the GPU).  Not looked at where states are given.
+ * Everything else as for gdr_gated_scan_fwd.
+ */
+GDR_API gdr_status_t gdr_gated_scan_bwd(const void *x, const void *a, const float *h0, const float *states,
+                                const void *dout, const float *dhT, void *dx, void *da, float *dh0,
+                                const int32_t *cu_seqlens, int B, int64_t T, int D, float b,
+                                gdr_dtype_t dtype, gdr_gate_t gate, gdr_source_t source, void *workspace,
+                                size_t workspace_bytes, gdr_stream_t stream);
+
+/* Scratch bytes of gdr_gated_scan_bwd without states; B sequences of T tokens, packed = 1: T
+ * tokens in all.  0 on invalid sizes, and where no scratch is needed. */
+GDR_API size_t gdr_gated_scan_bwd_workspace_size(int B, int64_t T, int D, int packed);
+
+/*
+ * The same recurrence token by token, for decoding: advances each sequence's state over T
+ * tokens (T = 1: one step) in place.  x, a, out [N, T, D] (dtype), state [N, D] fp32.  Nothing
+ * is allocated.  T = 0 leaves the state untouched.  Asynchronous on `stream`.
+ */
+GDR_API gdr_status_t gdr_gated_scan_recurrent_fwd(const void *x, const void *a, float *state, void *out, int N,
+                                          int64_t T, int D, float b, gdr_dtype_t dtype, gdr_gate_t gate,
+                                          gdr_source_t source, gdr_stream_t stream);
+
 /* Synchronise `stream`, then read and clear the current device's status word.
  * Returns GDR_OK, GDR_ERR_BAD_SEQLENS, GDR_ERR_TIMEOUT or GDR_ERR_CUDA. */
 GDR_API gdr_status_t gdr_get_status(gdr_stream_t stream);
