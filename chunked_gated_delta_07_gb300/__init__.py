@@ -33,7 +33,8 @@ EXPORTS = ("gdr_chunk_fwd", "gdr_chunk_fwd_ex", "gdr_chunk_fwd_workspace_size",
            "gdr_router_topk", "gdr_router_bias_update", "gdr_chunk_bwd_vec",
            "gdr_decay_fwd", "gdr_decay_bwd", "gdr_decay_workspace_size", "gdr_decay_recurrent_fwd",
            "gdr_layer_norm_fwd", "gdr_layer_norm_bwd", "gdr_layer_norm_bwd_ex", "gdr_layer_norm_bwd_workspace_size",
-           "gdr_gated_scan_fwd", "gdr_gated_scan_bwd", "gdr_gated_scan_bwd_workspace_size", "gdr_gated_scan_recurrent_fwd")
+           "gdr_gated_scan_fwd", "gdr_gated_scan_bwd", "gdr_gated_scan_bwd_workspace_size", "gdr_gated_scan_recurrent_fwd",
+           "gdr_add_norm_fwd", "gdr_add_norm_bwd", "gdr_norm_gate_fwd", "gdr_norm_gate_bwd", "gdr_block_norm_bwd_workspace_size")
 
 _lock = threading.Lock()
 _lib = None
@@ -72,6 +73,11 @@ _SIGS = {
     "gdr_gated_scan_bwd": (_I, [_P] * 10 + [_I, _I64, _I, _F, _I, _I, _I, _P, _SZ, _P]),
     "gdr_gated_scan_bwd_workspace_size": (_SZ, [_I, _I64, _I, _I]),
     "gdr_gated_scan_recurrent_fwd": (_I, [_P] * 4 + [_I, _I64, _I, _F, _I, _I, _I, _P]),
+    "gdr_add_norm_fwd": (_I, [_P] * 8 + [_I64, _I, _I, _F, _F, _I, _I, _P]),
+    "gdr_add_norm_bwd": (_I, [_P] * 10 + [_I64, _I, _I, _F, _I, _I, _P, _SZ, _P]),
+    "gdr_norm_gate_fwd": (_I, [_P] * 8 + [_I64, _I, _I, _F, _F, _I, _I, _I, _P]),
+    "gdr_norm_gate_bwd": (_I, [_P] * 11 + [_I64, _I, _I, _F, _I, _I, _I, _P, _SZ, _P]),
+    "gdr_block_norm_bwd_workspace_size": (_SZ, [_I64, _I, _I, _I]),
 }
 
 
@@ -539,6 +545,172 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, per_head=False, want_dweight=
     if rc != GDR_OK:
         raise GdrError(rc, "gdr_layer_norm_bwd_ex")
     return dx, dw, db
+
+
+# ---- the norms around a block ---------------------------------------------------------------
+GDR_NORM_LAYER, GDR_NORM_RMS = 0, 1
+GDR_ACT_SILU, GDR_ACT_SIGMOID = 0, 1
+_KINDS = {"layer": GDR_NORM_LAYER, "rms": GDR_NORM_RMS}
+_ACTS = {"silu": GDR_ACT_SILU, "sigmoid": GDR_ACT_SIGMOID}
+
+
+def gdr_add_norm_fwd(x, residual, weight, bias, sum, y, mean, rstd, rows, G, D, scale, eps, kind, dtype,
+                     stream=None) -> int:
+    return lib().gdr_add_norm_fwd(_ptr(x), _ptr(residual), _ptr(weight), _ptr(bias), _ptr(sum), _ptr(y), _ptr(mean),
+                                  _ptr(rstd), rows, G, D, float(scale), float(eps), kind, dtype, _stream(stream))
+
+
+def gdr_add_norm_bwd(dy, dsum, sum, mean, rstd, weight, dx, dresidual, dweight, dbias, rows, G, D, scale, kind, dtype,
+                     workspace=None, workspace_bytes=0, stream=None) -> int:
+    return lib().gdr_add_norm_bwd(_ptr(dy), _ptr(dsum), _ptr(sum), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(dx),
+                                  _ptr(dresidual), _ptr(dweight), _ptr(dbias), rows, G, D, float(scale), kind, dtype,
+                                  _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def gdr_norm_gate_fwd(x, gate, weight, bias, residual, y, mean, rstd, rows, G, D, scale, eps, kind, act, dtype,
+                      stream=None) -> int:
+    return lib().gdr_norm_gate_fwd(_ptr(x), _ptr(gate), _ptr(weight), _ptr(bias), _ptr(residual), _ptr(y), _ptr(mean),
+                                   _ptr(rstd), rows, G, D, float(scale), float(eps), kind, act, dtype, _stream(stream))
+
+
+def gdr_norm_gate_bwd(dy, x, gate, mean, rstd, weight, bias, dx, dgate, dweight, dbias, rows, G, D, scale, kind, act,
+                      dtype, workspace=None, workspace_bytes=0, stream=None) -> int:
+    return lib().gdr_norm_gate_bwd(_ptr(dy), _ptr(x), _ptr(gate), _ptr(mean), _ptr(rstd), _ptr(weight), _ptr(bias),
+                                   _ptr(dx), _ptr(dgate), _ptr(dweight), _ptr(dbias), rows, G, D, float(scale), kind,
+                                   act, dtype, _ptr(workspace), workspace_bytes, _stream(stream))
+
+
+def gdr_block_norm_bwd_workspace_size(rows, G, D, dtype=GDR_BF16) -> int:
+    return int(lib().gdr_block_norm_bwd_workspace_size(rows, G, D, dtype))
+
+
+def check_block_norm_inputs(x, weight=None, bias=None, mean=None, rstd=None, kind="rms", **like_x):
+    """Check the tensors of a norm around a block: weight, bias and statistics as
+    check_norm_inputs does, every other tensor like x (None is passed over).  Returns (rows, G, D)."""
+    sizes = check_norm_inputs(x, weight, bias, mean=mean, rstd=rstd)
+    if kind not in _KINDS:
+        raise ValueError(f"kind must be one of {sorted(_KINDS)}")
+    for name, t in like_x.items():
+        if t is not None:
+            _expect(name, t, x.shape, x.dtype, x.device)
+    return sizes
+
+
+def _norm_stats(x, kind, want_stats):
+    import torch
+    if not want_stats:
+        return None, None
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    return torch.empty_like(rstd) if kind == "layer" else None, rstd
+
+
+def add_norm_fwd(x, residual, weight=None, bias=None, scale=1.0, kind="rms", eps=1e-5, out=None, sum_out=None,
+                 want_stats=True, stream=None):
+    """The norm in front of a block with the residual stream's sum: r = residual + scale x, y = N(r);
+    returns (y, r, mean, rstd), without want_stats the latter two None, mean None for kind "rms".
+
+    x, residual [.., D] bf16 or fp32; kind "rms" or "layer"; weight, bias fp32 [D], or [G, D] with x
+    [.., G, D].  y is the norm of r as it is stored.  sum_out may be residual, and out may be x."""
+    import torch
+    if residual is None:
+        raise ValueError("residual is required")
+    rows, G, D = check_block_norm_inputs(x, weight, bias, kind=kind, residual=residual, out=out, sum_out=sum_out)
+    _require_cuda(x, "x")
+    if out is None:
+        out = torch.empty_like(x)
+    if sum_out is None:
+        sum_out = torch.empty_like(x)
+    mean, rstd = _norm_stats(x, kind, want_stats)
+    rc = gdr_add_norm_fwd(x, residual, weight, bias, sum_out, out, mean, rstd, rows, G, D, scale, eps, _KINDS[kind],
+                          dtype_code(x), stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_add_norm_fwd")
+    return out, sum_out, mean, rstd
+
+
+def _weight_grads(x, weight, per_head, want_dweight, want_dbias):
+    """dweight and dbias (None where not wanted) and G for a weight's shape."""
+    import torch
+    shape = weight.shape if weight is not None else x.shape[-2:] if per_head else x.shape[-1:]
+    dw, db = (torch.empty(shape, dtype=torch.float32, device=x.device) if w else None for w in (want_dweight, want_dbias))
+    return dw, db, max(1, x.shape[-2]) if len(shape) == 2 else 1
+
+
+def _need_stats(what, mean, rstd, kind):
+    if what is None or rstd is None:
+        raise ValueError("dy and rstd are required")
+    if (mean is None) != (kind == "rms"):
+        raise ValueError("mean goes with kind 'layer', and not with 'rms'")
+
+
+def add_norm_bwd(dy, r, rstd, mean=None, dr=None, weight=None, scale=1.0, kind="rms", per_head=False,
+                 want_dweight=True, want_dbias=False, stream=None, workspace=None):
+    """Backward of add_norm_fwd from its r, rstd and (kind "layer") mean, dr being the gradient of r
+    along the residual stream: returns (dx, dresidual, dweight, dbias), the latter two fp32 with
+    weight's shape (without a weight: [D], or [G, D] if per_head), None where not wanted.  With
+    scale 1 dx and dresidual are one tensor.  On a stream beside other calls it is given a
+    workspace of its own (gdr_block_norm_bwd_workspace_size bytes)."""
+    import torch
+    _need_stats(dy, mean, rstd, kind)
+    if per_head and r is not None and r.dim() < 2:
+        raise ValueError("per_head: r must be [.., G, D]")
+    rows, _, D = check_block_norm_inputs(r, weight, None, mean, rstd, kind, dy=dy, dr=dr)
+    _require_cuda(r, "r")
+    dw, db, G = _weight_grads(r, weight, per_head, want_dweight, want_dbias)
+    dres = torch.empty_like(r)
+    dx = torch.empty_like(r) if scale != 1.0 else None
+    rc = gdr_add_norm_bwd(dy, dr, r, mean, rstd, weight, dx, dres, dw, db, rows, G, D, scale, _KINDS[kind],
+                          dtype_code(r), workspace, _workspace_bytes(workspace, r.device), stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_add_norm_bwd")
+    return dres if dx is None else dx, dres, dw, db
+
+
+def norm_gate_fwd(x, gate, weight=None, bias=None, residual=None, scale=1.0, kind="rms", act="silu", eps=1e-5,
+                  out=None, want_stats=True, stream=None):
+    """The norm behind a block with its gate: y = [residual +] scale N(x) act(gate); returns
+    (y, mean, rstd), without want_stats the latter two None, mean None for kind "rms".
+
+    x, gate, residual [.., D] bf16 or fp32; act "silu" or "sigmoid"; kind, weight and bias as for
+    add_norm_fwd.  out may be one of the inputs."""
+    import torch
+    if gate is None:
+        raise ValueError("gate is required")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    rows, G, D = check_block_norm_inputs(x, weight, bias, kind=kind, gate=gate, residual=residual, out=out)
+    _require_cuda(x, "x")
+    if out is None:
+        out = torch.empty_like(x)
+    mean, rstd = _norm_stats(x, kind, want_stats)
+    rc = gdr_norm_gate_fwd(x, gate, weight, bias, residual, out, mean, rstd, rows, G, D, scale, eps, _KINDS[kind],
+                           _ACTS[act], dtype_code(x), stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_norm_gate_fwd")
+    return out, mean, rstd
+
+
+def norm_gate_bwd(dy, x, gate, rstd, mean=None, weight=None, bias=None, scale=1.0, kind="rms", act="silu",
+                  per_head=False, want_dweight=True, want_dbias=False, stream=None, workspace=None):
+    """Backward of norm_gate_fwd from its rstd and (kind "layer") mean: returns (dx, dgate, dweight,
+    dbias), the latter two as in add_norm_bwd (the residual's gradient is dy).  Workspace as there."""
+    import torch
+    _need_stats(dy, mean, rstd, kind)
+    if gate is None:
+        raise ValueError("gate is required")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    if per_head and x is not None and x.dim() < 2:
+        raise ValueError("per_head: x must be [.., G, D]")
+    rows, G, D = check_block_norm_inputs(x, weight, bias, mean, rstd, kind, dy=dy, gate=gate)
+    _require_cuda(x, "x")
+    dw, db, G = _weight_grads(x, weight if weight is not None else bias, per_head, want_dweight, want_dbias)
+    dx, dz = torch.empty_like(x), torch.empty_like(x)
+    rc = gdr_norm_gate_bwd(dy, x, gate, mean, rstd, weight, bias, dx, dz, dw, db, rows, G, D, scale, _KINDS[kind],
+                           _ACTS[act], dtype_code(x), workspace, _workspace_bytes(workspace, x.device), stream)
+    if rc != GDR_OK:
+        raise GdrError(rc, "gdr_norm_gate_bwd")
+    return dx, dz, dw, db
 
 
 # ---- gated scan: one decay per token and channel -----------------------------------------

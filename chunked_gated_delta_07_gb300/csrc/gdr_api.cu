@@ -13,6 +13,7 @@
 #include <utility>
 #include <vector>
 
+#include "gdr_block_norm.cuh"
 #include "gdr_decay.cuh"
 #include "gdr_internal.cuh"
 #include "gdr_scan.cuh"
@@ -759,6 +760,17 @@ gdr_status_t check_scan(int B, int64_t T, int D, float b, gdr_dtype_t dtype, gdr
 }
 inline size_t scan_states_bytes(const ScanShape &s) { return sizeof(float) * (size_t)(s.total / kScanTile) * s.D; }
 
+// Sizes and options of a norm around a block.
+gdr_status_t check_block_norm(const BlockNorm &n, gdr_dtype_t dtype) {
+    if (dtype != GDR_BF16 && dtype != GDR_F32) return GDR_ERR_INVALID_ARG;
+    if (n.kind != GDR_NORM_LAYER && n.kind != GDR_NORM_RMS) return GDR_ERR_INVALID_ARG;
+    if (n.act != GDR_ACT_SILU && n.act != GDR_ACT_SIGMOID) return GDR_ERR_INVALID_ARG;
+    if (n.rows < 0 || n.G < 1 || n.D < 1 || n.rows % n.G != 0) return GDR_ERR_INVALID_ARG;
+    if (!(n.eps >= 0.f) || !std::isfinite(n.eps) || !std::isfinite(n.scale)) return GDR_ERR_INVALID_ARG;
+    if (n.D > kNormMaxD || n.G > (1 << 20) || n.rows > ((int64_t)1 << 40)) return GDR_ERR_UNSUPPORTED;
+    return GDR_OK;
+}
+
 // No output may overlap an input or another output.
 bool outputs_clear(std::initializer_list<std::pair<const void *, size_t>> outs,
                    std::initializer_list<std::pair<const void *, size_t>> ins) {
@@ -769,6 +781,31 @@ bool outputs_clear(std::initializer_list<std::pair<const void *, size_t>> outs,
             if (overlaps(o->first, o->second, p->first, p->second)) return false;
     }
     return true;
+}
+
+// Row tensors of one size: each output may be one of the inputs itself (a row's element is read
+// before it is written), but not lie across one; outputs are apart.
+bool rows_clear(std::initializer_list<const void *> outs, std::initializer_list<const void *> ins, size_t bytes) {
+    for (auto o = outs.begin(); o != outs.end(); ++o) {
+        for (const void *i : ins)
+            if (*o != i && overlaps(*o, bytes, i, bytes)) return false;
+        for (auto p = o + 1; p != outs.end(); ++p)
+            if (overlaps(*o, bytes, *p, bytes)) return false;
+    }
+    return true;
+}
+
+// The scratch of a norm's backward pass, and its sums where there are no rows.
+gdr_status_t block_norm_bwd_scratch(const BlockNorm &n, gdr_dtype_t dtype, float *dweight, float *dbias, void *workspace,
+                                    size_t workspace_bytes, DeviceCtx **ctx, char **ws) {
+    if (!(*ctx = device_ctx())) return GDR_ERR_CUDA;
+    const size_t need = dweight || dbias ? block_norm_bwd_scratch_bytes(n.rows, n.G, n.D, dtype, (*ctx)->sms) : 0;
+    return take_workspace(*ctx, workspace, workspace_bytes, need, ws);
+}
+gdr_status_t no_rows(float *dweight, float *dbias, size_t bytes, cudaStream_t stream) {
+    if (dweight && cudaMemsetAsync(dweight, 0, bytes, stream) != cudaSuccess) return GDR_ERR_CUDA;
+    if (dbias && cudaMemsetAsync(dbias, 0, bytes, stream) != cudaSuccess) return GDR_ERR_CUDA;
+    return GDR_OK;
 }
 
 }  // namespace
@@ -1444,6 +1481,114 @@ gdr_status_t gdr_gated_scan_recurrent_fwd(const void *x, const void *a, float *s
                    cudaSuccess
                ? GDR_OK
                : GDR_ERR_CUDA;
+}
+
+gdr_status_t gdr_add_norm_fwd(const void *x, const void *residual, const float *weight, const float *bias,
+                              void *sum, void *y, float *mean, float *rstd, int64_t rows, int G, int D, float scale,
+                              float eps, gdr_norm_kind_t kind, gdr_dtype_t dtype, gdr_stream_t stream) {
+    const BlockNorm n{rows, G, D, scale, eps, kind, GDR_ACT_SILU};
+    const gdr_status_t st = check_block_norm(n, dtype);
+    if (st != GDR_OK) return st;
+    if (kind == GDR_NORM_RMS && mean) return GDR_ERR_INVALID_ARG;
+    if (rows == 0) return GDR_OK;
+    if (!x || !residual || !sum || !y) return GDR_ERR_INVALID_ARG;
+    const size_t xb = (size_t)rows * D * (dtype == GDR_BF16 ? 2 : 4), sb = sizeof(float) * (size_t)rows;
+    const size_t wb = sizeof(float) * (size_t)G * D;
+    if (!outputs_clear({{sum, xb}, {y, xb}, {mean, sb}, {rstd, sb}}, {{weight, wb}, {bias, wb}}) ||
+        !outputs_clear({{mean, sb}, {rstd, sb}}, {{x, xb}, {residual, xb}}) ||
+        !rows_clear({sum, y}, {x, residual}, xb) || sum == x || y == residual)
+        return GDR_ERR_INVALID_ARG;
+    DeviceCtx *ctx = device_ctx();
+    if (!ctx) return GDR_ERR_CUDA;
+    return launch_add_norm_fwd(x, residual, weight, bias, sum, y, mean, rstd, n, dtype, ctx->sms,
+                               (cudaStream_t)stream) == cudaSuccess
+               ? GDR_OK
+               : GDR_ERR_CUDA;
+}
+
+gdr_status_t gdr_add_norm_bwd(const void *dy, const void *dsum, const void *sum, const float *mean, const float *rstd,
+                              const float *weight, void *dx, void *dresidual, float *dweight, float *dbias,
+                              int64_t rows, int G, int D, float scale, gdr_norm_kind_t kind, gdr_dtype_t dtype,
+                              void *workspace, size_t workspace_bytes, gdr_stream_t stream_) {
+    const BlockNorm n{rows, G, D, scale, 0.f, kind, GDR_ACT_SILU};
+    gdr_status_t st = check_block_norm(n, dtype);
+    if (st != GDR_OK) return st;
+    if (!al16(workspace)) return GDR_ERR_INVALID_ARG;
+    const size_t xb = (size_t)rows * D * (dtype == GDR_BF16 ? 2 : 4), sb = sizeof(float) * (size_t)rows;
+    const size_t wb = sizeof(float) * (size_t)G * D;
+    cudaStream_t stream = (cudaStream_t)stream_;
+    if (rows == 0) return no_rows(dweight, dbias, wb, stream);
+    if (!dy || !sum || !rstd || !dresidual || (mean != nullptr) != (kind == GDR_NORM_LAYER)) return GDR_ERR_INVALID_ARG;
+    if (!outputs_clear({{dx, xb}, {dresidual, xb}, {dweight, wb}, {dbias, wb}}, {{mean, sb}, {rstd, sb}, {weight, wb}}) ||
+        !outputs_clear({{dweight, wb}, {dbias, wb}}, {{dy, xb}, {dsum, xb}, {sum, xb}}) ||
+        !rows_clear({dx, dresidual}, {dy, dsum, sum}, xb))
+        return GDR_ERR_INVALID_ARG;
+    DeviceCtx *ctx;
+    char *ws;
+    if ((st = block_norm_bwd_scratch(n, dtype, dweight, dbias, workspace, workspace_bytes, &ctx, &ws)) != GDR_OK) return st;
+    return launch_add_norm_bwd(dy, dsum, sum, mean, rstd, weight, dx, dresidual, dweight, dbias, n, dtype, ctx->sms,
+                               (float *)ws, stream) == cudaSuccess
+               ? GDR_OK
+               : GDR_ERR_CUDA;
+}
+
+gdr_status_t gdr_norm_gate_fwd(const void *x, const void *gate, const float *weight, const float *bias,
+                               const void *residual, void *y, float *mean, float *rstd, int64_t rows, int G, int D,
+                               float scale, float eps, gdr_norm_kind_t kind, gdr_act_t act, gdr_dtype_t dtype,
+                               gdr_stream_t stream) {
+    const BlockNorm n{rows, G, D, scale, eps, kind, act};
+    const gdr_status_t st = check_block_norm(n, dtype);
+    if (st != GDR_OK) return st;
+    if (kind == GDR_NORM_RMS && mean) return GDR_ERR_INVALID_ARG;
+    if (rows == 0) return GDR_OK;
+    if (!x || !gate || !y) return GDR_ERR_INVALID_ARG;
+    const size_t xb = (size_t)rows * D * (dtype == GDR_BF16 ? 2 : 4), sb = sizeof(float) * (size_t)rows;
+    const size_t wb = sizeof(float) * (size_t)G * D;
+    if (!outputs_clear({{y, xb}, {mean, sb}, {rstd, sb}}, {{weight, wb}, {bias, wb}}) ||
+        !outputs_clear({{mean, sb}, {rstd, sb}}, {{x, xb}, {gate, xb}, {residual, xb}}) ||
+        !rows_clear({y}, {x, gate, residual}, xb))
+        return GDR_ERR_INVALID_ARG;
+    DeviceCtx *ctx = device_ctx();
+    if (!ctx) return GDR_ERR_CUDA;
+    return launch_norm_gate_fwd(x, gate, weight, bias, residual, y, mean, rstd, n, dtype, ctx->sms,
+                                (cudaStream_t)stream) == cudaSuccess
+               ? GDR_OK
+               : GDR_ERR_CUDA;
+}
+
+gdr_status_t gdr_norm_gate_bwd(const void *dy, const void *x, const void *gate, const float *mean, const float *rstd,
+                               const float *weight, const float *bias, void *dx, void *dgate, float *dweight,
+                               float *dbias, int64_t rows, int G, int D, float scale, gdr_norm_kind_t kind,
+                               gdr_act_t act, gdr_dtype_t dtype, void *workspace, size_t workspace_bytes,
+                               gdr_stream_t stream_) {
+    const BlockNorm n{rows, G, D, scale, 0.f, kind, act};
+    gdr_status_t st = check_block_norm(n, dtype);
+    if (st != GDR_OK) return st;
+    if (!al16(workspace)) return GDR_ERR_INVALID_ARG;
+    const size_t xb = (size_t)rows * D * (dtype == GDR_BF16 ? 2 : 4), sb = sizeof(float) * (size_t)rows;
+    const size_t wb = sizeof(float) * (size_t)G * D;
+    cudaStream_t stream = (cudaStream_t)stream_;
+    if (rows == 0) return no_rows(dweight, dbias, wb, stream);
+    if (!dy || !x || !gate || !rstd || !dx || !dgate || (mean != nullptr) != (kind == GDR_NORM_LAYER))
+        return GDR_ERR_INVALID_ARG;
+    if (!outputs_clear({{dx, xb}, {dgate, xb}, {dweight, wb}, {dbias, wb}},
+                       {{mean, sb}, {rstd, sb}, {weight, wb}, {bias, wb}}) ||
+        !outputs_clear({{dweight, wb}, {dbias, wb}}, {{dy, xb}, {x, xb}, {gate, xb}}) ||
+        !rows_clear({dx, dgate}, {dy, x, gate}, xb))
+        return GDR_ERR_INVALID_ARG;
+    DeviceCtx *ctx;
+    char *ws;
+    if ((st = block_norm_bwd_scratch(n, dtype, dweight, dbias, workspace, workspace_bytes, &ctx, &ws)) != GDR_OK) return st;
+    return launch_norm_gate_bwd(dy, x, gate, mean, rstd, weight, bias, dx, dgate, dweight, dbias, n, dtype, ctx->sms,
+                                (float *)ws, stream) == cudaSuccess
+               ? GDR_OK
+               : GDR_ERR_CUDA;
+}
+
+size_t gdr_block_norm_bwd_workspace_size(int64_t rows, int G, int D, gdr_dtype_t dtype) {
+    if (rows < 1 || check_block_norm(BlockNorm{rows, G, D, 1.f, 0.f, GDR_NORM_RMS, GDR_ACT_SILU}, dtype) != GDR_OK) return 0;
+    DeviceCtx *ctx = device_ctx();
+    return block_norm_bwd_scratch_bytes(rows, G, D, dtype, ctx ? ctx->sms : 152);
 }
 
 gdr_status_t gdr_gate_cumsum(const void *a, float *G, const int32_t *cu_seqlens, int B,

@@ -1,0 +1,67 @@
+// gdr_block_norm.cuh -- the norms around a block, with what stands next to them in one pass:
+//     add_norm (in front):  r = residual + scale x,  y = N(r)
+//     norm_gate (behind):   y = [residual +] scale N(x) act(z)
+//     N(v) = vh w + b,  vh = (v - mu) s,  s = (mean((v - mu)^2) + eps)^{-1/2},  mu = mean(v) or 0 (rms)
+#pragma once
+
+#include "gdr_norm.cuh"
+
+namespace gdr {
+
+struct BlockNorm {
+    int64_t rows;
+    int G, D;
+    float scale, eps;
+    gdr_norm_kind_t kind;
+    gdr_act_t act;
+};
+
+size_t block_norm_bwd_scratch_bytes(int64_t rows, int G, int D, gdr_dtype_t dtype, int sms);
+cudaError_t launch_add_norm_fwd(const void *x, const void *res, const float *w, const float *b, void *sum, void *y,
+                                float *mean, float *rstd, const BlockNorm &n, gdr_dtype_t dtype, int sms,
+                                cudaStream_t stream);
+// dx may be null (not wanted)
+cudaError_t launch_add_norm_bwd(const void *dy, const void *dsum, const void *sum, const float *mean, const float *rstd,
+                                const float *w, void *dx, void *dres, float *dw, float *db, const BlockNorm &n,
+                                gdr_dtype_t dtype, int sms, float *scratch, cudaStream_t stream);
+cudaError_t launch_norm_gate_fwd(const void *x, const void *z, const float *w, const float *b, const void *res, void *y,
+                                 float *mean, float *rstd, const BlockNorm &n, gdr_dtype_t dtype, int sms,
+                                 cudaStream_t stream);
+cudaError_t launch_norm_gate_bwd(const void *dy, const void *x, const void *z, const float *mean, const float *rstd,
+                                 const float *w, const float *b, void *dx, void *dz, float *dw, float *db,
+                                 const BlockNorm &n, gdr_dtype_t dtype, int sms, float *scratch, cudaStream_t stream);
+
+#ifdef __CUDACC__
+namespace norm {
+
+// sigmoid(z); within 2^-20 of its value for bf16 tensors.  exp(-z) may be inf, giving 0.
+template <bool FINE> __device__ __forceinline__ float sigmoid_of(float z) {
+    if constexpr (FINE) return __frcp_rn(1.f + expf(-z));
+    return __fdividef(1.f, 1.f + __expf(-z));
+}
+
+template <typename T> __device__ __forceinline__ float rounded(float v) { return to_f32(from_f32<T>(v)); }
+
+// The place of a thread of a block: its weight row g, its row set, the columns of its pieces.
+struct Place {
+    int lane, gi, ri, g;
+    bool mine;
+    int64_t step, row_step, m, row;
+    __device__ __forceinline__ Place(int tpr, const NormShape &s) {
+        const int sub = threadIdx.x / tpr;
+        lane = threadIdx.x % tpr;
+        gi = sub % s.gpb;
+        ri = sub / s.gpb;
+        g = blockIdx.x * s.gpb + gi;
+        mine = ri < s.rpb && g < s.G;
+        step = (int64_t)gridDim.y * s.rpb;
+        row_step = step * s.G;
+        m = (int64_t)blockIdx.y * s.rpb + ri;
+        row = m * s.G + g;
+    }
+};
+
+}  // namespace norm
+#endif
+
+}  // namespace gdr

@@ -1,0 +1,201 @@
+// gdr_block_norm_bwd.cu -- gradients of the norms around a block (gdr_block_norm.cuh), from the
+// forward's statistics.  With vh = (v - mu) s and n = w dN, dN the gradient of N's output,
+//     through(n) = s (n - [mean(n)] - vh mean(n vh))            [layer norm alone]
+//     add_norm:   dN = dy,  dresidual = dr + through(n),  dx = scale dresidual
+//     norm_gate:  dN = scale dy act(z),  dx = through(n),  dz = scale dy (vh w + b) act'(z)
+//     dw = sum_r dN vh,  db = sum_r dN
+// Bound by HBM: each tensor crosses it once.  Rows in registers and inputs through a ring as in
+// the layer norm's backward pass, and as there the weights' sums stay in registers, one partial
+// sum per block, added in a fixed order by a second kernel.
+#include "gdr_block_norm.cuh"
+
+namespace gdr {
+namespace {
+
+using namespace norm;
+
+// GATE: dy, v = x, z [b] -> dx, dz; else dy, v = r [, dr] -> dx (may be null), dres.
+template <typename T, int TPR, int NV, int VEC, bool GATE, bool THREE>
+__global__ void __launch_bounds__(bwd_threads<TPR>(), VEC > 1 ? kThreadsPerSm / bwd_threads<TPR>() : 1)
+block_norm_bwd_kernel(const T *dy, const T *val, const T *third, const float *__restrict__ mean,
+                      const float *__restrict__ rstd, const float *__restrict__ w, const float *__restrict__ b, T *dx,
+                      T *dother, float *__restrict__ part, NormShape s, float scale, int rms, int act) {
+    constexpr int kThreads = bwd_threads<TPR>(), kTensors = 2 + THREE;
+    __shared__ float red[2][2][32];
+    let_next_start();
+    int turn = 0;
+    Place p(TPR, s);
+    constexpr int kDepth = VEC > 1 ? ring_depth<NV, kTensors>() : 2;
+    extern __shared__ uint4 ring[];
+    using Stream = RowStream<T, kThreads, TPR, NV, VEC>;
+    auto open = [&](const T *t, int k) {
+        Stream st{};
+        st.p = t + p.row * s.D + p.lane * VEC;
+        st.step = p.row_step * s.D;
+        st.ring = ring + k * kDepth * NV * kThreads + threadIdx.x;
+        st.p0 = t;
+        return st;
+    };
+    Stream ds = open(dy, 0), vs = open(val, 1), ts = open(THREE ? third : val, THREE ? 2 : 1);
+    auto ask = [&](int slot, bool on) {
+        ds.ask(slot, p.lane, s.D, on);
+        vs.ask(slot, p.lane, s.D, on);
+        if constexpr (THREE) ts.ask(slot, p.lane, s.D, on);
+        copies_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) ask(i, p.mine && p.m + i * p.step < s.sets);
+    auto stats = [&](int64_t m, int64_t row, float &mu, float &rs) {
+        const bool on = p.mine && m < s.sets;
+        mu = on && mean ? mean[row] : 0.f;
+        rs = on ? rstd[row] : 0.f;
+    };
+    float mu, rs;
+    stats(p.m, p.row, mu, rs);
+    float wv[NV][VEC], bv[NV][VEC], aw[NV][VEC], ab[NV][VEC];
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int c = (v * TPR + p.lane) * VEC + i;
+            const bool in = p.mine && c < s.D;
+            wv[v][i] = in && w ? w[(int64_t)p.g * s.D + c] : 1.f;
+            bv[v][i] = GATE && in && b ? b[(int64_t)p.g * s.D + c] : 0.f;
+            aw[v][i] = 0.f;
+            ab[v][i] = 0.f;
+        }
+    int slot = 0;
+    for (int64_t m0 = p.m - p.ri; m0 < s.sets; m0 += p.step, p.m += p.step, p.row += p.row_step) {
+        const bool on = p.mine && p.m < s.sets;
+        ask(slot == 0 ? kDepth - 1 : slot - 1, p.mine && p.m + (kDepth - 1) * p.step < s.sets);
+        float mu1, rs1;
+        stats(p.m + p.step, p.row + p.row_step, mu1, rs1);
+        copies_wait<kDepth - 1>();
+        typename Piece<T, VEC>::type rv[NV], rd[NV], rt[NV];
+        vs.read(slot, rv);
+        ds.read(slot, rd);
+        if constexpr (THREE) ts.read(slot, rt);
+        slot = slot == kDepth - 1 ? 0 : slot + 1;
+        float xv[NV][VEC], dv[NV][VEC], sum[2] = {0.f, 0.f};   // of n, of n vh
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+            const int c = (v * TPR + p.lane) * VEC;
+            const bool in = on && c < s.D;
+            widen<T, VEC>(rv[v], xv[v]);
+            widen<T, VEC>(rd[v], dv[v]);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) xv[v][i] = in ? (xv[v][i] - mu) * rs : 0.f;
+            if constexpr (GATE) {
+                float zv[VEC], oz[VEC];
+                widen<T, VEC>(rt[v], zv);
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) {
+                    const float g = sigmoid_of<sizeof(T) == 4>(zv[i]);
+                    const float d = scale * dv[v][i], n = fmaf(xv[v][i], wv[v][i], bv[v][i]);
+                    const float slope = act == GDR_ACT_SILU ? g * fmaf(zv[i], 1.f - g, 1.f) : g * (1.f - g);
+                    oz[i] = d * n * slope;
+                    dv[v][i] = d * (act == GDR_ACT_SILU ? zv[i] * g : g);
+                }
+                if (in) store_n<T, VEC>(dother + p.row * s.D + c, oz);
+            }
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                aw[v][i] = fmaf(dv[v][i], xv[v][i], aw[v][i]);
+                ab[v][i] += dv[v][i];
+                dv[v][i] *= wv[v][i];
+                sum[0] += dv[v][i];
+                sum[1] = fmaf(dv[v][i], xv[v][i], sum[1]);
+            }
+        }
+        row_sum<TPR, 2>(sum, red, turn);
+        const float c1 = rms ? 0.f : sum[0] * s.inv_d, c2 = sum[1] * s.inv_d;
+        if (on) {
+#pragma unroll
+            for (int v = 0; v < NV; ++v) {
+                const int c = (v * TPR + p.lane) * VEC;
+                if (c >= s.D) continue;
+                float o[VEC];
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) o[i] = rs * (dv[v][i] - c1 - xv[v][i] * c2);
+                if constexpr (GATE) {
+                    store_n<T, VEC>(dx + p.row * s.D + c, o);
+                } else {
+                    if constexpr (THREE) {
+                        float tv[VEC];
+                        widen<T, VEC>(rt[v], tv);
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) o[i] += tv[i];
+                    }
+                    store_n<T, VEC>(dother + p.row * s.D + c, o);
+                    if (dx) {
+#pragma unroll
+                        for (int i = 0; i < VEC; ++i) o[i] *= scale;
+                        store_n<T, VEC>(dx + p.row * s.D + c, o);
+                    }
+                }
+            }
+        }
+        mu = mu1;
+        rs = rs1;
+    }
+    // no copy of this thread's may still be on its way into the ring: those asked for past the
+    // last row fill it with zeros, and its memory is taken for the groups' sums below
+    copies_wait<0>();
+    if (!part) return;
+    block_partials<kThreads, TPR, NV, VEC>(aw, ab, part, (float *)ring, p.gi, p.ri, p.lane, p.g, p.mine, s);
+}
+
+template <typename T, bool GATE, bool THREE>
+cudaError_t bwd_t(const void *dy, const void *val, const void *third, const float *mean, const float *rstd, const float *w,
+                  const float *b, void *dx, void *dother, float *dw, float *db, const BlockNorm &bn, int sms, float *scratch,
+                  cudaStream_t stream) {
+    const NormPick p = pick_layout(bn.D, sizeof(T), in_pieces(bn.D, sizeof(T), {dy, val, third, dx, dother}));
+    const NormGrid n = norm_grid(p, bn.rows, bn.G, bn.D, 0.f, sms, 512);
+    float *part = dw || db ? scratch : nullptr;
+    const cudaError_t err = with_layout<T>(p, [&](auto tpr, auto nv, auto vec) {
+        auto kern = block_norm_bwd_kernel<T, tpr(), nv(), vec(), GATE, THREE>;
+        constexpr int kTensors = 2 + THREE;
+        const int smem = std::max(vec() > 1 ? kTensors * ring_depth<nv(), kTensors>() * n.threads * 16 * nv() : 0,
+                                  n.threads * 4 * nv() * vec());
+        const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (err != cudaSuccess) return err;
+        ProfScope prof(stream, GATE ? "norm_gate_bwd_kernel" : "add_norm_bwd_kernel");
+        kern<<<n.grid, n.threads, smem, stream>>>((const T *)dy, (const T *)val, (const T *)third, mean, rstd, w, b,
+                                                  (T *)dx, (T *)dother, part, n.s, bn.scale, bn.kind == GDR_NORM_RMS,
+                                                  bn.act);
+        count_launch();
+        return cudaGetLastError();
+    });
+    if (err != cudaSuccess || !part) return err;
+    return launch_norm_sum(part, dw, db, (int)n.grid.y, (int64_t)bn.G * bn.D, stream);
+}
+
+}  // namespace
+
+// As the layer norm's: the same blocks leave the same partial sums.
+size_t block_norm_bwd_scratch_bytes(int64_t rows, int G, int D, gdr_dtype_t dtype, int sms) {
+    return norm_bwd_scratch_bytes(rows, G, D, dtype, sms);
+}
+
+cudaError_t launch_add_norm_bwd(const void *dy, const void *dsum, const void *sum, const float *mean, const float *rstd,
+                                const float *w, void *dx, void *dres, float *dw, float *db, const BlockNorm &n,
+                                gdr_dtype_t dtype, int sms, float *scratch, cudaStream_t stream) {
+    if (dtype == GDR_BF16)
+        return dsum ? bwd_t<__nv_bfloat16, false, true>(dy, sum, dsum, mean, rstd, w, nullptr, dx, dres, dw, db, n, sms,
+                                                        scratch, stream)
+                    : bwd_t<__nv_bfloat16, false, false>(dy, sum, nullptr, mean, rstd, w, nullptr, dx, dres, dw, db, n,
+                                                         sms, scratch, stream);
+    return dsum ? bwd_t<float, false, true>(dy, sum, dsum, mean, rstd, w, nullptr, dx, dres, dw, db, n, sms, scratch, stream)
+                : bwd_t<float, false, false>(dy, sum, nullptr, mean, rstd, w, nullptr, dx, dres, dw, db, n, sms, scratch,
+                                             stream);
+}
+
+cudaError_t launch_norm_gate_bwd(const void *dy, const void *x, const void *z, const float *mean, const float *rstd,
+                                 const float *w, const float *b, void *dx, void *dz, float *dw, float *db,
+                                 const BlockNorm &n, gdr_dtype_t dtype, int sms, float *scratch, cudaStream_t stream) {
+    return dtype == GDR_BF16
+               ? bwd_t<__nv_bfloat16, true, true>(dy, x, z, mean, rstd, w, b, dx, dz, dw, db, n, sms, scratch, stream)
+               : bwd_t<float, true, true>(dy, x, z, mean, rstd, w, b, dx, dz, dw, db, n, sms, scratch, stream);
+}
+
+}  // namespace gdr

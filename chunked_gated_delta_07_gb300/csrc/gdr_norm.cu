@@ -25,155 +25,12 @@
 // of rows to a block, the first loads, the last stores and the sum of 304 partials weigh as much
 // as the rows between them.  16 elements a thread, which halves the threads of a row's exchanges,
 // gave 48.4, 167 and 65 us.
-#include <algorithm>
-#include <initializer_list>
-#include <type_traits>
-
-#include "gdr_internal.cuh"
+#include "gdr_norm.cuh"
 
 namespace gdr {
 namespace {
 
-constexpr unsigned kFull = 0xffffffffu;
-
-struct NormShape {
-    int64_t sets;   // rows / G
-    int G, D;
-    float eps, inv_d;
-    int gpb, rpb;   // weight rows and row sets of a block's thread groups
-};
-
-// VEC consecutive elements of a row as they are in memory: one element, or 16 bytes.
-template <typename T, int VEC> struct Piece {
-    using type = uint4;
-};
-template <typename T> struct Piece<T, 1> {
-    using type = T;
-};
-
-template <typename T, int VEC>
-__device__ __forceinline__ void widen(const typename Piece<T, VEC>::type &v, float (&x)[VEC]) {
-    if constexpr (VEC == 1) {
-        x[0] = to_f32(v);
-    } else {
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if constexpr (sizeof(T) == 4) {
-                x[i] = __uint_as_float(u[i]);
-            } else {
-                x[2 * i] = __uint_as_float(u[i] << 16);
-                x[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-            }
-        }
-    }
-}
-template <typename T, int VEC> __device__ __forceinline__ void store_n(T *p, const float (&x)[VEC]) {
-    if constexpr (VEC == 1) {
-        *p = from_f32<T>(x[0]);
-    } else if constexpr (sizeof(T) == 4) {
-        *(float4 *)p = make_float4(x[0], x[1], x[2], x[3]);
-    } else {
-        uint32_t u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-            u[i] = *(const uint32_t *)&h;
-        }
-        *(uint4 *)p = make_uint4(u[0], u[1], u[2], u[3]);
-    }
-}
-
-// Threads of a block: at least 256 (several rows), up to a row's; at least 512 in the
-// backward pass, whose blocks each write a partial sum of the weights' gradients.
-template <int TPR> constexpr int fwd_threads() { return TPR > 256 ? TPR : 256; }
-template <int TPR> constexpr int bwd_threads() { return TPR > 512 ? TPR : 512; }
-// Of either pass on an SM, as its registers allow (1536 in the forward pass: 60 us for the first
-// call above against 48).
-constexpr int kThreadsPerSm = 1024;
-
-// Rows under way per thread: loads of 16-byte pieces go through a ring in shared memory
-// (asynchronous copies, each thread reading back its own: no barrier), 4 rows deep where the
-// SM's blocks have room for it; single elements are loaded one row ahead in registers.
-constexpr int kRingBytesPerSm = 200 * 1024;
-template <int NV, int TENSORS> constexpr int ring_depth() {
-    constexpr int fit = kRingBytesPerSm / (kThreadsPerSm * 16 * NV * TENSORS);
-    return fit > 4 ? 4 : fit;
-}
-
-// The rows of one tensor as a thread takes them, one call of next() per step; `ahead` rows
-// have been asked for when a row is read.
-template <typename T, int THREADS, int TPR, int NV, int VEC> struct RowStream {
-    const T *p;        // the thread's first column in the next row to ask for
-    int64_t step;      // elements from row to row of the thread
-    uint4 *ring;       // [depth][NV][THREADS], at the thread
-    __device__ __forceinline__ void ask(int slot, int lane, int D, bool on) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int c = (i * TPR + lane) * VEC;
-            const unsigned dst = (unsigned)__cvta_generic_to_shared(ring + (slot * NV + i) * THREADS);
-            const int bytes = on && c < D ? 16 : 0;   // the rest of the 16 is filled with zeros
-            const T *src = bytes ? p + i * TPR * VEC : p0;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-        }
-        p += step;
-    }
-    const T *p0;       // any valid address of the tensor
-    __device__ __forceinline__ void read(int slot, uint4 (&v)[NV]) const {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] = ring[(slot * NV + i) * THREADS];
-    }
-};
-template <typename T, int THREADS, int TPR, int NV> struct RowStream<T, THREADS, TPR, NV, 1> {
-    const T *p;
-    int64_t step;
-    uint4 *ring;       // not used
-    T next[NV], cur[NV];
-    __device__ __forceinline__ void ask(int, int lane, int D, bool on) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            cur[i] = next[i];
-            next[i] = on && i * TPR + lane < D ? p[i * TPR] : from_f32<T>(0.f);
-        }
-        p += step;
-    }
-    const T *p0;
-    __device__ __forceinline__ void read(int, T (&v)[NV]) const {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) v[i] = cur[i];
-    }
-};
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// Sums of NS values over the TPR threads of a row.  Up to a warp: shuffles.  Beyond: a
-// shared-memory pass over the row's warps, two buffers taken in turn so that one barrier per
-// call is enough (every thread of the block calls).
-template <int TPR, int NS>
-__device__ __forceinline__ void row_sum(float (&v)[NS], float (*red)[NS][32], int &turn) {
-#pragma unroll
-    for (int o = (TPR < 32 ? TPR : 32) / 2; o; o >>= 1)
-#pragma unroll
-        for (int i = 0; i < NS; ++i) v[i] += __shfl_xor_sync(kFull, v[i], o);
-    if constexpr (TPR > 32) {
-        constexpr int kW = TPR / 32;
-        const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-        if (lane == 0)
-#pragma unroll
-            for (int i = 0; i < NS; ++i) red[turn][i][warp] = v[i];
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            float x = lane < kW ? red[turn][i][warp / kW * kW + lane] : 0.f;
-#pragma unroll
-            for (int o = kW / 2; o; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-            v[i] = __shfl_sync(kFull, x, 0);
-        }
-        turn ^= 1;
-    }
-}
+using namespace norm;
 
 template <typename T, int TPR, int NV, int VEC>
 __global__ void __launch_bounds__(fwd_threads<TPR>())
@@ -353,39 +210,7 @@ norm_bwd_kernel(const T *dy, const T *x, const float *__restrict__ mean, const f
     // last row fill it with zeros, and its memory is taken for the groups' sums below
     copies_wait<0>();
     if (!part) return;
-    // the block's partial sums, its row sets added in order through shared memory
-    const int64_t gd = (int64_t)s.G * s.D;
-    float *comb = (float *)ring;   // [NV * VEC][threads]
-    const int first = gi * TPR + lane;
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-        float(&a)[NV][VEC] = which ? ab : aw;
-        if (TPR < kThreads && s.rpb > 1) {
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < NV * VEC; ++k) comb[k * kThreads + threadIdx.x] = a[k / VEC][k % VEC];
-            __syncthreads();
-            if (mine && ri == 0)
-                for (int r = 1; r < s.rpb; ++r)
-#pragma unroll
-                    for (int k = 0; k < NV * VEC; ++k)
-                        a[k / VEC][k % VEC] += comb[k * kThreads + r * s.gpb * TPR + first];
-        }
-        if (!mine || ri != 0) continue;
-        float *dst = part + ((int64_t)which * gridDim.y + blockIdx.y) * gd + (int64_t)g * s.D;
-#pragma unroll
-        for (int v = 0; v < NV; ++v) {
-            const int c = (v * TPR + lane) * VEC;
-            if (c >= s.D) continue;
-            if constexpr (VEC % 4 == 0) {   // D is a multiple of VEC
-#pragma unroll
-                for (int i = 0; i < VEC; i += 4)
-                    *(float4 *)(dst + c + i) = make_float4(a[v][i], a[v][i + 1], a[v][i + 2], a[v][i + 3]);
-            } else {
-                dst[c] = a[v][0];
-            }
-        }
-    }
+    block_partials<kThreads, TPR, NV, VEC>(aw, ab, part, (float *)ring, gi, ri, lane, g, mine, s);
 }
 
 // out[c] = sum over the nb partial sums of column c, in a fixed order: 32 columns x 32
@@ -412,80 +237,6 @@ norm_sum_kernel(const float *__restrict__ part, float *__restrict__ dw, float *_
 #pragma unroll
     for (int o = 16; o; o >>= 1) a += __shfl_xor_sync(kFull, a, o);
     if (col == 0 && (int64_t)blockIdx.x * 32 + sl < gd) out[(int64_t)blockIdx.x * 32 + sl] = a;
-}
-
-// A row's layout over threads: TPR threads with NV pieces of VEC elements each.
-struct NormPick {
-    int tpr, nv, vec;
-};
-
-// The smallest group of threads that holds a row at 8 elements a thread (16 beyond 8192
-// columns): in 16-byte pieces where every row can be read that way, else in single elements, of
-// which 512 threads take 16 (the kernel alone: 20000 rows x 6001 fp32 backward, dy = x, 307 us, 1024
-// threads with 8 370; 4097 bf16 forward 138 and 170).
-NormPick pick_layout(int D, size_t es, bool pieces) {
-    const int vec = pieces ? (int)(16 / es) : 1, nv = 8 / vec;
-    for (int tpr = 8; tpr <= 1024; tpr *= pieces ? 2 : 4)
-        if (tpr * 8 >= D) return {tpr, nv, vec};
-    return {!pieces && D <= 8192 ? 512 : 1024, 2 * nv, vec};
-}
-
-struct NormGrid {
-    dim3 grid;   // groups of weight rows (up to 2^20) x blocks along the row sets
-    int threads;
-    NormShape s;
-};
-
-NormGrid norm_grid(const NormPick &p, int64_t rows, int G, int D, float eps, int sms, int least) {
-    NormGrid o{};
-    o.threads = std::max(p.tpr, least);
-    const int subs = o.threads / p.tpr;
-    o.s.sets = rows / G;
-    o.s.G = G;
-    o.s.D = D;
-    o.s.eps = eps;
-    o.s.inv_d = 1.f / (float)D;
-    o.s.gpb = std::min(G, subs);
-    o.s.rpb = subs / o.s.gpb;
-    const int64_t by = (G + o.s.gpb - 1) / o.s.gpb;
-    const int64_t want = (o.s.sets + o.s.rpb - 1) / o.s.rpb;
-    const int64_t most = std::max<int64_t>(1, (int64_t)sms * (kThreadsPerSm / o.threads) / by);
-    o.grid = dim3((unsigned)by, (unsigned)std::min(want, most));
-    return o;
-}
-
-// Calls f with the layout as compile-time constants.
-template <typename T, typename F> cudaError_t with_layout(const NormPick &p, F &&f) {
-    constexpr int V = 16 / sizeof(T);
-    using std::integral_constant;
-#define GDR_NORM_CASE(TPR_, NV_, VEC_)                                                             \
-    if (p.tpr == TPR_ && p.nv == NV_ && p.vec == VEC_)                                             \
-        return f(integral_constant<int, TPR_>{}, integral_constant<int, NV_>{}, integral_constant<int, VEC_>{});
-    constexpr int N = 8 / V;
-    GDR_NORM_CASE(8, N, V)
-    GDR_NORM_CASE(16, N, V)
-    GDR_NORM_CASE(32, N, V)
-    GDR_NORM_CASE(64, N, V)
-    GDR_NORM_CASE(128, N, V)
-    GDR_NORM_CASE(256, N, V)
-    GDR_NORM_CASE(512, N, V)
-    GDR_NORM_CASE(1024, N, V)
-    GDR_NORM_CASE(1024, 2 * N, V)
-    GDR_NORM_CASE(8, 8, 1)
-    GDR_NORM_CASE(32, 8, 1)
-    GDR_NORM_CASE(128, 8, 1)
-    GDR_NORM_CASE(512, 8, 1)
-    GDR_NORM_CASE(512, 16, 1)
-    GDR_NORM_CASE(1024, 16, 1)
-#undef GDR_NORM_CASE
-    return cudaErrorInvalidValue;
-}
-
-bool in_pieces(int D, size_t es, std::initializer_list<const void *> ptrs) {
-    if (D % (16 / es)) return false;
-    for (const void *p : ptrs)
-        if ((uintptr_t)p % 16) return false;
-    return true;
 }
 
 template <typename T>
@@ -526,15 +277,18 @@ cudaError_t bwd_t(const void *dy, const void *x, const float *mean, const float 
         return cudaGetLastError();
     });
     if (err != cudaSuccess || !part) return err;
-    const int64_t gd = (int64_t)G * D;
-    ProfScope prof(stream, "norm_sum_kernel");
-    const cudaError_t sum = launch_early(true, norm_sum_kernel, dim3((unsigned)((gd + 31) / 32), 2), 1024, 0, stream,
-                                         (const float *)part, dw, db, (int)n.grid.y, gd);
-    count_launch();
-    return sum;
+    return launch_norm_sum(part, dw, db, (int)n.grid.y, (int64_t)G * D, stream);
 }
 
 }  // namespace
+
+cudaError_t launch_norm_sum(const float *part, float *dw, float *db, int nb, int64_t gd, cudaStream_t stream) {
+    ProfScope prof(stream, "norm_sum_kernel");
+    const cudaError_t err = launch_early(true, norm_sum_kernel, dim3((unsigned)((gd + 31) / 32), 2), 1024, 0, stream,
+                                         part, dw, db, nb, gd);
+    count_launch();
+    return err;
+}
 
 size_t norm_bwd_scratch_bytes(int64_t rows, int G, int D, gdr_dtype_t dtype, int sms) {
     const size_t es = dtype == GDR_BF16 ? 2 : 4;

@@ -565,6 +565,76 @@ GDR_API gdr_status_t gdr_gated_scan_recurrent_fwd(const void *x, const void *a, 
                                           int64_t T, int D, float b, gdr_dtype_t dtype, gdr_gate_t gate,
                                           gdr_source_t source, gdr_stream_t stream);
 
+/* The norm of gdr_add_norm_* and gdr_norm_gate_*: with the mean taken off, or without. */
+typedef enum { GDR_NORM_LAYER = 0, GDR_NORM_RMS = 1 } gdr_norm_kind_t;
+/* The activation of gdr_norm_gate_*: z sigmoid(z), or sigmoid(z). */
+typedef enum { GDR_ACT_SILU = 0, GDR_ACT_SIGMOID = 1 } gdr_act_t;
+
+/*
+ * The norm in front of a block, with the residual stream's sum: row r becomes
+ *     sum = residual + scale x,   y = N(sum) = (sum - mean) rstd weight[r % G] + bias[r % G]
+ *     mean = sum over the row / D (GDR_NORM_LAYER) or 0 (GDR_NORM_RMS),
+ *     rstd = 1 / sqrt(sum((sum - mean)^2) / D + eps)
+ * The norm is that of the sum as it is stored, rounded to dtype.
+ *   x, residual, sum, y  [rows, D] in dtype (sum may be residual, and y may be x)
+ *   weight, bias         [G, D] fp32, or NULL (1 / 0); G as for gdr_layer_norm_fwd
+ *   mean, rstd           [rows] fp32, or NULL: what the backward pass reads; mean must be NULL
+ *                        for GDR_NORM_RMS
+ * rows >= 0 and a multiple of G; 1 <= D <= 16384 (GDR_ERR_UNSUPPORTED above); eps >= 0 and
+ * scale finite.  fp32 inside; any alignment of elements.  Asynchronous on `stream`.
+ */
+GDR_API gdr_status_t gdr_add_norm_fwd(const void *x, const void *residual, const float *weight, const float *bias,
+                              void *sum, void *y, float *mean, float *rstd, int64_t rows, int G, int D,
+                              float scale, float eps, gdr_norm_kind_t kind, gdr_dtype_t dtype,
+                              gdr_stream_t stream);
+
+/*
+ * Its backward pass, from the forward's sum and statistics; xh = (sum - mean) rstd, n = weight dy:
+ *     dresidual = dsum + rstd (n - mean_D(n) - xh mean_D(n xh))   (mean_D(n): GDR_NORM_LAYER alone)
+ *     dx = scale dresidual
+ *     dweight[g] = sum over rows r with r % G = g of dy xh,  dbias[g] = sum of dy
+ *   dy, dsum, sum, dx, dresidual [rows, D] in dtype; dsum (the gradient along the residual
+ *   stream) NULL: zero; dx NULL: not wanted; dx and dresidual may each be one of the inputs
+ *   dweight, dbias [G, D] fp32, or NULL (not wanted); mean NULL exactly for GDR_NORM_RMS
+ *   workspace as for gdr_layer_norm_bwd_ex, of gdr_block_norm_bwd_workspace_size(...) bytes
+ * The sums over rows are fp32 in a fixed order (no atomics).  Asynchronous on `stream`.
+ */
+GDR_API gdr_status_t gdr_add_norm_bwd(const void *dy, const void *dsum, const void *sum, const float *mean,
+                              const float *rstd, const float *weight, void *dx, void *dresidual,
+                              float *dweight, float *dbias, int64_t rows, int G, int D, float scale,
+                              gdr_norm_kind_t kind, gdr_dtype_t dtype, void *workspace,
+                              size_t workspace_bytes, gdr_stream_t stream);
+
+/*
+ * The norm behind a block, with its gate and the residual stream:
+ *     y = [residual +] scale N(x) act(gate),   N as above with x for sum
+ *   x, gate, residual, y [rows, D] in dtype; residual NULL: none; y may be one of the inputs
+ * Everything else as for gdr_add_norm_fwd.
+ */
+GDR_API gdr_status_t gdr_norm_gate_fwd(const void *x, const void *gate, const float *weight, const float *bias,
+                               const void *residual, void *y, float *mean, float *rstd, int64_t rows,
+                               int G, int D, float scale, float eps, gdr_norm_kind_t kind, gdr_act_t act,
+                               gdr_dtype_t dtype, gdr_stream_t stream);
+
+/*
+ * Its backward pass (the residual's gradient is dy itself); xh = (x - mean) rstd,
+ * d = scale dy act(gate), n = weight d:
+ *     dx = rstd (n - mean_D(n) - xh mean_D(n xh))   (mean_D(n): GDR_NORM_LAYER alone)
+ *     dgate = scale dy (xh weight + bias) act'(gate)
+ *     dweight[g] = sum over rows r with r % G = g of d xh,  dbias[g] = sum of d
+ *   dy, x, gate, dx, dgate [rows, D] in dtype; dx and dgate may each be one of the inputs
+ * Everything else as for gdr_add_norm_bwd.
+ */
+GDR_API gdr_status_t gdr_norm_gate_bwd(const void *dy, const void *x, const void *gate, const float *mean,
+                               const float *rstd, const float *weight, const float *bias, void *dx,
+                               void *dgate, float *dweight, float *dbias, int64_t rows, int G, int D,
+                               float scale, gdr_norm_kind_t kind, gdr_act_t act, gdr_dtype_t dtype,
+                               void *workspace, size_t workspace_bytes, gdr_stream_t stream);
+
+/* Scratch bytes of gdr_add_norm_bwd and gdr_norm_gate_bwd for these sizes (none where neither
+ * dweight nor dbias is wanted); 0 on invalid sizes. */
+GDR_API size_t gdr_block_norm_bwd_workspace_size(int64_t rows, int G, int D, gdr_dtype_t dtype);
+
 /* Synchronise `stream`, then read and clear the current device's status word.
  * Returns GDR_OK, GDR_ERR_BAD_SEQLENS, GDR_ERR_TIMEOUT or GDR_ERR_CUDA. */
 GDR_API gdr_status_t gdr_get_status(gdr_stream_t stream);
