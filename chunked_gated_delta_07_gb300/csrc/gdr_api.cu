@@ -748,7 +748,7 @@ gdr_status_t check_scan(int B, int64_t T, int D, float b, gdr_dtype_t dtype, gdr
     if (gate == GDR_GATE_BOUNDED && !(b > 0.f && std::isfinite(b))) return GDR_ERR_INVALID_ARG;
     if (T > kScanMaxTokens || (!packed && (int64_t)B * T > kScanMaxTokens)) return GDR_ERR_UNSUPPORTED;
     const int64_t total = packed ? T : (int64_t)B * T;
-    if (std::max<int64_t>(total, B) > ((int64_t)1 << 40) / D) return GDR_ERR_UNSUPPORTED;
+    if (D > kScanMaxD || std::max<int64_t>(total, B) > ((int64_t)1 << 40) / D) return GDR_ERR_UNSUPPORTED;
     *s = ScanShape{};
     s->cu = cu;
     s->N = B;
@@ -1477,7 +1477,7 @@ gdr_status_t gdr_gated_scan_recurrent_fwd(const void *x, const void *a, float *s
     if ((int64_t)N * D > (int64_t)1 << 38) return GDR_ERR_UNSUPPORTED;   // the grid's limit
     const size_t xb = (size_t)s.total * D * (dtype == GDR_BF16 ? 2 : 4), hb = sizeof(float) * (size_t)N * D;
     if (!outputs_clear({{out, xb}, {state, hb}}, {{x, xb}, {a, xb}})) return GDR_ERR_INVALID_ARG;
-    return launch_scan_step(x, a, state, out, N, (int)T, D, b, dtype, gate, source, (cudaStream_t)stream) ==
+    return launch_scan_step(x, a, state, out, s, dtype, gate, source, (cudaStream_t)stream) ==
                    cudaSuccess
                ? GDR_OK
                : GDR_ERR_CUDA;

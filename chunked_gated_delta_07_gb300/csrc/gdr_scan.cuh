@@ -18,21 +18,31 @@
 // chaining looks at the sign (where there can be cuts at all) instead of multiplying.
 #pragma once
 
+#include <cstdlib>
 #include <type_traits>
 
 #include "gdr_internal.cuh"
+#include "gdr_sm100.cuh"
+#include "gdr_tc.cuh"
 
 namespace gdr {
 
 constexpr int kScanTile = 128;      // tokens of a tile; the interval of the states kept for the backward pass
 constexpr int kScanChannels = 32;   // channels of a tile
 constexpr int kScanMaxCluster = 8;
+constexpr int kScanMaxD = 1 << 22;  // a tile's offsets are 32-bit
 constexpr int64_t kScanMaxTokens = 0x7fffffff - 2 * kScanTile * kScanMaxCluster;   // positions are 32-bit
+
+// The gates as the kernels tell them apart: a bound of at most 2 leaves alpha >= e^-2, which one
+// polynomial gives.
+enum ScanGate { kBounded = GDR_GATE_BOUNDED, kSoftplus = GDR_GATE_SOFTPLUS, kBoundedBy2 };
+constexpr int kScanPoly = 8;
 
 struct ScanShape {
     const int32_t *cu;   // offsets of packed sequences, or null: N sequences of T_per tokens
     int N, T_per, total, D;
     float b;
+    float2 poly[kScanPoly];   // of kBoundedBy2: 1 - alpha = s sum_k poly[k] s^k, s the sigmoid (each twice)
     int per_part;        // sequences of a part (a chain of tiles of its own)
     int parts, tiles, cluster;
 };
@@ -56,78 +66,144 @@ namespace scan {
 
 constexpr unsigned kFull = 0xffffffffu;
 
+// ---- pairs ------------------------------------------------------------------------------
+// A lane works on two channels at once: one instruction for both, where there is one.
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+__device__ __forceinline__ uint64_t bits(float2 v) {
+    uint64_t u;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(v.x), "f"(v.y));
+    return u;
+}
+__device__ __forceinline__ float2 unbits(uint64_t u) {
+    float2 v;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(u));
+    return v;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+    return unbits(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+    return unbits(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+    return unbits(d);
+}
+
 // ---- the gate ---------------------------------------------------------------------------
 // FINE (fp32 tensors): the library functions' accuracy.  Else the special-function unit's, within
 // a few 2^-23 of the value; what a long memory hangs on, 1 - alpha for alpha near 1, keeps its
-// relative accuracy in both (1 - e^g from a polynomial, and alpha from that).
-template <bool FINE> __device__ __forceinline__ float exp_of(float x) {
-    if constexpr (FINE) return expf(x);
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.44269504088896341f));
-    return y;
+// relative accuracy in both (1 - e^-n from a polynomial, and alpha from that).
+constexpr float kLog2e = 1.44269504088896341f;
+// 2^x
+__device__ __forceinline__ float2 exp2_fast(float2 x) {
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.y));
+    return x;
 }
-template <bool FINE> __device__ __forceinline__ float inverse(float x) {
-    if constexpr (FINE) return __frcp_rn(x);
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
+// e^(k x), kl = k log2 e
+template <bool FINE> __device__ __forceinline__ float2 exp_of(float2 x, float k, float kl) {
+    if constexpr (FINE) return make_float2(expf(k * x.x), expf(k * x.y));
+    return exp2_fast(mul2(x, both(kl)));
+}
+template <bool FINE> __device__ __forceinline__ float2 inverse(float2 x) {
+    if constexpr (FINE) return make_float2(__frcp_rn(x.x), __frcp_rn(x.y));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.y));
+    return x;
+}
+// max and min that keep a NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+    asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+    return a;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    asm("min.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+    return a;
 }
 
 struct Gate {
-    float alpha, w;     // the decay and the input's weight
-    float slope, dw;    // dg/da, and dw/dg dg/da
+    float2 alpha, w;     // the decay and the input's weight
+    float2 slope, dw;    // dg/da, and dw/dg dg/da
 };
 
-// e^g = alpha = 1 - left for g <= 0.  (e^g - 1) / g on [-1/2, 0] by a polynomial fitted to it
-// (relative error 1e-8 with these coefficients).
-template <bool FINE> __device__ __forceinline__ void decay_of(float g, float &alpha, float &left) {
-    const float e = exp_of<FINE>(g);
-    float p = 0.0011259226594120264f;
-    p = fmaf(p, g, 0.008193295449018478f);
-    p = fmaf(p, g, 0.04163204878568649f);
-    p = fmaf(p, g, 0.16666288673877716f);
-    p = fmaf(p, g, 0.49999985098838806f);
-    p = fmaf(p, g, 1.f);
-    const float near = -g * p;
-    const bool small = g > -0.5f;
-    left = small ? near : 1.f - e;
-    alpha = small ? 1.f - near : e;
-}
-
-template <bool FINE, int GATE, int SRC, bool GRAD> __device__ __forceinline__ Gate gate_of(float a, float b) {
+template <bool FINE, int GATE, int SRC, bool GRAD>
+__device__ __forceinline__ Gate gate_of(float2 a, const ScanShape &shape) {
     Gate o;
-    float left;
-    if constexpr (GATE == GDR_GATE_BOUNDED) {
-        const float c = a < -87.f ? -87.f : a;   // e^87 is finite; sigmoid is 0 below; a NaN stays
-        const float e = exp_of<FINE>(-c), s = inverse<FINE>(1.f + e);
-        const float g = -b * s;
-        decay_of<FINE>(g, o.alpha, left);
-        o.slope = g * (e * s);
+    float2 left;   // 1 - alpha
+    const float2 one = both(1.f), minus = both(-1.f);
+    const float b = shape.b;
+    if constexpr (GATE == kBoundedBy2) {
+        const float2 e = exp_of<FINE>(a, -1.f, -kLog2e), s = inverse<FINE>(add2(e, one));
+        if constexpr (GRAD) {
+            const float2 c = make_float2(min_nan(e.x, 1e38f), min_nan(e.y, 1e38f));
+            o.slope = mul2(mul2(s, both(-b)), mul2(c, s));
+        }
+        float2 p = shape.poly[kScanPoly - 1];
+#pragma unroll
+        for (int k = kScanPoly - 2; k >= 0; --k) p = fma2(p, s, shape.poly[k]);
+        left = mul2(s, p);
+        o.alpha = fma2(left, minus, one);
+    } else if constexpr (GATE == kBounded) {
+        // e^-a may be inf: the sigmoid is 0 then
+        const float2 e = exp_of<FINE>(a, -1.f, -kLog2e), s = inverse<FINE>(add2(e, one));
+        const float2 n = mul2(s, both(b));   // -g
+        if constexpr (GRAD) {
+            // g' = -b s (1 - s), 1 - s = e^-a s
+            const float2 c = make_float2(min_nan(e.x, 1e38f), min_nan(e.y, 1e38f));
+            o.slope = mul2(mul2(n, minus), mul2(c, s));
+        }
+        // (1 - e^-n) / n on [0, 1/2] by a polynomial fitted to it (relative error 1e-8 with these
+        // coefficients)
+        float2 p = both(-0.0011259226594120264f);
+        p = fma2(p, n, both(0.008193295449018478f));
+        p = fma2(p, n, both(-0.04163204878568649f));
+        p = fma2(p, n, both(0.16666288673877716f));
+        p = fma2(p, n, both(-0.49999985098838806f));
+        p = fma2(p, n, one);
+        const float2 near = mul2(n, p), above = fma2(near, minus, one);
+        const float2 far = FINE ? exp_of<FINE>(n, -1.f, -kLog2e) : exp_of<FINE>(s, -b, -b * kLog2e);
+        const float2 below = fma2(far, minus, one);
+        const bool s0 = n.x < 0.5f, s1 = n.y < 0.5f;
+        left = make_float2(s0 ? near.x : below.x, s1 ? near.y : below.y);
+        o.alpha = make_float2(s0 ? above.x : far.x, s1 ? above.y : far.y);
     } else {
         // e^{-softplus(a)} = 1 / (1 + e^a)
-        const float e = exp_of<FINE>(-fabsf(a)), lo = e * inverse<FINE>(1.f + e), hi = 1.f - lo;
-        o.alpha = a > 0.f ? lo : hi;
-        left = a > 0.f ? hi : lo;
-        o.slope = -left;
+        const float2 e = exp_of<FINE>(make_float2(fabsf(a.x), fabsf(a.y)), -1.f, -kLog2e);
+        const float2 lo = mul2(e, inverse<FINE>(add2(e, one))), hi = fma2(lo, minus, one);
+        const bool s0 = a.x > 0.f, s1 = a.y > 0.f;
+        o.alpha = make_float2(s0 ? lo.x : hi.x, s1 ? lo.y : hi.y);
+        left = make_float2(s0 ? hi.x : lo.x, s1 ? hi.y : lo.y);
+        if constexpr (GRAD) o.slope = mul2(left, minus);
     }
     if constexpr (SRC == GDR_SOURCE_PLAIN) {
-        o.w = 1.f;
-        o.dw = 0.f;
+        o.w = one;
+        o.dw = both(0.f);
     } else if constexpr (SRC == GDR_SOURCE_CONVEX) {
         o.w = left;
-        o.dw = -o.alpha * o.slope;
+        if constexpr (GRAD) o.dw = mul2(mul2(o.alpha, o.slope), minus);
     } else {
-        const float z = left * (1.f + o.alpha);   // 1 - alpha^2
-        // at z = 0 the weight is 0 and so is its gradient (slope / w goes with sqrt(left)); NaN stays
-        float r;
+        // w = sqrt(1 - alpha^2), w' = -alpha^2 / w g'.  At w = 0 g' is 0 too, and goes to it faster.
+        const float2 z = fma2(left, o.alpha, left);
+        float2 r = z;
+        if constexpr (GRAD) r = make_float2(max_nan(z.x, 1.2e-38f), max_nan(z.y, 1.2e-38f));
         if constexpr (FINE) {
-            o.w = sqrtf(z);
-            r = z > 0.f ? 1.f / o.w : 0.f;
+            r = make_float2(1.f / sqrtf(r.x), 1.f / sqrtf(r.y));
+            o.w = make_float2(sqrtf(z.x), sqrtf(z.y));
+        } else if constexpr (GRAD) {
+            asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(r.x));
+            asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(r.y));
+            o.w = mul2(z, r);
         } else {
-            r = z > 0.f ? rsqrtf(z) : 0.f;
-            o.w = z * r;
+            asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(o.w.x) : "f"(z.x));
+            asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(o.w.y) : "f"(z.y));
         }
-        if constexpr (GRAD) o.dw = -(o.alpha * o.alpha) * (o.slope * r);
+        if constexpr (GRAD) o.dw = mul2(mul2(mul2(o.alpha, o.alpha), minus), mul2(o.slope, r));
     }
     return o;
 }
@@ -142,6 +218,25 @@ struct Cursor {
     __device__ __forceinline__ void seek(const ScanShape &s, int first, int last, int token) {
         if (token >= from && token < to) return;
         int lo = first, hi = last - 1;   // the largest n that starts at or before the token is not empty
+        if (token >= to && to > 0 && n + 1 < last) {   // going up, mostly the next one
+            const int next = seq_start(s, n + 2);
+            if (token < next) {
+                ++n;
+                from = to;
+                to = next;
+                return;
+            }
+            lo = n + 1;
+        } else if (token < from && n > first) {   // going down, mostly the one before
+            const int prev = seq_start(s, n - 1);
+            if (token >= prev) {
+                --n;
+                to = from;
+                from = prev;
+                return;
+            }
+            hi = n - 1;
+        }
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
             if (seq_start(s, mid) <= token) lo = mid; else hi = mid - 1;
@@ -188,101 +283,169 @@ __device__ __forceinline__ bool offsets_ok(const ScanShape &s) {
 }
 
 // ---- chaining ---------------------------------------------------------------------------
-// out = A h + B, or B past a cut.
-__device__ __forceinline__ float through(float A, float B, float h, bool cuts) {
-    return fmaf(A, cuts && __float_as_int(A) < 0 ? 0.f : h, B);
+// A run of both channels: h_out = A h + B.
+struct Run {
+    float2 A, B;
+};
+__device__ __forceinline__ bool is_cut(float A) { return __float_as_int(A) < 0; }
+__device__ __forceinline__ float4 pack(const Run &r) { return make_float4(r.A.x, r.A.y, r.B.x, r.B.y); }
+__device__ __forceinline__ Run unpack(float4 v) { return Run{make_float2(v.x, v.y), make_float2(v.z, v.w)}; }
+// What comes out of a run for h going in; past a cut that is B.
+__device__ __forceinline__ float2 through(const Run &r, float2 h, bool cuts) {
+    if (cuts) h = make_float2(is_cut(r.A.x) ? 0.f : h.x, is_cut(r.A.y) ? 0.f : h.y);
+    return fma2(r.A, h, r.B);
 }
-// (A, B) := (A, B) followed by (a, b).
-__device__ __forceinline__ void follow(float &A, float &B, float a, float b, bool cuts) {
-    const bool cut = cuts && __float_as_int(a) < 0;
-    B = fmaf(a, cut ? 0.f : B, b);
-    A = cut ? a : cuts && __float_as_int(A) < 0 ? A : A * a;
+// The run f followed by the run r; a cut in either stays one.
+__device__ __forceinline__ Run follow(Run f, const Run &r, bool cuts) {
+    if (!cuts) return Run{mul2(f.A, r.A), fma2(r.A, f.B, r.B)};
+    const bool c0 = is_cut(r.A.x), c1 = is_cut(r.A.y);
+    Run o;
+    o.B = fma2(r.A, make_float2(c0 ? 0.f : f.B.x, c1 ? 0.f : f.B.y), r.B);
+    o.A.x = c0 ? r.A.x : is_cut(f.A.x) ? f.A.x : f.A.x * r.A.x;
+    o.A.y = c1 ? r.A.y : is_cut(f.A.y) ? f.A.y : f.A.y * r.A.y;
+    return o;
 }
 // A := A alpha; a cut stays one, also in front of a NaN.
-__device__ __forceinline__ void decay_past_cut(float &A, float alpha) {
-    if (__float_as_int(A) >= 0) A *= alpha;
+__device__ __forceinline__ void decay_past_cut(float2 &A, float2 alpha) {
+    if (!is_cut(A.x)) A.x *= alpha.x;
+    if (!is_cut(A.y)) A.y *= alpha.y;
+}
+__device__ __forceinline__ float2 other_half(float2 v) {
+    return make_float2(__shfl_xor_sync(kFull, v.x, 16), __shfl_xor_sync(kFull, v.y, 16));
 }
 
+// ---- clusters ------------------------------------------------------------------------------
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ void put_to_peer(const float4 *at, unsigned rank, float4 v) {
-    unsigned addr;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"((unsigned)__cvta_generic_to_shared(at)), "r"(rank));
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                 : "memory");
-}
+// The blocks of a cluster tell each other their tile's run, every step: a row of 16 lanes' pairs
+// into every peer's memory, each counted by the peer's barrier for the step (two of them taken in
+// turn; nobody can be two steps ahead, since a step needs everyone's).
+struct Peers {
+    float4 (*slot)[kScanMaxCluster][16];   // [2] steps
+    uint64_t *bar;                         // [2]
+    uint64_t limit_ns;
+
+    __device__ __forceinline__ static unsigned peer(const void *at, unsigned rank) {
+        unsigned a;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(sm100::smem_u32(at)), "r"(rank));
+        return a;
+    }
+    // Thread 0, once a step: what this block waits for.
+    __device__ __forceinline__ void expect(int step, int cluster) {
+        sm100::mbar_arrive_expect_tx(&bar[step & 1], cluster * 16 * (unsigned)sizeof(float4));
+    }
+    __device__ __forceinline__ void tell(int step, unsigned to, int rank, int l, float4 v) {
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [%0], {%1, %2, %3, %4}, [%5];" ::"r"(
+                         peer(&slot[step & 1][rank][l], to)),
+                     "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w), "r"(peer(&bar[step & 1], to))
+                     : "memory");
+    }
+    // Every thread; false when the wait ran out.
+    __device__ __forceinline__ bool wait(int step) {
+        const unsigned at = sm100::smem_u32(&bar[step & 1]), parity = step >> 1 & 1;
+        auto done = [&] {
+            unsigned ok;
+            asm volatile("{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 %0, 1, 0, p; }"
+                         : "=r"(ok)
+                         : "r"(at), "r"(parity)
+                         : "memory");
+            return ok != 0;
+        };
+        if (limit_ns == 0) return false;
+        if (done()) return true;
+        const uint64_t since = sm100::globaltimer_ns();
+        while (sm100::globaltimer_ns() - since < limit_ns)
+            if (done()) return true;
+        return false;
+    }
+};
 
 // ---- tiles of raw inputs ------------------------------------------------------------------
-// A warp copies the rows that its own lanes work on: 2 runs of L tokens, interleaved so that
-// both halves of the warp read the same token number without bank conflicts.
-template <typename T, int L> constexpr int kWarpTile = 2 * L * kScanChannels;   // elements
-
-// WIDE: 16 bytes a copy (rows and bases on 16-byte boundaries).  PAIR: what a lane reads itself,
-// where a lane's two channels can be copied asynchronously.  SINGLE: plain loads, element by element.
-enum CopyMode { kWide, kPair, kSingle };
-
-template <typename T> __host__ __device__ constexpr int wide_elems() { return 16 / (int)sizeof(T); }
-
-__device__ __forceinline__ void copy16(unsigned dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
+// TMA: a box of each tensor (rows and bases on 16-byte boundaries).  PAIR: a lane copies its own two
+// channels asynchronously, where they can be.  SINGLE: plain loads, element by element.
+enum CopyMode { kTma, kPair, kSingle };
 __device__ __forceinline__ void copy4(unsigned dst, const void *src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// Asks for the warp's part of NT tensors' tile; `row0` is the warp's first token, [lo, hi) the
-// part's.  Zeros take the place of what lies outside.
-template <typename T, int L, int NT>
-__device__ __forceinline__ void ask_tile(T *dst, const T *const (&src)[NT], int mode, int row0, int lo, int hi, int c0,
-                                         int D) {
-    const int lane = threadIdx.x & 31;
-    if (mode == kWide) {
-        constexpr int kPer = kScanChannels / wide_elems<T>();   // pieces of a row
-        constexpr int kStep = 32 / kPer;                        // rows of one round of the warp
-        const int r0 = lane / kPer, part = lane % kPer, c = c0 + part * wide_elems<T>();
+// A block's ring of DEPTH tiles of NT tensors, TOK tokens each; a lane's run is L of them.
+template <typename T, int L, int TOK, int NT, int DEPTH> struct Ring {
+    static constexpr int kTile = TOK * kScanChannels;   // elements
+    T *at;             // [DEPTH][NT][TOK][32]
+    uint64_t *full;    // [DEPTH]: the slot's boxes are there
+    int mode;
+    int issued;        // boxes' tiles asked for
+
+    __device__ __forceinline__ T *tile(int slot, int tensor) const { return at + (slot * NT + tensor) * kTile; }
+
+    // Every thread: asks for the tile from token `row` on, after the whole block is done with what
+    // was in the slot.  One lane of the warp whose turn it is issues the boxes.
+    __device__ __forceinline__ void ask(int slot, bool my_turn, const CUtensorMap *const (&maps)[NT],
+                                        const T *const (&src)[NT], int row, int lo, int hi, int c0, int D) {
+        if (mode == kTma) {
+            if (my_turn && (threadIdx.x & 31) == 0) {
+                sm100::mbar_arrive_expect_tx(&full[slot], NT * kTile * (unsigned)sizeof(T));
 #pragma unroll
-        for (int k = 0; k < 2 * L / kStep; ++k) {
-            const int r = r0 + k * kStep, t = row0 + (r & 1) * L + (r >> 1);
-            const bool on = t >= lo && t < hi && c < D;
-            const int64_t off = on ? (int64_t)t * D + c : 0;
-            const unsigned d = (unsigned)__cvta_generic_to_shared(dst + r * kScanChannels + part * wide_elems<T>());
-#pragma unroll
-            for (int i = 0; i < NT; ++i) copy16(d + i * kWarpTile<T, L> * (int)sizeof(T), src[i] + off, on ? 16 : 0);
+                for (int i = 0; i < NT; ++i) sm100::tma_load_2d(tile(slot, i), maps[i], c0, row, &full[slot]);
+            }
+            ++issued;
+            return;
         }
-        return;
-    }
-    const int half = lane >> 4, c = c0 + 2 * (lane & 15);
+        const int lane = threadIdx.x & 31, c = c0 + 2 * (lane & 15);
+        const int run = ((threadIdx.x >> 5) * 2 + (lane >> 4)) * L;
 #pragma unroll 2
-    for (int j = 0; j < L; ++j) {
-        const int t = row0 + half * L + j;
-        const bool on = t >= lo && t < hi;
-        const bool on0 = on && c < D, on1 = on && c + 1 < D;
-        const int64_t off = on0 ? (int64_t)t * D + c : 0;
-        T *d = dst + (2 * j + half) * kScanChannels + 2 * (lane & 15);
+        for (int j = run; j < run + L; ++j) {
+            const int t = row + j;
+            const bool on = t >= lo && t < hi;
+            const bool on0 = on && c < D, on1 = on && c + 1 < D;
+            const int64_t off = on0 ? (int64_t)t * D + c : 0;
 #pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            T *di = d + i * kWarpTile<T, L>;
-            if (mode == kPair) {
-                const unsigned da = (unsigned)__cvta_generic_to_shared(di);
-                copy4(da, src[i] + off, on0 ? 4 : 0);
-                if constexpr (sizeof(T) == 4) copy4(da + 4, src[i] + (on1 ? off + 1 : 0), on1 ? 4 : 0);
-            } else {
-                di[0] = on0 ? src[i][off] : from_f32<T>(0.f);
-                di[1] = on1 ? src[i][off + 1] : from_f32<T>(0.f);
+            for (int i = 0; i < NT; ++i) {
+                T *d = tile(slot, i) + j * kScanChannels + 2 * (lane & 15);
+                if (mode == kPair) {
+                    const unsigned da = sm100::smem_u32(d);
+                    copy4(da, src[i] + off, on0 ? 4 : 0);
+                    if constexpr (sizeof(T) == 4) copy4(da + 4, src[i] + (on1 ? off + 1 : 0), on1 ? 4 : 0);
+                } else {
+                    d[0] = on0 ? src[i][off] : from_f32<T>(0.f);
+                    d[1] = on1 ? src[i][off + 1] : from_f32<T>(0.f);
+                }
             }
         }
     }
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
+    // Closes a step's asking (also one that asked for nothing): every step, once.
+    __device__ __forceinline__ void close() {
+        if (mode != kTma) asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // Every thread: the slot's tile of `use` (its use'th) is there, or false where the wait ran out.
+    __device__ __forceinline__ bool wait(int slot, int use, uint64_t limit_ns) {
+        if (mode == kTma)
+            return limit_ns && sm100::mbar_try_wait(&full[slot], use & 1) ? true : wait_long(&full[slot], use & 1, limit_ns);
+        asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+        __syncwarp();
+        return true;
+    }
+    __device__ __noinline__ static bool wait_long(uint64_t *bar, int parity, uint64_t limit_ns) {
+        return sm100::mbar_wait(bar, parity, limit_ns);
+    }
+    // No copy of this block's is under way any more, also after a wait that ran out.
+    __device__ __forceinline__ void drain(bool lost) {
+        if (mode != kTma)
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
+        else if (lost)
+            for (int k = max(0, issued - DEPTH); k < issued; ++k)
+                sm100::mbar_wait(&full[k % DEPTH], k / DEPTH & 1, 2000000000ull);
+    }
+};
 
-// A lane's two channels of token j.
-template <typename T> __device__ __forceinline__ float2 read2(const T *tile, int j, int lane) {
-    const T *p = tile + (2 * j + (lane >> 4)) * kScanChannels + 2 * (lane & 15);
+// Two channels of a token, from the lane's place in a tile (run_at).
+template <typename T> __device__ __forceinline__ T *run_at(T *tile, int run, int l) {
+    return tile + run * kScanChannels + 2 * l;
+}
+template <typename T> __device__ __forceinline__ float2 read2(const T *run, int j) {
+    const T *p = run + j * kScanChannels;
     if constexpr (sizeof(T) == 4) {
         return *(const float2 *)p;
     } else {
@@ -290,27 +453,60 @@ template <typename T> __device__ __forceinline__ float2 read2(const T *tile, int
         return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
     }
 }
-template <typename T> __device__ __forceinline__ void write2(T *p, float a, float b) {
+template <typename T> __device__ __forceinline__ void write2(T *p, float2 x) {
     if constexpr (sizeof(T) == 4) {
-        *(float2 *)p = make_float2(a, b);
+        *(float2 *)p = x;
     } else {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x.x, x.y);
         *(uint32_t *)p = *(const uint32_t *)&v;
     }
 }
+// What a lane's L tokens from p outside [lo, hi) hold: gates of -inf, which keep the state and take
+// no input, and zeros in the other tensors.
+template <typename T, int L> __device__ __forceinline__ void blank(T *run, float value, int p, int lo, int hi) {
+#pragma unroll 1
+    for (int j = 0; j < L; ++j)
+        if (p + j < lo || p + j >= hi) run[j * kScanChannels] = run[j * kScanChannels + 1] = from_f32<T>(value);
+}
+// Two channels of a row of fp32 states, those that exist.
+__device__ __forceinline__ float2 load_state(const float *p, int64_t row, int D, int c) {
+    if (!p) return make_float2(0.f, 0.f);
+    p += row * D + c;
+    return make_float2(c < D ? p[0] : 0.f, c + 1 < D ? p[1] : 0.f);
+}
+__device__ __forceinline__ void store_state(float *p, int64_t row, int D, int c, float2 v) {
+    p += row * D + c;
+    if (c < D) p[0] = v.x;
+    if (c + 1 < D) p[1] = v.y;
+}
 
-// Calls f with the gate and the source as compile-time constants.
-template <typename F> cudaError_t with_form(gdr_gate_t gate, gdr_source_t source, F &&f) {
+// Calls f with the type, the gate and the source as compile-time constants; completes the shape.
+template <typename F>
+cudaError_t with_form(ScanShape &s, gdr_dtype_t dtype, gdr_gate_t gate, gdr_source_t source, F &&f) {
     using std::integral_constant;
-    auto by_source = [&](auto g) {
+    auto by_source = [&](auto t, auto g) {
         switch (source) {
-            case GDR_SOURCE_PLAIN: return f(g, integral_constant<int, GDR_SOURCE_PLAIN>{});
-            case GDR_SOURCE_CONVEX: return f(g, integral_constant<int, GDR_SOURCE_CONVEX>{});
-            default: return f(g, integral_constant<int, GDR_SOURCE_VARIANCE>{});
+            case GDR_SOURCE_PLAIN: return f(t, g, integral_constant<int, GDR_SOURCE_PLAIN>{});
+            case GDR_SOURCE_CONVEX: return f(t, g, integral_constant<int, GDR_SOURCE_CONVEX>{});
+            default: return f(t, g, integral_constant<int, GDR_SOURCE_VARIANCE>{});
         }
     };
-    return gate == GDR_GATE_BOUNDED ? by_source(integral_constant<int, GDR_GATE_BOUNDED>{})
-                                    : by_source(integral_constant<int, GDR_GATE_SOFTPLUS>{});
+    auto by_gate = [&](auto t) {
+        if (gate == GDR_GATE_SOFTPLUS) return by_source(t, integral_constant<int, kSoftplus>{});
+        if constexpr (sizeof(t) == 2) {   // fp32 tensors have the time for the exponential
+            if (s.b <= 2.f) {
+                // (1 - e^-n) / n on [0, 2] by a polynomial fitted to it, relative error 1.4e-8
+                static const double fit[kScanPoly] = {0.99999998631057,      -0.4999991992693423,    0.16665864060437813,
+                                                      -0.04163556673545308,  0.008272895784878453,   -0.0013234571801574847,
+                                                      0.00015753673867873683, -1.0291639928970174e-05};
+                double n = s.b;
+                for (int k = 0; k < kScanPoly; ++k, n *= s.b) s.poly[k].x = s.poly[k].y = (float)(fit[k] * n);
+                return by_source(t, integral_constant<int, kBoundedBy2>{});
+            }
+        }
+        return by_source(t, integral_constant<int, kBounded>{});
+    };
+    return dtype == GDR_BF16 ? by_gate(__nv_bfloat16{}) : by_gate(float{});
 }
 
 }  // namespace scan
@@ -321,21 +517,30 @@ cudaError_t launch_scan_fwd(const ScanFwd &t, ScanShape s, gdr_dtype_t dtype, gd
                             int sms, int *status, cudaStream_t stream);
 cudaError_t launch_scan_bwd(const ScanBwd &t, ScanShape s, gdr_dtype_t dtype, gdr_gate_t gate, gdr_source_t source,
                             int sms, int *status, cudaStream_t stream);
-cudaError_t launch_scan_step(const void *x, const void *a, float *state, void *out, int N, int T, int D, float b,
-                             gdr_dtype_t dtype, gdr_gate_t gate, gdr_source_t source, cudaStream_t stream);
+cudaError_t launch_scan_step(const void *x, const void *a, float *state, void *out, ScanShape s, gdr_dtype_t dtype,
+                             gdr_gate_t gate, gdr_source_t source, cudaStream_t stream);
+
+// The limit of a wait for the peers of a cluster: 2 s, or GDR_TC_WAIT_NS (the tests make waits
+// run out with it).
+inline uint64_t scan_wait_ns() {
+    const char *w = std::getenv("GDR_TC_WAIT_NS");
+    return w ? (uint64_t)std::strtoull(w, nullptr, 10) : 2000000000ull;
+}
 
 // Division of the work: `slots` blocks run at a time.  Sequences of one length are chains of
 // their own while there is room for all of them, else several follow each other in a part; then
 // the tiles along a part go to the blocks of a cluster, as many as there is room for.
-inline void scan_divide(ScanShape &s, int64_t slots) {
+inline void scan_divide(ScanShape &s, int64_t slots, int tok = kScanTile) {
     s.tiles = (s.D + kScanChannels - 1) / kScanChannels;
     const int64_t room = slots / s.tiles > 1 ? slots / s.tiles : 1;
     s.per_part = s.cu ? s.N : (int)((s.N + room - 1) / room);
     s.parts = (s.N + s.per_part - 1) / s.per_part;
     const int64_t tokens = s.cu ? s.total : (int64_t)s.per_part * s.T_per;
-    const int64_t most = room / s.parts, along = (tokens + kScanTile - 1) / kScanTile;
+    const int64_t most = room / s.parts, along = (tokens + tok - 1) / tok;
     int64_t c = most < along ? most : along;
-    s.cluster = (int)(c > kScanMaxCluster ? kScanMaxCluster : c < 1 ? 1 : c);
+    s.cluster = (int)(c > 8 ? 8 : c < 1 ? 1 : c);
+    if (const char *e = std::getenv("GDR_X_CS")) s.cluster = std::atoi(e) < along ? std::atoi(e) : (int)along;
+    if (s.cluster < 1) s.cluster = 1;
 }
 
 }  // namespace gdr

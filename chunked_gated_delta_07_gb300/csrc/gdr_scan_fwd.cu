@@ -16,234 +16,223 @@ namespace {
 using namespace scan;
 
 constexpr int kL = 16;                           // tokens of a lane's run
-constexpr int kWarps = kScanTile / (2 * kL);
+constexpr int kWarps = 4;
+constexpr int kTok = 2 * kL * kWarps;            // of a block's tile; divides 128, or 128 it
 constexpr int kThreads = 32 * kWarps;
 template <typename T> constexpr int kBlocksPerSm = sizeof(T) == 2 ? 4 : 3;
 template <typename T> constexpr int kDepth = sizeof(T) == 2 ? 3 : 2;   // tiles in shared memory
-template <typename T> constexpr int kTileBytes = kWarps * 2 * kWarpTile<T, kL> * (int)sizeof(T);
-template <typename T> constexpr int kSmem = kDepth<T> * kTileBytes<T>;
+template <typename T> using FwdRing = Ring<T, kL, kTok, 2, kDepth<T>>;
+template <typename T> constexpr int kSmem = kDepth<T> * 2 * FwdRing<T>::kTile * (int)sizeof(T) + 128;
+
+struct FwdMaps {
+    CUtensorMap x, a;
+};
 
 template <typename T, int GATE, int SRC>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm<T>)
-scan_fwd_kernel(const T *x, const T *a, const float *h0, T *out, float *hT, float *states, ScanShape s, int mode,
-                int pairs, int *status) {
+scan_fwd_kernel(const __grid_constant__ FwdMaps maps, const T *x, const T *a, const float *h0, T *out, float *hT,
+                float *states, const __grid_constant__ ScanShape s, int mode, int pairs, uint64_t limit_ns, int *status) {
     constexpr bool kFine = sizeof(T) == 4;
-    extern __shared__ uint4 ring_[];
+    extern __shared__ char smem[];
     __shared__ __align__(16) float4 agg[2][kWarps][16];
-    __shared__ __align__(16) float4 peer[2][kScanMaxCluster][16];
+    __shared__ __align__(16) float4 told[2][kScanMaxCluster][16];
+    __shared__ uint64_t bars[2], full[kDepth<T>];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = lane >> 4, l = lane & 15;
+    const int run_at0 = (warp * 2 + half) * kL;   // the lane's run in a tile
     const int CS = s.cluster, rank = blockIdx.x % CS, unit = blockIdx.x / CS;
-    const int c0 = unit % s.tiles * kScanChannels, c = c0 + 2 * l;
+    const int c0 = unit % s.tiles * kScanChannels, c = c0 + 2 * l, D = s.D;
     const int first = unit / s.tiles * s.per_part, last = min(s.N, first + s.per_part);
     if (!offsets_ok(s)) {
         if (threadIdx.x == 0) set_status(status, GDR_ERR_BAD_SEQLENS);
         return;
     }
     const int p0 = seq_start(s, first), p1 = seq_start(s, last);
-    const bool on0 = c < s.D, on1 = c + 1 < s.D;
-    if (s.cu && hT && hT != h0 && c0 + lane < s.D)   // sequences of no tokens
+    if (s.cu && hT && hT != h0 && c0 + lane < D)   // sequences of no tokens
         for (int n = first + warp + rank * kWarps; n < last; n += kWarps * CS)
             if (seq_start(s, n) == seq_start(s, n + 1))
-                hT[(int64_t)n * s.D + c0 + lane] = h0 ? h0[(int64_t)n * s.D + c0 + lane] : 0.f;
-    const int t0 = p0 / kScanTile, t1 = (p1 + kScanTile - 1) / kScanTile, steps = (t1 - t0 + CS - 1) / CS;
+                hT[(int64_t)n * D + c0 + lane] = h0 ? h0[(int64_t)n * D + c0 + lane] : 0.f;
+    const int t0 = p0 / kTok, t1 = (p1 + kTok - 1) / kTok, steps = (t1 - t0 + CS - 1) / CS;
     const bool many = last - first > 1;
-    T *ring = (T *)ring_ + warp * 2 * kWarpTile<T, kL>;
-    constexpr int kSlot = kWarps * 2 * kWarpTile<T, kL>;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kDepth<T>; ++i) sm100::mbar_init(&full[i], 1);
+        sm100::mbar_init(&bars[0], 1);
+        sm100::mbar_init(&bars[1], 1);
+        sm100::fence_mbar_init();
+    }
+    if (CS > 1)
+        cluster_sync();   // every peer runs, and its barriers are set up, before its memory is written to
+    else
+        __syncthreads();
+    FwdRing<T> ring{(T *)(((uintptr_t)smem + 127) & ~(uintptr_t)127), full, mode, 0};
+    const CUtensorMap *const map[2] = {&maps.x, &maps.a};
     const T *const src[2] = {x, a};
-    auto ask = [&](int i, int slot) {
-        const int64_t row = (int64_t)(t0 + i * (int64_t)CS + rank) * kScanTile + warp * 2 * kL;
-        if (i < steps && row < p1)
-            ask_tile<T, kL, 2>(ring + slot * kSlot, src, mode, (int)row, p0, p1, c0, s.D);
-        copies_commit();
+    auto ask = [&](int i, int slot) {   // the tile of step i
+        const int tile = t0 + i * CS + rank;
+        if (tile < t1) ring.ask(slot, warp == i % kWarps, map, src, tile * kTok, p0, p1, c0, D);
+        ring.close();
     };
-    for (int i = 0; i < kDepth<T> - 1; ++i) ask(i, i);
-    if (CS > 1) cluster_sync();   // every peer runs before its memory is written to
+    for (int i = 0; i < kDepth<T>; ++i) ask(i, i);
+    Peers peers{told, bars, limit_ns};
     Cursor cur{first, 0, -1};
-    float carry0 = 0.f, carry1 = 0.f;
-    int slot = 0;
-    for (int i = 0; i < steps; ++i) {
-        ask(i + kDepth<T> - 1, slot == 0 ? kDepth<T> - 1 : slot - 1);
-        copies_wait<kDepth<T> - 1>();
-        __syncwarp();
-        const T *tile = ring + slot * kSlot;
-        slot = slot == kDepth<T> - 1 ? 0 : slot + 1;
-        const bool cuts = many || i == 0;
-        const int64_t base = (int64_t)(t0 + i * (int64_t)CS + rank) * kScanTile;   // may lie behind the part
-        const int p = (int)min(base + (warp * 2 + half) * kL, (int64_t)p1);
-        const int lo = max(p, p0), hi = min(p + kL, p1);
-        const bool whole = hi - lo == kL;
-        const Marks m = marks_of(s, cur, first, last, p, lo, hi);
-        float al[kL][2], u[kL][2], A0 = 1.f, A1 = 1.f, B0 = 0.f, B1 = 0.f;
-#pragma unroll
-        for (int j = 0; j < kL; ++j) {
-            const float2 xv = read2(tile, j, lane), av = read2(tile + kWarpTile<T, kL>, j, lane);
-            const Gate g0 = gate_of<kFine, GATE, SRC, false>(av.x, s.b), g1 = gate_of<kFine, GATE, SRC, false>(av.y, s.b);
-            al[j][0] = g0.alpha;
-            al[j][1] = g1.alpha;
-            u[j][0] = SRC == GDR_SOURCE_PLAIN ? xv.x : g0.w * xv.x;
-            u[j][1] = SRC == GDR_SOURCE_PLAIN ? xv.y : g1.w * xv.y;
+    float2 carry = both(0.f);
+    bool lost = false;   // a wait ran out: the results are lost, but every block goes through its steps
+    // of the lane's run in the output's tile, in bytes
+    const unsigned lane_out = ((unsigned)run_at0 * (unsigned)D + (unsigned)c) * (unsigned)sizeof(T);
+    for (int i = 0, slot = 0, use = 0; i < steps; ++i) {
+        if (CS > 1 && threadIdx.x == 0 && !lost) peers.expect(i, CS);
+        const int base = (t0 + i * CS + rank) * kTok;   // may lie behind the part
+        const bool there = base < p1, cuts = many || i == 0;
+        // a tile that one sequence fills, and goes beyond on both sides
+        bool inner = false;
+        if (there) {
+            cur.seek(s, first, last, max(base, p0));
+            inner = cur.from < base && cur.to > base + kTok && mode == kTma && pairs;
+            if (!lost) lost = !__all_sync(kFull, ring.wait(slot, use, limit_ns));
         }
-        if (!whole) {
-#pragma unroll
-            for (int j = 0; j < kL; ++j)
-                if (p + j < lo || p + j >= hi) {
-                    al[j][0] = al[j][1] = 1.f;
-                    u[j][0] = u[j][1] = 0.f;
+        T *tx = run_at(ring.tile(slot, 0), run_at0, l), *ta = run_at(ring.tile(slot, 1), run_at0, l);
+        const int p = min(base, p1) + run_at0, lo = max(p, p0), hi = min(p + kL, p1);
+        float2 al[kL], u[kL];
+        Run run{both(1.f), both(0.f)};
+        Cursor mine = cur;
+        Marks m{0, 0};
+        if (there) {
+            if (!inner) {
+                m = marks_of(s, mine, first, last, p, lo, hi);
+                if (hi - lo < kL) {
+                    blank<T, kL>(tx, 0.f, p, lo, hi);
+                    blank<T, kL>(ta, -INFINITY, p, lo, hi);
+                    sm100::fence_proxy_async_smem();   // before the slot is filled again
                 }
-        }
-        if (m.first) {
-            int n = cur.n;
-#pragma unroll
-            for (int j = 0; j < kL; ++j)
-                if (m.first >> j & 1) {
-                    n = seq_from(s, n, p + j);
-                    const float *h = h0 + (int64_t)n * s.D + c;
-                    u[j][0] = fmaf(al[j][0], h0 && on0 ? h[0] : 0.f, u[j][0]);
-                    u[j][1] = fmaf(al[j][1], h0 && on1 ? h[1] : 0.f, u[j][1]);
-                    A0 = A1 = -1.f;
-                    B0 = u[j][0];
-                    B1 = u[j][1];
-                } else {
-                    B0 = fmaf(al[j][0], B0, u[j][0]);
-                    B1 = fmaf(al[j][1], B1, u[j][1]);
-                    decay_past_cut(A0, al[j][0]);
-                    decay_past_cut(A1, al[j][1]);
-                }
-        } else {
+            }
 #pragma unroll
             for (int j = 0; j < kL; ++j) {
-                B0 = fmaf(al[j][0], B0, u[j][0]);
-                B1 = fmaf(al[j][1], B1, u[j][1]);
-                A0 *= al[j][0];
-                A1 *= al[j][1];
+                const Gate g = gate_of<kFine, GATE, SRC, false>(read2(ta, j), s);
+                const float2 xv = read2(tx, j);
+                al[j] = g.alpha;
+                u[j] = SRC == GDR_SOURCE_PLAIN ? xv : mul2(g.w, xv);
             }
-        }
-        // the first half's run, then both; the second half's lanes need the first's
-        const float a0 = __shfl_xor_sync(kFull, A0, 16), a1 = __shfl_xor_sync(kFull, A1, 16);
-        const float b0 = __shfl_xor_sync(kFull, B0, 16), b1 = __shfl_xor_sync(kFull, B1, 16);
-        if (half == 0) {
-            float wa0 = A0, wa1 = A1, wb0 = B0, wb1 = B1;
-            follow(wa0, wb0, a0, b0, cuts);
-            follow(wa1, wb1, a1, b1, cuts);
-            agg[i & 1][warp][l] = make_float4(wa0, wa1, wb0, wb1);
-        }
-        __syncthreads();
-        float h0v, h1v;
-        if (CS == 1) {
-            float e0 = carry0, e1 = carry1;
-            h0v = e0;
-            h1v = e1;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float4 r = agg[i & 1][w][l];
-                if (w == warp) {
-                    h0v = e0;
-                    h1v = e1;
-                }
-                e0 = through(r.x, r.z, e0, cuts);
-                e1 = through(r.y, r.w, e1, cuts);
-            }
-            carry0 = e0;
-            carry1 = e1;
-        } else {
-            float pa0 = 1.f, pa1 = 1.f, pb0 = 0.f, pb1 = 0.f;   // of the warps in front; warp 0: of all
-            const int upto = warp == 0 ? kWarps : warp;
-            for (int w = 0; w < upto; ++w) {
-                const float4 r = agg[i & 1][w][l];
-                follow(pa0, pb0, r.x, r.z, cuts);
-                follow(pa1, pb1, r.y, r.w, cuts);
-            }
-            if (warp == 0) {
-                for (int r = half; r < CS; r += 2)
-                    put_to_peer(&peer[i & 1][rank][l], r, make_float4(pa0, pa1, pb0, pb1));
-                pa0 = pa1 = 1.f;
-                pb0 = pb1 = 0.f;
-            }
-            cluster_sync();
-            float e0 = carry0, e1 = carry1;
-            h0v = e0;
-            h1v = e1;
-            for (int r = 0; r < CS; ++r) {
-                const float4 v = peer[i & 1][r][l];
-                if (r == rank) {
-                    h0v = e0;
-                    h1v = e1;
-                }
-                e0 = through(v.x, v.z, e0, cuts);
-                e1 = through(v.y, v.w, e1, cuts);
-            }
-            carry0 = e0;
-            carry1 = e1;
-            h0v = through(pa0, pb0, h0v, cuts);
-            h1v = through(pa1, pb1, h1v, cuts);
-        }
-        if (half) {
-            h0v = through(a0, b0, h0v, cuts);
-            h1v = through(a1, b1, h1v, cuts);
-        }
-        if (whole && on1 && pairs && !(m.first | m.last)) {
-            if (out) {
-                T *o = out + (int64_t)p * s.D + c;
+            if (!m.first) {
 #pragma unroll
                 for (int j = 0; j < kL; ++j) {
-                    h0v = fmaf(al[j][0], h0v, u[j][0]);
-                    h1v = fmaf(al[j][1], h1v, u[j][1]);
-                    write2(o, h0v, h1v);
-                    o += s.D;
+                    run.B = fma2(al[j], run.B, u[j]);
+                    run.A = mul2(run.A, al[j]);
                 }
             } else {
+                int n = mine.n;
 #pragma unroll
-                for (int j = 0; j < kL; ++j) {
-                    h0v = fmaf(al[j][0], h0v, u[j][0]);
-                    h1v = fmaf(al[j][1], h1v, u[j][1]);
+                for (int j = 0; j < kL; ++j)
+                    if (m.first >> j & 1) {
+                        n = seq_from(s, n, p + j);
+                        u[j] = fma2(al[j], load_state(h0, n, D, c), u[j]);
+                        run = Run{both(-1.f), u[j]};
+                    } else {
+                        run.B = fma2(al[j], run.B, u[j]);
+                        decay_past_cut(run.A, al[j]);
+                    }
+            }
+        }
+        // the other half's run: the second half's lanes go through the first half's
+        const Run other{other_half(run.A), other_half(run.B)};
+        if (half == 0) agg[i & 1][warp][l] = pack(follow(run, other, cuts));
+        __syncthreads();
+        if (!lost) ask(i + kDepth<T>, slot);
+        float2 h;   // the state that enters the run
+        if (CS == 1) {
+            float2 e = carry;
+            h = e;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (w == warp) h = e;
+                e = through(unpack(agg[i & 1][w][l]), e, cuts);
+            }
+            carry = e;
+        } else {
+            Run front{both(1.f), both(0.f)}, all = front;   // the warps in front, and all
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (w == warp) front = all;
+                all = follow(all, unpack(agg[i & 1][w][l]), cuts);
+            }
+            if (!lost)
+                for (int r = 2 * warp + half; r < CS; r += 2 * kWarps) peers.tell(i, r, rank, l, pack(all));
+            if (!lost) lost = !__all_sync(kFull, peers.wait(i));
+            float2 e = carry;
+            h = e;
+            for (int r = 0; r < CS; ++r) {
+                if (r == rank) h = e;
+                e = through(unpack(told[i & 1][r][l]), e, cuts);
+            }
+            carry = e;
+            h = through(front, h, cuts);
+        }
+        if (half) h = through(other, h, cuts);
+        if (inner) {
+            if (c < D) {
+                if (out) {
+                    char *o = (char *)(out + (int64_t)base * D) + lane_out;
+#pragma unroll
+                    for (int j = 0; j < kL; ++j) {
+                        h = fma2(al[j], h, u[j]);
+                        write2((T *)o, h);
+                        o += D * (int)sizeof(T);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kL; ++j) h = fma2(al[j], h, u[j]);
                 }
             }
-        } else if (on0) {
-            int n = cur.n;
+        } else if (there && c < D) {
+            int n = mine.n;
 #pragma unroll
             for (int j = 0; j < kL; ++j) {
-                const bool cut = m.first >> j & 1;
-                h0v = fmaf(al[j][0], cut ? 0.f : h0v, u[j][0]);
-                h1v = fmaf(al[j][1], cut ? 0.f : h1v, u[j][1]);
-                if (cut) {   // as the sum above has it, whatever alpha is
-                    h0v = u[j][0];
-                    h1v = u[j][1];
-                }
+                h = m.first >> j & 1 ? u[j] : fma2(al[j], h, u[j]);
                 const int t = p + j;
                 if (t < lo || t >= hi) continue;
                 if (out) {
-                    T *o = out + (int64_t)t * s.D + c;
-                    o[0] = from_f32<T>(h0v);
-                    if (on1) o[1] = from_f32<T>(h1v);
+                    T *o = out + (int64_t)t * D + c;
+                    if (pairs) {
+                        write2(o, h);
+                    } else {
+                        o[0] = from_f32<T>(h.x);
+                        if (c + 1 < D) o[1] = from_f32<T>(h.y);
+                    }
                 }
                 if (hT && (m.last >> j & 1)) {
                     n = seq_from(s, n, t);
-                    hT[(int64_t)n * s.D + c] = h0v;
-                    if (on1) hT[(int64_t)n * s.D + c + 1] = h1v;
+                    store_state(hT, n, D, c, h);
                 }
             }
         }
-        // the state behind a tile's last token
-        if (states && half == 1 && warp == kWarps - 1 && p + kL == hi && base + kScanTile == hi) {
-            float *d = states + (int64_t)(base / kScanTile) * s.D + c;
-            if (on0) d[0] = h0v;
-            if (on1) d[1] = h1v;
+        // the state behind 128 tokens
+        if (states && there && half == 1 && warp == kWarps - 1 && hi == base + kTok && hi % kScanTile == 0)
+            store_state(states, hi / kScanTile - 1, D, c, h);
+        if (++slot == kDepth<T>) {
+            slot = 0;
+            ++use;
         }
     }
-    copies_wait<0>();
+    ring.drain(lost);
+    if (__syncthreads_or(lost) && threadIdx.x == 0) set_status(status, GDR_ERR_TIMEOUT);
+    if (CS > 1) cluster_sync();   // nobody leaves while a peer may still write to its memory
 }
 
 template <typename T, int GATE, int SRC>
 cudaError_t launch_fwd_t(const ScanFwd &t, ScanShape s, int sms, int *status, cudaStream_t stream) {
     auto kern = scan_fwd_kernel<T, GATE, SRC>;
-    scan_divide(s, (int64_t)sms * kBlocksPerSm<T>);
-    const bool wide = s.D % wide_elems<T>() == 0 && ((uintptr_t)t.x | (uintptr_t)t.a) % 16 == 0;
+    scan_divide(s, (int64_t)sms * kBlocksPerSm<T>, kTok);
+    FwdMaps maps{};
+    constexpr gdr_dtype_t kType = sizeof(T) == 2 ? GDR_BF16 : GDR_F32;
+    auto plane = [&](CUtensorMap *m, const void *p) {
+        return tc_make_plane_map(m, p, kType, s.D, s.total, kScanChannels, kTok);
+    };
+    const bool boxes = s.total > 0 && plane(&maps.x, t.x) && plane(&maps.a, t.a);
     const bool even = s.D % 2 == 0;
     const bool pair = sizeof(T) == 4 || (even && ((uintptr_t)t.x | (uintptr_t)t.a) % 4 == 0);
-    const int mode = wide ? kWide : pair ? kPair : kSingle;
+    const int mode = boxes ? kTma : pair ? kPair : kSingle;
     const int pairs = even && (uintptr_t)t.out % (2 * sizeof(T)) == 0;
     cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<T>);
     if (err != cudaSuccess) return err;
+    if (s.cluster > 8) cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((int64_t)s.tiles * s.parts * s.cluster));
     cfg.blockDim = dim3(kThreads);
@@ -256,8 +245,8 @@ cudaError_t launch_fwd_t(const ScanFwd &t, ScanShape s, int sms, int *status, cu
     cfg.attrs = &attr;
     cfg.numAttrs = s.cluster > 1 ? 1 : 0;
     ProfScope prof(stream, "scan_fwd_kernel");
-    err = cudaLaunchKernelEx(&cfg, kern, (const T *)t.x, (const T *)t.a, t.h0, (T *)t.out, t.hT, t.states, s, mode, pairs,
-                             status);
+    err = cudaLaunchKernelEx(&cfg, kern, maps, (const T *)t.x, (const T *)t.a, t.h0, (T *)t.out, t.hT, t.states, s, mode,
+                             pairs, scan_wait_ns(), status);
     count_launch();
     return err;
 }
@@ -267,7 +256,8 @@ cudaError_t launch_fwd_t(const ScanFwd &t, ScanShape s, int sms, int *status, cu
 template <typename T, int GATE, int SRC>
 __global__ void __launch_bounds__(256)
 scan_step_kernel(const T *__restrict__ x, const T *__restrict__ a, float *__restrict__ state, T *__restrict__ out,
-                 int64_t units, int T_, int D, float b) {
+                 int64_t units, const ScanShape s) {
+    const int T_ = s.T_per, D = s.D;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= units) return;
     const int64_t n = i / D, at = n * T_ * D + (i - n * D);
@@ -276,8 +266,8 @@ scan_step_kernel(const T *__restrict__ x, const T *__restrict__ a, float *__rest
     for (int t = 0; t < T_; ++t) {
         const int64_t next = at + (int64_t)(t + 1 < T_ ? t + 1 : t) * D;
         const T xn = x[next], an = a[next];
-        const Gate g = gate_of<sizeof(T) == 4, GATE, SRC, false>(to_f32(av), b);
-        h = fmaf(g.alpha, h, g.w * to_f32(xv));
+        const Gate g = gate_of<sizeof(T) == 4, GATE, SRC, false>(both(to_f32(av)), s);
+        h = fmaf(g.alpha.x, h, g.w.x * to_f32(xv));
         out[at + (int64_t)t * D] = from_f32<T>(h);
         xv = xn;
         av = an;
@@ -289,24 +279,19 @@ scan_step_kernel(const T *__restrict__ x, const T *__restrict__ a, float *__rest
 
 cudaError_t launch_scan_fwd(const ScanFwd &t, ScanShape s, gdr_dtype_t dtype, gdr_gate_t gate, gdr_source_t source,
                             int sms, int *status, cudaStream_t stream) {
-    return with_form(gate, source, [&](auto g, auto w) {
-        return dtype == GDR_BF16 ? launch_fwd_t<__nv_bfloat16, g(), w()>(t, s, sms, status, stream)
-                                 : launch_fwd_t<float, g(), w()>(t, s, sms, status, stream);
+    return with_form(s, dtype, gate, source, [&](auto type, auto g, auto w) {
+        return launch_fwd_t<decltype(type), g(), w()>(t, s, sms, status, stream);
     });
 }
 
-cudaError_t launch_scan_step(const void *x, const void *a, float *state, void *out, int N, int T, int D, float b,
-                             gdr_dtype_t dtype, gdr_gate_t gate, gdr_source_t source, cudaStream_t stream) {
-    return with_form(gate, source, [&](auto g, auto w) {
-        const int64_t units = (int64_t)N * D;
-        const unsigned grid = (unsigned)((units + 255) / 256);
+cudaError_t launch_scan_step(const void *x, const void *a, float *state, void *out, ScanShape s, gdr_dtype_t dtype,
+                             gdr_gate_t gate, gdr_source_t source, cudaStream_t stream) {
+    return with_form(s, dtype, gate, source, [&](auto type, auto g, auto w) {
+        using T = decltype(type);
+        const int64_t units = (int64_t)s.N * s.D;
         ProfScope prof(stream, "scan_step_kernel");
-        if (dtype == GDR_BF16)
-            scan_step_kernel<__nv_bfloat16, g(), w()><<<grid, 256, 0, stream>>>(
-                (const __nv_bfloat16 *)x, (const __nv_bfloat16 *)a, state, (__nv_bfloat16 *)out, units, T, D, b);
-        else
-            scan_step_kernel<float, g(), w()><<<grid, 256, 0, stream>>>((const float *)x, (const float *)a, state,
-                                                                        (float *)out, units, T, D, b);
+        scan_step_kernel<T, g(), w()><<<(unsigned)((units + 255) / 256), 256, 0, stream>>>((const T *)x, (const T *)a, state,
+                                                                                         (T *)out, units, s);
         count_launch();
         return cudaGetLastError();
     });

@@ -1037,6 +1037,21 @@ bool tc_make_tile_map(CUtensorMap *map, const void *base, int width, int H, int6
     return make_tile_map(map, base, width, H, rows, box_rows);
 }
 
+bool tc_make_plane_map(CUtensorMap *map, const void *base, gdr_dtype_t dtype, int64_t width, int64_t rows, int box_width,
+                       int box_rows) {
+    auto fn = encode_fn();
+    const size_t es = dtype == GDR_BF16 ? 2 : 4;
+    if (!fn || ((uintptr_t)base & 15) || width * es % 16) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)std::max<int64_t>(rows, 1)};
+    cuuint64_t strides[1] = {(cuuint64_t)width * es};
+    cuuint32_t box[2] = {(cuuint32_t)box_width, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(map, dtype == GDR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+              const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tc_supported(gdr_dtype_t dtype, int dk, int dv, int chunk) {
     static_assert(kC == kTcTile, "tile length");
     return dtype == GDR_BF16 && dk == kD && dv == kD && (chunk == 16 || chunk == 32 || chunk == 64);

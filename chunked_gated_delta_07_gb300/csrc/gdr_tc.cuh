@@ -36,6 +36,11 @@ bool tc_make_map(CUtensorMap *map, const void *base, int H, int64_t rows);
 // The same for [rows][H][width] tensors (width a multiple of 64) and box_rows-row tiles.
 bool tc_make_tile_map(CUtensorMap *map, const void *base, int width, int H, int64_t rows, int box_rows);
 
+// Tensor map of a [rows][width] tensor for tiles of box_rows x box_width elements, rows of a tile
+// behind each other; false where it cannot be (rows and base in 16-byte steps).
+bool tc_make_plane_map(CUtensorMap *map, const void *base, gdr_dtype_t dtype, int64_t width, int64_t rows, int box_width,
+                       int box_rows);
+
 // The per-channel decay forward on the tensor cores (gdr_tc_vec.cu): bf16, d = 128,
 // tiles of 16, bounded gate.  `warm` holds the warm-up of every (segment, head),
 // written by launch_vec_warm on the same plan.
