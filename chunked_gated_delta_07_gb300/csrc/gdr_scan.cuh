@@ -18,6 +18,7 @@
 // chaining looks at the sign (where there can be cuts at all) instead of multiplying.
 #pragma once
 
+#include <atomic>
 #include <cstdlib>
 #include <type_traits>
 
@@ -29,7 +30,7 @@ namespace gdr {
 
 constexpr int kScanTile = 128;      // tokens of a tile; the interval of the states kept for the backward pass
 constexpr int kScanChannels = 32;   // channels of a tile
-constexpr int kScanMaxCluster = 8;
+constexpr int kScanMaxCluster = 16;
 constexpr int kScanMaxD = 1 << 22;  // a tile's offsets are 32-bit
 constexpr int64_t kScanMaxTokens = 0x7fffffff - 2 * kScanTile * kScanMaxCluster;   // positions are 32-bit
 
@@ -146,7 +147,8 @@ __device__ __forceinline__ Gate gate_of(float2 a, const ScanShape &shape) {
         }
         float2 p = shape.poly[kScanPoly - 1];
 #pragma unroll
-        for (int k = kScanPoly - 2; k >= 0; --k) p = fma2(p, s, shape.poly[k]);
+        for (int k = kScanPoly - 2; k >= 0; --k)
+            p = make_float2(fmaf(p.x, s.x, shape.poly[k].x), fmaf(p.y, s.y, shape.poly[k].x));
         left = mul2(s, p);
         o.alpha = fma2(left, minus, one);
     } else if constexpr (GATE == kBounded) {
@@ -381,11 +383,12 @@ template <typename T, int L, int TOK, int NT, int DEPTH> struct Ring {
     __device__ __forceinline__ T *tile(int slot, int tensor) const { return at + (slot * NT + tensor) * kTile; }
 
     // Every thread: asks for the tile from token `row` on, after the whole block is done with what
-    // was in the slot.  One lane of the warp whose turn it is issues the boxes.
-    __device__ __forceinline__ void ask(int slot, bool my_turn, const CUtensorMap *const (&maps)[NT],
-                                        const T *const (&src)[NT], int row, int lo, int hi, int c0, int D) {
+    // was in the slot.  The boxes are issued by a lane of one warp, which costs that warp some 400
+    // cycles; the warps take turns.
+    __device__ __forceinline__ void ask(int slot, int turn, const CUtensorMap *const (&maps)[NT], const T *const (&src)[NT],
+                                        int row, int lo, int hi, int c0, int D) {
         if (mode == kTma) {
-            if (my_turn && (threadIdx.x & 31) == 0) {
+            if (threadIdx.x == 32 * (turn % (TOK / (2 * L)))) {
                 sm100::mbar_arrive_expect_tx(&full[slot], NT * kTile * (unsigned)sizeof(T));
 #pragma unroll
                 for (int i = 0; i < NT; ++i) sm100::tma_load_2d(tile(slot, i), maps[i], c0, row, &full[slot]);
@@ -527,20 +530,87 @@ inline uint64_t scan_wait_ns() {
     return w ? (uint64_t)std::strtoull(w, nullptr, 10) : 2000000000ull;
 }
 
-// Division of the work: `slots` blocks run at a time.  Sequences of one length are chains of
-// their own while there is room for all of them, else several follow each other in a part; then
-// the tiles along a part go to the blocks of a cluster, as many as there is room for.
-inline void scan_divide(ScanShape &s, int64_t slots, int tok = kScanTile) {
+// Division of the work: `slots` blocks run at a time, and clusters of 2^k blocks as many as room[k]
+// says.  Sequences of one length are chains of their own while there is room for all of them, else
+// several follow each other in a part; then the tiles along a part go to the blocks of a cluster, as
+// many as leave all clusters running at once.  More of them, in turns, would wait for each other:
+// 262144 tokens of 2048 channels 820 us with clusters of 8 (one round), 920 with 16 (two); 65536
+// packed tokens of 1000 channels 235 with 8, 179 with 16 (one round both).
+constexpr int kScanSizes = 5;   // 1, 2, 4, 8, 16 blocks
+inline void scan_divide(ScanShape &s, const int (&room)[kScanSizes], int tok) {
     s.tiles = (s.D + kScanChannels - 1) / kScanChannels;
-    const int64_t room = slots / s.tiles > 1 ? slots / s.tiles : 1;
-    s.per_part = s.cu ? s.N : (int)((s.N + room - 1) / room);
+    const int64_t fit = room[0] / s.tiles > 1 ? room[0] / s.tiles : 1;
+    s.per_part = s.cu ? s.N : (int)((s.N + fit - 1) / fit);
     s.parts = (s.N + s.per_part - 1) / s.per_part;
     const int64_t tokens = s.cu ? s.total : (int64_t)s.per_part * s.T_per;
-    const int64_t most = room / s.parts, along = (tokens + tok - 1) / tok;
-    int64_t c = most < along ? most : along;
-    s.cluster = (int)(c > 8 ? 8 : c < 1 ? 1 : c);
-    if (const char *e = std::getenv("GDR_X_CS")) s.cluster = std::atoi(e) < along ? std::atoi(e) : (int)along;
-    if (s.cluster < 1) s.cluster = 1;
+    const int64_t units = (int64_t)s.parts * s.tiles, along = (tokens + tok - 1) / tok;
+    s.cluster = 1;
+    for (int k = 1; k < kScanSizes; ++k)
+        if ((1 << k) < 2 * along && units <= room[k]) s.cluster = 1 << k;
 }
+
+#ifdef __CUDACC__
+// How many blocks, and clusters of 2, 4, 8 and 16 blocks, of a kernel run at a time on the current
+// device; asked for once per kernel and device.
+template <typename K> cudaError_t scan_room(K kern, int threads, int smem, int sms, std::atomic<int> (&known)[16][kScanSizes],
+                                            int (&room)[kScanSizes]) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const bool keep = dev < 16;
+    if (keep && known[dev][0].load(std::memory_order_acquire) > 0) {
+        for (int k = 0; k < kScanSizes; ++k) room[k] = known[dev][k].load(std::memory_order_relaxed);
+        return cudaSuccess;
+    }
+    if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return err;
+    int per_sm = 0;
+    if ((err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem)) != cudaSuccess) return err;
+    room[0] = per_sm * sms;
+    for (int k = 1; k < kScanSizes; ++k) {
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(1u << k);
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cudaLaunchAttribute attr{};
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 1u << k;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if ((err = cudaOccupancyMaxActiveClusters(&room[k], kern, &cfg)) != cudaSuccess) return err;
+    }
+    if (keep)
+        for (int k = kScanSizes - 1; k >= 0; --k) known[dev][k].store(room[k], std::memory_order_release);
+    return cudaSuccess;
+}
+
+// One launch: the attributes, the division, the clusters.
+template <typename K, typename... A>
+cudaError_t scan_launch(K kern, ScanShape &s, int threads, int smem, int tok, int sms,
+                        std::atomic<int> (&known)[16][kScanSizes], const char *name, cudaStream_t stream, A... args) {
+    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+    int room[kScanSizes];
+    if ((err = scan_room(kern, threads, smem, sms, known, room)) != cudaSuccess) return err;
+    scan_divide(s, room, tok);
+    const int64_t blocks = (int64_t)s.tiles * s.parts * s.cluster;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)s.cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = s.cluster > 1 ? 1 : 0;
+    ProfScope prof(stream, name);
+    err = cudaLaunchKernelEx(&cfg, kern, s, args...);
+    count_launch();
+    return err;
+}
+#endif
 
 }  // namespace gdr

@@ -24,26 +24,25 @@ using namespace scan;
 constexpr int kL = 8;
 constexpr int kWarps = kScanTile / (2 * kL);
 constexpr int kThreads = 32 * kWarps;
-template <typename T> constexpr int kBlocksPerSm = 2;
-template <typename T> constexpr int kDepth = sizeof(T) == 2 ? 4 : 2;
-template <typename T> using BwdRing = Ring<T, kL, kScanTile, 3, kDepth<T>>;
-template <typename T> constexpr int kSmem = kDepth<T> * 3 * BwdRing<T>::kTile * (int)sizeof(T) + 128;
+constexpr int kBlocksPerSm = 2;
+constexpr int kDepth = 2;
+template <typename T> using BwdRing = Ring<T, kL, kScanTile, 3, kDepth>;
+template <typename T> constexpr int kSmem = kDepth * 3 * BwdRing<T>::kTile * (int)sizeof(T) + 128;
 
 struct BwdMaps {
     CUtensorMap x, a, dout;
 };
 
 template <typename T, int GATE, int SRC>
-__global__ void __launch_bounds__(kThreads, kBlocksPerSm<T>)
-scan_bwd_kernel(const __grid_constant__ BwdMaps maps, const T *x, const T *a, const T *dout, const float *__restrict__ h0,
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm)
+scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ BwdMaps maps, const T *x, const T *a, const T *dout, const float *__restrict__ h0,
                 const float *__restrict__ dhT, const float *__restrict__ states, T *dx, T *da, float *dh0,
-                const __grid_constant__ ScanShape s, int mode, int pairs, uint64_t limit_ns, int *status) {
+                int mode, int pairs, uint64_t limit_ns, int *status) {
     constexpr bool kFine = sizeof(T) == 4;
     extern __shared__ char smem[];
-    __shared__ __align__(16) float4 agg[2][kWarps][16];    // A, and the gradient's B
-    __shared__ __align__(16) float2 aggh[2][kWarps][16];   // the state's B
+    __shared__ __align__(16) float4 agg[2][2][kWarps][16];   // the states' runs, and the gradients', last warp first
     __shared__ __align__(16) float4 told[2][kScanMaxCluster][16];
-    __shared__ uint64_t bars[2], full[kDepth<T>];
+    __shared__ uint64_t bars[2], full[kDepth];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = lane >> 4, l = lane & 15;
     const int run_at0 = (warp * 2 + half) * kL;   // the lane's run in a tile
     const int CS = s.cluster, rank = blockIdx.x % CS, unit = blockIdx.x / CS;
@@ -61,7 +60,7 @@ scan_bwd_kernel(const __grid_constant__ BwdMaps maps, const T *x, const T *a, co
     const int t0 = p0 / kScanTile, t1 = (p1 + kScanTile - 1) / kScanTile, steps = (t1 - t0 + CS - 1) / CS;
     const bool many = last - first > 1;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kDepth<T>; ++i) sm100::mbar_init(&full[i], 1);
+        for (int i = 0; i < kDepth; ++i) sm100::mbar_init(&full[i], 1);
         sm100::mbar_init(&bars[0], 1);
         sm100::mbar_init(&bars[1], 1);
         sm100::fence_mbar_init();
@@ -76,10 +75,10 @@ scan_bwd_kernel(const __grid_constant__ BwdMaps maps, const T *x, const T *a, co
     // step i of this block: tile t1 - 1 - (i CS + rank), none below t0
     auto ask = [&](int i, int slot) {
         const int tile = t1 - 1 - (i * CS + rank);
-        if (tile >= t0) ring.ask(slot, warp == i % kWarps, map, src, tile * kScanTile, p0, p1, c0, D);
+        if (tile >= t0) ring.ask(slot, i, map, src, tile * kScanTile, p0, p1, c0, D);
         ring.close();
     };
-    for (int i = 0; i < kDepth<T>; ++i) ask(i, i);
+    for (int i = 0; i < kDepth; ++i) ask(i, i);
     Peers peers{told, bars, limit_ns};
     Cursor cur{first, 0, -1};
     float2 carry = both(0.f);
@@ -165,50 +164,51 @@ scan_bwd_kernel(const __grid_constant__ BwdMaps maps, const T *x, const T *a, co
                 pass(std::false_type{});
         }
         const Run oh{other_half(A), other_half(B)}, og{oh.A, other_half(R)};
-        if (half == 0) {   // states: this half's run, then the other's; gradients: the other's, then this one's
-            const Run f = follow(Run{A, B}, oh, cuts), g = follow(og, Run{A, R}, cuts);
-            agg[i & 1][warp][l] = make_float4(f.A.x, f.A.y, g.B.x, g.B.y);
-            aggh[i & 1][warp][l] = f.B;
+        // states: the first half's run, then the second's; gradients: the other way round, from the
+        // last warp on.  The first half's lanes chain the states, the second half's the gradients.
+        {
+            const Run f = half ? follow(Run{A, R}, og, cuts) : follow(Run{A, B}, oh, cuts);
+            agg[i & 1][half][half ? kWarps - 1 - warp : warp][l] = pack(f);
         }
         __syncthreads();
-        if (!lost && inner) ask(i + kDepth<T>, slot);
-        // the state that enters the run
-        for (int v = 0; v < warp; ++v) {
-            const float4 r = agg[i & 1][v][l];
-            h = through(Run{make_float2(r.x, r.y), aggh[i & 1][v][l]}, h, cuts);
-        }
-        if (half) h = through(oh, h, cuts);
-        // the gradient that enters it
+        if (!lost && inner) ask(i + kDepth, slot);
+        const int my_place = half ? kWarps - 1 - warp : warp;
         float2 r;
         if (CS == 1) {
-            float2 e = carry;
-            r = e;
+            float2 e = half ? carry : h, at = e;
 #pragma unroll
-            for (int v = kWarps - 1; v >= 0; --v) {
-                if (v == warp) r = e;
-                e = through(unpack(agg[i & 1][v][l]), e, cuts);
+            for (int v = 0; v < kWarps; ++v) {
+                if (v == my_place) at = e;
+                e = through(unpack(agg[i & 1][half][v][l]), e, cuts);
             }
-            carry = e;
+            carry = e;   // (of the second half's lanes)
+            const float2 theirs = other_half(at);
+            h = half ? theirs : at;
+            r = half ? at : theirs;
         } else {
-            Run behind{both(1.f), both(0.f)}, all = behind;   // the warps behind, and all
+            Run front{both(1.f), both(0.f)}, all = front;   // what comes before the warp, and all
 #pragma unroll
-            for (int v = kWarps - 1; v >= 0; --v) {
-                if (v == warp) behind = all;
-                all = follow(all, unpack(agg[i & 1][v][l]), cuts);
+            for (int v = 0; v < kWarps; ++v) {
+                if (v == my_place) front = all;
+                all = follow(all, unpack(agg[i & 1][half][v][l]), cuts);
             }
-            if (!lost)
-                for (int k = 2 * warp + half; k < CS; k += 2 * kWarps) peers.tell(i, k, rank, l, pack(all));
+            if (!lost && half)
+                for (int k = warp; k < CS; k += kWarps) peers.tell(i, k, rank, l, pack(all));
             if (!lost) lost = !__all_sync(kFull, peers.wait(i));
-            float2 e = carry;
-            r = e;
+            float2 e = carry, in = e;
             for (int k = 0; k < CS; ++k) {
-                if (k == rank) r = e;
+                if (k == rank) in = e;
                 e = through(unpack(told[i & 1][k][l]), e, cuts);
             }
             carry = e;
-            r = through(behind, r, cuts);
+            const float2 at = through(front, half ? in : h, cuts), theirs = other_half(at);
+            h = half ? theirs : at;
+            r = half ? at : theirs;
         }
-        if (!half) r = through(og, r, cuts);
+        if (half)
+            h = through(oh, h, cuts);
+        else
+            r = through(og, r, cuts);
         if (inner) {
             if (c < D) {
                 char *ox = (char *)(dx + (int64_t)base * D) + lane_out, *oa = (char *)(da + (int64_t)base * D) + lane_out;
@@ -252,9 +252,9 @@ scan_bwd_kernel(const __grid_constant__ BwdMaps maps, const T *x, const T *a, co
                 }
             }
             __syncthreads();   // the gates have been read again
-            if (!lost) ask(i + kDepth<T>, slot);
+            if (!lost) ask(i + kDepth, slot);
         }
-        if (++slot == kDepth<T>) {
+        if (++slot == kDepth) {
             slot = 0;
             ++use;
         }
@@ -266,8 +266,6 @@ scan_bwd_kernel(const __grid_constant__ BwdMaps maps, const T *x, const T *a, co
 
 template <typename T, int GATE, int SRC>
 cudaError_t launch_bwd_t(const ScanBwd &t, ScanShape s, int sms, int *status, cudaStream_t stream) {
-    auto kern = scan_bwd_kernel<T, GATE, SRC>;
-    scan_divide(s, (int64_t)sms * kBlocksPerSm<T>);
     BwdMaps maps{};
     constexpr gdr_dtype_t kType = sizeof(T) == 2 ? GDR_BF16 : GDR_F32;
     auto plane = [&](CUtensorMap *m, const void *p) {
@@ -278,24 +276,10 @@ cudaError_t launch_bwd_t(const ScanBwd &t, ScanShape s, int sms, int *status, cu
     const bool even = s.D % 2 == 0;
     const int mode = boxes ? kTma : sizeof(T) == 4 || (even && ins % 4 == 0) ? kPair : kSingle;
     const int pairs = even && outs % (2 * sizeof(T)) == 0;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<T>);
-    if (err != cudaSuccess) return err;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((int64_t)s.tiles * s.parts * s.cluster));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem<T>;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)s.cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = s.cluster > 1 ? 1 : 0;
-    ProfScope prof(stream, "scan_bwd_kernel");
-    err = cudaLaunchKernelEx(&cfg, kern, maps, (const T *)t.x, (const T *)t.a, (const T *)t.dout, t.h0, t.dhT, t.states,
-                             (T *)t.dx, (T *)t.da, t.dh0, s, mode, pairs, scan_wait_ns(), status);
-    count_launch();
-    return err;
+    static std::atomic<int> known[16][kScanSizes];
+    return scan_launch(scan_bwd_kernel<T, GATE, SRC>, s, kThreads, kSmem<T>, kScanTile, sms, known, "scan_bwd_kernel", stream,
+                       maps, (const T *)t.x, (const T *)t.a, (const T *)t.dout, t.h0, t.dhT, t.states, (T *)t.dx, (T *)t.da,
+                       t.dh0, mode, pairs, scan_wait_ns(), status);
 }
 
 }  // namespace

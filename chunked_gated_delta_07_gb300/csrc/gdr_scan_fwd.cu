@@ -20,9 +20,9 @@ constexpr int kWarps = 4;
 constexpr int kTok = 2 * kL * kWarps;            // of a block's tile; divides 128, or 128 it
 constexpr int kThreads = 32 * kWarps;
 template <typename T> constexpr int kBlocksPerSm = sizeof(T) == 2 ? 4 : 3;
-template <typename T> constexpr int kDepth = sizeof(T) == 2 ? 3 : 2;   // tiles in shared memory
-template <typename T> using FwdRing = Ring<T, kL, kTok, 2, kDepth<T>>;
-template <typename T> constexpr int kSmem = kDepth<T> * 2 * FwdRing<T>::kTile * (int)sizeof(T) + 128;
+constexpr int kDepth = 2;   // tiles in shared memory
+template <typename T> using FwdRing = Ring<T, kL, kTok, 2, kDepth>;
+template <typename T> constexpr int kSmem = kDepth * 2 * FwdRing<T>::kTile * (int)sizeof(T) + 128;
 
 struct FwdMaps {
     CUtensorMap x, a;
@@ -30,13 +30,13 @@ struct FwdMaps {
 
 template <typename T, int GATE, int SRC>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm<T>)
-scan_fwd_kernel(const __grid_constant__ FwdMaps maps, const T *x, const T *a, const float *h0, T *out, float *hT,
-                float *states, const __grid_constant__ ScanShape s, int mode, int pairs, uint64_t limit_ns, int *status) {
+scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ FwdMaps maps, const T *x, const T *a, const float *h0, T *out, float *hT,
+                float *states, int mode, int pairs, uint64_t limit_ns, int *status) {
     constexpr bool kFine = sizeof(T) == 4;
     extern __shared__ char smem[];
     __shared__ __align__(16) float4 agg[2][kWarps][16];
     __shared__ __align__(16) float4 told[2][kScanMaxCluster][16];
-    __shared__ uint64_t bars[2], full[kDepth<T>];
+    __shared__ uint64_t bars[2], full[kDepth];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, half = lane >> 4, l = lane & 15;
     const int run_at0 = (warp * 2 + half) * kL;   // the lane's run in a tile
     const int CS = s.cluster, rank = blockIdx.x % CS, unit = blockIdx.x / CS;
@@ -54,7 +54,7 @@ scan_fwd_kernel(const __grid_constant__ FwdMaps maps, const T *x, const T *a, co
     const int t0 = p0 / kTok, t1 = (p1 + kTok - 1) / kTok, steps = (t1 - t0 + CS - 1) / CS;
     const bool many = last - first > 1;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kDepth<T>; ++i) sm100::mbar_init(&full[i], 1);
+        for (int i = 0; i < kDepth; ++i) sm100::mbar_init(&full[i], 1);
         sm100::mbar_init(&bars[0], 1);
         sm100::mbar_init(&bars[1], 1);
         sm100::fence_mbar_init();
@@ -68,10 +68,10 @@ scan_fwd_kernel(const __grid_constant__ FwdMaps maps, const T *x, const T *a, co
     const T *const src[2] = {x, a};
     auto ask = [&](int i, int slot) {   // the tile of step i
         const int tile = t0 + i * CS + rank;
-        if (tile < t1) ring.ask(slot, warp == i % kWarps, map, src, tile * kTok, p0, p1, c0, D);
+        if (tile < t1) ring.ask(slot, i, map, src, tile * kTok, p0, p1, c0, D);
         ring.close();
     };
-    for (int i = 0; i < kDepth<T>; ++i) ask(i, i);
+    for (int i = 0; i < kDepth; ++i) ask(i, i);
     Peers peers{told, bars, limit_ns};
     Cursor cur{first, 0, -1};
     float2 carry = both(0.f);
@@ -135,7 +135,7 @@ scan_fwd_kernel(const __grid_constant__ FwdMaps maps, const T *x, const T *a, co
         const Run other{other_half(run.A), other_half(run.B)};
         if (half == 0) agg[i & 1][warp][l] = pack(follow(run, other, cuts));
         __syncthreads();
-        if (!lost) ask(i + kDepth<T>, slot);
+        if (!lost) ask(i + kDepth, slot);
         float2 h;   // the state that enters the run
         if (CS == 1) {
             float2 e = carry;
@@ -204,9 +204,9 @@ scan_fwd_kernel(const __grid_constant__ FwdMaps maps, const T *x, const T *a, co
             }
         }
         // the state behind 128 tokens
-        if (states && there && half == 1 && warp == kWarps - 1 && hi == base + kTok && hi % kScanTile == 0)
+        if (states && there && hi == p + kL && hi % kScanTile == 0)
             store_state(states, hi / kScanTile - 1, D, c, h);
-        if (++slot == kDepth<T>) {
+        if (++slot == kDepth) {
             slot = 0;
             ++use;
         }
@@ -218,8 +218,6 @@ scan_fwd_kernel(const __grid_constant__ FwdMaps maps, const T *x, const T *a, co
 
 template <typename T, int GATE, int SRC>
 cudaError_t launch_fwd_t(const ScanFwd &t, ScanShape s, int sms, int *status, cudaStream_t stream) {
-    auto kern = scan_fwd_kernel<T, GATE, SRC>;
-    scan_divide(s, (int64_t)sms * kBlocksPerSm<T>, kTok);
     FwdMaps maps{};
     constexpr gdr_dtype_t kType = sizeof(T) == 2 ? GDR_BF16 : GDR_F32;
     auto plane = [&](CUtensorMap *m, const void *p) {
@@ -230,25 +228,9 @@ cudaError_t launch_fwd_t(const ScanFwd &t, ScanShape s, int sms, int *status, cu
     const bool pair = sizeof(T) == 4 || (even && ((uintptr_t)t.x | (uintptr_t)t.a) % 4 == 0);
     const int mode = boxes ? kTma : pair ? kPair : kSingle;
     const int pairs = even && (uintptr_t)t.out % (2 * sizeof(T)) == 0;
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<T>);
-    if (err != cudaSuccess) return err;
-    if (s.cluster > 8) cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((int64_t)s.tiles * s.parts * s.cluster));
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem<T>;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = (unsigned)s.cluster;
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = s.cluster > 1 ? 1 : 0;
-    ProfScope prof(stream, "scan_fwd_kernel");
-    err = cudaLaunchKernelEx(&cfg, kern, maps, (const T *)t.x, (const T *)t.a, t.h0, (T *)t.out, t.hT, t.states, s, mode,
-                             pairs, scan_wait_ns(), status);
-    count_launch();
-    return err;
+    static std::atomic<int> known[16][kScanSizes];
+    return scan_launch(scan_fwd_kernel<T, GATE, SRC>, s, kThreads, kSmem<T>, kTok, sms, known, "scan_fwd_kernel", stream, maps,
+                       (const T *)t.x, (const T *)t.a, t.h0, (T *)t.out, t.hT, t.states, mode, pairs, scan_wait_ns(), status);
 }
 
 // One (sequence, channel) to a thread, the next token's inputs on their way while a token is
