@@ -88,7 +88,7 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
     for (int i = 0, slot = 0, use = 0; i < steps; ++i) {
         if (CS > 1 && threadIdx.x == 0 && !lost) peers.expect(i, CS);
         const int tile_no = t1 - 1 - (i * CS + rank);
-        const bool there = tile_no >= t0, cuts = many || i == steps - 1;   // a part's first token is in the last step
+        const bool there = tile_no >= t0;
         const int base = there ? tile_no * kScanTile : p0 - kScanTile;
         // a tile that one sequence fills, and goes beyond on both sides
         bool inner = false;
@@ -100,6 +100,7 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
             inner = cur.from < base && cur.to > base + kScanTile && mode == kTma && pairs;
             if (!lost) lost = !__all_sync(kFull, ring.wait(slot, use, limit_ns));
         }
+        const bool cuts = CS == 1 ? there && !inner : many || i == steps - 1;   // a part's first token is in the last step
         T *tx = run_at(ring.tile(slot, 0), run_at0, l), *ta = run_at(ring.tile(slot, 1), run_at0, l);
         T *td = run_at(ring.tile(slot, 2), run_at0, l);
         const int p = base + run_at0, lo = max(p, p0), hi = min(p + kL, p1);
@@ -163,52 +164,58 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
             else
                 pass(std::false_type{});
         }
-        const Run oh{other_half(A), other_half(B)}, og{oh.A, other_half(R)};
-        // states: the first half's run, then the second's; gradients: the other way round, from the
-        // last warp on.  The first half's lanes chain the states, the second half's the gradients.
-        {
-            const Run f = half ? follow(Run{A, R}, og, cuts) : follow(Run{A, B}, oh, cuts);
-            agg[i & 1][half][half ? kWarps - 1 - warp : warp][l] = pack(f);
-        }
-        __syncthreads();
-        if (!lost && inner) ask(i + kDepth, slot);
-        const int my_place = half ? kWarps - 1 - warp : warp;
         float2 r;
-        if (CS == 1) {
-            float2 e = half ? carry : h, at = e;
-#pragma unroll
-            for (int v = 0; v < kWarps; ++v) {
-                if (v == my_place) at = e;
-                e = through(unpack(agg[i & 1][half][v][l]), e, cuts);
+        auto chain = [&](auto cuts) {
+            const Run oh{other_half(A), other_half(B)}, og{oh.A, other_half(R)};
+            // states: the first half's run, then the second's; gradients: the other way round, from the
+            // last warp on.  The first half's lanes chain the states, the second half's the gradients.
+            {
+                const Run f = half ? follow(Run{A, R}, og, cuts) : follow(Run{A, B}, oh, cuts);
+                agg[i & 1][half][half ? kWarps - 1 - warp : warp][l] = pack(f);
             }
-            carry = e;   // (of the second half's lanes)
-            const float2 theirs = other_half(at);
-            h = half ? theirs : at;
-            r = half ? at : theirs;
-        } else {
-            Run front{both(1.f), both(0.f)}, all = front;   // what comes before the warp, and all
-#pragma unroll
-            for (int v = 0; v < kWarps; ++v) {
-                if (v == my_place) front = all;
-                all = follow(all, unpack(agg[i & 1][half][v][l]), cuts);
+            __syncthreads();
+            if (!lost && inner) ask(i + kDepth, slot);
+            const int my_place = half ? kWarps - 1 - warp : warp;
+            if (CS == 1) {
+                float2 e = half ? carry : h, at = e;
+    #pragma unroll
+                for (int v = 0; v < kWarps; ++v) {
+                    if (v == my_place) at = e;
+                    e = through(unpack(agg[i & 1][half][v][l]), e, cuts);
+                }
+                carry = e;   // (of the second half's lanes)
+                const float2 theirs = other_half(at);
+                h = half ? theirs : at;
+                r = half ? at : theirs;
+            } else {
+                Run front{both(1.f), both(0.f)}, all = front;   // what comes before the warp, and all
+    #pragma unroll
+                for (int v = 0; v < kWarps; ++v) {
+                    if (v == my_place) front = all;
+                    all = follow(all, unpack(agg[i & 1][half][v][l]), cuts);
+                }
+                if (!lost && half)
+                    for (int k = warp; k < CS; k += kWarps) peers.tell(i, k, rank, l, pack(all));
+                if (!lost) lost = !__all_sync(kFull, peers.wait(i));
+                float2 e = carry, in = e;
+                for (int k = 0; k < CS; ++k) {
+                    if (k == rank) in = e;
+                    e = through(unpack(told[i & 1][k][l]), e, cuts);
+                }
+                carry = e;
+                const float2 at = through(front, half ? in : h, cuts), theirs = other_half(at);
+                h = half ? theirs : at;
+                r = half ? at : theirs;
             }
-            if (!lost && half)
-                for (int k = warp; k < CS; k += kWarps) peers.tell(i, k, rank, l, pack(all));
-            if (!lost) lost = !__all_sync(kFull, peers.wait(i));
-            float2 e = carry, in = e;
-            for (int k = 0; k < CS; ++k) {
-                if (k == rank) in = e;
-                e = through(unpack(told[i & 1][k][l]), e, cuts);
-            }
-            carry = e;
-            const float2 at = through(front, half ? in : h, cuts), theirs = other_half(at);
-            h = half ? theirs : at;
-            r = half ? at : theirs;
-        }
-        if (half)
-            h = through(oh, h, cuts);
+            if (half)
+                h = through(oh, h, cuts);
+            else
+                r = through(og, r, cuts);
+        };
+        if (cuts)
+            chain(std::true_type{});
         else
-            r = through(og, r, cuts);
+            chain(std::false_type{});
         if (inner) {
             if (c < D) {
                 char *ox = (char *)(dx + (int64_t)base * D) + lane_out, *oa = (char *)(da + (int64_t)base * D) + lane_out;

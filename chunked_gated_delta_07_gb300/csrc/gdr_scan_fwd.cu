@@ -81,7 +81,7 @@ scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Fwd
     for (int i = 0, slot = 0, use = 0; i < steps; ++i) {
         if (CS > 1 && threadIdx.x == 0 && !lost) peers.expect(i, CS);
         const int base = (t0 + i * CS + rank) * kTok;   // may lie behind the part
-        const bool there = base < p1, cuts = many || i == 0;
+        const bool there = base < p1;
         // a tile that one sequence fills, and goes beyond on both sides
         bool inner = false;
         if (there) {
@@ -89,6 +89,7 @@ scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Fwd
             inner = cur.from < base && cur.to > base + kTok && mode == kTma && pairs;
             if (!lost) lost = !__all_sync(kFull, ring.wait(slot, use, limit_ns));
         }
+        const bool cuts = CS == 1 ? there && !inner : many || i == 0;
         T *tx = run_at(ring.tile(slot, 0), run_at0, l), *ta = run_at(ring.tile(slot, 1), run_at0, l);
         const int p = min(base, p1) + run_at0, lo = max(p, p0), hi = min(p + kL, p1);
         float2 al[kL], u[kL];
@@ -131,41 +132,47 @@ scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Fwd
                     }
             }
         }
-        // the other half's run: the second half's lanes go through the first half's
-        const Run other{other_half(run.A), other_half(run.B)};
-        if (half == 0) agg[i & 1][warp][l] = pack(follow(run, other, cuts));
-        __syncthreads();
-        if (!lost) ask(i + kDepth, slot);
         float2 h;   // the state that enters the run
-        if (CS == 1) {
-            float2 e = carry;
-            h = e;
+        auto chain = [&](auto cuts) {
+            // the other half's run: the second half's lanes go through the first half's
+            const Run other{other_half(run.A), other_half(run.B)};
+            if (half == 0) agg[i & 1][warp][l] = pack(follow(run, other, cuts));
+            __syncthreads();
+            if (!lost) ask(i + kDepth, slot);
+            if (CS == 1) {
+                float2 e = carry;
+                h = e;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (w == warp) h = e;
-                e = through(unpack(agg[i & 1][w][l]), e, cuts);
-            }
-            carry = e;
-        } else {
-            Run front{both(1.f), both(0.f)}, all = front;   // the warps in front, and all
+                for (int w = 0; w < kWarps; ++w) {
+                    if (w == warp) h = e;
+                    e = through(unpack(agg[i & 1][w][l]), e, cuts);
+                }
+                carry = e;
+            } else {
+                Run front{both(1.f), both(0.f)}, all = front;   // the warps in front, and all
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                if (w == warp) front = all;
-                all = follow(all, unpack(agg[i & 1][w][l]), cuts);
+                for (int w = 0; w < kWarps; ++w) {
+                    if (w == warp) front = all;
+                    all = follow(all, unpack(agg[i & 1][w][l]), cuts);
+                }
+                if (!lost)
+                    for (int r = 2 * warp + half; r < CS; r += 2 * kWarps) peers.tell(i, r, rank, l, pack(all));
+                if (!lost) lost = !__all_sync(kFull, peers.wait(i));
+                float2 e = carry;
+                h = e;
+                for (int r = 0; r < CS; ++r) {
+                    if (r == rank) h = e;
+                    e = through(unpack(told[i & 1][r][l]), e, cuts);
+                }
+                carry = e;
+                h = through(front, h, cuts);
             }
-            if (!lost)
-                for (int r = 2 * warp + half; r < CS; r += 2 * kWarps) peers.tell(i, r, rank, l, pack(all));
-            if (!lost) lost = !__all_sync(kFull, peers.wait(i));
-            float2 e = carry;
-            h = e;
-            for (int r = 0; r < CS; ++r) {
-                if (r == rank) h = e;
-                e = through(unpack(told[i & 1][r][l]), e, cuts);
-            }
-            carry = e;
-            h = through(front, h, cuts);
-        }
-        if (half) h = through(other, h, cuts);
+            if (half) h = through(other, h, cuts);
+        };
+        if (cuts)
+            chain(std::true_type{});
+        else
+            chain(std::false_type{});
         if (inner) {
             if (c < D) {
                 if (out) {
