@@ -5,6 +5,7 @@
 #pragma once
 
 #include "gdr_norm.cuh"
+#include "gdr_pairs.cuh"
 
 namespace gdr {
 
@@ -39,6 +40,9 @@ template <bool FINE> __device__ __forceinline__ float sigmoid_of(float z) {
     if constexpr (FINE) return __frcp_rn(1.f + expf(-z));
     return __fdividef(1.f, 1.f + __expf(-z));
 }
+template <bool FINE> __device__ __forceinline__ float2 sigmoid_of(float2 z) {
+    return make_float2(sigmoid_of<FINE>(z.x), sigmoid_of<FINE>(z.y));
+}
 
 template <typename T> __device__ __forceinline__ float rounded(float v) { return to_f32(from_f32<T>(v)); }
 
@@ -60,6 +64,28 @@ struct Place {
         row = m * s.G + g;
     }
 };
+
+// The weight (1 without) and the bias (0 without) of a thread's columns.
+template <typename P, int NV, int VEC, int TPR, typename V, int KP>
+__device__ __forceinline__ void load_affine(const float *w, const float *b, const Place &pl, const NormShape &s,
+                                            V (&wv)[NV][KP], V (&bv)[NV][KP]) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+        float we[VEC], be[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int c = (v * TPR + pl.lane) * VEC + i;
+            const bool in = pl.mine && c < s.D;
+            we[i] = in && w ? w[(int64_t)pl.g * s.D + c] : 1.f;
+            be[i] = in && b ? b[(int64_t)pl.g * s.D + c] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < KP; ++i) {
+            wv[v][i] = P::at(we, i);
+            bv[v][i] = P::at(be, i);
+        }
+    }
+}
 
 }  // namespace norm
 #endif

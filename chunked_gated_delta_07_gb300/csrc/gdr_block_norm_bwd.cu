@@ -14,18 +14,27 @@ namespace {
 
 using namespace norm;
 
+// Threads of a block, and of an SM.
+constexpr int kLeast = 256, kPerSm = 768;
+template <int TPR> constexpr int block_threads() { return TPR > kLeast ? TPR : kLeast; }
+template <int TPR> constexpr int block_per_sm() { return block_threads<TPR>() > kPerSm ? block_threads<TPR>() : kPerSm; }
+template <int TPR, int NV, int TENSORS> constexpr int block_depth() {
+    constexpr int d = ring_depth<NV, TENSORS, block_per_sm<TPR>()>();
+    return d > 0 ? d : 1;
+}
+
 // GATE: dy, v = x, z [b] -> dx, dz; else dy, v = r [, dr] -> dx (may be null), dres.
 template <typename T, int TPR, int NV, int VEC, bool GATE, bool THREE>
-__global__ void __launch_bounds__(bwd_threads<TPR>(), VEC > 1 ? kThreadsPerSm / bwd_threads<TPR>() : 1)
+__global__ void __launch_bounds__(block_threads<TPR>(), VEC > 1 ? block_per_sm<TPR>() / block_threads<TPR>() : 1)
 block_norm_bwd_kernel(const T *dy, const T *val, const T *third, const float *__restrict__ mean,
                       const float *__restrict__ rstd, const float *__restrict__ w, const float *__restrict__ b, T *dx,
                       T *dother, float *__restrict__ part, NormShape s, float scale, int rms, int act) {
-    constexpr int kThreads = bwd_threads<TPR>(), kTensors = 2 + THREE;
+    constexpr int kThreads = block_threads<TPR>(), kTensors = 2 + THREE;
     __shared__ float red[2][2][32];
     let_next_start();
     int turn = 0;
     Place p(TPR, s);
-    constexpr int kDepth = VEC > 1 ? ring_depth<NV, kTensors>() : 2;
+    constexpr int kDepth = VEC > 1 ? block_depth<TPR, NV, kTensors>() : 2;
     extern __shared__ uint4 ring[];
     using Stream = RowStream<T, kThreads, TPR, NV, VEC>;
     auto open = [&](const T *t, int k) {
@@ -52,18 +61,16 @@ block_norm_bwd_kernel(const T *dy, const T *val, const T *third, const float *__
     };
     float mu, rs;
     stats(p.m, p.row, mu, rs);
-    float wv[NV][VEC], bv[NV][VEC], aw[NV][VEC], ab[NV][VEC];
+    using P = Pairs<VEC>;
+    using V = typename P::type;
+    constexpr int kP = P::count;
+    V wv[NV][kP], bv[NV][kP], aw[NV][kP], ab[NV][kP];
+    load_affine<P, NV, VEC, TPR>(w, GATE ? b : nullptr, p, s, wv, bv);
 #pragma unroll
     for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int c = (v * TPR + p.lane) * VEC + i;
-            const bool in = p.mine && c < s.D;
-            wv[v][i] = in && w ? w[(int64_t)p.g * s.D + c] : 1.f;
-            bv[v][i] = GATE && in && b ? b[(int64_t)p.g * s.D + c] : 0.f;
-            aw[v][i] = 0.f;
-            ab[v][i] = 0.f;
-        }
+        for (int i = 0; i < kP; ++i) aw[v][i] = ab[v][i] = P::of(0.f);
+    const V scale2 = P::of(scale);
     int slot = 0;
     for (int64_t m0 = p.m - p.ri; m0 < s.sets; m0 += p.step, p.m += p.step, p.row += p.row_step) {
         const bool on = p.mine && p.m < s.sets;
@@ -76,56 +83,62 @@ block_norm_bwd_kernel(const T *dy, const T *val, const T *third, const float *__
         ds.read(slot, rd);
         if constexpr (THREE) ts.read(slot, rt);
         slot = slot == kDepth - 1 ? 0 : slot + 1;
-        float xv[NV][VEC], dv[NV][VEC], sum[2] = {0.f, 0.f};   // of n, of n vh
+        // dy is 0 where there is no row or column, so that nothing there counts
+        V xv[NV][kP], dv[NV][kP], sum0 = P::of(0.f), sum1 = P::of(0.f);   // of n, of n vh
+        const V rs2 = P::of(rs), off = P::of(-mu * rs);
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + p.lane) * VEC;
             const bool in = on && c < s.D;
-            widen<T, VEC>(rv[v], xv[v]);
-            widen<T, VEC>(rd[v], dv[v]);
+            float xe[VEC], de[VEC], ze[VEC], oz[VEC];
+            widen<T, VEC>(rv[v], xe);
+            widen<T, VEC>(rd[v], de);
+            if constexpr (GATE) widen<T, VEC>(rt[v], ze);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) xv[v][i] = in ? (xv[v][i] - mu) * rs : 0.f;
-            if constexpr (GATE) {
-                float zv[VEC], oz[VEC];
-                widen<T, VEC>(rt[v], zv);
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    const float g = sigmoid_of<sizeof(T) == 4>(zv[i]);
-                    const float d = scale * dv[v][i], n = fmaf(xv[v][i], wv[v][i], bv[v][i]);
-                    const float slope = act == GDR_ACT_SILU ? g * fmaf(zv[i], 1.f - g, 1.f) : g * (1.f - g);
-                    oz[i] = d * n * slope;
-                    dv[v][i] = d * (act == GDR_ACT_SILU ? zv[i] * g : g);
+            for (int i = 0; i < kP; ++i) {
+                const V xh = fma2(P::at(xe, i), rs2, off);
+                V d = P::at(de, i);
+                if constexpr (GATE) {
+                    const V z = P::at(ze, i), g = sigmoid_of<sizeof(T) == 4>(z), n = fma2(xh, wv[v][i], bv[v][i]);
+                    // act' = g (1 + z (1 - g)) (silu) or g (1 - g); 1 - g is 0 where g is 1, however large z is
+                    const V left = fma2(g, P::of(-1.f), P::of(1.f));
+                    const V a = act == GDR_ACT_SILU ? mul2(z, g) : g;
+                    const V slope = mul2(g, act == GDR_ACT_SILU ? fma2(z, left, P::of(1.f)) : left);
+                    d = mul2(scale2, d);
+                    P::put(oz, i, mul2(mul2(d, n), slope));
+                    d = mul2(d, a);
                 }
+                aw[v][i] = fma2(d, xh, aw[v][i]);
+                ab[v][i] = add2(ab[v][i], d);
+                d = mul2(d, wv[v][i]);
+                sum0 = add2(sum0, d);
+                sum1 = fma2(d, xh, sum1);
+                xv[v][i] = xh;
+                dv[v][i] = d;
+            }
+            if constexpr (GATE)
                 if (in) store_n<T, VEC>(dother + p.row * s.D + c, oz);
-            }
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) {
-                aw[v][i] = fmaf(dv[v][i], xv[v][i], aw[v][i]);
-                ab[v][i] += dv[v][i];
-                dv[v][i] *= wv[v][i];
-                sum[0] += dv[v][i];
-                sum[1] = fmaf(dv[v][i], xv[v][i], sum[1]);
-            }
         }
+        float sum[2] = {P::sum(sum0), P::sum(sum1)};
         row_sum<TPR, 2>(sum, red, turn);
-        const float c1 = rms ? 0.f : sum[0] * s.inv_d, c2 = sum[1] * s.inv_d;
+        // rs (dv - c1 - xh c2)
+        const V k1 = P::of(rms ? 0.f : -rs * sum[0] * s.inv_d), k2 = P::of(-rs * sum[1] * s.inv_d);
         if (on) {
 #pragma unroll
             for (int v = 0; v < NV; ++v) {
                 const int c = (v * TPR + p.lane) * VEC;
                 if (c >= s.D) continue;
                 float o[VEC];
-#pragma unroll
-                for (int i = 0; i < VEC; ++i) o[i] = rs * (dv[v][i] - c1 - xv[v][i] * c2);
                 if constexpr (GATE) {
+#pragma unroll
+                    for (int i = 0; i < kP; ++i) P::put(o, i, fma2(dv[v][i], rs2, fma2(xv[v][i], k2, k1)));
                     store_n<T, VEC>(dx + p.row * s.D + c, o);
                 } else {
-                    if constexpr (THREE) {
-                        float tv[VEC];
-                        widen<T, VEC>(rt[v], tv);
+                    float te[VEC];
+                    if constexpr (THREE) widen<T, VEC>(rt[v], te);
 #pragma unroll
-                        for (int i = 0; i < VEC; ++i) o[i] += tv[i];
-                    }
+                    for (int i = 0; i < kP; ++i)
+                        P::put(o, i, fma2(dv[v][i], rs2, fma2(xv[v][i], k2, THREE ? add2(k1, P::at(te, i)) : k1)));
                     store_n<T, VEC>(dother + p.row * s.D + c, o);
                     if (dx) {
 #pragma unroll
@@ -142,7 +155,15 @@ block_norm_bwd_kernel(const T *dy, const T *val, const T *third, const float *__
     // last row fill it with zeros, and its memory is taken for the groups' sums below
     copies_wait<0>();
     if (!part) return;
-    block_partials<kThreads, TPR, NV, VEC>(aw, ab, part, (float *)ring, p.gi, p.ri, p.lane, p.g, p.mine, s);
+    float sw[NV][VEC], sb[NV][VEC];
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int i = 0; i < kP; ++i) {
+            P::put(sw[v], i, aw[v][i]);
+            P::put(sb[v], i, ab[v][i]);
+        }
+    block_partials<kThreads, TPR, NV, VEC>(sw, sb, part, (float *)ring, p.gi, p.ri, p.lane, p.g, p.mine, s);
 }
 
 template <typename T, bool GATE, bool THREE>
@@ -150,12 +171,12 @@ cudaError_t bwd_t(const void *dy, const void *val, const void *third, const floa
                   const float *b, void *dx, void *dother, float *dw, float *db, const BlockNorm &bn, int sms, float *scratch,
                   cudaStream_t stream) {
     const NormPick p = pick_layout(bn.D, sizeof(T), in_pieces(bn.D, sizeof(T), {dy, val, third, dx, dother}));
-    const NormGrid n = norm_grid(p, bn.rows, bn.G, bn.D, 0.f, sms, 512);
+    const NormGrid n = norm_grid(p, bn.rows, bn.G, bn.D, 0.f, sms, kLeast, kPerSm);
     float *part = dw || db ? scratch : nullptr;
     const cudaError_t err = with_layout<T>(p, [&](auto tpr, auto nv, auto vec) {
         auto kern = block_norm_bwd_kernel<T, tpr(), nv(), vec(), GATE, THREE>;
         constexpr int kTensors = 2 + THREE;
-        const int smem = std::max(vec() > 1 ? kTensors * ring_depth<nv(), kTensors>() * n.threads * 16 * nv() : 0,
+        const int smem = std::max(vec() > 1 ? kTensors * block_depth<tpr(), nv(), kTensors>() * n.threads * 16 * nv() : 0,
                                   n.threads * 4 * nv() * vec());
         const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (err != cudaSuccess) return err;
@@ -172,9 +193,13 @@ cudaError_t bwd_t(const void *dy, const void *val, const void *third, const floa
 
 }  // namespace
 
-// As the layer norm's: the same blocks leave the same partial sums.
 size_t block_norm_bwd_scratch_bytes(int64_t rows, int G, int D, gdr_dtype_t dtype, int sms) {
-    return norm_bwd_scratch_bytes(rows, G, D, dtype, sms);
+    const size_t es = dtype == GDR_BF16 ? 2 : 4;
+    size_t need = 0;   // whichever layout the pointers' alignment allows
+    for (bool pieces : {true, false})
+        need = std::max(need, sizeof(float) * 2 * (size_t)G * D *
+                                  norm_grid(pick_layout(D, es, pieces), rows, G, D, 0.f, sms, kLeast, kPerSm).grid.y);
+    return need;
 }
 
 cudaError_t launch_add_norm_bwd(const void *dy, const void *dsum, const void *sum, const float *mean, const float *rstd,

@@ -74,8 +74,8 @@ constexpr int kThreadsPerSm = 1024;
 // (asynchronous copies, each thread reading back its own: no barrier), 4 rows deep where the
 // SM's blocks have room for it; single elements are loaded one row ahead in registers.
 constexpr int kRingBytesPerSm = 200 * 1024;
-template <int NV, int TENSORS> constexpr int ring_depth() {
-    constexpr int fit = kRingBytesPerSm / (kThreadsPerSm * 16 * NV * TENSORS);
+template <int NV, int TENSORS, int PER_SM = kThreadsPerSm> constexpr int ring_depth() {
+    constexpr int fit = kRingBytesPerSm / (PER_SM * 16 * NV * TENSORS);
     return fit > 4 ? 4 : fit;
 }
 
@@ -215,7 +215,8 @@ struct NormGrid {
     NormShape s;
 };
 
-inline NormGrid norm_grid(const NormPick &p, int64_t rows, int G, int D, float eps, int sms, int least) {
+inline NormGrid norm_grid(const NormPick &p, int64_t rows, int G, int D, float eps, int sms, int least,
+                          int per_sm = kThreadsPerSm) {
     NormGrid o{};
     o.threads = std::max(p.tpr, least);
     const int subs = o.threads / p.tpr;
@@ -228,7 +229,7 @@ inline NormGrid norm_grid(const NormPick &p, int64_t rows, int G, int D, float e
     o.s.rpb = subs / o.s.gpb;
     const int64_t by = (G + o.s.gpb - 1) / o.s.gpb;
     const int64_t want = (o.s.sets + o.s.rpb - 1) / o.s.rpb;
-    const int64_t most = std::max<int64_t>(1, (int64_t)sms * (kThreadsPerSm / o.threads) / by);
+    const int64_t most = std::max<int64_t>(1, (int64_t)sms * std::max(1, per_sm / o.threads) / by);
     o.grid = dim3((unsigned)by, (unsigned)std::min(want, most));
     return o;
 }

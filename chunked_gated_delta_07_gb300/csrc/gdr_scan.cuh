@@ -23,6 +23,7 @@
 #include <type_traits>
 
 #include "gdr_internal.cuh"
+#include "gdr_pairs.cuh"
 #include "gdr_sm100.cuh"
 #include "gdr_tc.cuh"
 
@@ -66,35 +67,6 @@ struct ScanBwd {
 namespace scan {
 
 constexpr unsigned kFull = 0xffffffffu;
-
-// ---- pairs ------------------------------------------------------------------------------
-// A lane works on two channels at once: one instruction for both, where there is one.
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
-__device__ __forceinline__ uint64_t bits(float2 v) {
-    uint64_t u;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(u) : "f"(v.x), "f"(v.y));
-    return u;
-}
-__device__ __forceinline__ float2 unbits(uint64_t u) {
-    float2 v;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(u));
-    return v;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
-    return unbits(d);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
-    return unbits(d);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
-    return unbits(d);
-}
 
 // ---- the gate ---------------------------------------------------------------------------
 // FINE (fp32 tensors): the library functions' accuracy.  Else the special-function unit's, within
