@@ -523,7 +523,7 @@ inline void scan_divide(ScanShape &s, const int (&room)[kScanSizes], int tok) {
 
 #ifdef __CUDACC__
 // How many blocks, and clusters of 2, 4, 8 and 16 blocks, of a kernel run at a time on the current
-// device; asked for once per kernel and device.
+// device; the kernel's attributes are set, and this is asked for, once per kernel and device.
 template <typename K> cudaError_t scan_room(K kern, int threads, int smem, int sms, std::atomic<int> (&known)[16][kScanSizes],
                                             int (&room)[kScanSizes]) {
     int dev = 0;
@@ -534,6 +534,7 @@ template <typename K> cudaError_t scan_room(K kern, int threads, int smem, int s
         for (int k = 0; k < kScanSizes; ++k) room[k] = known[dev][k].load(std::memory_order_relaxed);
         return cudaSuccess;
     }
+    if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return err;
     if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return err;
     int per_sm = 0;
     if ((err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem)) != cudaSuccess) return err;
@@ -560,10 +561,9 @@ template <typename K> cudaError_t scan_room(K kern, int threads, int smem, int s
 template <typename K, typename... A>
 cudaError_t scan_launch(K kern, ScanShape &s, int threads, int smem, int tok, int sms,
                         std::atomic<int> (&known)[16][kScanSizes], const char *name, cudaStream_t stream, A... args) {
-    cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (err != cudaSuccess) return err;
     int room[kScanSizes];
-    if ((err = scan_room(kern, threads, smem, sms, known, room)) != cudaSuccess) return err;
+    cudaError_t err = scan_room(kern, threads, smem, sms, known, room);
+    if (err != cudaSuccess) return err;
     scan_divide(s, room, tok);
     const int64_t blocks = (int64_t)s.tiles * s.parts * s.cluster;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;

@@ -97,7 +97,7 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
             // the state in front of the tile: kept by the forward pass behind the tile before
             if (base > p0) h = load_state(states, tile_no - 1, D, c);
             cur.seek(s, first, last, max(base, p0));
-            inner = cur.from < base && cur.to > base + kScanTile && mode == kTma && pairs;
+            inner = cur.from < base && cur.to > base + kScanTile;
             if (!lost) lost = !__all_sync(kFull, ring.wait(slot, use, limit_ns));
         }
         const bool cuts = CS == 1 ? there && !inner : many || i == steps - 1;   // a part's first token is in the last step
@@ -216,7 +216,7 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
             chain(std::true_type{});
         else
             chain(std::false_type{});
-        if (inner) {
+        if (inner && pairs) {
             if (c < D) {
                 char *ox = (char *)(dx + (int64_t)base * D) + lane_out, *oa = (char *)(da + (int64_t)base * D) + lane_out;
 #pragma unroll
@@ -258,6 +258,8 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
                     }
                 }
             }
+        }
+        if (!inner) {
             __syncthreads();   // the gates have been read again
             if (!lost) ask(i + kDepth, slot);
         }

@@ -86,7 +86,7 @@ scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Fwd
         bool inner = false;
         if (there) {
             cur.seek(s, first, last, max(base, p0));
-            inner = cur.from < base && cur.to > base + kTok && mode == kTma && pairs;
+            inner = cur.from < base && cur.to > base + kTok;
             if (!lost) lost = !__all_sync(kFull, ring.wait(slot, use, limit_ns));
         }
         const bool cuts = CS == 1 ? there && !inner : many || i == 0;
@@ -173,7 +173,7 @@ scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Fwd
             chain(std::true_type{});
         else
             chain(std::false_type{});
-        if (inner) {
+        if (inner && pairs) {
             if (c < D) {
                 if (out) {
                     char *o = (char *)(out + (int64_t)base * D) + lane_out;

@@ -333,3 +333,37 @@ def test_captured_and_replayed():
     ok()
     assert torch.equal(out, want[0]) and torch.equal(hT, want[1])
     assert all(torch.equal(p, q) for p, q in zip(grads, gwant))
+
+
+@pytest.mark.parametrize("D", [64, 63])
+def test_waits_that_run_out_are_reported(monkeypatch, D):
+    """GDR_TC_WAIT_NS=0: a wait not satisfied at once gives up (for the tile's copy, or for the other
+    blocks of a cluster).  The call returns, and the next one is right."""
+    i = inputs([5000], D, "bf16", 3)
+    want = gdr.gated_scan_fwd(i["x"], i["a"], h0=i["h0"], cu_seqlens=i["cu"], want_states=True)
+    grads = gdr.gated_scan_bwd(i["x"], i["a"], i["dout"], i["dhT"], i["h0"], want[2], i["cu"])
+    ok()
+    monkeypatch.setenv("GDR_TC_WAIT_NS", "0")
+    gdr.gated_scan_fwd(i["x"], i["a"], h0=i["h0"], cu_seqlens=i["cu"])
+    assert gdr.gdr_get_status() == gdr.GDR_ERR_TIMEOUT
+    gdr.gated_scan_bwd(i["x"], i["a"], i["dout"], i["dhT"], i["h0"], want[2], i["cu"])
+    assert gdr.gdr_get_status() == gdr.GDR_ERR_TIMEOUT
+    monkeypatch.delenv("GDR_TC_WAIT_NS")
+    got = gdr.gated_scan_fwd(i["x"], i["a"], h0=i["h0"], cu_seqlens=i["cu"], want_states=True)
+    again = gdr.gated_scan_bwd(i["x"], i["a"], i["dout"], i["dhT"], i["h0"], got[2], i["cu"])
+    ok()
+    assert all(torch.equal(p, q) for p, q in zip(want + grads, got + again))
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 131072, 96), (3, 30001, 40)])
+def test_long(B, T, D):
+    """Long sequences, in 64 bits on the GPU by blocks of tokens (the state carried from block to block)."""
+    i = inputs([T] * B, D, "f32", 17, packed=False)
+    out, hT, _ = gdr.gated_scan_fwd(i["x"], i["a"], h0=i["h0"], source="convex")
+    ok()
+    alpha, w, _, _ = ref.gates(i["a"].double(), 2.0, "bounded", "convex")
+    u, h = w * i["x"].double(), i["h0"].double()
+    for t in range(T):
+        h = torch.addcmul(u[:, t], alpha[:, t], h, out=u[:, t])
+    close(out, u.cpu(), BOUND32, "out")
+    close(hT, h.cpu(), BOUND32, "hT")
