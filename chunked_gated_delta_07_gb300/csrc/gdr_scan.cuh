@@ -69,23 +69,28 @@ namespace scan {
 constexpr unsigned kFull = 0xffffffffu;
 
 // ---- the gate ---------------------------------------------------------------------------
-// FINE (fp32 tensors): the library functions' accuracy.  Else the special-function unit's, within
-// a few 2^-23 of the value; what a long memory hangs on, 1 - alpha for alpha near 1, keeps its
-// relative accuracy in both (1 - e^-n from a polynomial, and alpha from that).
-constexpr float kLog2e = 1.44269504088896341f;
+// The special-function unit's accuracy, within a few 2^-23 of the value, also for fp32 tensors
+// (FINE), whose exponentials' arguments keep the rounding error of the product with log2 e: that
+// is |a| 2^-24 of the exponential, and the library function costs three times as much (8 x 2048
+// fp32 tokens 175 us, see below).  What a long memory hangs on, 1 - alpha for alpha near 1, keeps
+// its relative accuracy: 1 - e^-n comes from a polynomial, and alpha from that.
+constexpr float kLog2e = 1.44269504088896341f, kLog2eRest = 1.925963033500e-8f, kLn2 = 0.693147180559945f;
 // 2^x
 __device__ __forceinline__ float2 exp2_fast(float2 x) {
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.x));
     asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x.y));
     return x;
 }
-// e^(k x), kl = k log2 e
-template <bool FINE> __device__ __forceinline__ float2 exp_of(float2 x, float k, float kl) {
-    if constexpr (FINE) return make_float2(expf(k * x.x), expf(k * x.y));
-    return exp2_fast(mul2(x, both(kl)));
+// e^-x
+template <bool FINE> __device__ __forceinline__ float2 exp_minus(float2 x) {
+    const float2 hi = mul2(x, both(-kLog2e)), e = exp2_fast(hi);
+    if constexpr (!FINE) return e;
+    // x log2 e = -(hi + lo): 2^(hi + lo) = 2^hi (1 + lo ln 2); 2^hi is infinite from x = -88 on, and takes none
+    const float2 lo = fma2(x, both(-kLog2eRest), make_float2(fmaf(x.x, -kLog2e, -hi.x), fmaf(x.y, -kLog2e, -hi.y)));
+    const float2 c = mul2(lo, both(kLn2));
+    return make_float2(fabsf(x.x) < 87.f ? fmaf(e.x, c.x, e.x) : e.x, fabsf(x.y) < 87.f ? fmaf(e.y, c.y, e.y) : e.y);
 }
-template <bool FINE> __device__ __forceinline__ float2 inverse(float2 x) {
-    if constexpr (FINE) return make_float2(__frcp_rn(x.x), __frcp_rn(x.y));
+__device__ __forceinline__ float2 inverse(float2 x) {
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.x));
     asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x.y));
     return x;
@@ -112,7 +117,7 @@ __device__ __forceinline__ Gate gate_of(float2 a, const ScanShape &shape) {
     const float2 one = both(1.f), minus = both(-1.f);
     const float b = shape.b;
     if constexpr (GATE == kBoundedBy2) {
-        const float2 e = exp_of<FINE>(a, -1.f, -kLog2e), s = inverse<FINE>(add2(e, one));
+        const float2 e = exp_minus<FINE>(a), s = inverse(add2(e, one));
         if constexpr (GRAD) {
             const float2 c = make_float2(min_nan(e.x, 1e38f), min_nan(e.y, 1e38f));
             o.slope = mul2(mul2(s, both(-b)), mul2(c, s));
@@ -125,7 +130,7 @@ __device__ __forceinline__ Gate gate_of(float2 a, const ScanShape &shape) {
         o.alpha = fma2(left, minus, one);
     } else if constexpr (GATE == kBounded) {
         // e^-a may be inf: the sigmoid is 0 then
-        const float2 e = exp_of<FINE>(a, -1.f, -kLog2e), s = inverse<FINE>(add2(e, one));
+        const float2 e = exp_minus<FINE>(a), s = inverse(add2(e, one));
         const float2 n = mul2(s, both(b));   // -g
         if constexpr (GRAD) {
             // g' = -b s (1 - s), 1 - s = e^-a s
@@ -141,15 +146,15 @@ __device__ __forceinline__ Gate gate_of(float2 a, const ScanShape &shape) {
         p = fma2(p, n, both(-0.49999985098838806f));
         p = fma2(p, n, one);
         const float2 near = mul2(n, p), above = fma2(near, minus, one);
-        const float2 far = FINE ? exp_of<FINE>(n, -1.f, -kLog2e) : exp_of<FINE>(s, -b, -b * kLog2e);
+        const float2 far = FINE ? exp_minus<FINE>(n) : exp2_fast(mul2(s, both(-b * kLog2e)));
         const float2 below = fma2(far, minus, one);
         const bool s0 = n.x < 0.5f, s1 = n.y < 0.5f;
         left = make_float2(s0 ? near.x : below.x, s1 ? near.y : below.y);
         o.alpha = make_float2(s0 ? above.x : far.x, s1 ? above.y : far.y);
     } else {
         // e^{-softplus(a)} = 1 / (1 + e^a)
-        const float2 e = exp_of<FINE>(make_float2(fabsf(a.x), fabsf(a.y)), -1.f, -kLog2e);
-        const float2 lo = mul2(e, inverse<FINE>(add2(e, one))), hi = fma2(lo, minus, one);
+        const float2 e = exp_minus<FINE>(make_float2(fabsf(a.x), fabsf(a.y)));
+        const float2 lo = mul2(e, inverse(add2(e, one))), hi = fma2(lo, minus, one);
         const bool s0 = a.x > 0.f, s1 = a.y > 0.f;
         o.alpha = make_float2(s0 ? lo.x : hi.x, s1 ? lo.y : hi.y);
         left = make_float2(s0 ? hi.x : lo.x, s1 ? hi.y : lo.y);
@@ -166,10 +171,7 @@ __device__ __forceinline__ Gate gate_of(float2 a, const ScanShape &shape) {
         const float2 z = fma2(left, o.alpha, left);
         float2 r = z;
         if constexpr (GRAD) r = make_float2(max_nan(z.x, 1.2e-38f), max_nan(z.y, 1.2e-38f));
-        if constexpr (FINE) {
-            r = make_float2(1.f / sqrtf(r.x), 1.f / sqrtf(r.y));
-            o.w = make_float2(sqrtf(z.x), sqrtf(z.y));
-        } else if constexpr (GRAD) {
+        if constexpr (GRAD) {
             asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(r.x));
             asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(r.y));
             o.w = mul2(z, r);
@@ -468,16 +470,14 @@ cudaError_t with_form(ScanShape &s, gdr_dtype_t dtype, gdr_gate_t gate, gdr_sour
     };
     auto by_gate = [&](auto t) {
         if (gate == GDR_GATE_SOFTPLUS) return by_source(t, integral_constant<int, kSoftplus>{});
-        if constexpr (sizeof(t) == 2) {   // fp32 tensors have the time for the exponential
-            if (s.b <= 2.f) {
-                // (1 - e^-n) / n on [0, 2] by a polynomial fitted to it, relative error 1.4e-8
-                static const double fit[kScanPoly] = {0.99999998631057,      -0.4999991992693423,    0.16665864060437813,
-                                                      -0.04163556673545308,  0.008272895784878453,   -0.0013234571801574847,
-                                                      0.00015753673867873683, -1.0291639928970174e-05};
-                double n = s.b;
-                for (int k = 0; k < kScanPoly; ++k, n *= s.b) s.poly[k].x = s.poly[k].y = (float)(fit[k] * n);
-                return by_source(t, integral_constant<int, kBoundedBy2>{});
-            }
+        if (s.b <= 2.f) {
+            // (1 - e^-n) / n on [0, 2] by a polynomial fitted to it, relative error 1.4e-8
+            static const double fit[kScanPoly] = {0.99999998631057,       -0.4999991992693423,  0.16665864060437813,
+                                                  -0.04163556673545308,   0.008272895784878453, -0.0013234571801574847,
+                                                  0.00015753673867873683, -1.0291639928970174e-05};
+            double n = s.b;
+            for (int k = 0; k < kScanPoly; ++k, n *= s.b) s.poly[k].x = s.poly[k].y = (float)(fit[k] * n);
+            return by_source(t, integral_constant<int, kBoundedBy2>{});
         }
         return by_source(t, integral_constant<int, kBounded>{});
     };

@@ -96,9 +96,12 @@ scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Fwd
         Run run{both(1.f), both(0.f)};
         Cursor mine = cur;
         Marks m{0, 0};
+        bool at_start = false;   // a sequence starts with the run, and none within it
+        float2 start = both(0.f);
         if (there) {
             if (!inner) {
                 m = marks_of(s, mine, first, last, p, lo, hi);
+                at_start = m.first == 1;
                 if (hi - lo < kL) {
                     blank<T, kL>(tx, 0.f, p, lo, hi);
                     blank<T, kL>(ta, -INFINITY, p, lo, hi);
@@ -112,12 +115,14 @@ scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Fwd
                 al[j] = g.alpha;
                 u[j] = SRC == GDR_SOURCE_PLAIN ? xv : mul2(g.w, xv);
             }
-            if (!m.first) {
+            if (at_start) run.B = start = load_state(h0, mine.n, D, c);
+            if (!(m.first & ~1u)) {
 #pragma unroll
                 for (int j = 0; j < kL; ++j) {
                     run.B = fma2(al[j], run.B, u[j]);
                     run.A = mul2(run.A, al[j]);
                 }
+                if (at_start) run.A = both(-1.f);
             } else {
                 int n = mine.n;
 #pragma unroll
@@ -173,26 +178,26 @@ scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Fwd
             chain(std::true_type{});
         else
             chain(std::false_type{});
-        if (inner && pairs) {
-            if (c < D) {
-                if (out) {
-                    char *o = (char *)(out + (int64_t)base * D) + lane_out;
+        if (at_start) h = start;
+        if (there && c < D && pairs && hi - lo == kL && !(m.first & ~1u) && !(hT && (m.last & ~(1u << (kL - 1))))) {
+            if (out) {
+                char *o = (char *)(out + (int64_t)base * D) + lane_out;
 #pragma unroll
-                    for (int j = 0; j < kL; ++j) {
-                        h = fma2(al[j], h, u[j]);
-                        write2((T *)o, h);
-                        o += D * (int)sizeof(T);
-                    }
-                } else {
-#pragma unroll
-                    for (int j = 0; j < kL; ++j) h = fma2(al[j], h, u[j]);
+                for (int j = 0; j < kL; ++j) {
+                    h = fma2(al[j], h, u[j]);
+                    write2((T *)o, h);
+                    o += D * (int)sizeof(T);
                 }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kL; ++j) h = fma2(al[j], h, u[j]);
             }
+            if (hT && m.last) store_state(hT, seq_from(s, mine.n, p + kL - 1), D, c, h);
         } else if (there && c < D) {
             int n = mine.n;
 #pragma unroll
             for (int j = 0; j < kL; ++j) {
-                h = m.first >> j & 1 ? u[j] : fma2(al[j], h, u[j]);
+                h = !at_start && (m.first >> j & 1) ? u[j] : fma2(al[j], h, u[j]);
                 const int t = p + j;
                 if (t < lo || t >= hi) continue;
                 if (out) {
