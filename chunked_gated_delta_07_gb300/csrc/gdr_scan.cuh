@@ -339,66 +339,108 @@ struct Peers {
 };
 
 // ---- tiles of raw inputs ------------------------------------------------------------------
-// TMA: a box of each tensor (rows and bases on 16-byte boundaries).  PAIR: a lane copies its own two
-// channels asynchronously, where they can be.  SINGLE: plain loads, element by element.
-enum CopyMode { kTma, kPair, kSingle };
+// BOXES: a TMA box of each tensor (rows and bases on 16-byte boundaries).  ROWS: each row's 16-byte
+// pieces that hold one of its channels, by a bulk copy; the lanes then move their run's channels to
+// where a box would have them.  PAIRS: a lane copies its own two channels (fp32).
+//
+// 8 x 4096 bf16 tokens forward: 2048 channels in boxes 96 us; FIGURES
+enum CopyMode { kBoxes, kRows, kPairs };
 __device__ __forceinline__ void copy4(unsigned dst, const void *src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy16(unsigned dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 
 // A block's ring of DEPTH tiles of NT tensors, TOK tokens each; a lane's run is L of them.
 template <typename T, int L, int TOK, int NT, int DEPTH> struct Ring {
-    static constexpr int kTile = TOK * kScanChannels;   // elements
-    T *at;             // [DEPTH][NT][TOK][32]
-    uint64_t *full;    // [DEPTH]: the slot's boxes are there
-    int mode;
-    int issued;        // boxes' tiles asked for
+    static constexpr int kRow = kScanChannels * (int)sizeof(T);   // bytes of a row as it is read
+    static constexpr int kRawRow = kRow + 16;                     // and of its pieces
+    char *at;          // [DEPTH][NT] tiles of TOK rows, 128-byte aligned
+    uint64_t *full;    // [DEPTH]: the slot's copies are there
+    int mode, pitch;   // bytes from row to row of a run that has not been moved
+    int issued;        // tiles asked for by boxes
 
-    __device__ __forceinline__ T *tile(int slot, int tensor) const { return at + (slot * NT + tensor) * kTile; }
+    __host__ __device__ static constexpr int bytes(bool rows) { return DEPTH * NT * TOK * (rows ? kRawRow : kRow); }
+    __device__ __forceinline__ Ring(char *smem, uint64_t *bars, int mode_)
+        : at(smem), full(bars), mode(mode_), pitch(mode_ == kRows ? kRawRow : kRow), issued(0) {}
+    // Thread 0, before the first use.
+    __device__ __forceinline__ void init() {
+        for (int i = 0; i < DEPTH; ++i) sm100::mbar_init(&full[i], 1);
+    }
+    __device__ __forceinline__ char *tile(int slot, int tensor) const { return at + (slot * NT + tensor) * TOK * pitch; }
+    // A lane's two channels of its run's first token; the others follow, kScanChannels elements apart.
+    __device__ __forceinline__ T *run(int slot, int tensor, int first, int l) const {
+        return (T *)(tile(slot, tensor) + first * pitch) + 2 * l;
+    }
 
     // Every thread: asks for the tile from token `row` on, after the whole block is done with what
     // was in the slot.  The boxes are issued by a lane of one warp, which costs that warp some 400
     // cycles; the warps take turns.
     __device__ __forceinline__ void ask(int slot, int turn, const CUtensorMap *const (&maps)[NT], const T *const (&src)[NT],
                                         int row, int lo, int hi, int c0, int D) {
-        if (mode == kTma) {
+        if (mode == kBoxes) {
             if (threadIdx.x == 32 * (turn % (TOK / (2 * L)))) {
-                sm100::mbar_arrive_expect_tx(&full[slot], NT * kTile * (unsigned)sizeof(T));
+                sm100::mbar_arrive_expect_tx(&full[slot], NT * TOK * kRow);
 #pragma unroll
                 for (int i = 0; i < NT; ++i) sm100::tma_load_2d(tile(slot, i), maps[i], c0, row, &full[slot]);
             }
             ++issued;
-            return;
+        } else if (mode == kRows) {
+            ask_rows(tile(slot, 0), src[0], src[1], src[NT - 1], row, lo, hi, c0, D);
+        } else {
+            ask_pairs(tile(slot, 0), src[0], src[1], src[NT - 1], row, lo, hi, c0, D);
         }
-        const int lane = threadIdx.x & 31, c = c0 + 2 * (lane & 15);
-        const int run = ((threadIdx.x >> 5) * 2 + (lane >> 4)) * L;
+    }
+    // The warp's own rows, as many of them at once as have pieces for its lanes.  A piece of 16 bytes
+    // that holds one of the row's elements lies within the allocation that holds that element.
+    // (These are functions apart that take values: they are called once a step at most, and would
+    // cost the steps' code registers.)
+    __device__ __noinline__ static void ask_rows(char *to, const T *s0, const T *s1, const T *s2, int row, int lo, int hi,
+                                                 int c0, int D) {
+        const T *const src[3] = {s0, s1, s2};
+        constexpr int kPieces = kRawRow / 16, kAtOnce = 32 / kPieces;
+        const int lane = threadIdx.x & 31, mine = lane / kPieces, piece = lane % kPieces;
+        const int first = (threadIdx.x >> 5) * 2 * L, width = min(kScanChannels, D - c0) * (int)sizeof(T);
+        if (mine >= kAtOnce) return;
 #pragma unroll 2
-        for (int j = run; j < run + L; ++j) {
+        for (int r = mine; r < 2 * L; r += kAtOnce) {
+            const int t = row + first + r;
+            if (t < lo || t >= hi) continue;
+            const int64_t off = (int64_t)t * D + c0;
+#pragma unroll
+            for (int k = 0; k < NT; ++k) {
+                const uintptr_t p = (uintptr_t)(src[k] + off), q = (p & ~(uintptr_t)15) + 16 * piece;
+                if (q < p + width)
+                    copy16(sm100::smem_u32(to + (k * TOK + first + r) * kRawRow + 16 * piece), (const void *)q);
+            }
+        }
+    }
+    __device__ __noinline__ static void ask_pairs(char *to, const T *s0, const T *s1, const T *s2, int row, int lo, int hi,
+                                                  int c0, int D) {
+        const T *const src[3] = {s0, s1, s2};
+        const int lane = threadIdx.x & 31, c = c0 + 2 * (lane & 15);
+        const int first = ((threadIdx.x >> 5) * 2 + (lane >> 4)) * L;
+#pragma unroll 4
+        for (int j = first; j < first + L; ++j) {
             const int t = row + j;
-            const bool on = t >= lo && t < hi;
-            const bool on0 = on && c < D, on1 = on && c + 1 < D;
+            const bool on0 = t >= lo && t < hi && c < D, on1 = on0 && c + 1 < D;
             const int64_t off = on0 ? (int64_t)t * D + c : 0;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                T *d = tile(slot, i) + j * kScanChannels + 2 * (lane & 15);
-                if (mode == kPair) {
-                    const unsigned da = sm100::smem_u32(d);
-                    copy4(da, src[i] + off, on0 ? 4 : 0);
-                    if constexpr (sizeof(T) == 4) copy4(da + 4, src[i] + (on1 ? off + 1 : 0), on1 ? 4 : 0);
-                } else {
-                    d[0] = on0 ? src[i][off] : from_f32<T>(0.f);
-                    d[1] = on1 ? src[i][off + 1] : from_f32<T>(0.f);
-                }
+                const unsigned d = sm100::smem_u32(to + (i * TOK + j) * kRow) + 2 * (lane & 15) * (unsigned)sizeof(T);
+                copy4(d, src[i] + off, on0 ? 4 : 0);
+                copy4(d + 4, src[i] + (on1 ? off + 1 : 0), on1 ? 4 : 0);
             }
         }
     }
     // Closes a step's asking (also one that asked for nothing): every step, once.
     __device__ __forceinline__ void close() {
-        if (mode != kTma) asm volatile("cp.async.commit_group;" ::: "memory");
+        if (mode != kBoxes) asm volatile("cp.async.commit_group;" ::: "memory");
     }
     // Every thread: the slot's tile of `use` (its use'th) is there, or false where the wait ran out.
     __device__ __forceinline__ bool wait(int slot, int use, uint64_t limit_ns) {
-        if (mode == kTma)
+        if (mode == kBoxes)
             return limit_ns && sm100::mbar_try_wait(&full[slot], use & 1) ? true : wait_long(&full[slot], use & 1, limit_ns);
         asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
         __syncwarp();
@@ -407,9 +449,41 @@ template <typename T, int L, int TOK, int NT, int DEPTH> struct Ring {
     __device__ __noinline__ static bool wait_long(uint64_t *bar, int parity, uint64_t limit_ns) {
         return sm100::mbar_wait(bar, parity, limit_ns);
     }
+    // The whole warp: moves the channels of its runs from where the rows' copies put them; rows
+    // come to lie 16 bytes closer, so a row is read before anything is written over it.
+    __device__ __forceinline__ void move(int slot, const T *const (&src)[NT], int token, int c0, int D) const {
+        move_rows(tile(slot, 0), src[0], src[1], src[NT - 1], token, c0, D);
+    }
+    __device__ __noinline__ static void move_rows(char *at, const T *s0, const T *s1, const T *s2, int token, int c0, int D) {
+        const T *const src[3] = {s0, s1, s2};
+        const int lane = threadIdx.x & 31, l = lane & 15, first = ((threadIdx.x >> 5) * 2 + (lane >> 4)) * L;
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            const char *raw = at + (i * TOK + first) * kRawRow;
+            T *to = (T *)raw + 2 * l;
+            const T *p = src[i] + (int64_t)(token + first) * D + c0;
+#pragma unroll 1
+            for (int j = 0; j < L; j += 4) {
+                T v[4][2];
+#pragma unroll
+                for (int k = 0; k < 4; ++k, raw += kRawRow, p += D) {
+                    const T *q = (const T *)(raw + ((uintptr_t)p & 15)) + 2 * l;
+                    v[k][0] = q[0];
+                    v[k][1] = q[1];
+                }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; ++k, to += kScanChannels) {
+                    to[0] = v[k][0];
+                    to[1] = v[k][1];
+                }
+            }
+            __syncwarp();
+        }
+    }
     // No copy of this block's is under way any more, also after a wait that ran out.
     __device__ __forceinline__ void drain(bool lost) {
-        if (mode != kTma)
+        if (mode != kBoxes)
             asm volatile("cp.async.wait_group 0;" ::: "memory");
         else if (lost)
             for (int k = max(0, issued - DEPTH); k < issued; ++k)
@@ -417,10 +491,6 @@ template <typename T, int L, int TOK, int NT, int DEPTH> struct Ring {
     }
 };
 
-// Two channels of a token, from the lane's place in a tile (run_at).
-template <typename T> __device__ __forceinline__ T *run_at(T *tile, int run, int l) {
-    return tile + run * kScanChannels + 2 * l;
-}
 template <typename T> __device__ __forceinline__ float2 read2(const T *run, int j) {
     const T *p = run + j * kScanChannels;
     if constexpr (sizeof(T) == 4) {
@@ -521,11 +591,14 @@ inline void scan_divide(ScanShape &s, const int (&room)[kScanSizes], int tok) {
         if ((1 << k) < 2 * along && units <= room[k]) s.cluster = 1 << k;
 }
 
+using ScanRoom = std::atomic<int>[16][kScanSizes];   // by device
+
 #ifdef __CUDACC__
 // How many blocks, and clusters of 2, 4, 8 and 16 blocks, of a kernel run at a time on the current
-// device; the kernel's attributes are set, and this is asked for, once per kernel and device.
-template <typename K> cudaError_t scan_room(K kern, int threads, int smem, int sms, std::atomic<int> (&known)[16][kScanSizes],
-                                            int (&room)[kScanSizes]) {
+// device; the kernel's attributes are set (`most` bytes of shared memory in any of its modes), and this is
+// asked for, once per kernel, mode and device.
+template <typename K>
+cudaError_t scan_room(K kern, int threads, int smem, int most, int sms, ScanRoom &known, int (&room)[kScanSizes]) {
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
@@ -534,7 +607,7 @@ template <typename K> cudaError_t scan_room(K kern, int threads, int smem, int s
         for (int k = 0; k < kScanSizes; ++k) room[k] = known[dev][k].load(std::memory_order_relaxed);
         return cudaSuccess;
     }
-    if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return err;
+    if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess) return err;
     if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return err;
     int per_sm = 0;
     if ((err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem)) != cudaSuccess) return err;
@@ -559,10 +632,10 @@ template <typename K> cudaError_t scan_room(K kern, int threads, int smem, int s
 
 // One launch: the attributes, the division, the clusters.
 template <typename K, typename... A>
-cudaError_t scan_launch(K kern, ScanShape &s, int threads, int smem, int tok, int sms,
-                        std::atomic<int> (&known)[16][kScanSizes], const char *name, cudaStream_t stream, A... args) {
+cudaError_t scan_launch(K kern, ScanShape &s, int threads, int smem, int most, int tok, int sms,
+                        ScanRoom &known, const char *name, cudaStream_t stream, A... args) {
     int room[kScanSizes];
-    cudaError_t err = scan_room(kern, threads, smem, sms, known, room);
+    cudaError_t err = scan_room(kern, threads, smem, most, sms, known, room);
     if (err != cudaSuccess) return err;
     scan_divide(s, room, tok);
     const int64_t blocks = (int64_t)s.tiles * s.parts * s.cluster;

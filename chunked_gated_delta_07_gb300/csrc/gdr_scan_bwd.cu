@@ -27,7 +27,6 @@ constexpr int kThreads = 32 * kWarps;
 constexpr int kBlocksPerSm = 2;
 constexpr int kDepth = 2;
 template <typename T> using BwdRing = Ring<T, kL, kScanTile, 3, kDepth>;
-template <typename T> constexpr int kSmem = kDepth * 3 * BwdRing<T>::kTile * (int)sizeof(T) + 128;
 
 struct BwdMaps {
     CUtensorMap x, a, dout;
@@ -59,8 +58,9 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
                 dh0[(int64_t)n * D + c0 + lane] = dhT ? dhT[(int64_t)n * D + c0 + lane] : 0.f;
     const int t0 = p0 / kScanTile, t1 = (p1 + kScanTile - 1) / kScanTile, steps = (t1 - t0 + CS - 1) / CS;
     const bool many = last - first > 1;
+    BwdRing<T> ring((char *)(((uintptr_t)smem + 127) & ~(uintptr_t)127), full, mode);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kDepth; ++i) sm100::mbar_init(&full[i], 1);
+        ring.init();
         sm100::mbar_init(&bars[0], 1);
         sm100::mbar_init(&bars[1], 1);
         sm100::fence_mbar_init();
@@ -69,7 +69,6 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
         cluster_sync();   // every peer runs, and its barriers are set up, before its memory is written to
     else
         __syncthreads();
-    BwdRing<T> ring{(T *)(((uintptr_t)smem + 127) & ~(uintptr_t)127), full, mode, 0};
     const CUtensorMap *const map[3] = {&maps.x, &maps.a, &maps.dout};
     const T *const src[3] = {x, a, dout};
     // step i of this block: tile t1 - 1 - (i CS + rank), none below t0
@@ -99,10 +98,11 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
             cur.seek(s, first, last, max(base, p0));
             inner = cur.from < base && cur.to > base + kScanTile;
             if (!lost) lost = !__all_sync(kFull, ring.wait(slot, use, limit_ns));
+            if (mode == kRows) ring.move(slot, src, base, c0, D);
         }
         const bool cuts = CS == 1 ? there && !inner : many || i == steps - 1;   // a part's first token is in the last step
-        T *tx = run_at(ring.tile(slot, 0), run_at0, l), *ta = run_at(ring.tile(slot, 1), run_at0, l);
-        T *td = run_at(ring.tile(slot, 2), run_at0, l);
+        T *tx = ring.run(slot, 0, run_at0, l), *ta = ring.run(slot, 1, run_at0, l);
+        T *td = ring.run(slot, 2, run_at0, l);
         const int p = base + run_at0, lo = max(p, p0), hi = min(p + kL, p1);
         Cursor mine = cur;
         Marks m{0, 0};
@@ -295,12 +295,12 @@ cudaError_t launch_bwd_t(const ScanBwd &t, ScanShape s, int sms, int *status, cu
         return tc_make_plane_map(m, p, kType, s.D, s.total, kScanChannels, kScanTile);
     };
     const bool boxes = s.total > 0 && plane(&maps.x, t.x) && plane(&maps.a, t.a) && plane(&maps.dout, t.dout);
-    const uintptr_t ins = (uintptr_t)t.x | (uintptr_t)t.a | (uintptr_t)t.dout, outs = (uintptr_t)t.dx | (uintptr_t)t.da;
-    const bool even = s.D % 2 == 0;
-    const int mode = boxes ? kTma : sizeof(T) == 4 || (even && ins % 4 == 0) ? kPair : kSingle;
-    const int pairs = even && outs % (2 * sizeof(T)) == 0;
-    static std::atomic<int> known[16][kScanSizes];
-    return scan_launch(scan_bwd_kernel<T, GATE, SRC>, s, kThreads, kSmem<T>, kScanTile, sms, known, "scan_bwd_kernel", stream,
+    const uintptr_t outs = (uintptr_t)t.dx | (uintptr_t)t.da;
+    const int mode = boxes ? kBoxes : sizeof(T) == 2 ? kRows : kPairs;
+    const int pairs = s.D % 2 == 0 && outs % (2 * sizeof(T)) == 0;
+    static ScanRoom known[2];   // with rows, without
+    const int smem = BwdRing<T>::bytes(mode == kRows) + 128, most = BwdRing<T>::bytes(true) + 128;
+    return scan_launch(scan_bwd_kernel<T, GATE, SRC>, s, kThreads, smem, most, kScanTile, sms, known[mode != kRows], "scan_bwd_kernel", stream,
                        maps, (const T *)t.x, (const T *)t.a, (const T *)t.dout, t.h0, t.dhT, t.states, (T *)t.dx, (T *)t.da,
                        t.dh0, mode, pairs, scan_wait_ns(), status);
 }

@@ -22,7 +22,6 @@ constexpr int kThreads = 32 * kWarps;
 template <typename T> constexpr int kBlocksPerSm = sizeof(T) == 2 ? 4 : 3;
 constexpr int kDepth = 2;   // tiles in shared memory
 template <typename T> using FwdRing = Ring<T, kL, kTok, 2, kDepth>;
-template <typename T> constexpr int kSmem = kDepth * 2 * FwdRing<T>::kTile * (int)sizeof(T) + 128;
 
 struct FwdMaps {
     CUtensorMap x, a;
@@ -53,8 +52,9 @@ scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Fwd
                 hT[(int64_t)n * D + c0 + lane] = h0 ? h0[(int64_t)n * D + c0 + lane] : 0.f;
     const int t0 = p0 / kTok, t1 = (p1 + kTok - 1) / kTok, steps = (t1 - t0 + CS - 1) / CS;
     const bool many = last - first > 1;
+    FwdRing<T> ring((char *)(((uintptr_t)smem + 127) & ~(uintptr_t)127), full, mode);
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kDepth; ++i) sm100::mbar_init(&full[i], 1);
+        ring.init();
         sm100::mbar_init(&bars[0], 1);
         sm100::mbar_init(&bars[1], 1);
         sm100::fence_mbar_init();
@@ -63,7 +63,6 @@ scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Fwd
         cluster_sync();   // every peer runs, and its barriers are set up, before its memory is written to
     else
         __syncthreads();
-    FwdRing<T> ring{(T *)(((uintptr_t)smem + 127) & ~(uintptr_t)127), full, mode, 0};
     const CUtensorMap *const map[2] = {&maps.x, &maps.a};
     const T *const src[2] = {x, a};
     auto ask = [&](int i, int slot) {   // the tile of step i
@@ -88,9 +87,10 @@ scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Fwd
             cur.seek(s, first, last, max(base, p0));
             inner = cur.from < base && cur.to > base + kTok;
             if (!lost) lost = !__all_sync(kFull, ring.wait(slot, use, limit_ns));
+            if (mode == kRows) ring.move(slot, src, base, c0, D);
         }
         const bool cuts = CS == 1 ? there && !inner : many || i == 0;
-        T *tx = run_at(ring.tile(slot, 0), run_at0, l), *ta = run_at(ring.tile(slot, 1), run_at0, l);
+        T *tx = ring.run(slot, 0, run_at0, l), *ta = ring.run(slot, 1, run_at0, l);
         const int p = min(base, p1) + run_at0, lo = max(p, p0), hi = min(p + kL, p1);
         float2 al[kL], u[kL];
         Run run{both(1.f), both(0.f)};
@@ -236,12 +236,12 @@ cudaError_t launch_fwd_t(const ScanFwd &t, ScanShape s, int sms, int *status, cu
         return tc_make_plane_map(m, p, kType, s.D, s.total, kScanChannels, kTok);
     };
     const bool boxes = s.total > 0 && plane(&maps.x, t.x) && plane(&maps.a, t.a);
-    const bool even = s.D % 2 == 0;
-    const bool pair = sizeof(T) == 4 || (even && ((uintptr_t)t.x | (uintptr_t)t.a) % 4 == 0);
-    const int mode = boxes ? kTma : pair ? kPair : kSingle;
-    const int pairs = even && (uintptr_t)t.out % (2 * sizeof(T)) == 0;
-    static std::atomic<int> known[16][kScanSizes];
-    return scan_launch(scan_fwd_kernel<T, GATE, SRC>, s, kThreads, kSmem<T>, kTok, sms, known, "scan_fwd_kernel", stream, maps,
+    // fp32 channels by pairs: their rows leave room for fewer blocks
+    const int mode = boxes ? kBoxes : sizeof(T) == 2 ? kRows : kPairs;
+    const int pairs = s.D % 2 == 0 && (uintptr_t)t.out % (2 * sizeof(T)) == 0;
+    static ScanRoom known[2];   // with rows, without
+    const int smem = FwdRing<T>::bytes(mode == kRows) + 128, most = FwdRing<T>::bytes(true) + 128;
+    return scan_launch(scan_fwd_kernel<T, GATE, SRC>, s, kThreads, smem, most, kTok, sms, known[mode != kRows], "scan_fwd_kernel", stream, maps,
                        (const T *)t.x, (const T *)t.a, t.h0, (T *)t.out, t.hT, t.states, mode, pairs, scan_wait_ns(), status);
 }
 
