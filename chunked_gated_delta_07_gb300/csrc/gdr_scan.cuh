@@ -353,25 +353,28 @@ __device__ __forceinline__ void copy16(unsigned dst, const void *src) {
 }
 
 // A block's ring of DEPTH tiles of NT tensors, TOK tokens each; a lane's run is L of them.
-template <typename T, int L, int TOK, int NT, int DEPTH> struct Ring {
+// Boxes have kernels of their own (BOXES).
+template <typename T, int L, int TOK, int NT, int DEPTH, bool BOXES> struct Ring {
     static constexpr int kRow = kScanChannels * (int)sizeof(T);   // bytes of a row as it is read
     static constexpr int kRawRow = kRow + 16;                     // and of its pieces
     char *at;          // [DEPTH][NT] tiles of TOK rows, 128-byte aligned
     uint64_t *full;    // [DEPTH]: the slot's copies are there
-    int mode, pitch;   // bytes from row to row of a run that has not been moved
+    int mode;
     int issued;        // tiles asked for by boxes
 
     __host__ __device__ static constexpr int bytes(bool rows) { return DEPTH * NT * TOK * (rows ? kRawRow : kRow); }
     __device__ __forceinline__ Ring(char *smem, uint64_t *bars, int mode_)
-        : at(smem), full(bars), mode(mode_), pitch(mode_ == kRows ? kRawRow : kRow), issued(0) {}
+        : at(smem), full(bars), mode(BOXES ? kBoxes : mode_), issued(0) {}
+    // Bytes from row to row before rows are moved.
+    __device__ __forceinline__ int pitch() const { return !BOXES && mode == kRows ? kRawRow : kRow; }
     // Thread 0, before the first use.
     __device__ __forceinline__ void init() {
         for (int i = 0; i < DEPTH; ++i) sm100::mbar_init(&full[i], 1);
     }
-    __device__ __forceinline__ char *tile(int slot, int tensor) const { return at + (slot * NT + tensor) * TOK * pitch; }
+    __device__ __forceinline__ char *tile(int slot, int tensor) const { return at + (slot * NT + tensor) * TOK * pitch(); }
     // A lane's two channels of its run's first token; the others follow, kScanChannels elements apart.
     __device__ __forceinline__ T *run(int slot, int tensor, int first, int l) const {
-        return (T *)(tile(slot, tensor) + first * pitch) + 2 * l;
+        return (T *)(tile(slot, tensor) + first * pitch()) + 2 * l;
     }
 
     // Every thread: asks for the tile from token `row` on, after the whole block is done with what
@@ -379,7 +382,7 @@ template <typename T, int L, int TOK, int NT, int DEPTH> struct Ring {
     // cycles; the warps take turns.
     __device__ __forceinline__ void ask(int slot, int turn, const CUtensorMap *const (&maps)[NT], const T *const (&src)[NT],
                                         int row, int lo, int hi, int c0, int D) {
-        if (mode == kBoxes) {
+        if constexpr (BOXES) {
             if (threadIdx.x == 32 * (turn % (TOK / (2 * L)))) {
                 sm100::mbar_arrive_expect_tx(&full[slot], NT * TOK * kRow);
 #pragma unroll
@@ -436,11 +439,11 @@ template <typename T, int L, int TOK, int NT, int DEPTH> struct Ring {
     }
     // Closes a step's asking (also one that asked for nothing): every step, once.
     __device__ __forceinline__ void close() {
-        if (mode != kBoxes) asm volatile("cp.async.commit_group;" ::: "memory");
+        if constexpr (!BOXES) asm volatile("cp.async.commit_group;" ::: "memory");
     }
     // Every thread: the slot's tile of `use` (its use'th) is there, or false where the wait ran out.
     __device__ __forceinline__ bool wait(int slot, int use, uint64_t limit_ns) {
-        if (mode == kBoxes)
+        if constexpr (BOXES)
             return limit_ns && sm100::mbar_try_wait(&full[slot], use & 1) ? true : wait_long(&full[slot], use & 1, limit_ns);
         asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
         __syncwarp();
@@ -483,7 +486,7 @@ template <typename T, int L, int TOK, int NT, int DEPTH> struct Ring {
     }
     // No copy of this block's is under way any more, also after a wait that ran out.
     __device__ __forceinline__ void drain(bool lost) {
-        if (mode != kBoxes)
+        if constexpr (!BOXES)
             asm volatile("cp.async.wait_group 0;" ::: "memory");
         else if (lost)
             for (int k = max(0, issued - DEPTH); k < issued; ++k)
@@ -595,10 +598,9 @@ using ScanRoom = std::atomic<int>[16][kScanSizes];   // by device
 
 #ifdef __CUDACC__
 // How many blocks, and clusters of 2, 4, 8 and 16 blocks, of a kernel run at a time on the current
-// device; the kernel's attributes are set (`most` bytes of shared memory in any of its modes), and this is
-// asked for, once per kernel, mode and device.
+// device; the kernel's attributes are set, and this is asked for, once per kernel and device.
 template <typename K>
-cudaError_t scan_room(K kern, int threads, int smem, int most, int sms, ScanRoom &known, int (&room)[kScanSizes]) {
+cudaError_t scan_room(K kern, int threads, int smem, int sms, ScanRoom &known, int (&room)[kScanSizes]) {
     int dev = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
@@ -607,7 +609,7 @@ cudaError_t scan_room(K kern, int threads, int smem, int most, int sms, ScanRoom
         for (int k = 0; k < kScanSizes; ++k) room[k] = known[dev][k].load(std::memory_order_relaxed);
         return cudaSuccess;
     }
-    if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most)) != cudaSuccess) return err;
+    if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem)) != cudaSuccess) return err;
     if ((err = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess) return err;
     int per_sm = 0;
     if ((err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, threads, smem)) != cudaSuccess) return err;
@@ -632,10 +634,10 @@ cudaError_t scan_room(K kern, int threads, int smem, int most, int sms, ScanRoom
 
 // One launch: the attributes, the division, the clusters.
 template <typename K, typename... A>
-cudaError_t scan_launch(K kern, ScanShape &s, int threads, int smem, int most, int tok, int sms,
+cudaError_t scan_launch(K kern, ScanShape &s, int threads, int smem, int tok, int sms,
                         ScanRoom &known, const char *name, cudaStream_t stream, A... args) {
     int room[kScanSizes];
-    cudaError_t err = scan_room(kern, threads, smem, most, sms, known, room);
+    cudaError_t err = scan_room(kern, threads, smem, sms, known, room);
     if (err != cudaSuccess) return err;
     scan_divide(s, room, tok);
     const int64_t blocks = (int64_t)s.tiles * s.parts * s.cluster;

@@ -26,13 +26,13 @@ constexpr int kWarps = kScanTile / (2 * kL);
 constexpr int kThreads = 32 * kWarps;
 constexpr int kBlocksPerSm = 2;
 constexpr int kDepth = 2;
-template <typename T> using BwdRing = Ring<T, kL, kScanTile, 3, kDepth>;
+template <typename T, bool BOXES> using BwdRing = Ring<T, kL, kScanTile, 3, kDepth, BOXES>;
 
 struct BwdMaps {
     CUtensorMap x, a, dout;
 };
 
-template <typename T, int GATE, int SRC>
+template <typename T, int GATE, int SRC, bool BOXES>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ BwdMaps maps, const T *x, const T *a, const T *dout, const float *__restrict__ h0,
                 const float *__restrict__ dhT, const float *__restrict__ states, T *dx, T *da, float *dh0,
@@ -58,7 +58,7 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
                 dh0[(int64_t)n * D + c0 + lane] = dhT ? dhT[(int64_t)n * D + c0 + lane] : 0.f;
     const int t0 = p0 / kScanTile, t1 = (p1 + kScanTile - 1) / kScanTile, steps = (t1 - t0 + CS - 1) / CS;
     const bool many = last - first > 1;
-    BwdRing<T> ring((char *)(((uintptr_t)smem + 127) & ~(uintptr_t)127), full, mode);
+    BwdRing<T, BOXES> ring((char *)(((uintptr_t)smem + 127) & ~(uintptr_t)127), full, mode);
     if (threadIdx.x == 0) {
         ring.init();
         sm100::mbar_init(&bars[0], 1);
@@ -98,7 +98,7 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
             cur.seek(s, first, last, max(base, p0));
             inner = cur.from < base && cur.to > base + kScanTile;
             if (!lost) lost = !__all_sync(kFull, ring.wait(slot, use, limit_ns));
-            if (mode == kRows) ring.move(slot, src, base, c0, D);
+            if (!BOXES && mode == kRows) ring.move(slot, src, base, c0, D);
         }
         const bool cuts = CS == 1 ? there && !inner : many || i == steps - 1;   // a part's first token is in the last step
         T *tx = ring.run(slot, 0, run_at0, l), *ta = ring.run(slot, 1, run_at0, l);
@@ -298,11 +298,15 @@ cudaError_t launch_bwd_t(const ScanBwd &t, ScanShape s, int sms, int *status, cu
     const uintptr_t outs = (uintptr_t)t.dx | (uintptr_t)t.da;
     const int mode = boxes ? kBoxes : sizeof(T) == 2 ? kRows : kPairs;
     const int pairs = s.D % 2 == 0 && outs % (2 * sizeof(T)) == 0;
-    static ScanRoom known[2];   // with rows, without
-    const int smem = BwdRing<T>::bytes(mode == kRows) + 128, most = BwdRing<T>::bytes(true) + 128;
-    return scan_launch(scan_bwd_kernel<T, GATE, SRC>, s, kThreads, smem, most, kScanTile, sms, known[mode != kRows], "scan_bwd_kernel", stream,
+    auto run = [&](auto by_boxes, ScanRoom &known) {
+        constexpr bool kB = by_boxes();
+        const int smem = BwdRing<T, kB>::bytes(mode == kRows) + 128;
+        return scan_launch(scan_bwd_kernel<T, GATE, SRC, kB>, s, kThreads, smem, kScanTile, sms, known, "scan_bwd_kernel", stream,
                        maps, (const T *)t.x, (const T *)t.a, (const T *)t.dout, t.h0, t.dhT, t.states, (T *)t.dx, (T *)t.da,
                        t.dh0, mode, pairs, scan_wait_ns(), status);
+    };
+    static ScanRoom boxed, other;
+    return mode == kBoxes ? run(std::true_type{}, boxed) : run(std::false_type{}, other);
 }
 
 }  // namespace

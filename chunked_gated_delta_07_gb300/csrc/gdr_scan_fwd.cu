@@ -21,13 +21,13 @@ constexpr int kTok = 2 * kL * kWarps;            // of a block's tile; divides 1
 constexpr int kThreads = 32 * kWarps;
 template <typename T> constexpr int kBlocksPerSm = sizeof(T) == 2 ? 4 : 3;
 constexpr int kDepth = 2;   // tiles in shared memory
-template <typename T> using FwdRing = Ring<T, kL, kTok, 2, kDepth>;
+template <typename T, bool BOXES> using FwdRing = Ring<T, kL, kTok, 2, kDepth, BOXES>;
 
 struct FwdMaps {
     CUtensorMap x, a;
 };
 
-template <typename T, int GATE, int SRC>
+template <typename T, int GATE, int SRC, bool BOXES>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm<T>)
 scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ FwdMaps maps, const T *x, const T *a, const float *h0, T *out, float *hT,
                 float *states, int mode, int pairs, uint64_t limit_ns, int *status) {
@@ -52,7 +52,7 @@ scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Fwd
                 hT[(int64_t)n * D + c0 + lane] = h0 ? h0[(int64_t)n * D + c0 + lane] : 0.f;
     const int t0 = p0 / kTok, t1 = (p1 + kTok - 1) / kTok, steps = (t1 - t0 + CS - 1) / CS;
     const bool many = last - first > 1;
-    FwdRing<T> ring((char *)(((uintptr_t)smem + 127) & ~(uintptr_t)127), full, mode);
+    FwdRing<T, BOXES> ring((char *)(((uintptr_t)smem + 127) & ~(uintptr_t)127), full, mode);
     if (threadIdx.x == 0) {
         ring.init();
         sm100::mbar_init(&bars[0], 1);
@@ -87,7 +87,7 @@ scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Fwd
             cur.seek(s, first, last, max(base, p0));
             inner = cur.from < base && cur.to > base + kTok;
             if (!lost) lost = !__all_sync(kFull, ring.wait(slot, use, limit_ns));
-            if (mode == kRows) ring.move(slot, src, base, c0, D);
+            if (!BOXES && mode == kRows) ring.move(slot, src, base, c0, D);
         }
         const bool cuts = CS == 1 ? there && !inner : many || i == 0;
         T *tx = ring.run(slot, 0, run_at0, l), *ta = ring.run(slot, 1, run_at0, l);
@@ -239,10 +239,14 @@ cudaError_t launch_fwd_t(const ScanFwd &t, ScanShape s, int sms, int *status, cu
     // fp32 channels by pairs: their rows leave room for fewer blocks
     const int mode = boxes ? kBoxes : sizeof(T) == 2 ? kRows : kPairs;
     const int pairs = s.D % 2 == 0 && (uintptr_t)t.out % (2 * sizeof(T)) == 0;
-    static ScanRoom known[2];   // with rows, without
-    const int smem = FwdRing<T>::bytes(mode == kRows) + 128, most = FwdRing<T>::bytes(true) + 128;
-    return scan_launch(scan_fwd_kernel<T, GATE, SRC>, s, kThreads, smem, most, kTok, sms, known[mode != kRows], "scan_fwd_kernel", stream, maps,
+    auto run = [&](auto by_boxes, ScanRoom &known) {
+        constexpr bool kB = by_boxes();
+        const int smem = FwdRing<T, kB>::bytes(mode == kRows) + 128;
+        return scan_launch(scan_fwd_kernel<T, GATE, SRC, kB>, s, kThreads, smem, kTok, sms, known, "scan_fwd_kernel", stream, maps,
                        (const T *)t.x, (const T *)t.a, t.h0, (T *)t.out, t.hT, t.states, mode, pairs, scan_wait_ns(), status);
+    };
+    static ScanRoom boxed, other;
+    return mode == kBoxes ? run(std::true_type{}, boxed) : run(std::false_type{}, other);
 }
 
 // One (sequence, channel) to a thread, the next token's inputs on their way while a token is
