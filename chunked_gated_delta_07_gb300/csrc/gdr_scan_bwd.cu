@@ -28,6 +28,11 @@ constexpr int kBlocksPerSm = 2;
 constexpr int kDepth = 2;
 template <typename T, bool BOXES> using BwdRing = Ring<T, kL, kScanTile, 3, kDepth, BOXES>;
 
+// Sequences that start with a run or end with it, and none within it.
+__device__ __forceinline__ bool plain_marks(const Marks &m) {
+    return !(m.first & ~1u) && !(m.last & ~(1u << (kL - 1)));
+}
+
 struct BwdMaps {
     CUtensorMap x, a, dout;
 };
@@ -104,13 +109,12 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
         T *tx = ring.run(slot, 0, run_at0, l), *ta = ring.run(slot, 1, run_at0, l);
         T *td = ring.run(slot, 2, run_at0, l);
         const int p = base + run_at0, lo = max(p, p0), hi = min(p + kL, p1);
-        Cursor mine = cur;
-        Marks m{0, 0};
         // l_t = S r + l0,  alpha h_{t-1} g' + w' x g' = c1 h + c0
         float2 w[kL], S[kL], l0[kL], k1[kL], k0[kL];
         float2 A = both(1.f), B = both(0.f), R = both(0.f);
-        bool plain = true;
         if (there) {
+            Cursor mine = cur;
+            Marks m{0, 0};
             if (!inner) {
                 m = marks_of(s, mine, first, last, p, lo, hi);
                 if (hi - lo < kL) {
@@ -161,8 +165,7 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
                 }
             };
             // a sequence that starts with the run or ends with it: what enters there is known
-            plain = !(m.first & ~1u) && !(m.last & ~(1u << (kL - 1)));
-            if (plain) {
+            if (plain_marks(m)) {
                 if (m.first) B = load_state(h0, mine.n, D, c);
                 if (m.last) R = load_state(dhT, seq_from(s, mine.n, p + kL - 1), D, c);
                 pass(std::false_type{});
@@ -226,12 +229,7 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
             chain(std::true_type{});
         else
             chain(std::false_type{});
-        // nothing enters past a first token, nor in front of a last one
-        if (plain && (m.first | m.last)) {
-            if (m.first) h = both(0.f);   // (k0 has what was there)
-            if (m.last) r = both(0.f);
-        }
-        if (there && c < D && pairs && plain && hi - lo == kL) {
+        auto put = [&] {   // a run of tokens that are all the part's, with pairs of channels
             char *ox = (char *)(dx + (int64_t)base * D) + lane_out, *oa = (char *)(da + (int64_t)base * D) + lane_out;
 #pragma unroll
             for (int j = 0; j < kL; ++j) {
@@ -241,35 +239,48 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
                 ox += D * (int)sizeof(T);
                 oa += D * (int)sizeof(T);
             }
-            if (dh0 && m.first) {
-                const Gate g = gate_of<kFine, GATE, SRC, false>(read2(ta, 0), s);
-                store_state(dh0, mine.n, D, c, mul2(g.alpha, fma2(S[0], r, l0[0])));
-            }
+        };
+        if (inner && pairs) {
+            if (c < D) put();
         } else if (there && c < D) {
-            const int from = m.first ? __ffs(m.first) - 1 : kL, upto = 31 - __clz(m.last);
-            int n = mine.n;
-#pragma unroll
-            for (int j = 0; j < kL; ++j) {
-                const int t = p + j;
-                if (t < lo || t >= hi) continue;
-                const float2 lam = j <= upto ? l0[j] : fma2(S[j], r, l0[j]);
-                const float2 gx = mul2(w[j], lam), ga = mul2(lam, j >= from ? k0[j] : fma2(k1[j], h, k0[j]));
-                T *ox = dx + (int64_t)t * D + c, *oa = da + (int64_t)t * D + c;
-                if (pairs) {
-                    write2(ox, gx);
-                    write2(oa, ga);
-                } else {
-                    ox[0] = from_f32<T>(gx.x);
-                    oa[0] = from_f32<T>(ga.x);
-                    if (c + 1 < D) {
-                        ox[1] = from_f32<T>(gx.y);
-                        oa[1] = from_f32<T>(ga.y);
-                    }
+            // (looked up again: what the steps above need not keep costs them no registers)
+            Cursor mine = cur;
+            const Marks m = inner ? Marks{0, 0} : marks_of(s, mine, first, last, p, lo, hi);
+            if (pairs && hi - lo == kL && plain_marks(m)) {
+                // nothing enters past a first token (k0 has what was there), nor in front of a last one
+                if (m.first) h = both(0.f);
+                if (m.last) r = both(0.f);
+                put();
+                if (dh0 && m.first) {
+                    const Gate g = gate_of<kFine, GATE, SRC, false>(read2(ta, 0), s);
+                    store_state(dh0, mine.n, D, c, mul2(g.alpha, fma2(S[0], r, l0[0])));
                 }
-                if (dh0 && (m.first >> j & 1)) {
-                    n = seq_from(s, n, t);
-                    const Gate g = gate_of<kFine, GATE, SRC, false>(read2(ta, j), s);
-                    store_state(dh0, n, D, c, mul2(g.alpha, lam));
+            } else {
+                const int from = m.first ? __ffs(m.first) - 1 : kL, upto = 31 - __clz(m.last);
+                int n = mine.n;
+    #pragma unroll
+                for (int j = 0; j < kL; ++j) {
+                    const int t = p + j;
+                    if (t < lo || t >= hi) continue;
+                    const float2 lam = j <= upto ? l0[j] : fma2(S[j], r, l0[j]);
+                    const float2 gx = mul2(w[j], lam), ga = mul2(lam, j >= from ? k0[j] : fma2(k1[j], h, k0[j]));
+                    T *ox = dx + (int64_t)t * D + c, *oa = da + (int64_t)t * D + c;
+                    if (pairs) {
+                        write2(ox, gx);
+                        write2(oa, ga);
+                    } else {
+                        ox[0] = from_f32<T>(gx.x);
+                        oa[0] = from_f32<T>(ga.x);
+                        if (c + 1 < D) {
+                            ox[1] = from_f32<T>(gx.y);
+                            oa[1] = from_f32<T>(ga.y);
+                        }
+                    }
+                    if (dh0 && (m.first >> j & 1)) {
+                        n = seq_from(s, n, t);
+                        const Gate g = gate_of<kFine, GATE, SRC, false>(read2(ta, j), s);
+                        store_state(dh0, n, D, c, mul2(g.alpha, lam));
+                    }
                 }
             }
         }
