@@ -615,7 +615,7 @@ def add_norm_fwd(x, residual, weight=None, bias=None, scale=1.0, kind="rms", eps
     if residual is None:
         raise ValueError("residual is required")
     rows, G, D = check_block_norm_inputs(x, weight, bias, kind=kind, residual=residual, out=out, sum_out=sum_out)
-    _require_cuda(x, "x")
+    _require_here(x)
     if out is None:
         out = torch.empty_like(x)
     if sum_out is None:
@@ -655,7 +655,7 @@ def add_norm_bwd(dy, r, rstd, mean=None, dr=None, weight=None, scale=1.0, kind="
     if per_head and r is not None and r.dim() < 2:
         raise ValueError("per_head: r must be [.., G, D]")
     rows, _, D = check_block_norm_inputs(r, weight, None, mean, rstd, kind, dy=dy, dr=dr)
-    _require_cuda(r, "r")
+    _require_here(r, "r")
     dw, db, G = _weight_grads(r, weight, per_head, want_dweight, want_dbias)
     dres = torch.empty_like(r)
     dx = torch.empty_like(r) if scale != 1.0 else None
@@ -679,7 +679,7 @@ def norm_gate_fwd(x, gate, weight=None, bias=None, residual=None, scale=1.0, kin
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
     rows, G, D = check_block_norm_inputs(x, weight, bias, kind=kind, gate=gate, residual=residual, out=out)
-    _require_cuda(x, "x")
+    _require_here(x)
     if out is None:
         out = torch.empty_like(x)
     mean, rstd = _norm_stats(x, kind, want_stats)
@@ -703,7 +703,7 @@ def norm_gate_bwd(dy, x, gate, rstd, mean=None, weight=None, bias=None, scale=1.
     if per_head and x is not None and x.dim() < 2:
         raise ValueError("per_head: x must be [.., G, D]")
     rows, G, D = check_block_norm_inputs(x, weight, bias, mean, rstd, kind, dy=dy, gate=gate)
-    _require_cuda(x, "x")
+    _require_here(x)
     dw, db, G = _weight_grads(x, weight if weight is not None else bias, per_head, want_dweight, want_dbias)
     dx, dz = torch.empty_like(x), torch.empty_like(x)
     rc = gdr_norm_gate_bwd(dy, x, gate, mean, rstd, weight, bias, dx, dz, dw, db, rows, G, D, scale, _KINDS[kind],
@@ -789,7 +789,7 @@ def gated_scan_fwd(x, a, h0=None, cu_seqlens=None, b=2.0, gate="bounded", source
     behind every 128th token of the B T tokens."""
     import torch
     T, D, N = check_scan_inputs(x, a, h0, cu_seqlens, out=out, hT=hT, states=states)
-    _require_cuda(x, "x")
+    _require_here(x)
     g, w = _scan_form(gate, source)
     if out is None:
         out = torch.empty_like(x)
@@ -812,7 +812,7 @@ def gated_scan_bwd(x, a, dout, dhT=None, h0=None, states=None, cu_seqlens=None, 
     if dout is None:
         raise ValueError("dout is required")
     T, D, N = check_scan_inputs(x, a, h0, cu_seqlens, dout=dout, dhT=dhT, states=states)
-    _require_cuda(x, "x")
+    _require_here(x)
     g, w = _scan_form(gate, source)
     dx, da = torch.empty_like(x), torch.empty_like(a)
     dh0 = torch.empty((N, D), dtype=torch.float32, device=x.device) if want_dh0 else None
@@ -830,7 +830,7 @@ def gated_scan_recurrent_fwd(x, a, state, b=2.0, gate="bounded", source="plain",
     if state is None:
         raise ValueError("state is required")
     T, D, N = check_scan_inputs(x, a, h0=state, out=out)
-    _require_cuda(x, "x")
+    _require_here(x)
     g, w = _scan_form(gate, source)
     if out is None:
         out = torch.empty_like(x)
@@ -930,6 +930,14 @@ def _expect(name, t, shape, dtype, device):
 def _require_cuda(t, name="q"):
     if not t.is_cuda:
         raise ValueError(f"{name} is on {t.device}: the library runs on CUDA devices only")
+
+
+def _require_here(t, name="x"):
+    """On a CUDA device, and the current one: a call runs on the current device's stream."""
+    import torch
+    _require_cuda(t, name)
+    if t.device.index != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}: not the current device")
 
 
 def check_sequence_inputs(q, k, v, a, beta, h0=None, cu_seqlens=None, per_channel=False,

@@ -14,7 +14,12 @@ namespace {
 
 using namespace norm;
 
-// Threads of a block, and of an SM.
+// Threads of a block, and of an SM, as registers allow: a row's 8 elements of three tensors, the
+// weights and both sums (524288 rows x 128 norm_gate: 512 threads an SM 131 us, 768 121, 1024 141 with
+// spills; 8191 rows x 2048 add_norm: 35, 35, 41).
+//
+// Measured (bf16): norm_gate 524288 x 128 with 16 weight rows 121 to 124 us, 5.5 TB/s, 82% of a copy's
+// rate; add_norm 8191 x 2048 35 us, 4.8 TB/s, 72% (8 us of it the sum of the partials).
 constexpr int kLeast = 256, kPerSm = 768;
 template <int TPR> constexpr int block_threads() { return TPR > kLeast ? TPR : kLeast; }
 template <int TPR> constexpr int block_per_sm() { return block_threads<TPR>() > kPerSm ? block_threads<TPR>() : kPerSm; }

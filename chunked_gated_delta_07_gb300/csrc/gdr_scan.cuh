@@ -70,9 +70,9 @@ constexpr unsigned kFull = 0xffffffffu;
 
 // ---- the gate ---------------------------------------------------------------------------
 // The special-function unit's accuracy, within a few 2^-23 of the value, also for fp32 tensors
-// (FINE), whose exponentials' arguments keep the rounding error of the product with log2 e: that
-// is |a| 2^-24 of the exponential, and the library function costs three times as much (8 x 2048
-// fp32 tokens 175 us, see below).  What a long memory hangs on, 1 - alpha for alpha near 1, keeps
+// (FINE), whose exponentials' arguments keep the rounding error of the product with log2 e, which
+// is |a| 2^-24 of the exponential (8 x 2048 fp32 tokens of 2048 channels forward 71 us; with the
+// library's exponentials, reciprocals and roots 175).  What a long memory hangs on, 1 - alpha for alpha near 1, keeps
 // its relative accuracy: 1 - e^-n comes from a polynomial, and alpha from that.
 constexpr float kLog2e = 1.44269504088896341f, kLog2eRest = 1.925963033500e-8f, kLn2 = 0.693147180559945f;
 // 2^x
@@ -295,7 +295,9 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;" ::: "memory");
     asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
 }
-// The blocks of a cluster tell each other their tile's run, every step: a row of 16 lanes' pairs
+// The blocks of a cluster tell each other their tile's run, every step (with the cluster's barrier
+// instead, whose release waits for the outputs' stores too, 262144 tokens took 932 us against 860 at
+// the time): a row of 16 lanes' pairs
 // into every peer's memory, each counted by the peer's barrier for the step (two of them taken in
 // turn; nobody can be two steps ahead, since a step needs everyone's).
 struct Peers {
@@ -343,7 +345,10 @@ struct Peers {
 // pieces that hold one of its channels, by a bulk copy; the lanes then move their run's channels to
 // where a box would have them.  PAIRS: a lane copies its own two channels (fp32).
 //
-// 8 x 4096 bf16 tokens forward: 2048 channels in boxes 96 us; FIGURES
+// 8 x 4096 bf16 tokens, forward and backward: 2048 channels in boxes 95 and 203 us, 2046 and 2047 in
+// rows 182 and 341, 233 and 439 (with bulk copies of whole rows 226 and 450, 277 and 545: the copy
+// unit takes some 16 cycles a row; element by element 2047 channels 690 and 1200).  8 x 2048 fp32
+// tokens of 2047 channels: pairs 193 and 295, rows 179 and 388 (fewer blocks fit).
 enum CopyMode { kBoxes, kRows, kPairs };
 __device__ __forceinline__ void copy4(unsigned dst, const void *src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");

@@ -521,12 +521,13 @@ typedef enum {
  *              the token axis (all B T tokens one after the other), which the backward pass
  *              starts from.  total / 128 is rounded down.
  *   b          bound of the bounded gate, > 0 and finite (not looked at for softplus)
- * D >= 1; B >= 1; T >= 0; at most 2^31 - 2304 tokens in all and 2^40 elements; sequences of no
+ * 1 <= D <= 2^22; B >= 1; T >= 0; at most 2^31 - 4097 tokens in all and 2^40 elements; sequences of no
  * tokens pass h0 on to hT.  Element alignment is enough (16-byte pointers with D a multiple of
  * 16 bytes are read fastest).  fp32 inside.  A NaN or an infinity stays in its channel's state
  * to the end of the sequence (an infinity may become a NaN); other channels and sequences
  * never see it.  Outputs must not overlap inputs.  Bad offsets: GDR_ERR_BAD_SEQLENS in the
- * status word, nothing is written.  No scratch; asynchronous on `stream`; deterministic.
+ * status word, nothing is written; waits are bounded (GDR_ERR_TIMEOUT).  No scratch; asynchronous
+ * on `stream`; deterministic.
  */
 GDR_API gdr_status_t gdr_gated_scan_fwd(const void *x, const void *a, const float *h0, void *out, float *hT,
                                 float *states, const int32_t *cu_seqlens, int B, int64_t T, int D, float b,

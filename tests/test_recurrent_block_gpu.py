@@ -111,3 +111,13 @@ def test_the_example_runs():
     losses = ex.train([ex.RecurrentBlock() for _ in range(2)], steps=3, batch=2, tokens=130)
     assert len(losses) == 3 and all(v == v and v < float("inf") for v in losses)
     assert gdr.gdr_get_status() == gdr.GDR_OK
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    x, h, w = torch.zeros(1, 4, 8, device="cuda"), torch.zeros(1, 8, device="cuda"), torch.ones(1, 4, device="cuda")
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 1)
+    for call in (lambda: gdr.gated_scan_fwd(x, x), lambda: gdr.gated_scan_bwd(x, x, x),
+                 lambda: gdr.gated_scan_recurrent_fwd(x, x, h), lambda: gdr.add_norm_fwd(x, x),
+                 lambda: gdr.add_norm_bwd(x, x, w), lambda: gdr.norm_gate_fwd(x, x), lambda: gdr.norm_gate_bwd(x, x, x, w)):
+        with pytest.raises(ValueError, match="current"):
+            call()

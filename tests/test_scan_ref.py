@@ -63,7 +63,8 @@ def step(**kw):
 
 COMMON = [(dict(T=-1), INV), (dict(D=0), INV), (dict(b=0.0), INV), (dict(b=float("nan")), INV), (dict(b=float("inf")), INV),
           (dict(dtype=5), INV), (dict(gate=2), INV), (dict(source=3), INV), (dict(x=None), INV), (dict(a=None), INV),
-          (dict(T=1 << 31), UNS), (dict(T=1 << 30, D=1 << 11), UNS)]
+          (dict(T=1 << 31), UNS), (dict(T=1 << 30, D=1 << 11), UNS),
+          (dict(T=(1 << 31) - 4096), UNS), (dict(D=(1 << 22) + 1), UNS)]
 
 
 @pytest.mark.parametrize("kw,code", COMMON + [
