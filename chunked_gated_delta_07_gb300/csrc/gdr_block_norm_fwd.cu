@@ -146,9 +146,10 @@ block_norm_fwd_kernel(const T *x, const T *z, const T *res, const float *__restr
 template <typename T, bool GATE, bool RES>
 cudaError_t fwd_t(const void *x, const void *z, const void *res, const float *w, const float *b, void *sum, void *y,
                   float *mean, float *rstd, const BlockNorm &bn, int sms, cudaStream_t stream) {
-    const NormPick p = pick_layout(bn.D, sizeof(T), in_pieces(bn.D, sizeof(T), {x, z, res, sum, y}));
+    const bool pieces = in_pieces(bn.D, sizeof(T), {x, z, res, sum, y});
+    const NormPick p = GATE ? pick_block(bn.D, sizeof(T), pieces) : pick_layout(bn.D, sizeof(T), pieces);
     const NormGrid n = norm_grid(p, bn.rows, bn.G, bn.D, bn.eps, sms, 256);
-    return with_layout<T>(p, [&](auto tpr, auto nv, auto vec) {
+    return with_layout<T, true>(p, [&](auto tpr, auto nv, auto vec) {
         auto kern = block_norm_fwd_kernel<T, tpr(), nv(), vec(), GATE, RES>;
         constexpr int kTensors = 1 + GATE + RES;
         const int smem = vec() > 1 ? kTensors * ring_depth<nv(), kTensors>() * n.threads * 16 * nv() : 0;

@@ -234,8 +234,9 @@ inline NormGrid norm_grid(const NormPick &p, int64_t rows, int G, int D, float e
     return o;
 }
 
-// Calls f with the layout as compile-time constants.
-template <typename T, typename F> cudaError_t with_layout(const NormPick &p, F &&f) {
+// Calls f with the layout as compile-time constants (WIDE: single elements, 8 to each of 1024 threads,
+// too).
+template <typename T, bool WIDE = false, typename F> cudaError_t with_layout(const NormPick &p, F &&f) {
     constexpr int V = 16 / sizeof(T);
     using std::integral_constant;
 #define GDR_NORM_CASE(TPR_, NV_, VEC_)                                                             \
@@ -256,6 +257,7 @@ template <typename T, typename F> cudaError_t with_layout(const NormPick &p, F &
     GDR_NORM_CASE(128, 8, 1)
     GDR_NORM_CASE(512, 8, 1)
     GDR_NORM_CASE(512, 16, 1)
+    if constexpr (WIDE) { GDR_NORM_CASE(1024, 8, 1) }
     GDR_NORM_CASE(1024, 16, 1)
 #undef GDR_NORM_CASE
     return cudaErrorInvalidValue;
