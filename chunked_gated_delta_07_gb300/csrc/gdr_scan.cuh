@@ -223,6 +223,37 @@ struct Cursor {
     }
 };
 
+// The sequence of token t, going up from n, or down: steps that double while they stay on n's side of
+// it and halve where they would not, so that any number of sequences without tokens in between costs
+// its logarithm in loads (5 to 900 tokens between three times 20000 empty ones: 3.1 ms forward and 4.9
+// backward with steps of one).
+__device__ __forceinline__ int seq_from(const ScanShape &s, int n, int t) {
+    int step = 1;
+    while (seq_start(s, n + 1) <= t) {
+        const int m = n + min(step, s.N - n);
+        if (seq_start(s, m) <= t) {
+            n = m;
+            step += step;
+        } else {
+            step = (step + 1) >> 1;
+        }
+    }
+    return n;
+}
+__device__ __forceinline__ int seq_back(const ScanShape &s, int n, int t) {
+    int step = 1;
+    while (seq_start(s, n) > t) {
+        const int m = n - min(step, n);
+        if (step == 1 || seq_start(s, m) > t) {
+            n = m;
+            step += step;
+        } else {
+            step >>= 1;
+        }
+    }
+    return n;
+}
+
 // First and last tokens of sequences among the L tokens from p, as bits; [lo, hi) are those
 // of them that belong to the part.
 struct Marks {
@@ -238,18 +269,11 @@ __device__ __forceinline__ Marks marks_of(const ScanShape &s, Cursor &c, int fro
         m.last |= 1u << (q - 1 - p);
         if (q == hi) break;
         m.first |= 1u << (q - p);
-        const int at = q;
-        do q = seq_start(s, ++n);   // past empty sequences; the part's end is beyond `at`
-        while (q <= at);
+        n = seq_from(s, n, q) + 1;   // past empty sequences; the part's end is beyond q
+        q = seq_start(s, n);
     }
     return m;
 }
-// The sequence of token t, going up from n.
-__device__ __forceinline__ int seq_from(const ScanShape &s, int n, int t) {
-    while (seq_start(s, n + 1) <= t) ++n;
-    return n;
-}
-
 // Whether the offsets are 0 = c0 <= c1 <= .. <= cN = total; the whole block calls.
 __device__ __forceinline__ bool offsets_ok(const ScanShape &s) {
     if (!s.cu) return true;

@@ -158,7 +158,7 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
                 for (int j = kL - 1; j >= 0; --j) {
                     float2 d = read2(td, j);
                     if (marked && (m.last >> j & 1)) {
-                        while (seq_start(s, n) > p + j) --n;
+                        n = seq_back(s, n, p + j);
                         d = add2(d, load_state(dhT, n, D, c));
                         R = both(0.f);
                     }

@@ -169,6 +169,31 @@ def test_many_tiles(lens, D):
     check(inputs(lens, D, "bf16", 11), "bf16", source="variance")
 
 
+@pytest.mark.parametrize("dtype,D", [("bf16", 40), ("f32", 33)])
+def test_very_many_empty_sequences(dtype, D):
+    """What holds tokens is as without them, bit for bit, and an empty sequence passes its state on."""
+    lens, at = [], []
+    for n, gap in ((5, 50000), (300, 3), (1, 70001), (2, 1), (900, 30000), (129, 2), (7, 9000)):
+        at.append(len(lens))
+        lens += [n] + [0] * gap
+    i = inputs(lens, D, dtype, 21)
+    full = {k: i[k] for k in ("h0", "dhT")}
+    cu = torch.tensor(np.concatenate([[0], np.cumsum([lens[n] for n in at])]), dtype=torch.int32, device="cuda")
+    rows = torch.tensor(at, device="cuda")
+    few = {k: v[rows].contiguous() for k, v in full.items()}
+    res = []
+    for c, st in ((cu, few), (i["cu"], full)):
+        out, hT, kept = gdr.gated_scan_fwd(i["x"], i["a"], h0=st["h0"], cu_seqlens=c, want_states=True, source="variance")
+        res.append((out, hT, kept) + gdr.gated_scan_bwd(i["x"], i["a"], i["dout"], st["dhT"], st["h0"], kept, c, source="variance"))
+    ok()
+    (out, hT, kept, dx, da, dh0), (out2, hT2, kept2, dx2, da2, dh02) = res
+    for p, q in ((out, out2), (kept, kept2), (dx, dx2), (da, da2), (hT, hT2[rows]), (dh0, dh02[rows])):
+        assert torch.equal(p, q)
+    empty = torch.ones(len(lens), dtype=torch.bool, device="cuda")
+    empty[rows] = False
+    assert torch.equal(hT2[empty], full["h0"][empty]) and torch.equal(dh02[empty], full["dhT"][empty])
+
+
 def test_long_memory():
     """Decays of 1 - 1e-4 to 1 - 1e-7, fp32 states: the decay keeps the relative accuracy of 1 - alpha.
     Inputs of one sign, so that an error of the decay does not average out."""
