@@ -362,6 +362,13 @@ struct Peers {
             if (done()) return true;
         return false;
     }
+    // After a wait that ran out: what peers have told is not all counted, and the cluster's barrier does
+    // not wait for such stores; a millisecond is a thousand times their way.  (With no wait run out
+    // every store has been counted, by the last step's wait.)
+    __device__ __forceinline__ static void settle() {
+        const uint64_t since = sm100::globaltimer_ns();
+        while (sm100::globaltimer_ns() - since < 1000000) {}
+    }
 };
 
 // ---- tiles of raw inputs ------------------------------------------------------------------
