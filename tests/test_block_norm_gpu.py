@@ -267,3 +267,63 @@ def test_workspaces_streams_and_graphs():
     want = call(i, r)
     ok()
     assert all(torch.equal(u, v) for u, v in zip(got[:3], want[:3]))
+
+
+def test_forward_on_streams_and_captured():
+    sets = [inputs((700 + n, D), False, "bf16", n) for n, D in enumerate((256, 250, 2048))]
+    call = lambda i: gdr.add_norm_fwd(i["x"], i["res"], i["w"], i["b"], kind="layer") + \
+        gdr.norm_gate_fwd(i["x"], i["z"], i["w"], residual=i["res"])[::2]  # noqa: E731
+    want = [call(i) for i in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        got = []
+        for i, st in zip(sets, streams):
+            with torch.cuda.stream(st):
+                got.append(call(i))
+        torch.cuda.synchronize()
+        for p, q in zip(want, got):
+            assert all(torch.equal(u, v) for u, v in zip(p, q))
+    i = {k: torch.zeros_like(v) for k, v in sets[1].items()}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call(i)
+    for k, v in sets[1].items():
+        i[k].copy_(v)
+    graph.replay()
+    ok()
+    assert all(torch.equal(u, v) for u, v in zip(got, want[1]))
+
+
+@pytest.mark.parametrize("D", [2048, 1001])
+def test_offsets_beyond_32_bits(D):
+    """More than 2^31 elements: the first and the last rows, and what lies around the outputs left alone."""
+    rows = (1 << 31) // D + 300
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    x, z, dy = (torch.empty(rows, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(3))
+    w = torch.randn(D, generator=gen, device="cuda")
+    flat = torch.full(((rows + 2) * D,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = flat[D:-D].view(rows, D)
+    y, _, rstd = gdr.norm_gate_fwd(x, z, w, out=out)
+    assert (flat[:D] == 7).all() and (flat[-D:] == 7).all()
+    dx, dz, _, _ = gdr.norm_gate_bwd(dy, x, z, rstd, weight=w)
+    ok()
+    for part in (slice(0, 50), slice(rows - 50, rows)):
+        f = lambda t: d(t[part])  # noqa: E731
+        close(y[part], ref.gate(f(x), f(z), d(w), None, None, 1.0, "rms", "silu", 1e-5), BOUND16, "y")
+        s = ref.stats(f(x), "rms", 1e-5)
+        want = ref.gate_back(f(dy), f(x), f(z), *s, d(w), None, 1.0, "rms", "silu", w.shape)
+        close(dx[part], want[0], BOUND16, "dx")
+        close(dz[part], want[1], BOUND16, "dgate")
+    del dx, dz
+    y, r, _, rstd = gdr.add_norm_fwd(x, z, w, scale=0.5)
+    dx, dres, _, _ = gdr.add_norm_bwd(dy, r, rstd, weight=w, scale=0.5)
+    ok()
+    for part in (slice(0, 50), slice(rows - 50, rows)):
+        f = lambda t: d(t[part])  # noqa: E731
+        close(r[part], f(z) + 0.5 * f(x), BOUND16, "r")
+        m, s = ref.stats(f(r), "rms", 1e-5)
+        close(y[part], ref.norm(f(r), d(w), None, "rms", 1e-5), BOUND16, "y")
+        want = ref.add_back(f(dy), None, f(r), m, s, d(w), 0.5, "rms", w.shape)
+        close(dx[part], want[0], BOUND16, "dx")
+        close(dres[part], want[1], BOUND16, "dresidual")

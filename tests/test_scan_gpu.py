@@ -392,3 +392,77 @@ def test_long(B, T, D):
         h = torch.addcmul(u[:, t], alpha[:, t], h, out=u[:, t])
     close(out, u.cpu(), BOUND32, "out")
     close(hT, h.cpu(), BOUND32, "hT")
+
+
+@pytest.mark.parametrize("D", [65536, 65537])
+def test_offsets_beyond_32_bits(D):
+    """More than 2^31 elements: the first and the last channels, in 64 bits, and rows behind the tokens left alone."""
+    T = 33000
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x, a, dout = (torch.empty(1, T, D, dtype=torch.bfloat16, device="cuda").normal_(generator=gen) for _ in range(3))
+    flat = torch.full(((T + 2) * D,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = flat[D:-D].view(1, T, D)
+    h0, dhT = (torch.randn(1, D, generator=gen, device="cuda") for _ in range(2))
+    _, hT, states = gdr.gated_scan_fwd(x, a, h0=h0, out=out, want_states=True, source="convex")
+    dx, da, dh0 = gdr.gated_scan_bwd(x, a, dout, dhT, h0, states, source="convex")
+    ok()
+    assert (flat[:D] == 7).all() and (flat[-D:] == 7).all()
+    for cols in (slice(0, 2), slice(D - 3, D)):
+        one = lambda t: t[..., cols].reshape(-1, t[..., cols].shape[-1])  # noqa: E731
+        form = dict(b=2.0, gate="bounded", source="convex")
+        h, last = ref.forward(one(x), one(a), one(h0), [T], **form)
+        close(one(out), h, BOUND16, "out")
+        close(one(hT), last, BOUND32, "hT")
+        close(one(states), h[127::128], BOUND32, "states")
+        gx, ga, g0 = ref.backward(one(x), one(a), one(h0), one(dout), one(dhT), [T], **form)
+        close(one(dx), gx, BOUND16, "dx")
+        close(one(da), ga, BOUND16, "da")
+        close(one(dh0), g0, BOUND32, "dh0")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_the_most_channels(dtype):
+    """2^22 channels, one more refused."""
+    D, T = 1 << 22, 130
+    i = inputs([T], D, dtype, 3, packed=False)
+    out, hT, states = gdr.gated_scan_fwd(i["x"], i["a"], h0=i["h0"], want_states=True)
+    dx, da, dh0 = gdr.gated_scan_bwd(i["x"], i["a"], i["dout"], i["dhT"], i["h0"], states)
+    ok()
+    for cols in (slice(0, 33), slice(D - 33, D)):
+        one = lambda t: t[..., cols].reshape(-1, 33)  # noqa: E731
+        form = dict(b=2.0, gate="bounded", source="plain")
+        h, last = ref.forward(one(i["x"]), one(i["a"]), one(i["h0"]), [T], **form)
+        tol = BOUND16 if dtype == "bf16" else BOUND32
+        close(one(out), h, tol, "out")
+        close(one(hT), last, BOUND32, "hT")
+        gx, ga, g0 = ref.backward(one(i["x"]), one(i["a"]), one(i["h0"]), one(i["dout"]), one(i["dhT"]), [T], **form)
+        close(one(dx), gx, tol, "dx")
+        close(one(da), ga, tol, "da")
+        close(one(dh0), g0, BOUND32, "dh0")
+    x = torch.zeros(1, 1, D + 1, device="cuda")
+    with pytest.raises(gdr.GdrError) as e:
+        gdr.gated_scan_fwd(x, x)
+    assert e.value.code == gdr.GDR_ERR_UNSUPPORTED
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 63), ("f32", 63), ("f32", 64)])
+def test_captured_forms(dtype, D):
+    """Rows and pairs, with the states kept, and single tokens behind the prompt, in one graph."""
+    i, other = inputs([900, 0, 150], D, dtype, 8), inputs([900, 0, 150], D, dtype, 9)
+    tok = [torch.randn(3, 1, D, device="cuda").to(DT[dtype]) for _ in range(2)]
+
+    def step(i):
+        out, hT, states = gdr.gated_scan_fwd(i["x"], i["a"], h0=i["h0"], cu_seqlens=i["cu"], want_states=True)
+        grads = gdr.gated_scan_bwd(i["x"], i["a"], i["dout"], i["dhT"], i["h0"], states, i["cu"])
+        return (out, hT.clone(), states, gdr.gated_scan_recurrent_fwd(*tok, hT), hT) + grads
+
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step(i)
+    for k in ("x", "a", "dout", "h0", "dhT"):
+        i[k].copy_(other[k])
+    for _ in range(2):
+        graph.replay()
+    want = step(other)
+    ok()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
