@@ -225,8 +225,8 @@ struct Cursor {
 
 // The sequence of token t, going up from n, or down: steps that double while they stay on n's side of
 // it and halve where they would not, so that any number of sequences without tokens in between costs
-// its logarithm in loads (5 to 900 tokens between three times 20000 empty ones: 3.1 ms forward and 4.9
-// backward with steps of one).
+// its logarithm in loads (four sequences with three times 20000 empty ones between them: 435 us forward
+// and 263 backward; with steps of one 3109 and 4948).
 __device__ __forceinline__ int seq_from(const ScanShape &s, int n, int t) {
     int step = 1;
     while (seq_start(s, n + 1) <= t) {
@@ -376,10 +376,10 @@ struct Peers {
 // pieces that hold one of its channels, by a bulk copy; the lanes then move their run's channels to
 // where a box would have them.  PAIRS: a lane copies its own two channels (fp32).
 //
-// 8 x 4096 bf16 tokens, forward and backward: 2048 channels in boxes 95 and 203 us, 2046 and 2047 in
-// rows 182 and 341, 233 and 439 (with bulk copies of whole rows 226 and 450, 277 and 545: the copy
+// 8 x 4096 bf16 tokens, forward and backward: 2048 channels in boxes 95 and 207 us, 2046 and 2047 in
+// rows 181 and 342, 235 and 445 (with bulk copies of whole rows 226 and 450, 277 and 545: the copy
 // unit takes some 16 cycles a row; element by element 2047 channels 690 and 1200).  8 x 2048 fp32
-// tokens of 2047 channels: pairs 193 and 295, rows 179 and 388 (fewer blocks fit).
+// tokens of 2047 channels: pairs 204 and 293, rows, at the time, 179 and 388 (fewer blocks fit).
 enum CopyMode { kBoxes, kRows, kPairs };
 __device__ __forceinline__ void copy4(unsigned dst, const void *src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
