@@ -175,7 +175,7 @@ template <typename T, bool GATE, bool THREE>
 cudaError_t bwd_t(const void *dy, const void *val, const void *third, const float *mean, const float *rstd, const float *w,
                   const float *b, void *dx, void *dother, float *dw, float *db, const BlockNorm &bn, int sms, float *scratch,
                   cudaStream_t stream) {
-    const NormPick p = pick_block(bn.D, sizeof(T), in_pieces(bn.D, sizeof(T), {dy, val, third, dx, dother}));
+    const NormPick p = pick_block(bn.D, sizeof(T), in_pieces(bn.D, sizeof(T), {dy, val, third, dx, dother}), true);
     const NormGrid n = norm_grid(p, bn.rows, bn.G, bn.D, 0.f, sms, kLeast, kPerSm);
     float *part = dw || db ? scratch : nullptr;
     const cudaError_t err = with_layout<T, true>(p, [&](auto tpr, auto nv, auto vec) {
@@ -203,7 +203,7 @@ size_t block_norm_bwd_scratch_bytes(int64_t rows, int G, int D, gdr_dtype_t dtyp
     size_t need = 0;   // whichever layout the pointers' alignment allows
     for (bool pieces : {true, false})
         need = std::max(need, sizeof(float) * 2 * (size_t)G * D *
-                                  norm_grid(pick_block(D, es, pieces), rows, G, D, 0.f, sms, kLeast, kPerSm).grid.y);
+                                  norm_grid(pick_block(D, es, pieces, true), rows, G, D, 0.f, sms, kLeast, kPerSm).grid.y);
     return need;
 }
 

@@ -147,7 +147,7 @@ template <typename T, bool GATE, bool RES>
 cudaError_t fwd_t(const void *x, const void *z, const void *res, const float *w, const float *b, void *sum, void *y,
                   float *mean, float *rstd, const BlockNorm &bn, int sms, cudaStream_t stream) {
     const bool pieces = in_pieces(bn.D, sizeof(T), {x, z, res, sum, y});
-    const NormPick p = GATE ? pick_block(bn.D, sizeof(T), pieces) : pick_layout(bn.D, sizeof(T), pieces);
+    const NormPick p = pick_block(bn.D, sizeof(T), pieces, GATE);
     const NormGrid n = norm_grid(p, bn.rows, bn.G, bn.D, bn.eps, sms, 256);
     return with_layout<T, true>(p, [&](auto tpr, auto nv, auto vec) {
         auto kern = block_norm_fwd_kernel<T, tpr(), nv(), vec(), GATE, RES>;

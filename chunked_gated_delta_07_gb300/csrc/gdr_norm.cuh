@@ -234,8 +234,8 @@ inline NormGrid norm_grid(const NormPick &p, int64_t rows, int G, int D, float e
     return o;
 }
 
-// Calls f with the layout as compile-time constants (WIDE: single elements, 8 to each of 1024 threads,
-// too).
+// Calls f with the layout as compile-time constants (WIDE: single elements also 8 to each of 16, 64, 256
+// or 1024 threads).
 template <typename T, bool WIDE = false, typename F> cudaError_t with_layout(const NormPick &p, F &&f) {
     constexpr int V = 16 / sizeof(T);
     using std::integral_constant;
@@ -257,7 +257,12 @@ template <typename T, bool WIDE = false, typename F> cudaError_t with_layout(con
     GDR_NORM_CASE(128, 8, 1)
     GDR_NORM_CASE(512, 8, 1)
     GDR_NORM_CASE(512, 16, 1)
-    if constexpr (WIDE) { GDR_NORM_CASE(1024, 8, 1) }
+    if constexpr (WIDE) {
+        GDR_NORM_CASE(16, 8, 1)
+        GDR_NORM_CASE(64, 8, 1)
+        GDR_NORM_CASE(256, 8, 1)
+        GDR_NORM_CASE(1024, 8, 1)
+    }
     GDR_NORM_CASE(1024, 16, 1)
 #undef GDR_NORM_CASE
     return cudaErrorInvalidValue;

@@ -327,3 +327,13 @@ def test_offsets_beyond_32_bits(D):
         want = ref.add_back(f(dy), None, f(r), m, s, d(w), 0.5, "rms", w.shape)
         close(dx[part], want[0], BOUND16, "dx")
         close(dres[part], want[1], BOUND16, "dresidual")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("shape", [(900, 65), (700, 127), (301, 501), (150, 1025), (260, 2047), (90, 4095), (41, 6001)])
+def test_odd_widths(shape, dtype):
+    """Single elements, every number of threads to a row."""
+    i = inputs(shape, False, dtype, sum(shape))
+    check_add(i, dtype, "layer", 0.5)
+    check_gate(i, dtype, "rms", "silu", 0.5)
+    check_gate(inputs((shape[0] // 5 + 1, 3, shape[1]), True, dtype, 1), dtype, "layer", "sigmoid", 1.0)
