@@ -40,7 +40,7 @@ namespace norm {
 // add_norm 175 -> 66 us, its backward 147 -> 86, norm_gate 140 -> 77, its backward 169 -> 107), and,
 // where `wide` says so, rows of 4097 to 8192 to 1024 threads: three tensors' 16 elements do not fit
 // into a thread (8192 rows x 4097 bf16: norm_gate 157 -> 147 us, its backward 373 -> 292, add_norm's
-// 287 -> 235; add_norm itself 87 -> 121, which keeps 512).
+// 287 -> 245; add_norm itself 87 -> 121, which keeps 512).
 inline NormPick pick_block(int D, size_t es, bool pieces, bool wide) {
     if (!pieces && D <= 4096) {
         int tpr = 8;

@@ -90,7 +90,7 @@ block_norm_bwd_kernel(const T *dy, const T *val, const T *third, const float *__
         slot = slot == kDepth - 1 ? 0 : slot + 1;
         // dy is 0 where there is no row or column, so that nothing there counts
         V xv[NV][kP], dv[NV][kP], sum0 = P::of(0.f), sum1 = P::of(0.f);   // of n, of n vh
-        const V rs2 = P::of(rs), off = P::of(-mu * rs);
+        const V rs2 = P::of(rs), off = P::of(-mu);   // the mean comes off first: x rs - mu rs would round mu rs
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
             const int c = (v * TPR + p.lane) * VEC;
@@ -101,7 +101,7 @@ block_norm_bwd_kernel(const T *dy, const T *val, const T *third, const float *__
             if constexpr (GATE) widen<T, VEC>(rt[v], ze);
 #pragma unroll
             for (int i = 0; i < kP; ++i) {
-                const V xh = fma2(P::at(xe, i), rs2, off);
+                const V xh = mul2(add2(P::at(xe, i), off), rs2);
                 V d = P::at(de, i);
                 if constexpr (GATE) {
                     const V z = P::at(ze, i), g = sigmoid_of<sizeof(T) == 4>(z), n = fma2(xh, wv[v][i], bv[v][i]);
