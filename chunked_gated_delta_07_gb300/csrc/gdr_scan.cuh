@@ -35,8 +35,11 @@ constexpr int kScanMaxCluster = 16;
 constexpr int kScanMaxD = 1 << 22;  // a tile's offsets are 32-bit
 constexpr int64_t kScanMaxTokens = 0x7fffffff - 2 * kScanTile * kScanMaxCluster;   // positions are 32-bit
 
-// The gates as the kernels tell them apart: a bound of at most 2 leaves alpha >= e^-2, which one
-// polynomial gives.
+// The gates as the kernels tell them apart.  With a bound of at most 2, alpha >= e^-2, bf16 tensors take
+// 1 - alpha from one polynomial (8 x 4096 tokens of 2048 channels forward 95 us, with an exponential beside
+// it 107).  What 1 - alpha is off by counts 1 / alpha times in alpha: up to 21 * 2^-24 of it at b = 2 and s = 1,
+// where a memory is of a token, 4 * 2^-24 at b = 1 (emulated with an exact sigmoid s).  fp32 tensors take the
+// exponential at any bound (8 x 2048 tokens forward 74 us, by that polynomial 70).
 enum ScanGate { kBounded = GDR_GATE_BOUNDED, kSoftplus = GDR_GATE_SOFTPLUS, kBoundedBy2 };
 constexpr int kScanPoly = 8;
 
@@ -69,11 +72,12 @@ namespace scan {
 constexpr unsigned kFull = 0xffffffffu;
 
 // ---- the gate ---------------------------------------------------------------------------
-// The special-function unit's accuracy, within a few 2^-23 of the value, also for fp32 tensors
-// (FINE), whose exponentials' arguments keep the rounding error of the product with log2 e, which
-// is |a| 2^-24 of the exponential (8 x 2048 fp32 tokens of 2048 channels forward 71 us; with the
-// library's exponentials, reciprocals and roots 175).  What a long memory hangs on, 1 - alpha for alpha near 1, keeps
-// its relative accuracy: 1 - e^-n comes from a polynomial, and alpha from that.
+// The special-function unit's accuracy, also for fp32 tensors (FINE), whose exponentials' arguments keep
+// the rounding error of the product with log2 e, which is |a| 2^-24 of the exponential (8 x 2048 fp32
+// tokens of 2048 channels, bound 8, forward 76 us; bound 2 with the library's exponentials, reciprocals and
+// roots 175).  alpha of fp32 tensors is off by at most (n (1.25 (1 - s) + 1) + 1.75) 2^-22 of itself, n = b s; with
+// bounds of at most 2 that holds without the argument's error, which is n 2^-23.  What a long memory hangs on,
+// 1 - alpha for alpha near 1, keeps its relative accuracy: 1 - e^-n comes from a polynomial, and alpha from that.
 constexpr float kLog2e = 1.44269504088896341f, kLog2eRest = 1.925963033500e-8f, kLn2 = 0.693147180559945f;
 // 2^x
 __device__ __forceinline__ float2 exp2_fast(float2 x) {
@@ -116,7 +120,7 @@ __device__ __forceinline__ Gate gate_of(float2 a, const ScanShape &shape) {
     float2 left;   // 1 - alpha
     const float2 one = both(1.f), minus = both(-1.f);
     const float b = shape.b;
-    if constexpr (GATE == kBoundedBy2) {
+    if constexpr (GATE == kBoundedBy2 && !FINE) {
         const float2 e = exp_minus<FINE>(a), s = inverse(add2(e, one));
         if constexpr (GRAD) {
             const float2 c = make_float2(min_nan(e.x, 1e38f), min_nan(e.y, 1e38f));
@@ -128,7 +132,7 @@ __device__ __forceinline__ Gate gate_of(float2 a, const ScanShape &shape) {
             p = make_float2(fmaf(p.x, s.x, shape.poly[k].x), fmaf(p.y, s.y, shape.poly[k].x));
         left = mul2(s, p);
         o.alpha = fma2(left, minus, one);
-    } else if constexpr (GATE == kBounded) {
+    } else if constexpr (GATE != kSoftplus) {
         // e^-a may be inf: the sigmoid is 0 then
         const float2 e = exp_minus<FINE>(a), s = inverse(add2(e, one));
         const float2 n = mul2(s, both(b));   // -g
@@ -146,7 +150,7 @@ __device__ __forceinline__ Gate gate_of(float2 a, const ScanShape &shape) {
         p = fma2(p, n, both(-0.49999985098838806f));
         p = fma2(p, n, one);
         const float2 near = mul2(n, p), above = fma2(near, minus, one);
-        const float2 far = FINE ? exp_minus<FINE>(n) : exp2_fast(mul2(s, both(-b * kLog2e)));
+        const float2 far = FINE && GATE == kBounded ? exp_minus<FINE>(n) : exp2_fast(mul2(s, both(-b * kLog2e)));
         const float2 below = fma2(far, minus, one);
         const bool s0 = n.x < 0.5f, s1 = n.y < 0.5f;
         left = make_float2(s0 ? near.x : below.x, s1 ? near.y : below.y);
@@ -379,7 +383,7 @@ struct Peers {
 // 8 x 4096 bf16 tokens, forward and backward: 2048 channels in boxes 95 and 207 us, 2046 and 2047 in
 // rows 181 and 342, 235 and 445 (with bulk copies of whole rows 226 and 450, 277 and 545: the copy
 // unit takes some 16 cycles a row; element by element 2047 channels 690 and 1200).  8 x 2048 fp32
-// tokens of 2047 channels: pairs 204 and 293, rows, at the time, 179 and 388 (fewer blocks fit).
+// tokens of 2047 channels: pairs 208 and 302, rows, at the time, 179 and 388 (fewer blocks fit).
 enum CopyMode { kBoxes, kRows, kPairs };
 __device__ __forceinline__ void copy4(unsigned dst, const void *src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -580,7 +584,7 @@ cudaError_t with_form(ScanShape &s, gdr_dtype_t dtype, gdr_gate_t gate, gdr_sour
     auto by_gate = [&](auto t) {
         if (gate == GDR_GATE_SOFTPLUS) return by_source(t, integral_constant<int, kSoftplus>{});
         if (s.b <= 2.f) {
-            // (1 - e^-n) / n on [0, 2] by a polynomial fitted to it, relative error 1.4e-8
+            // (1 - e^-n) / n on [0, 2] by a polynomial fitted to it, within 1.8e-8 (4.1e-8 of itself at n = 2)
             static const double fit[kScanPoly] = {0.99999998631057,       -0.4999991992693423,  0.16665864060437813,
                                                   -0.04163556673545308,   0.008272895784878453, -0.0013234571801574847,
                                                   0.00015753673867873683, -1.0291639928970174e-05};

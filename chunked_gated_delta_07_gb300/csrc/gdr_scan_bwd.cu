@@ -14,7 +14,7 @@
 // in shared memory is read once.
 //
 // Measured (bf16): 8 x 4096 tokens of 2048 channels 205 us, 3.3 TB/s, 49% of a copy's rate; fp32, 8 x
-// 2048: 139 us, 72%.  Bound like the forward pass by its arithmetic in its order (57 instructions an
+// 2048: 138 us, 73%.  Bound like the forward pass by its arithmetic in its order (57 instructions an
 // element, 52% of the issue slots), on 256 blocks for 304 places: with two sequences to a block the
 // SMs that have one block end early, with one sequence to a block there are two rounds.
 #include <algorithm>

@@ -6,7 +6,7 @@
 // inputs of its run in registers, from the run's own pair to the second pass over it.
 //
 // Measured (2048 channels, bf16): 8 x 4096 tokens 92 to 95 us, 4.3 TB/s, 64% of a copy's rate; one
-// sequence of 262144 tokens 774 us, 62%.  fp32, 8 x 2048: 71 us, 85%.  What bounds the bf16 calls is
+// sequence of 262144 tokens 774 us, 62%.  fp32, 8 x 2048: 74 us, 82%.  What bounds the bf16 calls is
 // the arithmetic in its order: 29 instructions an element (14 of them the gate's), four warps to a
 // scheduler since 16 tokens' decays and inputs of two channels take 64 registers, and the steps
 // of a tile (its copy, the gates, two exchanges, the second pass) one after the other; issue slots
