@@ -366,9 +366,18 @@ struct Peers {
             if (done()) return true;
         return false;
     }
-    // After a wait that ran out: what peers have told is not all counted, and the cluster's barrier does
-    // not wait for such stores; a millisecond is a thousand times their way.  (With no wait run out
-    // every store has been counted, by the last step's wait.)
+    // The block's end; every thread calls, none with a copy under way.  Nobody leaves while a peer may
+    // still write to its memory: behind the cluster's barrier every peer has sent its last run.  With no wait
+    // run out all of them have been counted, by the last step's wait.  Where one has (a lost block), what
+    // was sent is not all counted, and the barrier does not wait for such stores: the block stays a
+    // millisecond longer, a thousand times their way.
+    __device__ __forceinline__ static void leave(bool lost, int cluster, int *status) {
+        lost = __syncthreads_or(lost);
+        if (lost && threadIdx.x == 0) set_status(status, GDR_ERR_TIMEOUT);
+        if (cluster == 1) return;
+        cluster_sync();
+        if (lost && threadIdx.x == 0) settle();
+    }
     __device__ __forceinline__ static void settle() {
         const uint64_t since = sm100::globaltimer_ns();
         while (sm100::globaltimer_ns() - since < 1000000) {}

@@ -299,11 +299,7 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
         }
     }
     ring.drain(lost);
-    if (__syncthreads_or(lost) && threadIdx.x == 0) {
-        set_status(status, GDR_ERR_TIMEOUT);
-        if (CS > 1) peers.settle();
-    }
-    if (CS > 1) cluster_sync();   // nobody leaves while a peer may still write to its memory
+    peers.leave(lost, CS, status);
 }
 
 template <typename T, int GATE, int SRC>
