@@ -47,7 +47,7 @@ struct ScanShape {
     const int32_t *cu;   // offsets of packed sequences, or null: N sequences of T_per tokens
     int N, T_per, total, D;
     float b;
-    float2 poly[kScanPoly];   // of kBoundedBy2: 1 - alpha = s sum_k poly[k] s^k, s the sigmoid (each twice)
+    float poly[kScanPoly];   // of kBoundedBy2: 1 - alpha = s sum_k poly[k] s^k, s the sigmoid
     int per_part;        // sequences of a part (a chain of tiles of its own)
     int parts, tiles, cluster;
 };
@@ -126,10 +126,10 @@ __device__ __forceinline__ Gate gate_of(float2 a, const ScanShape &shape) {
             const float2 c = make_float2(min_nan(e.x, 1e38f), min_nan(e.y, 1e38f));
             o.slope = mul2(mul2(s, both(-b)), mul2(c, s));
         }
-        float2 p = shape.poly[kScanPoly - 1];
+        float2 p = both(shape.poly[kScanPoly - 1]);
 #pragma unroll
         for (int k = kScanPoly - 2; k >= 0; --k)
-            p = make_float2(fmaf(p.x, s.x, shape.poly[k].x), fmaf(p.y, s.y, shape.poly[k].x));
+            p = make_float2(fmaf(p.x, s.x, shape.poly[k]), fmaf(p.y, s.y, shape.poly[k]));
         left = mul2(s, p);
         o.alpha = fma2(left, minus, one);
     } else if constexpr (GATE != kSoftplus) {
@@ -385,15 +385,16 @@ struct Peers {
 };
 
 // ---- tiles of raw inputs ------------------------------------------------------------------
-// BOXES: a TMA box of each tensor (rows and bases on 16-byte boundaries).  ROWS: each row's 16-byte
-// pieces that hold one of its channels, by a bulk copy; the lanes then move their run's channels to
-// where a box would have them.  PAIRS: a lane copies its own two channels (fp32).
+// BOXES: a TMA box of each tensor (rows and bases on 16-byte boundaries).  ROWS (bf16): the 16-byte pieces
+// of each row that hold one of its channels, each by a lane's asynchronous copy; the lanes then move their
+// run's channels to where a box would have them.  PAIRS (fp32): a lane copies its own two channels.
 //
 // 8 x 4096 bf16 tokens, forward and backward: 2048 channels in boxes 95 and 207 us, 2046 and 2047 in
 // rows 181 and 342, 235 and 445 (with bulk copies of whole rows 226 and 450, 277 and 545: the copy
 // unit takes some 16 cycles a row; element by element 2047 channels 690 and 1200).  8 x 2048 fp32
 // tokens of 2047 channels: pairs 208 and 302, rows, at the time, 179 and 388 (fewer blocks fit).
 enum CopyMode { kBoxes, kRows, kPairs };
+template <typename T, bool BOXES> constexpr CopyMode copy_mode() { return BOXES ? kBoxes : sizeof(T) == 2 ? kRows : kPairs; }
 __device__ __forceinline__ void copy4(unsigned dst, const void *src, int bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -404,26 +405,24 @@ __device__ __forceinline__ void copy16(unsigned dst, const void *src) {
 // A block's ring of DEPTH tiles of NT tensors, TOK tokens each; a lane's run is L of them.
 // Boxes have kernels of their own (BOXES).
 template <typename T, int L, int TOK, int NT, int DEPTH, bool BOXES> struct Ring {
+    static constexpr CopyMode kMode = copy_mode<T, BOXES>();
     static constexpr int kRow = kScanChannels * (int)sizeof(T);   // bytes of a row as it is read
     static constexpr int kRawRow = kRow + 16;                     // and of its pieces
+    static constexpr int kPitch = kMode == kRows ? kRawRow : kRow;   // from row to row, before rows are moved
+    static constexpr int kBytes = DEPTH * NT * TOK * kPitch;
     char *at;          // [DEPTH][NT] tiles of TOK rows, 128-byte aligned
     uint64_t *full;    // [DEPTH]: the slot's copies are there
-    int mode;
     int issued;        // tiles asked for by boxes
 
-    __host__ __device__ static constexpr int bytes(bool rows) { return DEPTH * NT * TOK * (rows ? kRawRow : kRow); }
-    __device__ __forceinline__ Ring(char *smem, uint64_t *bars, int mode_)
-        : at(smem), full(bars), mode(BOXES ? kBoxes : mode_), issued(0) {}
-    // Bytes from row to row before rows are moved.
-    __device__ __forceinline__ int pitch() const { return !BOXES && mode == kRows ? kRawRow : kRow; }
+    __device__ __forceinline__ Ring(char *smem, uint64_t *bars) : at(smem), full(bars), issued(0) {}
     // Thread 0, before the first use.
     __device__ __forceinline__ void init() {
         for (int i = 0; i < DEPTH; ++i) sm100::mbar_init(&full[i], 1);
     }
-    __device__ __forceinline__ char *tile(int slot, int tensor) const { return at + (slot * NT + tensor) * TOK * pitch(); }
+    __device__ __forceinline__ char *tile(int slot, int tensor) const { return at + (slot * NT + tensor) * TOK * kPitch; }
     // A lane's two channels of its run's first token; the others follow, kScanChannels elements apart.
     __device__ __forceinline__ T *run(int slot, int tensor, int first, int l) const {
-        return (T *)(tile(slot, tensor) + first * pitch()) + 2 * l;
+        return (T *)(tile(slot, tensor) + first * kPitch) + 2 * l;
     }
 
     // Every thread: asks for the tile from token `row` on, after the whole block is done with what
@@ -431,14 +430,14 @@ template <typename T, int L, int TOK, int NT, int DEPTH, bool BOXES> struct Ring
     // cycles; the warps take turns.
     __device__ __forceinline__ void ask(int slot, int turn, const CUtensorMap *const (&maps)[NT], const T *const (&src)[NT],
                                         int row, int lo, int hi, int c0, int D) {
-        if constexpr (BOXES) {
+        if constexpr (kMode == kBoxes) {
             if (threadIdx.x == 32 * (turn % (TOK / (2 * L)))) {
                 sm100::mbar_arrive_expect_tx(&full[slot], NT * TOK * kRow);
 #pragma unroll
                 for (int i = 0; i < NT; ++i) sm100::tma_load_2d(tile(slot, i), maps[i], c0, row, &full[slot]);
             }
             ++issued;
-        } else if (mode == kRows) {
+        } else if constexpr (kMode == kRows) {
             ask_rows(tile(slot, 0), src[0], src[1], src[NT - 1], row, lo, hi, c0, D);
         } else {
             ask_pairs(tile(slot, 0), src[0], src[1], src[NT - 1], row, lo, hi, c0, D);
@@ -450,6 +449,7 @@ template <typename T, int L, int TOK, int NT, int DEPTH, bool BOXES> struct Ring
     // cost the steps' code registers.)
     __device__ __noinline__ static void ask_rows(char *to, const T *s0, const T *s1, const T *s2, int row, int lo, int hi,
                                                  int c0, int D) {
+        static_assert(sizeof(T) == 2);
         const T *const src[3] = {s0, s1, s2};
         constexpr int kPieces = kRawRow / 16, kAtOnce = 32 / kPieces;
         const int lane = threadIdx.x & 31, mine = lane / kPieces, piece = lane % kPieces;
@@ -470,6 +470,7 @@ template <typename T, int L, int TOK, int NT, int DEPTH, bool BOXES> struct Ring
     }
     __device__ __noinline__ static void ask_pairs(char *to, const T *s0, const T *s1, const T *s2, int row, int lo, int hi,
                                                   int c0, int D) {
+        static_assert(sizeof(T) == 4);   // the copies' 4 bytes
         const T *const src[3] = {s0, s1, s2};
         const int lane = threadIdx.x & 31, c = c0 + 2 * (lane & 15);
         const int first = ((threadIdx.x >> 5) * 2 + (lane >> 4)) * L;
@@ -598,7 +599,7 @@ cudaError_t with_form(ScanShape &s, gdr_dtype_t dtype, gdr_gate_t gate, gdr_sour
                                                   -0.04163556673545308,   0.008272895784878453, -0.0013234571801574847,
                                                   0.00015753673867873683, -1.0291639928970174e-05};
             double n = s.b;
-            for (int k = 0; k < kScanPoly; ++k, n *= s.b) s.poly[k].x = s.poly[k].y = (float)(fit[k] * n);
+            for (int k = 0; k < kScanPoly; ++k, n *= s.b) s.poly[k] = (float)(fit[k] * n);
             return by_source(t, integral_constant<int, kBoundedBy2>{});
         }
         return by_source(t, integral_constant<int, kBounded>{});

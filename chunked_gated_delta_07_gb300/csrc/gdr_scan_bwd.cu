@@ -46,7 +46,7 @@ template <typename T, int GATE, int SRC, bool BOXES>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ BwdMaps maps, const T *x, const T *a, const T *dout, const float *__restrict__ h0,
                 const float *__restrict__ dhT, const float *__restrict__ states, T *dx, T *da, float *dh0,
-                int mode, int pairs, uint64_t limit_ns, int *status) {
+                int pairs, uint64_t limit_ns, int *status) {
     constexpr bool kFine = sizeof(T) == 4;
     extern __shared__ char smem[];
     __shared__ __align__(16) float4 agg[2][2][kWarps][16];   // the states' runs, and the gradients', last warp first
@@ -68,7 +68,7 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
                 dh0[(int64_t)n * D + c0 + lane] = dhT ? dhT[(int64_t)n * D + c0 + lane] : 0.f;
     const int t0 = p0 / kScanTile, t1 = (p1 + kScanTile - 1) / kScanTile, steps = (t1 - t0 + CS - 1) / CS;
     const bool many = last - first > 1;
-    BwdRing<T, BOXES> ring((char *)(((uintptr_t)smem + 127) & ~(uintptr_t)127), full, mode);
+    BwdRing<T, BOXES> ring((char *)(((uintptr_t)smem + 127) & ~(uintptr_t)127), full);
     if (threadIdx.x == 0) {
         ring.init();
         sm100::mbar_init(&bars[0], 1);
@@ -108,7 +108,7 @@ scan_bwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Bwd
             cur.seek(s, first, last, max(base, p0));
             inner = cur.from < base && cur.to > base + kScanTile;
             if (!lost) lost = !__all_sync(kFull, ring.wait(slot, use, limit_ns));
-            if (!BOXES && mode == kRows) ring.move(slot, src, base, c0, D);
+            if constexpr (ring.kMode == kRows) ring.move(slot, src, base, c0, D);
         }
         const bool cuts = CS == 1 ? there && !inner : many || i == steps - 1;   // a part's first token is in the last step
         T *tx = ring.run(slot, 0, run_at0, l), *ta = ring.run(slot, 1, run_at0, l);
@@ -311,17 +311,16 @@ cudaError_t launch_bwd_t(const ScanBwd &t, ScanShape s, int sms, int *status, cu
     };
     const bool boxes = s.total > 0 && plane(&maps.x, t.x) && plane(&maps.a, t.a) && plane(&maps.dout, t.dout);
     const uintptr_t outs = (uintptr_t)t.dx | (uintptr_t)t.da;
-    const int mode = boxes ? kBoxes : sizeof(T) == 2 ? kRows : kPairs;
     const int pairs = s.D % 2 == 0 && outs % (2 * sizeof(T)) == 0;
     auto run = [&](auto by_boxes, ScanRoom &known) {
         constexpr bool kB = by_boxes();
-        const int smem = BwdRing<T, kB>::bytes(mode == kRows) + 128;
+        const int smem = BwdRing<T, kB>::kBytes + 128;
         return scan_launch(scan_bwd_kernel<T, GATE, SRC, kB>, s, kThreads, smem, kScanTile, sms, known, "scan_bwd_kernel", stream,
                        maps, (const T *)t.x, (const T *)t.a, (const T *)t.dout, t.h0, t.dhT, t.states, (T *)t.dx, (T *)t.da,
-                       t.dh0, mode, pairs, scan_wait_ns(), status);
+                       t.dh0, pairs, scan_wait_ns(), status);
     };
     static ScanRoom boxed, other;
-    return mode == kBoxes ? run(std::true_type{}, boxed) : run(std::false_type{}, other);
+    return boxes ? run(std::true_type{}, boxed) : run(std::false_type{}, other);
 }
 
 }  // namespace

@@ -35,7 +35,7 @@ struct FwdMaps {
 template <typename T, int GATE, int SRC, bool BOXES>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm<T>)
 scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ FwdMaps maps, const T *x, const T *a, const float *h0, T *out, float *hT,
-                float *states, int mode, int pairs, uint64_t limit_ns, int *status) {
+                float *states, int pairs, uint64_t limit_ns, int *status) {
     constexpr bool kFine = sizeof(T) == 4;
     extern __shared__ char smem[];
     __shared__ __align__(16) float4 agg[2][kWarps][16];
@@ -57,7 +57,7 @@ scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Fwd
                 hT[(int64_t)n * D + c0 + lane] = h0 ? h0[(int64_t)n * D + c0 + lane] : 0.f;
     const int t0 = p0 / kTok, t1 = (p1 + kTok - 1) / kTok, steps = (t1 - t0 + CS - 1) / CS;
     const bool many = last - first > 1;
-    FwdRing<T, BOXES> ring((char *)(((uintptr_t)smem + 127) & ~(uintptr_t)127), full, mode);
+    FwdRing<T, BOXES> ring((char *)(((uintptr_t)smem + 127) & ~(uintptr_t)127), full);
     if (threadIdx.x == 0) {
         ring.init();
         sm100::mbar_init(&bars[0], 1);
@@ -92,7 +92,7 @@ scan_fwd_kernel(const __grid_constant__ ScanShape s, const __grid_constant__ Fwd
             cur.seek(s, first, last, max(base, p0));
             inner = cur.from < base && cur.to > base + kTok;
             if (!lost) lost = !__all_sync(kFull, ring.wait(slot, use, limit_ns));
-            if (!BOXES && mode == kRows) ring.move(slot, src, base, c0, D);
+            if constexpr (ring.kMode == kRows) ring.move(slot, src, base, c0, D);
         }
         const bool cuts = CS == 1 ? there && !inner : many || i == 0;
         T *tx = ring.run(slot, 0, run_at0, l), *ta = ring.run(slot, 1, run_at0, l);
@@ -240,17 +240,15 @@ cudaError_t launch_fwd_t(const ScanFwd &t, ScanShape s, int sms, int *status, cu
         return tc_make_plane_map(m, p, kType, s.D, s.total, kScanChannels, kTok);
     };
     const bool boxes = s.total > 0 && plane(&maps.x, t.x) && plane(&maps.a, t.a);
-    // fp32 channels by pairs: their rows leave room for fewer blocks
-    const int mode = boxes ? kBoxes : sizeof(T) == 2 ? kRows : kPairs;
     const int pairs = s.D % 2 == 0 && (uintptr_t)t.out % (2 * sizeof(T)) == 0;
     auto run = [&](auto by_boxes, ScanRoom &known) {
         constexpr bool kB = by_boxes();
-        const int smem = FwdRing<T, kB>::bytes(mode == kRows) + 128;
+        const int smem = FwdRing<T, kB>::kBytes + 128;
         return scan_launch(scan_fwd_kernel<T, GATE, SRC, kB>, s, kThreads, smem, kTok, sms, known, "scan_fwd_kernel", stream, maps,
-                       (const T *)t.x, (const T *)t.a, t.h0, (T *)t.out, t.hT, t.states, mode, pairs, scan_wait_ns(), status);
+                       (const T *)t.x, (const T *)t.a, t.h0, (T *)t.out, t.hT, t.states, pairs, scan_wait_ns(), status);
     };
     static ScanRoom boxed, other;
-    return mode == kBoxes ? run(std::true_type{}, boxed) : run(std::false_type{}, other);
+    return boxes ? run(std::true_type{}, boxed) : run(std::false_type{}, other);
 }
 
 // One (sequence, channel) to a thread, the next token's inputs on their way while a token is
