@@ -37,9 +37,10 @@ namespace norm {
 
 // As the layer norm's, but of single elements rows of up to 4096 go to the smallest power of two of
 // threads with 8 each, there every other one (16384 rows x 2047 bf16 on 256 threads against 512:
-// add_norm 175 -> 66 us, its backward 147 -> 86, norm_gate 140 -> 77, its backward 169 -> 107), and,
-// where `wide` says so, rows of 4097 to 8192 to 1024 threads: three tensors' 16 elements do not fit
-// into a thread (8192 rows x 4097 bf16: norm_gate 157 -> 147 us, its backward 373 -> 292, add_norm's
+// add_norm 175 -> 66 us, its backward 147 -> 86, norm_gate 140 -> 77, its backward 169 -> 107; from 2049
+// columns on both take 512, and 256 threads of 16 were not measured there: 11000 rows x 3001 add_norm 128 us,
+// norm_gate 105).  Where `wide` says so, rows of 4097 to 8192 go to 1024 threads: three tensors' 16 elements do
+// not fit into a thread (8192 rows x 4097 bf16: norm_gate 157 -> 147 us, its backward 373 -> 290, add_norm's
 // 287 -> 245; add_norm itself 87 -> 121, which keeps 512).
 inline NormPick pick_block(int D, size_t es, bool pieces, bool wide) {
     if (!pieces && D <= 4096) {
@@ -51,7 +52,9 @@ inline NormPick pick_block(int D, size_t es, bool pieces, bool wide) {
     return pick_layout(D, es, pieces);
 }
 
-// sigmoid(z); within 2^-20 of its value for bf16 tensors.  exp(-z) may be inf, giving 0.
+// sigmoid(z): within 2^-21 of its value for fp32 tensors; for bf16 ones, whose exponential and division are
+// the fast ones, within (4 + 1.2 |z|) 2^-23, far below a step of bf16.  exp(-z) may be inf, which
+// gives 0: below z = -88.7, for bf16 tensors below -87.3, where the value is below 2^-126.
 template <bool FINE> __device__ __forceinline__ float sigmoid_of(float z) {
     if constexpr (FINE) return __frcp_rn(1.f + expf(-z));
     return __fdividef(1.f, 1.f + __expf(-z));

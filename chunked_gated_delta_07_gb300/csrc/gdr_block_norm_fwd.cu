@@ -4,7 +4,7 @@
 // registers of a group of threads, 8 elements each, and the next rows of every input are on
 // their way through a ring in shared memory; the variance is the mean of squared deviations.
 // Measured (bf16): add_norm 32768 x 2048 95 us, 5.6 TB/s, 85% of a copy's rate; norm_gate 524288 x
-// 128 with 16 weight rows 65 to 68 us, 6.0 TB/s, 89 to 93% (28 instructions an element, 79% of the
+// 128 with 16 weight rows 65 to 68 us, 6.0 TB/s, 89 to 93% (28 instructions an element, 78% of the
 // issue slots).
 // add_norm norms the sum as it is stored, rounded to the tensors' type, so that the backward
 // pass, which reads that sum, differentiates what was computed.

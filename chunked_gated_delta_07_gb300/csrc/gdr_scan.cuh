@@ -389,10 +389,10 @@ struct Peers {
 // of each row that hold one of its channels, each by a lane's asynchronous copy; the lanes then move their
 // run's channels to where a box would have them.  PAIRS (fp32): a lane copies its own two channels.
 //
-// 8 x 4096 bf16 tokens, forward and backward: 2048 channels in boxes 95 and 207 us, 2046 and 2047 in
-// rows 181 and 342, 235 and 445 (with bulk copies of whole rows 226 and 450, 277 and 545: the copy
+// 8 x 4096 bf16 tokens, forward and backward: 2048 channels in boxes 95 and 204 us, 2046 and 2047 in
+// rows 184 and 340, 236 and 448 (with bulk copies of whole rows 226 and 450, 277 and 545: the copy
 // unit takes some 16 cycles a row; element by element 2047 channels 690 and 1200).  8 x 2048 fp32
-// tokens of 2047 channels: pairs 208 and 302, rows, at the time, 179 and 388 (fewer blocks fit).
+// tokens of 2047 channels: pairs 206 and 287, rows, at the time, 179 and 388 (fewer blocks fit).
 enum CopyMode { kBoxes, kRows, kPairs };
 template <typename T, bool BOXES> constexpr CopyMode copy_mode() { return BOXES ? kBoxes : sizeof(T) == 2 ? kRows : kPairs; }
 __device__ __forceinline__ void copy4(unsigned dst, const void *src, int bytes) {

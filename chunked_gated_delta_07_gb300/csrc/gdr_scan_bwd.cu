@@ -13,8 +13,8 @@
 // after the chaining one multiplication and addition each gives what was missing, and the tile
 // in shared memory is read once.
 //
-// Measured (bf16): 8 x 4096 tokens of 2048 channels 205 us, 3.3 TB/s, 49% of a copy's rate; fp32, 8 x
-// 2048: 138 us, 73%.  Bound like the forward pass by its arithmetic in its order (57 instructions an
+// Measured (bf16): 8 x 4096 tokens of 2048 channels 201 to 204 us, 3.3 TB/s, 50% of a copy's rate; fp32, 8 x
+// 2048: 136 us, 74%.  Bound like the forward pass by its arithmetic in its order (57 instructions an
 // element, 52% of the issue slots), on 256 blocks for 304 places: with two sequences to a block the
 // SMs that have one block end early, with one sequence to a block there are two rounds.
 #include <algorithm>

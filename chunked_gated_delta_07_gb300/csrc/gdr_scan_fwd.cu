@@ -5,12 +5,12 @@
 // channels: copies bring the tiles ahead into shared memory while a lane keeps the decays and
 // inputs of its run in registers, from the run's own pair to the second pass over it.
 //
-// Measured (2048 channels, bf16): 8 x 4096 tokens 92 to 95 us, 4.3 TB/s, 64% of a copy's rate; one
-// sequence of 262144 tokens 774 us, 62%.  fp32, 8 x 2048: 74 us, 82%.  What bounds the bf16 calls is
+// Measured (2048 channels, bf16): 8 x 4096 tokens 93 to 95 us, 4.3 TB/s, 64% of a copy's rate; one
+// sequence of 262144 tokens 777 us, 62%.  fp32, 8 x 2048: 74 us, 82%.  What bounds the bf16 calls is
 // the arithmetic in its order: 29 instructions an element (14 of them the gate's), four warps to a
 // scheduler since 16 tokens' decays and inputs of two channels take 64 registers, and the steps
 // of a tile (its copy, the gates, two exchanges, the second pass) one after the other; issue slots
-// 62% taken.  Runs of 8 tokens with more blocks on an SM: 128 to 150 us (the exchanges weigh twice).
+// 61% taken.  Runs of 8 tokens with more blocks on an SM: 128 to 150 us (the exchanges weigh twice).
 #include <algorithm>
 
 #include "gdr_scan.cuh"

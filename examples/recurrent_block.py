@@ -96,8 +96,8 @@ class RecurrentBlock(torch.nn.Module):
 
     @torch.no_grad()
     def serve(self, u, r, state):
-        """A prompt or single tokens: u, r [B, T, width], state [B, heads head_dim] fp32, updated in
-        place.  Returns (u, r)."""
+        """A prompt or single tokens: u, r [B, T, width], state [B, heads head_dim] fp32; r and state are
+        updated in place.  Returns (u, r)."""
         y, _, _, _ = gdr.add_norm_fwd(u, r, self.norm, scale=self.scale, sum_out=r, want_stats=False)
         x, a = y @ self.w_x, y @ self.w_a + self.far
         if u.shape[1] == 1:

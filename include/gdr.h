@@ -520,12 +520,15 @@ typedef enum {
  *   states     [total / 128, D] fp32, or NULL: row i is the state behind token 128 i + 127 of
  *              the token axis (all B T tokens one after the other), which the backward pass
  *              starts from.  total / 128 is rounded down.
- *   b          bound of the bounded gate, > 0 and finite (not looked at for softplus)
+ *   b          bound of the bounded gate, > 0 and finite, one for all channels and without a
+ *              gradient (not looked at for softplus)
  * 1 <= D <= 2^22; B >= 1; T >= 0; at most 2^31 - 4097 tokens in all and 2^40 elements; sequences of no
  * tokens pass h0 on to hT.  Element alignment is enough (16-byte pointers with D a multiple of
  * 16 bytes are read fastest).  fp32 inside.  A NaN or an infinity stays in its channel's state
  * to the end of the sequence (an infinity may become a NaN); other channels and sequences
- * never see it.  Outputs must not overlap inputs.  Bad offsets: GDR_ERR_BAD_SEQLENS in the
+ * never see it.  The decays of a stretch of tokens are multiplied in fp32 before they meet the state, so
+ * that what is left of a state (backward: of a gradient) behind it may be off by 2^-150 of that state,
+ * besides the roundings in proportion.  Outputs must not overlap inputs.  Bad offsets: GDR_ERR_BAD_SEQLENS in the
  * status word, nothing is written; waits are bounded (GDR_ERR_TIMEOUT).  No scratch; asynchronous
  * on `stream`; deterministic.
  */
